@@ -293,6 +293,95 @@ msm_status msm_scan_complex_bwd(const void* x, const void* delta, const float* A
                                 float alpha, msm_dtype io, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Operators of the block around the scan: the gated delta rule (a recurrence with a matrix
+ * state, beside the scan's diagonal one), layer norm, and the norm and clipping of gradients.
+ * The conventions above hold for them; parameters, gates, states and statistics are fp32, and
+ * workspaces are 16-byte aligned (MSM_ERR_INVALID_ARG otherwise).
+ * ------------------------------------------------------------------------------------------- */
+
+/* Gated delta rule.  For every sequence and value head h, with a state S of K x V and the
+ * query / key head h / (H / Hk):
+ *     e_t = v_t - exp(g_t) S_{t-1}^T k_t          (what the decayed state gets wrong at k_t)
+ *     S_t = exp(g_t) S_{t-1} + beta_t k_t e_t^T
+ *     o_t = scale S_t^T q_t
+ * q, k: (Bt, L, Hk, K), v, o: (Bt, L, H, V) in the io dtype; g (log decay, normally <= 0) and
+ * beta: (Bt, L, H) fp32; S0, last_S: (Bt, H, K, V) fp32, S0 NULL meaning zero, last_S written
+ * when non-NULL.
+ * Packed sequences: with seq_offsets (device memory, Bt + 1 int32 values, not decreasing,
+ * from 0 to L) the token arrays hold L rows in all, (L, Hk, K) and so on, and sequence b is
+ * rows seq_offsets[b] ... seq_offsets[b+1] - 1; it may be empty, and then last_S = S0.
+ * The offsets are read on the device: rows outside the arrays are never touched, whatever they
+ * hold, but a token that no sequence covers leaves its output unwritten.
+ * Requirements: Bt, L, Hk, H, K, V >= 1, H a multiple of Hk, K <= 256 (else
+ * MSM_ERR_UNSUPPORTED), V <= 2^20, H <= 65535, fewer than 2^31 tokens, scale finite.  Outputs
+ * must not overlap an input.  All sums are fp32; with bf16 inputs the products run on bf16
+ * matrix cores over values cut into parts that keep 24 bits (16 bits where the result is
+ * rounded to bf16 anyway). */
+size_t msm_delta_rule_fwd_workspace_bytes(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K,
+                                          int64_t V, int32_t packed, msm_dtype io);
+msm_status msm_delta_rule_fwd(const void* q, const void* k, const void* v, const float* g,
+                              const float* beta, const int32_t* seq_offsets, const float* S0,
+                              void* o, float* last_S, int64_t Bt, int64_t L, int64_t Hk, int64_t H,
+                              int64_t K, int64_t V, float scale, msm_dtype io, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(do o) + <dlast_S, last_S> (dlast_S NULL: zero): dq, dk, dv in the io dtype
+ * (dq and dk summed over the value heads that share a key head), dg, dbeta fp32, dS0 fp32 when
+ * non-NULL.  The forward is recomputed inside; nothing of it is saved.  The workspace holds two
+ * states per chunk of 64 tokens.  Everything else as msm_delta_rule_fwd. */
+size_t msm_delta_rule_bwd_workspace_bytes(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K,
+                                          int64_t V, int32_t packed, msm_dtype io);
+msm_status msm_delta_rule_bwd(const void* q, const void* k, const void* v, const float* g,
+                              const float* beta, const int32_t* seq_offsets, const float* S0,
+                              const void* do_, const float* dlast_S, void* dq, void* dk, void* dv,
+                              float* dg, float* dbeta, float* dS0, int64_t Bt, int64_t L,
+                              int64_t Hk, int64_t H, int64_t K, int64_t V, float scale,
+                              msm_dtype io, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* One token of the gated delta rule for Bt sequences: q, k (Bt, Hk, K), v, o (Bt, H, V) io;
+ * g, beta (Bt, H) fp32; S (Bt, H, K, V) fp32, read and overwritten IN PLACE.  Needs no
+ * workspace.  S must not overlap anything else. */
+msm_status msm_delta_rule_step(const void* q, const void* k, const void* v, const float* g,
+                               const float* beta, float* S, void* o, int64_t Bt, int64_t Hk,
+                               int64_t H, int64_t K, int64_t V, float scale, msm_dtype io,
+                               void* stream);
+
+/* Layer norm over the last dimension of x (rows, D):
+ *     y = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ * x, y io dtype; weight, bias (D,) fp32, NULL meaning ones and zeros; mean, rstd (rows,) fp32,
+ * written when non-NULL.  1 <= rows < 2^31, 1 <= D <= 2^30, eps >= 0 and finite.  y must not
+ * overlap x. */
+msm_status msm_layer_norm_fwd(const void* x, const float* weight, const float* bias, void* y,
+                              float* mean, float* rstd, int64_t rows, int64_t D, float eps,
+                              msm_dtype io, void* stream);
+
+/* Gradients of sum(dy y) from the forward's mean and rstd: dx (rows, D) io; dweight, dbias (D,)
+ * fp32, each written when non-NULL (the workspace may be NULL when both are). */
+size_t msm_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t D, msm_dtype io);
+msm_status msm_layer_norm_bwd(const void* x, const float* weight, const void* dy,
+                              const float* mean, const float* rstd, void* dx, float* dweight,
+                              float* dbias, int64_t rows, int64_t D, msm_dtype io,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Global 2-norm over count tensors: grads[i] points to numel[i] contiguous elements of dtype
+ * dtypes[i] (MSM_F32 or MSM_BF16, mixed freely; numel[i] may be 0).  The three arrays are HOST
+ * memory, read during the call only.  norm: one fp32 value on the device.  count may be 0. */
+size_t msm_grad_norm_workspace_bytes(int64_t count);
+msm_status msm_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes,
+                         int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Clipping by the global norm: out[i] = grads[i] * min(1, max_norm / (norm + eps)); norm
+ * receives the norm before clipping.  out NULL, or out[i] == grads[i], scales in place (and
+ * writes nothing when the factor is 1); otherwise out[i] must not overlap a gradient.  A norm
+ * that is NaN makes every gradient NaN; an infinite norm scales by 0.  max_norm >= 0, eps >= 0.
+ * Workspace as msm_grad_norm. */
+msm_status msm_grad_clip(const void* const* grads, void* const* out, const int64_t* numel,
+                         const int32_t* dtypes, int64_t count, float max_norm, float eps,
+                         float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,6 +14,9 @@ fallback implementation.
                                delta_softplus=True)
     grads = msm_selective_scan_bwd(x, delta, A, B, C, dy, 0.9, 1.0, Dskip, z=z, delta_bias=bias,
                                    delta_softplus=True)        # also dz, ddelta_bias
+
+The operators of the block around the scan (gated delta rule, layer norm, gradient clipping) are
+in ``ops`` and are importable from here under their C names too.
 """
 from __future__ import annotations
 
@@ -124,6 +127,7 @@ def load_library():
     lib.msm_scan_complex_bwd.argtypes = [P] * 19 + [I64, I64, I64, I64, F, F, ctypes.c_int, P, SZ,
                                                     P]
     lib.msm_scan_complex_bwd.restype = ctypes.c_int
+    ops.declare(lib)
     _lib = lib
     return lib
 
@@ -641,3 +645,14 @@ def msm_scan_complex_bwd(x, delta, A, B, C, dy, beta, alpha, Dskip=None, *, h0=N
     if st != 0:
         raise MsmError(st, "msm_scan_complex_bwd")
     return o
+
+
+# ----------------------------------------------------------------------------------------------
+# operators of the block around the scan
+# ----------------------------------------------------------------------------------------------
+
+from . import ops  # noqa: E402
+from .ops import *  # noqa: E402,F401,F403
+
+__all__ += ops.__all__
+EXPORTED_SYMBOLS += ops.SYMBOLS

@@ -17,9 +17,13 @@ LIB = os.path.join(PKG, "libmsm.so")
 # (source, extra flags): the recurrence kernels are built once per (bf16 I/O, variant) pair --
 # variant 0 plain, 1 fused extras, 2 fused extras with the zero-order hold -- all in parallel
 _PARTS = [("-DMSM_IO_BF16=%d" % io, "-DMSM_EXT=%d" % ext) for io in (0, 1) for ext in (0, 1, 2)]
+# the chunked gated delta rule: one build per I/O type and padded key size
+_DELTA = [("-DMSM_IO_BF16=%d" % io, "-DMSM_KP=%d" % kp) for io in (0, 1) for kp in (32, 64, 128, 256)]
 SOURCES = ([("msm_api.cpp", ()), ("msm_launch.hip", ()), ("msm_bwd_wide.hip", ()),
             ("msm_step.hip", ()), ("msm_cfwd.hip", ()), ("msm_cbwd.hip", ())]
-           + [("msm_fwd.hip", f) for f in _PARTS] + [("msm_bwd.hip", f) for f in _PARTS])
+           + [("msm_fwd.hip", f) for f in _PARTS] + [("msm_bwd.hip", f) for f in _PARTS]
+           + [("ops_api.cpp", ()), ("ops_delta_step.hip", ()), ("ops_norm.hip", ()),
+              ("ops_clip.hip", ())] + [("ops_delta.hip", f) for f in _DELTA])
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
