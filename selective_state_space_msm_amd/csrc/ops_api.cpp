@@ -70,6 +70,9 @@ msm_status delta_shape(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K, 
   s->NT = packed ? 1 : ceil_div(L, s->C);
   s->nslots = packed ? L / s->C + Bt : Bt * s->NT;
   if (s->nslots > kGridX) return MSM_ERR_INVALID_ARG;
+  // the rows of a chunk are addressed with 32-bit byte offsets
+  const int64_t es = io == MSM_BF16 ? 2 : 4, widest = Hk * K > H * V ? Hk * K : H * V;
+  if (s->C * widest * es >= ((int64_t)1 << 31)) return MSM_ERR_UNSUPPORTED;
   return MSM_OK;
 }
 
@@ -79,7 +82,8 @@ struct DeltaLayout {
 
 DeltaLayout delta_layout(const DeltaShape& s, msm_dtype io, bool bwd) {
   const size_t n = (size_t)(s.nslots * s.H), C = (size_t)s.C, KP = (size_t)s.KP, VP = (size_t)s.VP;
-  const size_t mat = align_up(n * C * C * (io == MSM_BF16 ? 3 * 2 : 4));
+  // blocks of 32 x 32 on and below the diagonal
+  const size_t mat = n * (1024 * (C / 32) * (C / 32 + 1) / 2) * (io == MSM_BF16 ? 3 * 2 : 4);
   DeltaLayout l{};
   size_t at = 0;
   auto take = [&at](size_t bytes) {

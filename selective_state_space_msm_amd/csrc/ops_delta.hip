@@ -44,8 +44,10 @@ constexpr int KP = MSM_KP;
 constexpr int C = delta_chunk(MSM_IO_BF16, KP);
 constexpr int NB = KP / 32;       // blocks of 32 state rows
 constexpr int CB = C / 32;        // blocks of 32 tokens
-constexpr int LD = KP + Math::pad;
 constexpr int LDT = C + Math::pad;
+constexpr int UK = KP / Math::kPer;                 // 16-byte units of a row of keys
+constexpr int UT = 32 / Math::kPer;                 // and of a row of a chunk matrix's blocks
+using TriM = Tri<Math, C>;
 constexpr int TP = Math::kPlanes;
 constexpr int kVec = 5 * C;
 constexpr int kDots = 4 * C + 4;
@@ -110,10 +112,27 @@ __device__ __forceinline__ void invert(const float* Ms, float* Ti, int wave, int
   __syncthreads();
 }
 
+// Keys and queries of a chunk into LDS.
+template <int THREADS>
+__device__ __forceinline__ void stage_two(E* Ks, E* Qs, __amdgpu_buffer_rsrc_t rk, __amdgpu_buffer_rsrc_t rq,
+                                          uint32_t stride, int K, bool vec, int tid) {
+  using Stage = RowStage<Math, KP, C, THREADS>;
+  if (vec) {
+    Stage k, q;
+    k.fetch(rk, stride, K, tid);
+    q.fetch(rq, stride, K, tid);
+    k.put(Ks, tid);
+    q.put(Qs, tid);
+  } else {
+    Stage::by_element(Ks, rk, stride, K, tid);
+    Stage::by_element(Qs, rq, stride, K, tid);
+  }
+}
+
 template <bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
-  __shared__ __attribute__((aligned(16))) E Ks[C * LD];
-  __shared__ __attribute__((aligned(16))) E Qs[C * LD];
+  __shared__ __attribute__((aligned(16))) E Ks[C * KP];
+  __shared__ __attribute__((aligned(16))) E Qs[C * KP];
   __shared__ __attribute__((aligned(16))) float Ms[C * LDM];
   __shared__ __attribute__((aligned(16))) float Ti[C * LDM];
   __shared__ double Gd[C];
@@ -122,10 +141,10 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   const int64_t slot = blockIdx.x, h = blockIdx.y;
   const ChunkRows ch = chunk_rows<C>(p, slot);
   if (ch.n == 0) return;
-  const int64_t sh = slot * p.H + h, hk = h / (p.H / p.Hk), stride = p.Hk * p.K;
-  const int64_t at = (ch.row0 * p.Hk + hk) * p.K;
-  stage_rows<Math, KP, C, LD, 256>(Ks, static_cast<const E*>(p.k) + at, stride, ch.n, (int)p.K, p.vec_k, tid);
-  stage_rows<Math, KP, C, LD, 256>(Qs, static_cast<const E*>(p.q) + at, stride, ch.n, (int)p.K, p.vec_k, tid);
+  const int64_t sh = slot * p.H + h, hk = h / (p.H / p.Hk);
+  const auto rk = head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, Math::es, ch.n);
+  const auto rq = head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, Math::es, ch.n);
+  stage_two<256>(Ks, Qs, rk, rq, (uint32_t)(p.Hk * p.K * Math::es), (int)p.K, p.vec_k, tid);
   if (wave == 0) {
     // running sum of the log decay in fp64: its differences keep fp32 accuracy
     const bool on = lane < ch.n;
@@ -154,17 +173,18 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   }
   __syncthreads();
   // Gram tiles on and below the diagonal; 16 x 16, one wavefront each
-  TE* Pg = static_cast<TE*>(p.P) + sh * TP * C * C;
-  TE* Mg = BWD ? static_cast<TE*>(p.M) + sh * TP * C * C : nullptr;
+  TE* Pg = static_cast<TE*>(p.P) + sh * TP * TriM::kPlane;
+  TE* Mg = BWD ? static_cast<TE*>(p.M) + sh * TP * TriM::kPlane : nullptr;
   for (int t = wave; t < (C / 16) * (C / 16); t += 4) {
     const int mt = t / (C / 16), nt = t % (C / 16);
+    if (nt / 2 > mt / 2) continue;  // no block is kept there
     f32x4 kk = zero4(), qk = zero4();
     if (nt <= mt) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const auto B = Math::load<1>(Ks + (16 * nt + n) * LD + 32 * b + 8 * j, 0);
-        Math::mma(kk, Math::load<1>(Ks + (16 * mt + n) * LD + 32 * b + 8 * j, 0), B);
-        Math::mma(qk, Math::load<1>(Qs + (16 * mt + n) * LD + 32 * b + 8 * j, 0), B);
+        const auto B = load_row<Math, UK, 1>(Ks, 16 * nt + n, 32 * b + 8 * j, 0);
+        Math::mma(kk, load_row<Math, UK, 1>(Ks, 16 * mt + n, 32 * b + 8 * j, 0), B);
+        Math::mma(qk, load_row<Math, UK, 1>(Qs, 16 * mt + n, 32 * b + 8 * j, 0), B);
       }
     }
 #pragma unroll
@@ -173,21 +193,27 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
       const float D = col <= row ? exp_of(Gd[row] - Gd[col]) : 0.f;
       const float m = col < row ? D * kk[r] : 0.f;
       Ms[row * LDM + col] = m * bt[col];
-      Math::store1<TP>(Pg + row * C + col, C * C, col <= row ? p.scale * D * qk[r] : 0.f);
-      if (BWD) Math::store1<TP>(Mg + row * C + col, C * C, m);
+      Math::store1<TP>(Pg + TriM::at(row, col), TriM::kPlane, col <= row ? p.scale * D * qk[r] : 0.f);
+      if (BWD) Math::store1<TP>(Mg + TriM::at(row, col), TriM::kPlane, m);
     }
   }
   __syncthreads();
   invert(Ms, Ti, wave, lane);
-  TE* Tg = static_cast<TE*>(p.T) + sh * TP * C * C;
+  TE* Tg = static_cast<TE*>(p.T) + sh * TP * TriM::kPlane;
   for (int u = tid; u < C * C / 8; u += 256) {
     const int row = u / (C / 8), c = (u % (C / 8)) * 8;
+    if (c / 32 > row / 32) continue;
     f32x4 a = zero4(), b = zero4();
     if (c / 16 <= row / 16) {  // blocks above the diagonal were not written
       a = *reinterpret_cast<const f32x4*>(Ti + row * LDM + c);
       b = *reinterpret_cast<const f32x4*>(Ti + row * LDM + c + 4);
     }
-    Math::store_planes<TP>(Tg + row * C + c, C * C, a, b);
+    if constexpr (Math::bf16) {
+      Math::store_planes<TP>(Tg + TriM::at(row, c), TriM::kPlane, a, b);
+    } else {
+      *reinterpret_cast<f32x4*>(Tg + TriM::at(row, c)) = a;
+      *reinterpret_cast<f32x4*>(Tg + TriM::at(row, c + 4)) = b;
+    }
   }
 }
 
@@ -199,35 +225,134 @@ struct Cols {
   f32x4 t[BLOCKS][2];
 };
 
-// Rows of this lane: row0 + 8 j + 4 s + r of every 32-row block.
-template <class IO, int BLOCKS>
-__device__ __forceinline__ Cols<BLOCKS> load_cols(const IO* base, int64_t stride, int rows, bool col_ok, int j) {
+template <int BLOCKS>
+__device__ __forceinline__ Cols<BLOCKS> zero_cols() {
   Cols<BLOCKS> x;
 #pragma unroll
-  for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 32 * b + 8 * j + 4 * s + r;
-        float v = 0.f;
-        if (col_ok && row < rows) {
-          if constexpr (sizeof(IO) == 2)
-            v = MathBF16::widen(base[row * stride]);
-          else
-            v = base[row * stride];
-        }
-        x.t[b][s][r] = v;
-      }
+  for (int b = 0; b < BLOCKS; ++b) x.t[b][0] = x.t[b][1] = zero4();
   return x;
 }
 
-// Left factor rows of a tile with permuted row numbering: row 32 b + 8 (m / 4) + 4 s + m % 4 for
-// lane m.
-__device__ __forceinline__ int perm_row(int b, int s, int lane) {
-  const int m = lane & 15;
-  return 32 * b + 8 * (m >> 2) + 4 * s + (m & 3);
+// f(b, t, r, row) for every value a lane holds; row is the lane's row less 8 j.
+template <int BLOCKS, class F>
+__device__ __forceinline__ void each(F f) {
+#pragma unroll
+  for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) f(b, t, r, 32 * b + 4 * t + r);
 }
+
+// fp32 columns through a resource whose rows are `stride` bytes apart; `at` is this lane's first
+// row and column.
+template <int BLOCKS>
+__device__ __forceinline__ Cols<BLOCKS> load_cols(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t stride) {
+  Cols<BLOCKS> x;
+  each<BLOCKS>([&](int b, int t, int r, int row) { x.t[b][t][r] = io<float>::bload(rs, at + row * stride, 0); });
+  return x;
+}
+template <int BLOCKS>
+__device__ __forceinline__ void store_cols(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t stride, const Cols<BLOCKS>& x) {
+  each<BLOCKS>([&](int b, int t, int r, int row) { io<float>::bstore(rs, at + row * stride, 0, x.t[b][t][r]); });
+}
+
+// The chunk's rows of v, o or do: raw I/O elements between load and use.
+using IO = io<Math::storage>;
+struct RawCols {
+  IO::raw v[8 * CB];
+  __device__ __forceinline__ void fetch(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t stride) {
+    each<CB>([&](int b, int t, int r, int row) { v[8 * b + 4 * t + r] = IO::bload(rs, at + row * stride, 0); });
+  }
+  __device__ __forceinline__ Cols<CB> widen() const {
+    Cols<CB> x;
+    each<CB>([&](int b, int t, int r, int) { x.t[b][t][r] = IO::widen(v[8 * b + 4 * t + r]); });
+    return x;
+  }
+};
+__device__ __forceinline__ void store_out(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t stride, const Cols<CB>& x) {
+  each<CB>([&](int b, int t, int r, int row) { IO::bstore(rs, at + row * stride, 0, x.t[b][t][r]); });
+}
+
+// Left factor rows of a tile with permuted row numbering: row 32 b + 8 (m / 4) + 4 t + m % 4 for
+// lane m.
+__device__ __forceinline__ int perm_row(int b, int t, int lane) {
+  const int m = lane & 15;
+  return 32 * b + 8 * (m >> 2) + 4 * t + (m & 3);
+}
+
+// c += left x B for a left factor of keys or queries, 32 state rows per block.
+template <int N>
+__device__ __forceinline__ void mma_rows(Cols<CB>& c, const E* lds, int b, const Part<N>& B, int lane, int j) {
+#pragma unroll
+  for (int rb = 0; rb < CB; ++rb)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      Math::mma(c.t[rb][t], load_row<Math, UK, 1>(lds, perm_row(rb, t, lane), 32 * b + 8 * j, 0), B);
+}
+// c += (chunk matrix) B, or its transpose
+template <int NA, int NB_>
+__device__ __forceinline__ void mma_tri(Cols<CB>& c, const TE* lds, const Part<NB_> (&B)[CB], int lane, int j) {
+#pragma unroll
+  for (int rb = 0; rb < CB; ++rb)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int b = 0; b <= rb; ++b)
+        Math::mma(c.t[rb][t], load_row<Math, UT, NA>(lds + TriM::block(rb, b), perm_row(0, t, lane), 8 * j, TriM::kPlane), B[b]);
+}
+template <int NA, int NB_>
+__device__ __forceinline__ void mma_tri_t(Cols<CB>& c, const TE* lds, const Part<NB_> (&B)[CB], int lane, int j) {
+#pragma unroll
+  for (int rb = 0; rb < CB; ++rb)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int b = rb; b < CB; ++b)
+        Math::mma(c.t[rb][t], load_col<Math, UT, NA>(lds + TriM::block(b, rb), 8 * j, 4 * t, 8, lane, TriM::kPlane), B[b]);
+}
+template <int N>
+__device__ __forceinline__ void split_all(Part<N> (&B)[CB], const Cols<CB>& x) {
+#pragma unroll
+  for (int b = 0; b < CB; ++b) B[b] = Math::split<N>(x.t[b][0], x.t[b][1]);
+}
+
+// What a chunk needs, fetched while the chunk before it is computed.
+template <int TRIS, int PLANES2>
+struct ChunkFetch {
+  static constexpr int THREADS = 64 * kWavesScan;
+  RowStage<Math, KP, C, THREADS> k, q;
+  TriStage<Math, C, TP, THREADS> t;
+  TriStage<Math, C, PLANES2, THREADS> p;
+  TriStage<Math, C, TP, THREADS> m;
+  float ev;
+  __device__ __forceinline__ void fetch(const DeltaArgs& a, int64_t sh, int64_t row0, int64_t hk, int rows, int tid) {
+    if (a.vec_k) {
+      const uint32_t stride = (uint32_t)(a.Hk * a.K * Math::es);
+      k.fetch(head_rsrc(a.k, row0, a.Hk, hk, a.K, Math::es, rows), stride, (int)a.K, tid);
+      q.fetch(head_rsrc(a.q, row0, a.Hk, hk, a.K, Math::es, rows), stride, (int)a.K, tid);
+    }
+    t.fetch(TriStage<Math, C, TP, THREADS>::rsrc(a.T, sh, TP), tid);
+    if constexpr (TRIS > 1) p.fetch(TriStage<Math, C, PLANES2, THREADS>::rsrc(a.P, sh, TP), tid);
+    if constexpr (TRIS > 2) m.fetch(TriStage<Math, C, TP, THREADS>::rsrc(a.M, sh, TP), tid);
+    ev = io<float>::bload(make_rsrc_u32(a.vec + sh * kVec, 3 * C * 4), tid * 4, 0);
+  }
+  __device__ __forceinline__ void put(const DeltaArgs& a, E* Ks, E* Qs, TE* Ts, TE* Ps, TE* Ms, float* evs, int64_t row0,
+                                      int64_t hk, int rows, int tid) const {
+    if (a.vec_k) {
+      k.put(Ks, tid);
+      q.put(Qs, tid);
+    } else {
+      const uint32_t stride = (uint32_t)(a.Hk * a.K * Math::es);
+      RowStage<Math, KP, C, THREADS>::by_element(Ks, head_rsrc(a.k, row0, a.Hk, hk, a.K, Math::es, rows), stride, (int)a.K, tid);
+      RowStage<Math, KP, C, THREADS>::by_element(Qs, head_rsrc(a.q, row0, a.Hk, hk, a.K, Math::es, rows), stride, (int)a.K, tid);
+    }
+    t.put(Ts, tid);
+    if constexpr (TRIS > 1) p.put(Ps, tid);
+    if constexpr (TRIS > 2) m.put(Ms, tid);
+    if (tid < 3 * C) evs[tid] = ev;
+  }
+};
 
 template <bool BWD>
 __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p) {
@@ -235,114 +360,78 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
   // parts of what the output is made of; the backward needs the state's share of it to fp32 and
   // the chunk's own share not at all
   constexpr int OP = BWD ? TP : Math::kOutParts;
-  __shared__ __attribute__((aligned(16))) E Ks[C * LD];
-  __shared__ __attribute__((aligned(16))) E Qs[C * LD];
-  __shared__ __attribute__((aligned(16))) TE Ts[TP * C * LDT];
-  __shared__ __attribute__((aligned(16))) TE Ps[BWD ? 8 : OP * C * LDT];
+  using Fetch = ChunkFetch<BWD ? 1 : 2, OP>;
+  __shared__ __attribute__((aligned(16))) E Ks[C * KP];
+  __shared__ __attribute__((aligned(16))) E Qs[C * KP];
+  __shared__ __attribute__((aligned(16))) TE Ts[TriStage<Math, C, TP, THREADS>::kLds];
+  __shared__ __attribute__((aligned(16))) TE Ps[BWD ? 8 : TriStage<Math, C, OP, THREADS>::kLds];
   __shared__ __attribute__((aligned(16))) float ev[3 * C];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
   const int64_t s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-  const int64_t vb = (int64_t)blockIdx.y * kWavesScan + wave, col = vb * 16 + n;
-  const bool on = vb * 16 < p.VP, col_ok = col < p.V;
+  const int vb = blockIdx.y * kWavesScan + wave, col = vb * 16 + n;
+  const bool on = vb * 16 < p.VP;
   const SeqRows seq = seq_rows<C>(p, s);
-  const int64_t state = ((s * p.H + h) * p.K) * p.V + col;
+  const uint32_t vstride = (uint32_t)(p.H * p.V * Math::es), wstride = (uint32_t)(p.VP * 4);
+  const uint32_t vat = col < p.V ? 8 * j * vstride + col * Math::es : kOutside;   // v, o, do
+  const uint32_t wat = on ? 8 * j * wstride + col * 4 : kOutside;                 // workspace columns
+  const uint32_t sat = col < p.V ? (8 * j * (uint32_t)p.V + col) * 4 : kOutside;  // states
+  const uint32_t sbytes = (uint32_t)(p.K * p.V * 4);
 
-  Cols<NB> S;
-  if (p.S0)
-    S = load_cols<float, NB>(p.S0 + state, p.V, (int)p.K, col_ok, j);
-  else
-#pragma unroll
-    for (int b = 0; b < NB; ++b) S.t[b][0] = S.t[b][1] = zero4();
+  Cols<NB> S = zero_cols<NB>();
+  if (p.S0) S = load_cols<NB>(make_rsrc_u32(p.S0 + (s * p.H + h) * p.K * p.V, sbytes), sat, (uint32_t)(p.V * 4));
 
   const int64_t chunks = (seq.len + C - 1) / C;
+  Fetch next;
+  RawCols vnext, dnext;
+  const auto fetch = [&](int64_t c) {
+    const int64_t row0 = seq.row0 + c * C, left = seq.len - c * C;
+    const int rows = (int)(left < C ? left : C);
+    next.fetch(p, (seq.slot0 + c) * p.H + h, row0, hk, rows, tid);
+    vnext.fetch(head_rsrc(p.v, row0, p.H, h, p.V, Math::es, rows), vat, vstride);
+    if (BWD) dnext.fetch(head_rsrc(p.do_, row0, p.H, h, p.V, Math::es, rows), vat, vstride);
+  };
+  if (chunks > 0) fetch(0);
   for (int64_t c = 0; c < chunks; ++c) {
     const int64_t row0 = seq.row0 + c * C, sh = (seq.slot0 + c) * p.H + h;
     const int rows = (int)(seq.len - c * C < C ? seq.len - c * C : C);
-    const int64_t at = (row0 * p.Hk + hk) * p.K;
     __syncthreads();  // the last chunk's reads are done
-    stage_rows<Math, KP, C, LD, THREADS>(Ks, static_cast<const E*>(p.k) + at, p.Hk * p.K, rows, (int)p.K, p.vec_k, tid);
-    stage_rows<Math, KP, C, LD, THREADS>(Qs, static_cast<const E*>(p.q) + at, p.Hk * p.K, rows, (int)p.K, p.vec_k, tid);
-    stage_planes<Math, C, LDT, TP, THREADS>(Ts, static_cast<const TE*>(p.T) + sh * TP * C * C, tid);
-    if constexpr (!BWD) stage_planes<Math, C, LDT, OP, THREADS>(Ps, static_cast<const TE*>(p.P) + sh * TP * C * C, tid);
-    for (int i = tid; i < 3 * C; i += THREADS) ev[i] = p.vec[sh * kVec + i];
+    next.put(p, Ks, Qs, Ts, Ps, nullptr, ev, row0, hk, rows, tid);
+    Cols<CB> R = vnext.widen(), dO;
+    if (BWD) dO = dnext.widen();
     __syncthreads();
+    if (c + 1 < chunks) fetch(c + 1);
     if (!on) continue;
     const float* eG = ev + 8 * j;           // this lane's rows of the chunk's row factors
     const float* eK = ev + C + 8 * j;
     const float* bt = ev + 2 * C + 8 * j;
     const float last = ev[C - 1];           // decay over the whole chunk
+    const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
 
-    Cols<CB> R = load_cols<E, CB>(static_cast<const E*>(p.v) + (row0 * p.H + h) * p.V + col, p.H * p.V, rows, col_ok, j);
-    if (BWD) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            p.S[(sh * KP + 32 * b + 8 * j + 4 * t + r) * p.VP + col] = S.t[b][t][r];
-    }
+    if (BWD) store_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), wat, wstride, S);
     // products with the state: predictions K S and readouts Q S
-    Cols<CB> KS, O;
-#pragma unroll
-    for (int b = 0; b < CB; ++b) KS.t[b][0] = KS.t[b][1] = O.t[b][0] = O.t[b][1] = zero4();
+    Cols<CB> KS = zero_cols<CB>(), O = zero_cols<CB>();
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const auto B = Math::split<TP>(S.t[b][0], S.t[b][1]);
-      const auto BO = Math::first<OP>(B);
-#pragma unroll
-      for (int rb = 0; rb < CB; ++rb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int e = perm_row(rb, t, lane) * LD + 32 * b + 8 * j;
-          Math::mma(KS.t[rb][t], Math::load<1>(Ks + e, 0), B);
-          Math::mma(O.t[rb][t], Math::load<1>(Qs + e, 0), BO);
-        }
+      mma_rows(KS, Ks, b, B, lane, j);
+      mma_rows(O, Qs, b, Math::first<OP>(B), lane, j);
     }
     // errors of the chunk: E = T (V - e^G K S)
-    Part<TP> RB[CB];
-#pragma unroll
-    for (int b = 0; b < CB; ++b) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float x = eG[32 * b + 4 * t + r];
-          R.t[b][t][r] = fmaf(-x, KS.t[b][t][r], R.t[b][t][r]);
-          O.t[b][t][r] *= x * p.scale;
-          if (BWD) p.pred[(sh * C + 32 * b + 8 * j + 4 * t + r) * p.VP + col] = x * KS.t[b][t][r];
-        }
-      RB[b] = Math::split<TP>(R.t[b][0], R.t[b][1]);
-    }
-    Cols<CB> U;  // first E, then U = beta E
-#pragma unroll
-    for (int rb = 0; rb < CB; ++rb)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4 a = zero4();
-#pragma unroll
-        for (int b = 0; b <= rb; ++b)
-          Math::mma(a, Math::load<TP>(Ts + perm_row(rb, t, lane) * LDT + 32 * b + 8 * j, C * LDT), RB[b]);
-        U.t[rb][t] = a;
-      }
-    if (BWD) {
-#pragma unroll
-      for (int b = 0; b < CB; ++b)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            p.E[(sh * C + 32 * b + 8 * j + 4 * t + r) * p.VP + col] = U.t[b][t][r];
-    }
-#pragma unroll
-    for (int b = 0; b < CB; ++b)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) U.t[b][t][r] *= bt[32 * b + 4 * t + r];
-    if (BWD) {
+    each<CB>([&](int b, int t, int r, int row) {
+      const float x = eG[row];
+      KS.t[b][t][r] *= x;
+      R.t[b][t][r] -= KS.t[b][t][r];
+      O.t[b][t][r] *= x * p.scale;
+    });
+    if (BWD) store_cols<CB>(rows_ws(p.pred), wat, wstride, KS);
+    Part<TP> B[CB];
+    split_all(B, R);
+    Cols<CB> U = zero_cols<CB>();
+    mma_tri<TP>(U, Ts, B, lane, j);
+    if (BWD) store_cols<CB>(rows_ws(p.E), wat, wstride, U);
+    each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= bt[row]; });
+    if constexpr (BWD) {
       // rows of dO . (scale e^G Q S0) over this wavefront's columns
-      const Cols<CB> dO = load_cols<E, CB>(static_cast<const E*>(p.do_) + (row0 * p.H + h) * p.V + col, p.H * p.V, rows, col_ok, j);
       float x[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = i < 8 * CB ? O.t[(i / 8) % CB][(i / 4) % 2][i % 4] * dO.t[(i / 8) % CB][(i / 4) % 2][i % 4] : 0.f;
@@ -350,35 +439,13 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
       if (n < 8 * CB) p.dots[(sh * (p.VP / 16) + vb) * kDots + 32 * (n / 8) + 8 * j + n % 8] = sum;
     } else {
       Part<OP> UO[CB];
-#pragma unroll
-      for (int b = 0; b < CB; ++b) UO[b] = Math::split<OP>(U.t[b][0], U.t[b][1]);
-#pragma unroll
-      for (int rb = 0; rb < CB; ++rb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int b = 0; b <= rb; ++b)
-            Math::mma(O.t[rb][t], Math::load<OP>(Ps + perm_row(rb, t, lane) * LDT + 32 * b + 8 * j, C * LDT), UO[b]);
-      E* op = static_cast<E*>(p.o) + (row0 * p.H + h) * p.V + col;
-#pragma unroll
-      for (int b = 0; b < CB; ++b)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = 32 * b + 8 * j + 4 * t + r;
-            if (col_ok && row < rows) op[row * p.H * p.V] = Math::narrow(O.t[b][t][r]);
-          }
+      split_all(UO, U);
+      mma_tri<OP>(O, Ps, UO, lane, j);
+      store_out(head_rsrc(p.o, row0, p.H, h, p.V, Math::es, rows), vat, vstride, O);
     }
     // state after the chunk
-#pragma unroll
-    for (int b = 0; b < CB; ++b) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) U.t[b][t][r] *= eK[32 * b + 4 * t + r];
-      RB[b] = Math::split<TP>(U.t[b][0], U.t[b][1]);
-    }
+    each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= eK[row]; });
+    split_all(B, U);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -386,198 +453,124 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
         f32x4 a = S.t[b][t] * last;
 #pragma unroll
         for (int rb = 0; rb < CB; ++rb)
-          Math::mma(a, Math::load_t<1>(Ks + (32 * rb + 8 * j) * LD, LD, 0, lane, 32 * b + 4 * t, 8), RB[rb]);
+          Math::mma(a, load_col<Math, UK, 1>(Ks, 32 * rb + 8 * j, 32 * b + 4 * t, 8, lane, 0), B[rb]);
         S.t[b][t] = a;
       }
   }
-  if (on && col_ok && p.last_S) {
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 32 * b + 8 * j + 4 * t + r;
-          if (row < p.K) p.last_S[state + row * p.V] = S.t[b][t][r];
-        }
-  }
+  if (on && p.last_S)
+    store_cols<NB>(make_rsrc_u32(p.last_S + (s * p.H + h) * p.K * p.V, sbytes), sat, (uint32_t)(p.V * 4), S);
 }
 
 // ---- rev -----------------------------------------------------------------------------------
 
 __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p) {
   constexpr int THREADS = 64 * kWavesScan;
-  __shared__ __attribute__((aligned(16))) E Ks[C * LD];
-  __shared__ __attribute__((aligned(16))) E Qs[C * LD];
-  __shared__ __attribute__((aligned(16))) TE Ts[TP * C * LDT];
-  __shared__ __attribute__((aligned(16))) TE Ps[TP * C * LDT];
-  __shared__ __attribute__((aligned(16))) TE Ms[TP * C * LDT];
+  constexpr int kTri = TriStage<Math, C, TP, THREADS>::kLds;
+  __shared__ __attribute__((aligned(16))) E Ks[C * KP];
+  __shared__ __attribute__((aligned(16))) E Qs[C * KP];
+  __shared__ __attribute__((aligned(16))) TE Ts[kTri];
+  __shared__ __attribute__((aligned(16))) TE Ps[kTri];
+  __shared__ __attribute__((aligned(16))) TE Ms[kTri];
   __shared__ __attribute__((aligned(16))) float ev[3 * C];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
   const int64_t s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-  const int64_t vb = (int64_t)blockIdx.y * kWavesScan + wave, col = vb * 16 + n;
-  const bool on = vb * 16 < p.VP, col_ok = col < p.V;
+  const int vb = blockIdx.y * kWavesScan + wave, col = vb * 16 + n;
+  const bool on = vb * 16 < p.VP;
   const SeqRows seq = seq_rows<C>(p, s);
-  const int64_t state = ((s * p.H + h) * p.K) * p.V + col;
+  const uint32_t vstride = (uint32_t)(p.H * p.V * Math::es), wstride = (uint32_t)(p.VP * 4);
+  const uint32_t vat = col < p.V ? 8 * j * vstride + col * Math::es : kOutside;
+  const uint32_t wat = on ? 8 * j * wstride + col * 4 : kOutside;
+  const uint32_t sat = col < p.V ? (8 * j * (uint32_t)p.V + col) * 4 : kOutside;
+  const uint32_t sbytes = (uint32_t)(p.K * p.V * 4);
 
-  Cols<NB> S;  // the adjoint of the state
-  if (p.dlast_S)
-    S = load_cols<float, NB>(p.dlast_S + state, p.V, (int)p.K, col_ok, j);
-  else
-#pragma unroll
-    for (int b = 0; b < NB; ++b) S.t[b][0] = S.t[b][1] = zero4();
+  Cols<NB> S = zero_cols<NB>();  // the adjoint of the state
+  if (p.dlast_S) S = load_cols<NB>(make_rsrc_u32(p.dlast_S + (s * p.H + h) * p.K * p.V, sbytes), sat, (uint32_t)(p.V * 4));
 
   const int64_t chunks = (seq.len + C - 1) / C;
+  ChunkFetch<3, TP> next;
+  RawCols dnext;
+  const auto fetch = [&](int64_t c) {
+    const int64_t row0 = seq.row0 + c * C, left = seq.len - c * C;
+    const int rows = (int)(left < C ? left : C);
+    next.fetch(p, (seq.slot0 + c) * p.H + h, row0, hk, rows, tid);
+    dnext.fetch(head_rsrc(p.do_, row0, p.H, h, p.V, Math::es, rows), vat, vstride);
+  };
+  if (chunks > 0) fetch(chunks - 1);
   for (int64_t c = chunks - 1; c >= 0; --c) {
     const int64_t row0 = seq.row0 + c * C, sh = (seq.slot0 + c) * p.H + h;
     const int rows = (int)(seq.len - c * C < C ? seq.len - c * C : C);
-    const int64_t at = (row0 * p.Hk + hk) * p.K;
     __syncthreads();
-    stage_rows<Math, KP, C, LD, THREADS>(Ks, static_cast<const E*>(p.k) + at, p.Hk * p.K, rows, (int)p.K, p.vec_k, tid);
-    stage_rows<Math, KP, C, LD, THREADS>(Qs, static_cast<const E*>(p.q) + at, p.Hk * p.K, rows, (int)p.K, p.vec_k, tid);
-    stage_planes<Math, C, LDT, TP, THREADS>(Ts, static_cast<const TE*>(p.T) + sh * TP * C * C, tid);
-    stage_planes<Math, C, LDT, TP, THREADS>(Ps, static_cast<const TE*>(p.P) + sh * TP * C * C, tid);
-    stage_planes<Math, C, LDT, TP, THREADS>(Ms, static_cast<const TE*>(p.M) + sh * TP * C * C, tid);
-    for (int i = tid; i < 3 * C; i += THREADS) ev[i] = p.vec[sh * kVec + i];
+    next.put(p, Ks, Qs, Ts, Ps, Ms, ev, row0, hk, rows, tid);
+    Cols<CB> dO = dnext.widen();
     __syncthreads();
+    const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
+    const Cols<CB> Er = load_cols<CB>(rows_ws(p.E), wat, wstride);
+    const Cols<CB> pred = load_cols<CB>(rows_ws(p.pred), wat, wstride);
+    const uint32_t state_ws = (uint32_t)(KP * p.VP * 4);
+    const Cols<NB> S0 = load_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, state_ws), wat, wstride);
+    if (c > 0) fetch(c - 1);
     if (!on) continue;
     const float* eG = ev + 8 * j;
     const float* eK = ev + C + 8 * j;
     const float* bt = ev + 2 * C + 8 * j;
     const float last = ev[C - 1];
-    const int64_t vat = (row0 * p.H + h) * p.V + col;
-    Cols<CB> dO = load_cols<E, CB>(static_cast<const E*>(p.do_) + vat, p.H * p.V, rows, col_ok, j);
-    const Cols<CB> Er = load_cols<float, CB>(p.E + sh * C * p.VP + col, p.VP, C, true, j);
 
-    // the adjoint after this chunk, kept for the gradients of q and k, and <S0, dS1>
-    float dot = 0.f;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t i = (sh * KP + 32 * b + 8 * j + 4 * t + r) * p.VP + col;
-          p.dS[i] = S.t[b][t][r];
-          dot = fmaf(p.S[i], S.t[b][t][r], dot);
-        }
-    dot *= last;
-
+    // the adjoint after this chunk, kept for the gradients of q and k
+    store_cols<NB>(make_rsrc_u32(p.dS + sh * KP * p.VP, state_ws), wat, wstride, S);
     // W = e^{G_C - G} (K dS) + P^T dO
-    Cols<CB> W;
+    Cols<CB> W = zero_cols<CB>();
 #pragma unroll
-    for (int b = 0; b < CB; ++b) W.t[b][0] = W.t[b][1] = zero4();
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const auto B = Math::split<TP>(S.t[b][0], S.t[b][1]);
-#pragma unroll
-      for (int rb = 0; rb < CB; ++rb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          Math::mma(W.t[rb][t], Math::load<1>(Ks + perm_row(rb, t, lane) * LD + 32 * b + 8 * j, 0), B);
-    }
-    Part<1> dOB[CB];
+    for (int b = 0; b < NB; ++b) mma_rows(W, Ks, b, Math::split<TP>(S.t[b][0], S.t[b][1]), lane, j);
     float uw[16];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          uw[8 * b + 4 * t + r] = 0.f;
-          if (b < CB) {
-            f32x4& w = W.t[b % CB][t];
-            w[r] *= eK[32 * b + 4 * t + r];
-            uw[8 * b + 4 * t + r] = bt[32 * b + 4 * t + r] * Er.t[b % CB][t][r] * w[r];
-          }
-        }
-#pragma unroll
-    for (int b = 0; b < CB; ++b) dOB[b] = Math::split<1>(dO.t[b][0], dO.t[b][1]);
-#pragma unroll
-    for (int rb = 0; rb < CB; ++rb)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int b = rb; b < CB; ++b)
-          Math::mma(W.t[rb][t], Math::load_t<TP>(Ps + (32 * b + 8 * j) * LDT, LDT, C * LDT, lane, 32 * rb + 4 * t, 8), dOB[b]);
+    for (int i = 0; i < 16; ++i) uw[i] = 0.f;
+    each<CB>([&](int b, int t, int r, int row) {
+      W.t[b][t][r] *= eK[row];
+      uw[8 * b + 4 * t + r] = bt[row] * Er.t[b][t][r] * W.t[b][t][r];
+    });
+    Part<1> dOB[CB];
+    split_all(dOB, dO);
+    mma_tri_t<TP>(W, Ps, dOB, lane, j);
     // dV = T^T (beta W)
+    Cols<CB> dV = zero_cols<CB>(), x;
     Part<TP> B[CB];
-    Cols<CB> dV;
-#pragma unroll
-    for (int b = 0; b < CB; ++b) {
-      f32x4 x[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[t][r] = W.t[b][t][r] * bt[32 * b + 4 * t + r];
-      B[b] = Math::split<TP>(x[0], x[1]);
-    }
-#pragma unroll
-    for (int rb = 0; rb < CB; ++rb)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4 a = zero4();
-#pragma unroll
-        for (int b = rb; b < CB; ++b)
-          Math::mma(a, Math::load_t<TP>(Ts + (32 * b + 8 * j) * LDT, LDT, C * LDT, lane, 32 * rb + 4 * t, 8), B[b]);
-        dV.t[rb][t] = a;
-      }
+    each<CB>([&](int b, int t, int r, int row) { x.t[b][t][r] = W.t[b][t][r] * bt[row]; });
+    split_all(B, x);
+    mma_tri_t<TP>(dV, Ts, B, lane, j);
     // Y = W - stril(D K K^T)^T dV
+    each<CB>([&](int b, int t, int r, int) { x.t[b][t][r] = -dV.t[b][t][r]; });
+    split_all(B, x);
+    mma_tri_t<TP>(W, Ms, B, lane, j);
+    float ye[16], dp[16], dot = 0.f;
 #pragma unroll
-    for (int b = 0; b < CB; ++b) B[b] = Math::split<TP>(-dV.t[b][0], -dV.t[b][1]);
-#pragma unroll
-    for (int rb = 0; rb < CB; ++rb)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int b = rb; b < CB; ++b)
-          Math::mma(W.t[rb][t], Math::load_t<TP>(Ms + (32 * b + 8 * j) * LDT, LDT, C * LDT, lane, 32 * rb + 4 * t, 8), B[b]);
-    {
-      const Cols<CB> pred = load_cols<float, CB>(p.pred + sh * C * p.VP + col, p.VP, C, true, j);
-      float x[16], y[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int b = (i / 8) % CB, t = (i / 4) % 2, r = i % 4;
-        x[i] = i < 8 * CB ? W.t[b][t][r] * Er.t[b][t][r] : 0.f;
-        y[i] = i < 8 * CB ? dV.t[b][t][r] * pred.t[b][t][r] : 0.f;
-      }
-      float* dots = p.dots + (sh * (p.VP / 16) + vb) * kDots;
-      const float sx = sum_rows16(x, lane), sy = sum_rows16(y, lane), sw = sum_rows16(uw, lane);
-      if (n < 8 * CB) {
-        dots[C + 32 * (n / 8) + 8 * j + n % 8] = sx;
-        dots[2 * C + 32 * (n / 8) + 8 * j + n % 8] = sy;
-        dots[3 * C + 32 * (n / 8) + 8 * j + n % 8] = sw;
-      }
-#pragma unroll
-      for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
-      if (lane == 0) dots[4 * C] = dot;
+    for (int i = 0; i < 16; ++i) ye[i] = dp[i] = 0.f;
+    each<CB>([&](int b, int t, int r, int) {
+      ye[8 * b + 4 * t + r] = W.t[b][t][r] * Er.t[b][t][r];
+      dp[8 * b + 4 * t + r] = dV.t[b][t][r] * pred.t[b][t][r];
+    });
+    each<NB>([&](int b, int t, int r, int) { dot = fmaf(S0.t[b][t][r], S.t[b][t][r], dot); });
+    dot *= last;
+    float* dots = p.dots + (sh * (p.VP / 16) + vb) * kDots;
+    const float sy = sum_rows16(ye, lane), sp = sum_rows16(dp, lane), sw = sum_rows16(uw, lane);
+    if (n < 8 * CB) {
+      const int row = 32 * (n / 8) + 8 * j + n % 8;
+      dots[C + row] = sy;
+      dots[2 * C + row] = sp;
+      dots[3 * C + row] = sw;
     }
-    E* dvp = static_cast<E*>(p.dv) + vat;
 #pragma unroll
-    for (int b = 0; b < CB; ++b)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 32 * b + 8 * j + 4 * t + r;
-          p.dV[(sh * C + row) * p.VP + col] = dV.t[b][t][r];
-          if (col_ok && row < rows) dvp[row * p.H * p.V] = Math::narrow(dV.t[b][t][r]);
-        }
+    for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
+    if (lane == 0) dots[4 * C] = dot;
+    store_cols<CB>(rows_ws(p.dV), wat, wstride, dV);
+    store_out(head_rsrc(p.dv, row0, p.H, h, p.V, Math::es, rows), vat, vstride, dV);
     // dS0 = e^{G_C} dS1 + Q^T (scale e^G dO) - K^T (e^G dV)
     Part<TP> BQ[CB];
-#pragma unroll
-    for (int b = 0; b < CB; ++b) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float x = eG[32 * b + 4 * t + r];
-          dO.t[b][t][r] *= x * p.scale;
-          dV.t[b][t][r] *= -x;
-        }
-      BQ[b] = Math::split<TP>(dO.t[b][0], dO.t[b][1]);
-      B[b] = Math::split<TP>(dV.t[b][0], dV.t[b][1]);
-    }
+    each<CB>([&](int b, int t, int r, int row) {
+      dO.t[b][t][r] *= eG[row] * p.scale;
+      dV.t[b][t][r] *= -eG[row];
+    });
+    split_all(BQ, dO);
+    split_all(B, dV);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -585,23 +578,14 @@ __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p)
         f32x4 a = S.t[b][t] * last;
 #pragma unroll
         for (int rb = 0; rb < CB; ++rb) {
-          Math::mma(a, Math::load_t<1>(Qs + (32 * rb + 8 * j) * LD, LD, 0, lane, 32 * b + 4 * t, 8), BQ[rb]);
-          Math::mma(a, Math::load_t<1>(Ks + (32 * rb + 8 * j) * LD, LD, 0, lane, 32 * b + 4 * t, 8), B[rb]);
+          Math::mma(a, load_col<Math, UK, 1>(Qs, 32 * rb + 8 * j, 32 * b + 4 * t, 8, lane, 0), BQ[rb]);
+          Math::mma(a, load_col<Math, UK, 1>(Ks, 32 * rb + 8 * j, 32 * b + 4 * t, 8, lane, 0), B[rb]);
         }
         S.t[b][t] = a;
       }
   }
-  if (on && col_ok && p.dS0) {
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 32 * b + 8 * j + 4 * t + r;
-          if (row < p.K) p.dS0[state + row * p.V] = S.t[b][t][r];
-        }
-  }
+  if (on && p.dS0)
+    store_cols<NB>(make_rsrc_u32(p.dS0 + (s * p.H + h) * p.K * p.V, sbytes), sat, (uint32_t)(p.V * 4), S);
 }
 
 // ---- grad ----------------------------------------------------------------------------------
@@ -616,8 +600,8 @@ constexpr int LDV = VB + Math::pad;
 __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p) {
   constexpr int THREADS = 64 * kWavesGrad;
   constexpr int kStage = (1 + 2 * TP) * C * LDV, kPair = 2 * GP * C * LDT;
-  __shared__ __attribute__((aligned(16))) E Ks[C * LD];
-  __shared__ __attribute__((aligned(16))) E Qs[C * LD];
+  __shared__ __attribute__((aligned(16))) E Ks[C * KP];
+  __shared__ __attribute__((aligned(16))) E Qs[C * KP];
   // first the staged columns of dO, dV and U, then the token-pair matrices X and Z + Z^T
   __shared__ __attribute__((aligned(16))) TE buf[kStage > kPair ? kStage : kPair];
   __shared__ __attribute__((aligned(16))) float ev[3 * C];
@@ -628,8 +612,9 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   const ChunkRows ch = chunk_rows<C>(p, slot);
   if (ch.n == 0) return;
   const int64_t at = (ch.row0 * p.Hk + hk) * p.K;
-  stage_rows<Math, KP, C, LD, THREADS>(Ks, static_cast<const E*>(p.k) + at, p.Hk * p.K, ch.n, (int)p.K, p.vec_k, tid);
-  stage_rows<Math, KP, C, LD, THREADS>(Qs, static_cast<const E*>(p.q) + at, p.Hk * p.K, ch.n, (int)p.K, p.vec_k, tid);
+  stage_two<THREADS>(Ks, Qs, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, Math::es, ch.n),
+                     head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, Math::es, ch.n), (uint32_t)(p.Hk * p.K * Math::es),
+                     (int)p.K, p.vec_k, tid);
   E* dOs = reinterpret_cast<E*>(buf);
   TE* dVs = buf + C * LDV;
   TE* Us = dVs + TP * C * LDV;
@@ -657,22 +642,20 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
 #pragma unroll
       for (int t = 0; t < kTilesGrad; ++t) a1[m][t] = a2[m][t] = a3[m][t] = zero4();
     }
+    const auto rdo = head_rsrc(p.do_, ch.row0, p.H, h, p.V, Math::es, ch.n);
+    const auto rdv = make_rsrc_u32(p.dV + sh * C * p.VP, (uint32_t)(C * p.VP * 4));
+    const auto re = make_rsrc_u32(p.E + sh * C * p.VP, (uint32_t)(C * p.VP * 4));
     for (int64_t v0 = 0; v0 < p.VP; v0 += VB) {
       __syncthreads();  // ev is there; the previous columns have been used
       for (int u = tid; u < C * VB / 8; u += THREADS) {
         const int row = u / (VB / 8), c = (u % (VB / 8)) * 8;
-        const E* src = static_cast<const E*>(p.do_) + ((ch.row0 + row) * p.H + h) * p.V + v0 + c;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          dOs[row * LDV + c + i] = (row < ch.n && v0 + c + i < p.V) ? src[i] : E(0);
-        f32x4 a = zero4(), b = zero4(), d = zero4(), e = zero4();
-        if (v0 + c < p.VP) {
-          const int64_t w = (sh * C + row) * p.VP + v0 + c;
-          a = *reinterpret_cast<const f32x4*>(p.dV + w);
-          b = *reinterpret_cast<const f32x4*>(p.dV + w + 4);
-          d = *reinterpret_cast<const f32x4*>(p.E + w) * ev[2 * C + row];
-          e = *reinterpret_cast<const f32x4*>(p.E + w + 4) * ev[2 * C + row];
-        }
+          dOs[row * LDV + c + i] = (E)IO::bload(rdo, v0 + c + i < p.V ? (uint32_t)(row * p.H * p.V + v0 + c + i) * Math::es : kOutside, 0);
+        const uint32_t w = v0 + c < p.VP ? (uint32_t)(row * p.VP + v0 + c) * 4 : kOutside;
+        const f32x4 a = __builtin_bit_cast(f32x4, bload16(rdv, w)), b = __builtin_bit_cast(f32x4, bload16(rdv, w + 16));
+        const f32x4 d = __builtin_bit_cast(f32x4, bload16(re, w)) * ev[2 * C + row];
+        const f32x4 e = __builtin_bit_cast(f32x4, bload16(re, w + 16)) * ev[2 * C + row];
         Math::store_planes<TP>(dVs + row * LDV + c, C * LDV, a, b);
         Math::store_planes<TP>(Us + row * LDV + c, C * LDV, d, e);
       }
@@ -726,9 +709,9 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
         if (m <= wave) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const auto B = Math::load<1>(Ks + (16 * m + n) * LD + 32 * b + 8 * j, 0);
-            Math::mma(qk, Math::load<1>(Qs + (16 * wave + n) * LD + 32 * b + 8 * j, 0), B);
-            Math::mma(kk, Math::load<1>(Ks + (16 * wave + n) * LD + 32 * b + 8 * j, 0), B);
+            const auto B = load_row<Math, UK, 1>(Ks, 16 * m + n, 32 * b + 8 * j, 0);
+            Math::mma(qk, load_row<Math, UK, 1>(Qs, 16 * wave + n, 32 * b + 8 * j, 0), B);
+            Math::mma(kk, load_row<Math, UK, 1>(Ks, 16 * wave + n, 32 * b + 8 * j, 0), B);
           }
         }
         float below = 0.f;
@@ -803,8 +786,8 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
       for (int b = 0; b < CB; ++b)
 #pragma unroll
         for (int t = 0; t < kTilesGrad; ++t) {
-          const auto kt = Math::load_t<1>(Ks + (32 * b + 8 * j) * LD, LD, 0, lane, 16 * (tile0 + t), 4);
-          const auto qt = Math::load_t<1>(Qs + (32 * b + 8 * j) * LD, LD, 0, lane, 16 * (tile0 + t), 4);
+          const auto kt = load_col<Math, UK, 1>(Ks, 32 * b + 8 * j, 16 * (tile0 + t), 4, lane, 0);
+          const auto qt = load_col<Math, UK, 1>(Qs, 32 * b + 8 * j, 16 * (tile0 + t), 4, lane, 0);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (m / 2 >= b)

@@ -45,7 +45,8 @@ struct MathF32 {
   struct Part {
     float v[8];
   };
-  static constexpr int pad = 4;  // elements added to an LDS row
+  static constexpr int kPer = 4;  // elements of a 16-byte unit
+  static constexpr int pad = 4;   // elements added to a padded LDS row
   static __device__ __forceinline__ float widen(float x) { return x; }
   static __device__ __forceinline__ float narrow(float x) { return x; }
 
@@ -65,6 +66,25 @@ struct MathF32 {
     Part<N> a;
 #pragma unroll
     for (int i = 0; i < 8; ++i) a.v[i] = c[i * ld];
+    return a;
+  }
+  template <int N>
+  static __device__ __forceinline__ Part<N> load_sw(const float* row, int unit, int sw, int) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(row + (unit ^ sw) * 4);
+    const f32x4 b = *reinterpret_cast<const f32x4*>(row + ((unit + 1) ^ sw) * 4);
+    return Part<N>{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+  }
+  template <int U, int N>
+  static __device__ __forceinline__ Part<N> load_sw_t(const float* lds, int row0, int c, int spread, int lane, int) {
+    const int m = lane & 15, col = c + spread * (m >> 2);
+    Part<N> a;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // swizzle<U> of row0 + i with row0 a multiple of 8
+      const int sw = U >= 16 ? (((i & 3) << 2) | ((row0 >> 3) & 3))
+                             : (U == 8 ? ((((i >> 1) & 1) << 2) | ((row0 >> 3) & 3)) : ((row0 >> 3) & 3));
+      a.v[i] = lds[(row0 + i) * U * 4 + ((col / 4) ^ sw) * 4 + (m & 3)];
+    }
     return a;
   }
   template <int N>
@@ -111,6 +131,7 @@ struct MathBF16 {
   struct Part {
     bf16x8 p[N];
   };
+  static constexpr int kPer = 8;
   static constexpr int pad = 8;
   static __device__ __forceinline__ float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
   static __device__ __forceinline__ uint16_t narrow(float x) {
@@ -141,6 +162,30 @@ struct MathBF16 {
       } v;
       v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(c + n * plane));
       v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(c + n * plane + 4 * ld));
+      a.p[n] = __builtin_bit_cast(bf16x8, v);
+    }
+    return a;
+  }
+  template <int N>
+  static __device__ __forceinline__ Part<N> load_sw(const uint16_t* row, int unit, int sw, int plane) {
+    return load<N>(row + (unit ^ sw) * 8, plane);
+  }
+  template <int U, int N>
+  static __device__ __forceinline__ Part<N> load_sw_t(const uint16_t* lds, int row0, int c, int spread, int lane,
+                                                      int plane) {
+    typedef __attribute__((address_space(3))) s16x4* lds4;
+    const int i = lane & 15, row = row0 + (i >> 2), col = c + spread * (i & 3);
+    const int sw = U >= 16 ? (((i >> 2) << 2) | ((row0 >> 3) & 3))
+                           : (U == 8 ? (((i >> 3) << 2) | ((row0 >> 3) & 3)) : ((row0 >> 3) & 3));
+    const uint16_t* p = lds + row * U * 8 + ((col / 8) ^ sw) * 8 + col % 8;
+    Part<N> a;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      struct {
+        s16x4 lo, hi;
+      } v;
+      v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + n * plane));
+      v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + n * plane + 4 * U * 8));
       a.p[n] = __builtin_bit_cast(bf16x8, v);
     }
     return a;
@@ -248,55 +293,113 @@ __device__ __forceinline__ ChunkRows chunk_rows(const DeltaArgs& p, int64_t slot
   return ChunkRows{r.row0 + at, (int)(left < C ? left : C)};
 }
 
-// ---- staging ----
-// Rows [0, n) of a (rows, K) slab whose rows are `stride` elements apart, into LDS rows of LD
-// elements, zero-filled to C rows and KP columns.
-template <class M, int KP, int C, int LD, int THREADS>
-__device__ __forceinline__ void stage_rows(typename M::elem* lds, const void* src, int64_t stride,
-                                           int n, int K, bool vec, int tid) {
-  using E = typename M::elem;
-  constexpr int PER = 16 / M::es, UNITS = KP / PER;
-  const E* base = static_cast<const E*>(src);
-  if (vec) {
-    u32x4 w[(C * UNITS + THREADS - 1) / THREADS];
-#pragma unroll
-    for (int i = 0; i < (C * UNITS + THREADS - 1) / THREADS; ++i) {
-      const int u = tid + i * THREADS, row = u / UNITS, c = (u % UNITS) * PER;
-      w[i] = u32x4{0, 0, 0, 0};
-      if (row < n && c < K) w[i] = *reinterpret_cast<const u32x4*>(base + row * stride + c);
-    }
-#pragma unroll
-    for (int i = 0; i < (C * UNITS + THREADS - 1) / THREADS; ++i) {
-      const int u = tid + i * THREADS, row = u / UNITS, c = (u % UNITS) * PER;
-      if (row < C) *reinterpret_cast<u32x4*>(lds + row * LD + c) = w[i];
-    }
-  } else {
-    for (int u = tid; u < C * KP; u += THREADS) {
-      const int row = u / KP, c = u % KP;
-      lds[row * LD + c] = (row < n && c < K) ? base[row * stride + c] : E(0);
-    }
-  }
+// ---- LDS layout ----
+// Rows of U 16-byte units without padding; unit u of row r lies at position u ^ swizzle<U>(r).
+// The readers below take 16 rows 8 (m / 4) + m % 4 (+ 4 s) at one unit, or 4 consecutive rows
+// times 4 consecutive units: either way the swizzle spreads the 16 addresses over all banks.
+// It depends on row bits 0, 1, 3 and 4 alone, so a lane's swizzle is the same in all its reads.
+template <int U>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (U == 4) return (r >> 3) & 3;
+  if constexpr (U == 8) return (((r >> 1) & 1) << 2) | ((r >> 3) & 3);
+  return ((r & 3) << 2) | ((r >> 3) & 3);
 }
 
-// `planes` chunk matrices [C][C] from the workspace into LDS rows of LDT elements.
-template <class M, int C, int LDT, int PLANES, int THREADS>
-__device__ __forceinline__ void stage_planes(typename M::telem* lds, const void* src, int tid) {
-  using E = typename M::telem;
-  constexpr int PER = 16 / (int)sizeof(E), UNITS = PLANES * C * C / PER;
-  constexpr int N = (UNITS + THREADS - 1) / THREADS;
-  const E* base = static_cast<const E*>(src);
-  u32x4 w[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int u = tid + i * THREADS;
-    if (UNITS % THREADS == 0 || u < UNITS) w[i] = *reinterpret_cast<const u32x4*>(base + (int64_t)u * PER);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int u = tid + i * THREADS, e = u * PER, row = e / C, c = e % C;  // row counts all planes' rows
-    if (UNITS % THREADS == 0 || u < UNITS) *reinterpret_cast<u32x4*>(lds + row * LDT + c) = w[i];
-  }
+// Left factor of a product over 32 columns from column c (a multiple of 8) of a row.
+template <class M, int U, int N, typename TE>
+__device__ __forceinline__ typename M::template Part<N> load_row(const TE* lds, int row, int c, int plane) {
+  return M::template load_sw<N>(lds + row * U * M::kPer, c / M::kPer, swizzle<U>(row), plane);
 }
+// The same transposed: eight consecutive rows from row0, of the column this lane supplies: lane m
+// has column c + spread (m / 4) + m % 4.
+template <class M, int U, int N, typename TE>
+__device__ __forceinline__ typename M::template Part<N> load_col(const TE* lds, int row0, int c, int spread,
+                                                                 int lane, int plane) {
+  return M::template load_sw_t<U, N>(lds, row0, c, spread, lane, plane);
+}
+
+// ---- staging ----
+constexpr uint32_t kOutside = 0x80000000u;  // an offset past any resource: reads zero, writes nothing
+
+__device__ __forceinline__ u32x4 bload16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// The rows of one head of a chunk: (rows, heads, size) arrays, `stride` bytes from row to row and
+// `bytes` of each row.  Rows past the chunk read as zero and are never written.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t head_rsrc(const void* base, int64_t row0, int64_t heads, int64_t h,
+                                                             int64_t size, int es, int rows) {
+  const char* p = static_cast<const char*>(base) + ((row0 * heads + h) * size) * es;
+  return make_rsrc(p, rows > 0 ? ((rows - 1) * heads + 1) * size * es : 0);
+}
+
+// q or k rows of a chunk, on their way from memory to swizzled LDS rows of KP elements; rows and
+// columns past the chunk's are zero.
+template <class M, int KP, int C, int THREADS>
+struct RowStage {
+  static constexpr int U = KP / M::kPer, N = (C * U + THREADS - 1) / THREADS;
+  static_assert(C * U % THREADS == 0, "whole passes");
+  u32x4 w[N];
+
+  static __device__ __forceinline__ uint32_t offset(int i, int tid, uint32_t stride, int K) {
+    const int u = tid + i * THREADS, row = u / U, c = ((u % U) ^ swizzle<U>(row)) * M::kPer;
+    return c < K ? row * stride + c * M::es : kOutside;
+  }
+  __device__ __forceinline__ void fetch(__amdgpu_buffer_rsrc_t r, uint32_t stride, int K, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = bload16(r, offset(i, tid, stride, K));
+  }
+  __device__ __forceinline__ void put(typename M::elem* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + (tid + i * THREADS) * M::kPer) = w[i];
+  }
+  // rows that cannot be read 16 bytes at a time
+  static __device__ __forceinline__ void by_element(typename M::elem* lds, __amdgpu_buffer_rsrc_t r,
+                                                    uint32_t stride, int K, int tid) {
+    using T = io<typename M::storage>;
+    for (int u = tid; u < C * KP; u += THREADS) {
+      const int row = u / KP, c = u % KP;
+      const auto x = T::bload(r, c < K ? row * stride + c * M::es : kOutside, 0);
+      lds[row * KP + ((c / M::kPer) ^ swizzle<U>(row)) * M::kPer + c % M::kPer] = (typename M::elem)x;
+    }
+  }
+};
+
+// Chunk matrices (lower triangular, C x C) are kept as their 32 x 32 blocks on and below the
+// diagonal, (0,0), (1,0), (1,1), each in swizzled rows, in memory as in LDS; planes follow each
+// other.
+template <class M, int C>
+struct Tri {
+  static constexpr int U = 32 / M::kPer, kBlock = 32 * 32, kPlane = kBlock * (C / 32) * (C / 32 + 1) / 2;
+  static __device__ __forceinline__ int block(int rb, int kb) { return (rb * (rb + 1) / 2 + kb) * kBlock; }
+  // place of an element on or below the block diagonal
+  static __device__ __forceinline__ int at(int row, int col) {
+    const int r = row & 31, c = col & 31;
+    return block(row >> 5, col >> 5) + r * 32 + ((c / M::kPer) ^ swizzle<U>(r)) * M::kPer + c % M::kPer;
+  }
+};
+
+// `PLANES` planes of a chunk matrix on their way from memory to LDS.
+template <class M, int C, int PLANES, int THREADS>
+struct TriStage {
+  static constexpr int kUnits = PLANES * Tri<M, C>::kPlane / M::kPer;
+  static constexpr int N = (kUnits + THREADS - 1) / THREADS;
+  static constexpr int kLds = N * THREADS * M::kPer;  // elements of LDS, whole passes
+  u32x4 w[N];
+  __device__ __forceinline__ void fetch(__amdgpu_buffer_rsrc_t r, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = bload16(r, (tid + i * THREADS) * 16);
+  }
+  __device__ __forceinline__ void put(typename M::telem* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(lds + (tid + i * THREADS) * M::kPer) = w[i];
+  }
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t sh, int planes) {
+    constexpr int es = (int)sizeof(typename M::telem);
+    return make_rsrc_u32(static_cast<const char*>(base) + sh * planes * Tri<M, C>::kPlane * es,
+                         PLANES * Tri<M, C>::kPlane * es);
+  }
+};
 
 // Sums of 16 register values over the 16 lanes of a group: lane l ends with the sum of value
 // l & 15 (pairings as in reduce_scatter32).

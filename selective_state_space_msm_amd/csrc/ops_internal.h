@@ -40,9 +40,9 @@ struct DeltaArgs {
   float* dS0;
   // workspace; sh = slot * H + head numbers the chunks
   float* vec;           // [sh][5 C]: e^G, e^(G_last - G), beta, G as doubles
-  void* T;              // [sh][planes][C][C]  inverse of the chunk's unit lower system
-  void* P;              // [sh][planes][C][C]  scale D tril(Q K^T)
-  void* M;              // [sh][planes][C][C]  D stril(K K^T)            (backward)
+  void* T;              // [sh][planes][blocks]  inverse of the chunk's unit lower system
+  void* P;              // [sh][planes][blocks]  scale D tril(Q K^T)
+  void* M;              // [sh][planes][blocks]  D stril(K K^T)            (backward)
   float* S;             // [sh][KP][VP] state before the chunk          (backward)
   float* dS;            // [sh][KP][VP] adjoint of the state after it   (backward)
   float* E;             // [sh][C][VP] prediction errors                (backward)
