@@ -77,13 +77,13 @@ msm_status delta_shape(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K, 
 }
 
 struct DeltaLayout {
-  size_t vec, T, P, M, S, dS, E, dV, pred, dots, total;
+  size_t vec, T, P, kq, M, S, dS, E, dV, pred, dots, total;
 };
 
 DeltaLayout delta_layout(const DeltaShape& s, msm_dtype io, bool bwd) {
   const size_t n = (size_t)(s.nslots * s.H), C = (size_t)s.C, KP = (size_t)s.KP, VP = (size_t)s.VP;
   // blocks of 32 x 32 on and below the diagonal
-  const size_t mat = n * (1024 * (C / 32) * (C / 32 + 1) / 2) * (io == MSM_BF16 ? 3 * 2 : 4);
+  const size_t mat = n * (1024 * (C / 32) * (C / 32 + 1) / 2) * 3 * 2;
   DeltaLayout l{};
   size_t at = 0;
   auto take = [&at](size_t bytes) {
@@ -94,6 +94,7 @@ DeltaLayout delta_layout(const DeltaShape& s, msm_dtype io, bool bwd) {
   l.vec = take(n * 5 * C * 4);
   l.T = take(mat);
   l.P = take(mat);
+  l.kq = take((size_t)(s.nslots * s.Hk) * 2 * msm::delta_in_planes(io == MSM_BF16) * C * KP * 2);
   if (bwd) {
     l.M = take(mat);
     l.S = take(n * KP * VP * 4);
@@ -122,6 +123,7 @@ DeltaArgs delta_args(const DeltaShape& s, const DeltaLayout& l, msm_dtype io, co
   a.vec = reinterpret_cast<float*>(ws + l.vec);
   a.T = ws + l.T;
   a.P = ws + l.P;
+  a.kq = ws + l.kq;
   a.M = ws + l.M;
   a.S = reinterpret_cast<float*>(ws + l.S);
   a.dS = reinterpret_cast<float*>(ws + l.dS);
@@ -141,6 +143,7 @@ DeltaArgs delta_args(const DeltaShape& s, const DeltaLayout& l, msm_dtype io, co
   a.VP = s.VP;
   a.scale = scale;
   a.vec_k = s.K * (int64_t)elem_bytes(io) % 16 == 0 && aligned(q, 16) && aligned(k, 16);
+  a.kq_direct = a.vec_k && io == MSM_BF16;
   return a;
 }
 

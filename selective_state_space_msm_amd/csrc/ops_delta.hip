@@ -30,32 +30,34 @@
 //          registers, each wavefront owning all K rows of 16 columns
 //   rev    the same walk backwards for dS
 //   grad   one workgroup per chunk and key head: dQ, dK and the sums for dbeta and dg
+#include <type_traits>
+
 #include "ops_delta.hpp"
 
 namespace msm {
 namespace {
 
-#if MSM_IO_BF16
-using Math = MathBF16;
-#else
-using Math = MathF32;
-#endif
 constexpr int KP = MSM_KP;
 constexpr int C = delta_chunk(MSM_IO_BF16, KP);
 constexpr int NB = KP / 32;       // blocks of 32 state rows
 constexpr int CB = C / 32;        // blocks of 32 tokens
-constexpr int LDT = C + Math::pad;
-constexpr int UK = KP / Math::kPer;                 // 16-byte units of a row of keys
-constexpr int UT = 32 / Math::kPer;                 // and of a row of a chunk matrix's blocks
-using TriM = Tri<Math, C>;
-constexpr int TP = Math::kPlanes;
+constexpr int UK = KP / 8;        // 16-byte units of a row of keys
+constexpr int kIn = MSM_IO_BF16 ? 1 : 3;        // parts of an input
+constexpr int TP = 3;                           // parts of an fp32 value
+constexpr int kOutParts = MSM_IO_BF16 ? 2 : 3;  // of what is rounded to the I/O type: 16 bits carry a bf16
+constexpr int kRows = C * KP;                   // elements of a plane of keys
+using TriM = Tri<C>;
+constexpr int kTri = TP * TriM::kPlane;         // elements of a chunk matrix
 constexpr int kVec = 5 * C;
 constexpr int kDots = 4 * C + 4;
 constexpr int kWavesScan = 4;     // wavefronts of a scan workgroup, 16 columns each
-using E = Math::elem;
-using TE = Math::telem;
-template <int N>
-using Part = Math::Part<N>;
+#if MSM_IO_BF16
+using IO = io<bf16_storage>;
+using elem = uint16_t;
+#else
+using IO = io<float>;
+using elem = float;
+#endif
 
 __device__ __forceinline__ float exp_of(double x) { return exp2_fast((float)(x * 1.4426950408889634)); }
 
@@ -112,27 +114,57 @@ __device__ __forceinline__ void invert(const float* Ms, float* Ti, int wave, int
   __syncthreads();
 }
 
-// Keys and queries of a chunk into LDS.
+// Rows of keys or queries into swizzled LDS planes; rows and columns past the chunk's are zero.
+// With `ws` the planes also go to memory, for kernels that then load them into LDS unchanged: fp32
+// inputs in their parts, and rows that cannot be read 16 bytes at a time.
 template <int THREADS>
-__device__ __forceinline__ void stage_two(E* Ks, E* Qs, __amdgpu_buffer_rsrc_t rk, __amdgpu_buffer_rsrc_t rq,
-                                          uint32_t stride, int K, bool vec, int tid) {
-  using Stage = RowStage<Math, KP, C, THREADS>;
-  if (vec) {
-    Stage k, q;
-    k.fetch(rk, stride, K, tid);
-    q.fetch(rq, stride, K, tid);
-    k.put(Ks, tid);
-    q.put(Qs, tid);
-  } else {
-    Stage::by_element(Ks, rk, stride, K, tid);
-    Stage::by_element(Qs, rq, stride, K, tid);
+__device__ __forceinline__ void stage_rows(uint16_t* lds, uint16_t* ws, __amdgpu_buffer_rsrc_t r, uint32_t stride,
+                                           int K, bool vec, int tid) {
+  constexpr int N = C * UK / THREADS;
+  static_assert(C * UK % THREADS == 0, "whole passes");
+  f32x4 a[N][2];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int u = tid + i * THREADS, row = u / UK, c = ((u % UK) ^ swizzle<UK>(row)) * 8;
+    const uint32_t at = row * stride + c * IO::es;
+    if (vec) {
+      a[i][0] = bload4(r, c < K ? at : kOutside);
+      if (!MSM_IO_BF16) a[i][1] = bload4(r, c + 4 < K ? at + 16 : kOutside);
+    } else {
+      uint32_t x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const auto v = IO::bload(r, c + e < K ? at + e * IO::es : kOutside, 0);
+        x[e] = __builtin_bit_cast(uint32_t, v);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (MSM_IO_BF16) {
+          a[i][0][e] = __uint_as_float(x[2 * e] | (x[2 * e + 1] << 16));
+        } else {
+          a[i][0][e] = __uint_as_float(x[e]);
+          a[i][1][e] = __uint_as_float(x[4 + e]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int u = tid + i * THREADS;
+    Part<kIn> s;
+    if constexpr (kIn == 1)
+      s.p[0] = __builtin_bit_cast(bf16x8, a[i][0]);
+    else
+      s = split<kIn>(a[i][0], a[i][1]);
+    store_parts(lds + u * 8, kRows, s);
+    if (ws) store_parts(ws + u * 8, kRows, s);
   }
 }
 
 template <bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
-  __shared__ __attribute__((aligned(16))) E Ks[C * KP];
-  __shared__ __attribute__((aligned(16))) E Qs[C * KP];
+  __shared__ __attribute__((aligned(16))) uint16_t Ks[kIn * kRows];
+  __shared__ __attribute__((aligned(16))) uint16_t Qs[kIn * kRows];
   __shared__ __attribute__((aligned(16))) float Ms[C * LDM];
   __shared__ __attribute__((aligned(16))) float Ti[C * LDM];
   __shared__ double Gd[C];
@@ -141,10 +173,12 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   const int64_t slot = blockIdx.x, h = blockIdx.y;
   const ChunkRows ch = chunk_rows<C>(p, slot);
   if (ch.n == 0) return;
-  const int64_t sh = slot * p.H + h, hk = h / (p.H / p.Hk);
-  const auto rk = head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, Math::es, ch.n);
-  const auto rq = head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, Math::es, ch.n);
-  stage_two<256>(Ks, Qs, rk, rq, (uint32_t)(p.Hk * p.K * Math::es), (int)p.K, p.vec_k, tid);
+  const int64_t sh = slot * p.H + h, group = p.H / p.Hk, hk = h / group;
+  const uint32_t stride = (uint32_t)(p.Hk * p.K * IO::es);
+  uint16_t* ws = p.kq_direct || h % group != 0 ? nullptr : static_cast<uint16_t*>(p.kq) + (slot * p.Hk + hk) * 2 * kIn * kRows;
+  stage_rows<256>(Ks, ws, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
+  stage_rows<256>(Qs, ws ? ws + kIn * kRows : nullptr, head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride,
+                  (int)p.K, p.vec_k, tid);
   if (wave == 0) {
     // running sum of the log decay in fp64: its differences keep fp32 accuracy
     const bool on = lane < ch.n;
@@ -173,8 +207,8 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   }
   __syncthreads();
   // Gram tiles on and below the diagonal; 16 x 16, one wavefront each
-  TE* Pg = static_cast<TE*>(p.P) + sh * TP * TriM::kPlane;
-  TE* Mg = BWD ? static_cast<TE*>(p.M) + sh * TP * TriM::kPlane : nullptr;
+  uint16_t* Pg = static_cast<uint16_t*>(p.P) + sh * kTri;
+  uint16_t* Mg = BWD ? static_cast<uint16_t*>(p.M) + sh * kTri : nullptr;
   for (int t = wave; t < (C / 16) * (C / 16); t += 4) {
     const int mt = t / (C / 16), nt = t % (C / 16);
     if (nt / 2 > mt / 2) continue;  // no block is kept there
@@ -182,9 +216,9 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
     if (nt <= mt) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const auto B = load_row<Math, UK, 1>(Ks, 16 * nt + n, 32 * b + 8 * j, 0);
-        Math::mma(kk, load_row<Math, UK, 1>(Ks, 16 * mt + n, 32 * b + 8 * j, 0), B);
-        Math::mma(qk, load_row<Math, UK, 1>(Qs, 16 * mt + n, 32 * b + 8 * j, 0), B);
+        const auto B = load_row<UK, kIn>(Ks, 16 * nt + n, 32 * b + 8 * j, kRows);
+        mma(kk, load_row<UK, kIn>(Ks, 16 * mt + n, 32 * b + 8 * j, kRows), B);
+        mma(qk, load_row<UK, kIn>(Qs, 16 * mt + n, 32 * b + 8 * j, kRows), B);
       }
     }
 #pragma unroll
@@ -193,13 +227,13 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
       const float D = col <= row ? exp_of(Gd[row] - Gd[col]) : 0.f;
       const float m = col < row ? D * kk[r] : 0.f;
       Ms[row * LDM + col] = m * bt[col];
-      Math::store1<TP>(Pg + TriM::at(row, col), TriM::kPlane, col <= row ? p.scale * D * qk[r] : 0.f);
-      if (BWD) Math::store1<TP>(Mg + TriM::at(row, col), TriM::kPlane, m);
+      store_parts1<TP>(Pg + TriM::at(row, col), TriM::kPlane, col <= row ? p.scale * D * qk[r] : 0.f);
+      if (BWD) store_parts1<TP>(Mg + TriM::at(row, col), TriM::kPlane, m);
     }
   }
   __syncthreads();
   invert(Ms, Ti, wave, lane);
-  TE* Tg = static_cast<TE*>(p.T) + sh * TP * TriM::kPlane;
+  uint16_t* Tg = static_cast<uint16_t*>(p.T) + sh * kTri;
   for (int u = tid; u < C * C / 8; u += 256) {
     const int row = u / (C / 8), c = (u % (C / 8)) * 8;
     if (c / 32 > row / 32) continue;
@@ -208,12 +242,7 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
       a = *reinterpret_cast<const f32x4*>(Ti + row * LDM + c);
       b = *reinterpret_cast<const f32x4*>(Ti + row * LDM + c + 4);
     }
-    if constexpr (Math::bf16) {
-      Math::store_planes<TP>(Tg + TriM::at(row, c), TriM::kPlane, a, b);
-    } else {
-      *reinterpret_cast<f32x4*>(Tg + TriM::at(row, c)) = a;
-      *reinterpret_cast<f32x4*>(Tg + TriM::at(row, c + 4)) = b;
-    }
+    store_parts(Tg + TriM::at(row, c), TriM::kPlane, split<TP>(a, b));
   }
 }
 
@@ -258,7 +287,6 @@ __device__ __forceinline__ void store_cols(__amdgpu_buffer_rsrc_t rs, uint32_t a
 }
 
 // The chunk's rows of v, o or do: raw I/O elements between load and use.
-using IO = io<Math::storage>;
 struct RawCols {
   IO::raw v[8 * CB];
   __device__ __forceinline__ void fetch(__amdgpu_buffer_rsrc_t rs, uint32_t at, uint32_t stride) {
@@ -281,329 +309,445 @@ __device__ __forceinline__ int perm_row(int b, int t, int lane) {
   return 32 * b + 8 * (m >> 2) + 4 * t + (m & 3);
 }
 
-// c += left x B for a left factor of keys or queries, 32 state rows per block.
-template <int N>
-__device__ __forceinline__ void mma_rows(Cols<CB>& c, const E* lds, int b, const Part<N>& B, int lane, int j) {
+// Accumulators of all tiles of a chunk's 16 columns, in the order the tile sets below have.
+__device__ __forceinline__ f32x4 (&tiles(Cols<CB>& c))[2 * CB] { return reinterpret_cast<f32x4(&)[2 * CB]>(c); }
+
+// Left factors of a product with keys or queries over 32 state rows: all tokens of the chunk.
+struct RowTiles {
+  Part<kIn> a[2 * CB];
+  __device__ __forceinline__ void load(const uint16_t* lds, int b, int lane, int j) {
 #pragma unroll
-  for (int rb = 0; rb < CB; ++rb)
+    for (int i = 0; i < 2 * CB; ++i) a[i] = load_row<UK, kIn>(lds, perm_row(i / 2, i % 2, lane), 32 * b + 8 * j, kRows);
+  }
+};
+
+// Left factors of a product with a chunk matrix (or its transpose) over one block of tokens.
+template <int NA, bool TRANS>
+struct TriTiles {
+  Part<NA> a[CB][2 * CB];
+  __device__ __forceinline__ void load(const uint16_t* lds, int lane, int j) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-      Math::mma(c.t[rb][t], load_row<Math, UK, 1>(lds, perm_row(rb, t, lane), 32 * b + 8 * j, 0), B);
-}
-// c += (chunk matrix) B, or its transpose
-template <int NA, int NB_>
-__device__ __forceinline__ void mma_tri(Cols<CB>& c, const TE* lds, const Part<NB_> (&B)[CB], int lane, int j) {
+    for (int b = 0; b < CB; ++b)
 #pragma unroll
-  for (int rb = 0; rb < CB; ++rb)
+      for (int i = 0; i < 2 * CB; ++i) {
+        const int rb = i / 2, t = i % 2;
+        if (!TRANS && b <= rb) a[b][i] = load_row<4, NA>(lds + TriM::block(rb, b), perm_row(0, t, lane), 8 * j, TriM::kPlane);
+        if (TRANS && b >= rb) a[b][i] = load_col<4, NA>(lds + TriM::block(b, rb), 8 * j, 4 * t, 8, lane, TriM::kPlane);
+      }
+  }
+  template <int N>
+  __device__ __forceinline__ void mma(Cols<CB>& c, const Part<N> (&B)[CB]) const {
+    f32x4(&x)[2 * CB] = tiles(c);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int b = 0; b < CB; ++b)
 #pragma unroll
-      for (int b = 0; b <= rb; ++b)
-        Math::mma(c.t[rb][t], load_row<Math, UT, NA>(lds + TriM::block(rb, b), perm_row(0, t, lane), 8 * j, TriM::kPlane), B[b]);
-}
-template <int NA, int NB_>
-__device__ __forceinline__ void mma_tri_t(Cols<CB>& c, const TE* lds, const Part<NB_> (&B)[CB], int lane, int j) {
+      for (int sum = Terms<NA, N>::kMost - 1; sum >= 0; --sum)
 #pragma unroll
-  for (int rb = 0; rb < CB; ++rb)
+        for (int i = 0; i < NA; ++i)
+          if (Terms<NA, N>::in(sum, i))
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+            for (int k = 0; k < 2 * CB; ++k)
+              if (TRANS ? b >= k / 2 : b <= k / 2)
+                x[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[b][k].p[i], B[b].p[sum - i], x[k], 0, 0, 0);
+  }
+};
+
+// Left factors of a state update: 32 rows of K^T or Q^T over one block of tokens.
+struct ColTiles {
+  Part<kIn> a[CB][2];
+  __device__ __forceinline__ void load(const uint16_t* lds, int b, int lane, int j) {
 #pragma unroll
-      for (int b = rb; b < CB; ++b)
-        Math::mma(c.t[rb][t], load_col<Math, UT, NA>(lds + TriM::block(b, rb), 8 * j, 4 * t, 8, lane, TriM::kPlane), B[b]);
-}
+    for (int rb = 0; rb < CB; ++rb)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) a[rb][t] = load_col<UK, kIn>(lds, 32 * rb + 8 * j, 32 * b + 4 * t, 8, lane, kRows);
+  }
+  template <int N>
+  __device__ __forceinline__ void mma(f32x4 (&c)[2], const Part<N> (&B)[CB]) const {
+#pragma unroll
+    for (int rb = 0; rb < CB; ++rb) mma_tiles(c, a[rb], B[rb]);
+  }
+};
+
 template <int N>
 __device__ __forceinline__ void split_all(Part<N> (&B)[CB], const Cols<CB>& x) {
 #pragma unroll
-  for (int b = 0; b < CB; ++b) B[b] = Math::split<N>(x.t[b][0], x.t[b][1]);
+  for (int b = 0; b < CB; ++b) B[b] = split<N>(x.t[b][0], x.t[b][1]);
 }
 
-// What a chunk needs, fetched while the chunk before it is computed.
-template <int TRIS, int PLANES2>
-struct ChunkFetch {
-  static constexpr int THREADS = 64 * kWavesScan;
-  RowStage<Math, KP, C, THREADS> k, q;
-  TriStage<Math, C, TP, THREADS> t;
-  TriStage<Math, C, PLANES2, THREADS> p;
-  TriStage<Math, C, TP, THREADS> m;
-  float ev;
-  __device__ __forceinline__ void fetch(const DeltaArgs& a, int64_t sh, int64_t row0, int64_t hk, int rows, int tid) {
-    if (a.vec_k) {
-      const uint32_t stride = (uint32_t)(a.Hk * a.K * Math::es);
-      k.fetch(head_rsrc(a.k, row0, a.Hk, hk, a.K, Math::es, rows), stride, (int)a.K, tid);
-      q.fetch(head_rsrc(a.q, row0, a.Hk, hk, a.K, Math::es, rows), stride, (int)a.K, tid);
-    }
-    t.fetch(TriStage<Math, C, TP, THREADS>::rsrc(a.T, sh, TP), tid);
-    if constexpr (TRIS > 1) p.fetch(TriStage<Math, C, PLANES2, THREADS>::rsrc(a.P, sh, TP), tid);
-    if constexpr (TRIS > 2) m.fetch(TriStage<Math, C, TP, THREADS>::rsrc(a.M, sh, TP), tid);
-    ev = io<float>::bload(make_rsrc_u32(a.vec + sh * kVec, 3 * C * 4), tid * 4, 0);
+// Everything a chunk's 16-column walks share, loaded straight into LDS by all wavefronts.
+constexpr int kPasses = C * UK / (64 * kWavesScan);  // of a plane of keys
+static_assert(C * UK % (64 * kWavesScan) == 0, "whole passes");
+
+struct KeyRows {  // LDS
+  uint16_t k[kIn * kRows], q[kIn * kRows];
+  float ev[3 * C];  // e^G, e^(G_C - G), beta
+};
+template <int N>
+__device__ __forceinline__ void load_tri(uint16_t* lds, const void* base, int64_t sh, int wave, int lane) {
+  const auto r = make_rsrc_u32(static_cast<const uint16_t*>(base) + sh * kTri, N * TriM::kPlane * 2);
+#pragma unroll
+  for (int i = 0; i < (N * TriM::kPlane / 512 + kWavesScan - 1) / kWavesScan; ++i) {
+    const int pass = i * kWavesScan + wave;
+    if (pass < N * TriM::kPlane / 512) load_lds(r, lds + pass * 512, lane * 16, pass * 1024);
   }
-  __device__ __forceinline__ void put(const DeltaArgs& a, E* Ks, E* Qs, TE* Ts, TE* Ps, TE* Ms, float* evs, int64_t row0,
-                                      int64_t hk, int rows, int tid) const {
-    if (a.vec_k) {
-      k.put(Ks, tid);
-      q.put(Qs, tid);
-    } else {
-      const uint32_t stride = (uint32_t)(a.Hk * a.K * Math::es);
-      RowStage<Math, KP, C, THREADS>::by_element(Ks, head_rsrc(a.k, row0, a.Hk, hk, a.K, Math::es, rows), stride, (int)a.K, tid);
-      RowStage<Math, KP, C, THREADS>::by_element(Qs, head_rsrc(a.q, row0, a.Hk, hk, a.K, Math::es, rows), stride, (int)a.K, tid);
+}
+// Offsets of this thread's units of keys in their rows, when they are loaded from q and k.
+struct KeyOffsets {
+  uint32_t at[kPasses];
+  __device__ __forceinline__ KeyOffsets(const DeltaArgs& p, int tid) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int u = tid + i * 64 * kWavesScan, row = u / UK, c = ((u % UK) ^ swizzle<UK>(row)) * 8;
+      at[i] = !p.kq_direct ? lane_offset(u) : (c < p.K ? (uint32_t)(row * p.Hk * p.K + c) * IO::es : kOutside);
     }
-    t.put(Ts, tid);
-    if constexpr (TRIS > 1) p.put(Ps, tid);
-    if constexpr (TRIS > 2) m.put(Ms, tid);
-    if (tid < 3 * C) evs[tid] = ev;
+  }
+  static __device__ __forceinline__ uint32_t lane_offset(int u) { return (uint32_t)u * 16; }
+};
+__device__ __forceinline__ void load_keys(KeyRows& l, const DeltaArgs& p, const KeyOffsets& o, int64_t slot, int64_t sh,
+                                          int64_t row0, int64_t hk, int rows, int wave, int lane) {
+  if (p.kq_direct) {
+    const auto rk = head_rsrc(p.k, row0, p.Hk, hk, p.K, IO::es, rows);
+    const auto rq = head_rsrc(p.q, row0, p.Hk, hk, p.K, IO::es, rows);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      load_lds(rk, l.k + (i * kWavesScan + wave) * 512, o.at[i], 0);
+      load_lds(rq, l.q + (i * kWavesScan + wave) * 512, o.at[i], 0);
+    }
+  } else {
+    const auto r = make_rsrc_u32(static_cast<const uint16_t*>(p.kq) + (slot * p.Hk + hk) * 2 * kIn * kRows, 2 * kIn * kRows * 2);
+#pragma unroll
+    for (int n = 0; n < kIn; ++n)
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        load_lds(r, l.k + n * kRows + (i * kWavesScan + wave) * 512, o.at[i], n * kRows * 2);
+        load_lds(r, l.q + n * kRows + (i * kWavesScan + wave) * 512, o.at[i], (kIn + n) * kRows * 2);
+      }
+  }
+  // the first 3 C floats of vec are whole rows of 16-byte units; one wavefront loads them
+  if (wave == kWavesScan - 1 && lane < 3 * C / 4)
+    load_lds(make_rsrc_u32(p.vec + sh * kVec, 3 * C * 4), l.ev, lane * 16, 0);
+}
+
+// LDS of the walks: two chunks' worth where the 160 KB allow, so that the next chunk's loads run
+// under the present one's products.
+constexpr size_t kLdsMost = 160 * 1024 - 512;
+template <bool BWD>
+struct ScanChunk {
+  static constexpr int OP = BWD ? TP : kOutParts;
+  KeyRows r;
+  uint16_t t[kTri];
+  uint16_t p[BWD ? 8 : OP * TriM::kPlane];
+};
+struct Nothing {};
+
+// LDS reads stay on their side of this point; arithmetic and memory reads may pass.  The products
+// read their left factors one step ahead, and without it the reads would sink to their uses.
+__device__ __forceinline__ void hold_lds() { __builtin_amdgcn_sched_barrier(0x1F); }
+
+// This wavefront's place in a walk.
+struct Walk {
+  int tid, wave, lane, n, j, vb, col;
+  bool on;
+  int64_t s, h, hk;
+  SeqRows seq;
+  uint32_t vstride, wstride, vat, wat, sat, sbytes;
+  __device__ __forceinline__ Walk(const DeltaArgs& p) {
+    tid = threadIdx.x;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    lane = tid & 63;
+    n = lane & 15;
+    j = lane >> 4;
+    s = blockIdx.x / p.H;
+    h = blockIdx.x % p.H;
+    hk = h / (p.H / p.Hk);
+    vb = blockIdx.y * kWavesScan + wave;
+    col = vb * 16 + n;
+    on = vb * 16 < p.VP;
+    seq = seq_rows<C>(p, s);
+    vstride = (uint32_t)(p.H * p.V * IO::es);
+    wstride = (uint32_t)(p.VP * 4);
+    vat = col < p.V ? 8 * j * vstride + col * IO::es : kOutside;  // v, o, do, dv
+    wat = on ? 8 * j * wstride + col * 4 : kOutside;              // columns of the workspace
+    sat = col < p.V ? (8 * j * (uint32_t)p.V + col) * 4 : kOutside;  // states
+    sbytes = (uint32_t)(p.K * p.V * 4);
+  }
+  __device__ __forceinline__ int rows(int64_t c) const { return (int)(seq.len - c * C < C ? seq.len - c * C : C); }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t state(const float* base, const DeltaArgs& p) const {
+    return make_rsrc_u32(base + (s * p.H + h) * p.K * p.V, sbytes);
   }
 };
 
 template <bool BWD>
-__global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p) {
-  constexpr int THREADS = 64 * kWavesScan;
-  // parts of what the output is made of; the backward needs the state's share of it to fp32 and
-  // the chunk's own share not at all
-  constexpr int OP = BWD ? TP : Math::kOutParts;
-  using Fetch = ChunkFetch<BWD ? 1 : 2, OP>;
-  __shared__ __attribute__((aligned(16))) E Ks[C * KP];
-  __shared__ __attribute__((aligned(16))) E Qs[C * KP];
-  __shared__ __attribute__((aligned(16))) TE Ts[TriStage<Math, C, TP, THREADS>::kLds];
-  __shared__ __attribute__((aligned(16))) TE Ps[BWD ? 8 : TriStage<Math, C, OP, THREADS>::kLds];
-  __shared__ __attribute__((aligned(16))) float ev[3 * C];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
-  const int64_t s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-  const int vb = blockIdx.y * kWavesScan + wave, col = vb * 16 + n;
-  const bool on = vb * 16 < p.VP;
-  const SeqRows seq = seq_rows<C>(p, s);
-  const uint32_t vstride = (uint32_t)(p.H * p.V * Math::es), wstride = (uint32_t)(p.VP * 4);
-  const uint32_t vat = col < p.V ? 8 * j * vstride + col * Math::es : kOutside;   // v, o, do
-  const uint32_t wat = on ? 8 * j * wstride + col * 4 : kOutside;                 // workspace columns
-  const uint32_t sat = col < p.V ? (8 * j * (uint32_t)p.V + col) * 4 : kOutside;  // states
-  const uint32_t sbytes = (uint32_t)(p.K * p.V * 4);
+__device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, const ScanChunk<BWD>& l, Cols<NB>& S,
+                                           Cols<CB> R, const Cols<CB>& dO, int64_t c) {
+  constexpr int OP = ScanChunk<BWD>::OP;
+  const int lane = w.lane, j = w.j, n = w.n;
+  const int64_t sh = (w.seq.slot0 + c) * p.H + w.h;
+  const float* eG = l.r.ev + 8 * j;           // this lane's rows of the chunk's row factors
+  const float* eK = l.r.ev + C + 8 * j;
+  const float* bt = l.r.ev + 2 * C + 8 * j;
+  const float last = l.r.ev[C - 1];           // decay over the whole chunk
+  const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
 
-  Cols<NB> S = zero_cols<NB>();
-  if (p.S0) S = load_cols<NB>(make_rsrc_u32(p.S0 + (s * p.H + h) * p.K * p.V, sbytes), sat, (uint32_t)(p.V * 4));
-
-  const int64_t chunks = (seq.len + C - 1) / C;
-  Fetch next;
-  RawCols vnext, dnext;
-  const auto fetch = [&](int64_t c) {
-    const int64_t row0 = seq.row0 + c * C, left = seq.len - c * C;
-    const int rows = (int)(left < C ? left : C);
-    next.fetch(p, (seq.slot0 + c) * p.H + h, row0, hk, rows, tid);
-    vnext.fetch(head_rsrc(p.v, row0, p.H, h, p.V, Math::es, rows), vat, vstride);
-    if (BWD) dnext.fetch(head_rsrc(p.do_, row0, p.H, h, p.V, Math::es, rows), vat, vstride);
-  };
-  if (chunks > 0) fetch(0);
-  for (int64_t c = 0; c < chunks; ++c) {
-    const int64_t row0 = seq.row0 + c * C, sh = (seq.slot0 + c) * p.H + h;
-    const int rows = (int)(seq.len - c * C < C ? seq.len - c * C : C);
-    __syncthreads();  // the last chunk's reads are done
-    next.put(p, Ks, Qs, Ts, Ps, nullptr, ev, row0, hk, rows, tid);
-    Cols<CB> R = vnext.widen(), dO;
-    if (BWD) dO = dnext.widen();
-    __syncthreads();
-    if (c + 1 < chunks) fetch(c + 1);
-    if (!on) continue;
-    const float* eG = ev + 8 * j;           // this lane's rows of the chunk's row factors
-    const float* eK = ev + C + 8 * j;
-    const float* bt = ev + 2 * C + 8 * j;
-    const float last = ev[C - 1];           // decay over the whole chunk
-    const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
-
-    if (BWD) store_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), wat, wstride, S);
-    // products with the state: predictions K S and readouts Q S
-    Cols<CB> KS = zero_cols<CB>(), O = zero_cols<CB>();
+  if (BWD) store_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride, S);
+  // products with the state: predictions K S and readouts Q S
+  Cols<CB> KS = zero_cols<CB>(), O = zero_cols<CB>();
+  RowTiles fk[2], fq[2];
+  TriTiles<TP, false> ft;
+  TriTiles<OP, false> fp;
+  fk[0].load(l.r.k, 0, lane, j);
+  fq[0].load(l.r.q, 0, lane, j);
+  Part<TP> sb = split<TP>(S.t[0][0], S.t[0][1]);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const auto B = Math::split<TP>(S.t[b][0], S.t[b][1]);
-      mma_rows(KS, Ks, b, B, lane, j);
-      mma_rows(O, Qs, b, Math::first<OP>(B), lane, j);
-    }
-    // errors of the chunk: E = T (V - e^G K S)
-    each<CB>([&](int b, int t, int r, int row) {
-      const float x = eG[row];
-      KS.t[b][t][r] *= x;
-      R.t[b][t][r] -= KS.t[b][t][r];
-      O.t[b][t][r] *= x * p.scale;
-    });
-    if (BWD) store_cols<CB>(rows_ws(p.pred), wat, wstride, KS);
-    Part<TP> B[CB];
-    split_all(B, R);
-    Cols<CB> U = zero_cols<CB>();
-    mma_tri<TP>(U, Ts, B, lane, j);
-    if (BWD) store_cols<CB>(rows_ws(p.E), wat, wstride, U);
-    each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= bt[row]; });
-    if constexpr (BWD) {
-      // rows of dO . (scale e^G Q S0) over this wavefront's columns
-      float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = i < 8 * CB ? O.t[(i / 8) % CB][(i / 4) % 2][i % 4] * dO.t[(i / 8) % CB][(i / 4) % 2][i % 4] : 0.f;
-      const float sum = sum_rows16(x, lane);
-      if (n < 8 * CB) p.dots[(sh * (p.VP / 16) + vb) * kDots + 32 * (n / 8) + 8 * j + n % 8] = sum;
+  for (int b = 0; b < NB; ++b) {
+    if (b + 1 < NB) {
+      fk[(b + 1) & 1].load(l.r.k, b + 1, lane, j);
+      fq[(b + 1) & 1].load(l.r.q, b + 1, lane, j);
     } else {
-      Part<OP> UO[CB];
-      split_all(UO, U);
-      mma_tri<OP>(O, Ps, UO, lane, j);
-      store_out(head_rsrc(p.o, row0, p.H, h, p.V, Math::es, rows), vat, vstride, O);
+      ft.load(l.t, lane, j);
     }
-    // state after the chunk
-    each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= eK[row]; });
-    split_all(B, U);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4 a = S.t[b][t] * last;
-#pragma unroll
-        for (int rb = 0; rb < CB; ++rb)
-          Math::mma(a, load_col<Math, UK, 1>(Ks, 32 * rb + 8 * j, 32 * b + 4 * t, 8, lane, 0), B[rb]);
-        S.t[b][t] = a;
-      }
+    hold_lds();
+    mma_tiles(tiles(KS), fk[b & 1].a, sb);
+    mma_tiles(tiles(O), fq[b & 1].a, first<OP>(sb));
+    if (b + 1 < NB) sb = split<TP>(S.t[(b + 1) % NB][0], S.t[(b + 1) % NB][1]);
   }
-  if (on && p.last_S)
-    store_cols<NB>(make_rsrc_u32(p.last_S + (s * p.H + h) * p.K * p.V, sbytes), sat, (uint32_t)(p.V * 4), S);
+  // errors of the chunk: E = T (V - e^G K S)
+  each<CB>([&](int b, int t, int r, int row) {
+    const float x = eG[row];
+    KS.t[b][t][r] *= x;
+    R.t[b][t][r] -= KS.t[b][t][r];
+    O.t[b][t][r] *= x * p.scale;
+  });
+  if (BWD) store_cols<CB>(rows_ws(p.pred), w.wat, w.wstride, KS);
+  Part<TP> B[CB];
+  split_all(B, R);
+  Cols<CB> U = zero_cols<CB>();
+  ColTiles fc[2];
+  if constexpr (!BWD) fp.load(l.p, lane, j);
+  fc[0].load(l.r.k, 0, lane, j);
+  hold_lds();
+  ft.mma(U, B);
+  if (BWD) store_cols<CB>(rows_ws(p.E), w.wat, w.wstride, U);
+  each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= bt[row]; });
+  if constexpr (BWD) {
+    // rows of dO . (scale e^G Q S0) over this wavefront's columns
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = i < 8 * CB ? O.t[(i / 8) % CB][(i / 4) % 2][i % 4] * dO.t[(i / 8) % CB][(i / 4) % 2][i % 4] : 0.f;
+    const float sum = sum_rows16(x, lane);
+    if (n < 8 * CB) p.dots[(sh * (p.VP / 16) + w.vb) * kDots + 32 * (n / 8) + 8 * j + n % 8] = sum;
+  } else {
+    Part<OP> UO[CB];
+    split_all(UO, U);
+    fp.mma(O, UO);
+    store_out(head_rsrc(p.o, w.seq.row0 + c * C, p.H, w.h, p.V, IO::es, w.rows(c)), w.vat, w.vstride, O);
+  }
+  // state after the chunk
+  each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= eK[row]; });
+  split_all(B, U);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (b + 1 < NB) fc[(b + 1) & 1].load(l.r.k, b + 1, lane, j);
+    hold_lds();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) S.t[b][t] *= last;
+    fc[b & 1].mma(S.t[b], B);
+  }
+}
+
+template <bool BWD>
+__global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p) {
+  constexpr bool kTwo = 2 * sizeof(ScanChunk<BWD>) <= kLdsMost;
+  __shared__ __attribute__((aligned(16))) ScanChunk<BWD> l0;
+  __shared__ __attribute__((aligned(16))) std::conditional_t<kTwo, ScanChunk<BWD>, Nothing> l1;
+  const Walk w(p);
+  const KeyOffsets ko(p, w.tid);
+  Cols<NB> S = zero_cols<NB>();
+  if (p.S0) S = load_cols<NB>(w.state(p.S0, p), w.sat, (uint32_t)(p.V * 4));
+  const int64_t chunks = (w.seq.len + C - 1) / C;
+  RawCols v, d;
+  const auto fetch = [&](ScanChunk<BWD>& l, int64_t c) {
+    const int64_t row0 = w.seq.row0 + c * C, slot = w.seq.slot0 + c, sh = slot * p.H + w.h;
+    const int rows = w.rows(c);
+    load_keys(l.r, p, ko, slot, sh, row0, w.hk, rows, w.wave, w.lane);
+    load_tri<TP>(l.t, p.T, sh, w.wave, w.lane);
+    if constexpr (!BWD) load_tri<ScanChunk<BWD>::OP>(l.p, p.P, sh, w.wave, w.lane);
+    v.fetch(head_rsrc(p.v, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
+    if (BWD) d.fetch(head_rsrc(p.do_, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
+  };
+  if constexpr (kTwo) {
+    const auto step = [&](ScanChunk<BWD>& here, ScanChunk<BWD>& next, int64_t c) {
+      sync_loads();  // `here` is loaded, and nothing reads `next` any more
+      const Cols<CB> R = v.widen(), dO = d.widen();
+      if (c + 1 < chunks) fetch(next, c + 1);
+      if (w.on) scan_chunk<BWD>(p, w, here, S, R, dO, c);
+    };
+    if (chunks > 0) fetch(l0, 0);
+    for (int64_t c = 0; c < chunks; c += 2) {
+      step(l0, l1, c);
+      if (c + 1 < chunks) step(l1, l0, c + 1);
+    }
+  } else {
+    for (int64_t c = 0; c < chunks; ++c) {
+      __syncthreads();
+      fetch(l0, c);
+      sync_loads();
+      if (w.on) scan_chunk<BWD>(p, w, l0, S, v.widen(), d.widen(), c);
+    }
+  }
+  if (w.on && p.last_S) store_cols<NB>(w.state(p.last_S, p), w.sat, (uint32_t)(p.V * 4), S);
 }
 
 // ---- rev -----------------------------------------------------------------------------------
 
-__global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p) {
-  constexpr int THREADS = 64 * kWavesScan;
-  constexpr int kTri = TriStage<Math, C, TP, THREADS>::kLds;
-  __shared__ __attribute__((aligned(16))) E Ks[C * KP];
-  __shared__ __attribute__((aligned(16))) E Qs[C * KP];
-  __shared__ __attribute__((aligned(16))) TE Ts[kTri];
-  __shared__ __attribute__((aligned(16))) TE Ps[kTri];
-  __shared__ __attribute__((aligned(16))) TE Ms[kTri];
-  __shared__ __attribute__((aligned(16))) float ev[3 * C];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
-  const int64_t s = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
-  const int vb = blockIdx.y * kWavesScan + wave, col = vb * 16 + n;
-  const bool on = vb * 16 < p.VP;
-  const SeqRows seq = seq_rows<C>(p, s);
-  const uint32_t vstride = (uint32_t)(p.H * p.V * Math::es), wstride = (uint32_t)(p.VP * 4);
-  const uint32_t vat = col < p.V ? 8 * j * vstride + col * Math::es : kOutside;
-  const uint32_t wat = on ? 8 * j * wstride + col * 4 : kOutside;
-  const uint32_t sat = col < p.V ? (8 * j * (uint32_t)p.V + col) * 4 : kOutside;
-  const uint32_t sbytes = (uint32_t)(p.K * p.V * 4);
+struct RevTri {
+  uint16_t t[kTri], p[kTri], m[kTri];
+};
 
-  Cols<NB> S = zero_cols<NB>();  // the adjoint of the state
-  if (p.dlast_S) S = load_cols<NB>(make_rsrc_u32(p.dlast_S + (s * p.H + h) * p.K * p.V, sbytes), sat, (uint32_t)(p.V * 4));
-
-  const int64_t chunks = (seq.len + C - 1) / C;
-  ChunkFetch<3, TP> next;
-  RawCols dnext;
-  const auto fetch = [&](int64_t c) {
-    const int64_t row0 = seq.row0 + c * C, left = seq.len - c * C;
-    const int rows = (int)(left < C ? left : C);
-    next.fetch(p, (seq.slot0 + c) * p.H + h, row0, hk, rows, tid);
-    dnext.fetch(head_rsrc(p.do_, row0, p.H, h, p.V, Math::es, rows), vat, vstride);
-  };
-  if (chunks > 0) fetch(chunks - 1);
-  for (int64_t c = chunks - 1; c >= 0; --c) {
-    const int64_t row0 = seq.row0 + c * C, sh = (seq.slot0 + c) * p.H + h;
-    const int rows = (int)(seq.len - c * C < C ? seq.len - c * C : C);
-    __syncthreads();
-    next.put(p, Ks, Qs, Ts, Ps, Ms, ev, row0, hk, rows, tid);
-    Cols<CB> dO = dnext.widen();
-    __syncthreads();
-    const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
-    const Cols<CB> Er = load_cols<CB>(rows_ws(p.E), wat, wstride);
-    const Cols<CB> pred = load_cols<CB>(rows_ws(p.pred), wat, wstride);
-    const uint32_t state_ws = (uint32_t)(KP * p.VP * 4);
-    const Cols<NB> S0 = load_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, state_ws), wat, wstride);
-    if (c > 0) fetch(c - 1);
-    if (!on) continue;
-    const float* eG = ev + 8 * j;
-    const float* eK = ev + C + 8 * j;
-    const float* bt = ev + 2 * C + 8 * j;
-    const float last = ev[C - 1];
-
-    // the adjoint after this chunk, kept for the gradients of q and k
-    store_cols<NB>(make_rsrc_u32(p.dS + sh * KP * p.VP, state_ws), wat, wstride, S);
-    // W = e^{G_C - G} (K dS) + P^T dO
-    Cols<CB> W = zero_cols<CB>();
+__device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, const KeyRows& l, const RevTri& x3,
+                                          Cols<NB>& S, Cols<CB> dO, const Cols<CB>& Er, const Cols<CB>& pred,
+                                          const Cols<NB>& S0, int64_t c) {
+  const int lane = w.lane, j = w.j, n = w.n;
+  const int64_t sh = (w.seq.slot0 + c) * p.H + w.h;
+  const float* eG = l.ev + 8 * j;
+  const float* eK = l.ev + C + 8 * j;
+  const float* bt = l.ev + 2 * C + 8 * j;
+  const float last = l.ev[C - 1];
+  // the adjoint after this chunk, kept for the gradients of q and k
+  store_cols<NB>(make_rsrc_u32(p.dS + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride, S);
+  float dot = 0.f;
+  each<NB>([&](int b, int t, int r, int) { dot = fmaf(S0.t[b][t][r], S.t[b][t][r], dot); });
+  dot *= last;
+  // W = e^{G_C - G} (K dS) + P^T dO
+  Cols<CB> W = zero_cols<CB>();
+  RowTiles fk[2];
+  TriTiles<TP, true> f3[2];
+  fk[0].load(l.k, 0, lane, j);
+  Part<TP> sb = split<TP>(S.t[0][0], S.t[0][1]);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) mma_rows(W, Ks, b, Math::split<TP>(S.t[b][0], S.t[b][1]), lane, j);
-    float uw[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) uw[i] = 0.f;
-    each<CB>([&](int b, int t, int r, int row) {
-      W.t[b][t][r] *= eK[row];
-      uw[8 * b + 4 * t + r] = bt[row] * Er.t[b][t][r] * W.t[b][t][r];
-    });
-    Part<1> dOB[CB];
-    split_all(dOB, dO);
-    mma_tri_t<TP>(W, Ps, dOB, lane, j);
-    // dV = T^T (beta W)
-    Cols<CB> dV = zero_cols<CB>(), x;
-    Part<TP> B[CB];
-    each<CB>([&](int b, int t, int r, int row) { x.t[b][t][r] = W.t[b][t][r] * bt[row]; });
-    split_all(B, x);
-    mma_tri_t<TP>(dV, Ts, B, lane, j);
-    // Y = W - stril(D K K^T)^T dV
-    each<CB>([&](int b, int t, int r, int) { x.t[b][t][r] = -dV.t[b][t][r]; });
-    split_all(B, x);
-    mma_tri_t<TP>(W, Ms, B, lane, j);
-    float ye[16], dp[16], dot = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ye[i] = dp[i] = 0.f;
-    each<CB>([&](int b, int t, int r, int) {
-      ye[8 * b + 4 * t + r] = W.t[b][t][r] * Er.t[b][t][r];
-      dp[8 * b + 4 * t + r] = dV.t[b][t][r] * pred.t[b][t][r];
-    });
-    each<NB>([&](int b, int t, int r, int) { dot = fmaf(S0.t[b][t][r], S.t[b][t][r], dot); });
-    dot *= last;
-    float* dots = p.dots + (sh * (p.VP / 16) + vb) * kDots;
-    const float sy = sum_rows16(ye, lane), sp = sum_rows16(dp, lane), sw = sum_rows16(uw, lane);
-    if (n < 8 * CB) {
-      const int row = 32 * (n / 8) + 8 * j + n % 8;
-      dots[C + row] = sy;
-      dots[2 * C + row] = sp;
-      dots[3 * C + row] = sw;
-    }
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
-    if (lane == 0) dots[4 * C] = dot;
-    store_cols<CB>(rows_ws(p.dV), wat, wstride, dV);
-    store_out(head_rsrc(p.dv, row0, p.H, h, p.V, Math::es, rows), vat, vstride, dV);
-    // dS0 = e^{G_C} dS1 + Q^T (scale e^G dO) - K^T (e^G dV)
-    Part<TP> BQ[CB];
-    each<CB>([&](int b, int t, int r, int row) {
-      dO.t[b][t][r] *= eG[row] * p.scale;
-      dV.t[b][t][r] *= -eG[row];
-    });
-    split_all(BQ, dO);
-    split_all(B, dV);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4 a = S.t[b][t] * last;
-#pragma unroll
-        for (int rb = 0; rb < CB; ++rb) {
-          Math::mma(a, load_col<Math, UK, 1>(Qs, 32 * rb + 8 * j, 32 * b + 4 * t, 8, lane, 0), BQ[rb]);
-          Math::mma(a, load_col<Math, UK, 1>(Ks, 32 * rb + 8 * j, 32 * b + 4 * t, 8, lane, 0), B[rb]);
-        }
-        S.t[b][t] = a;
-      }
+  for (int b = 0; b < NB; ++b) {
+    if (b + 1 < NB)
+      fk[(b + 1) & 1].load(l.k, b + 1, lane, j);
+    else
+      f3[0].load(x3.p, lane, j);
+    hold_lds();
+    mma_tiles(tiles(W), fk[b & 1].a, sb);
+    if (b + 1 < NB) sb = split<TP>(S.t[(b + 1) % NB][0], S.t[(b + 1) % NB][1]);
   }
-  if (on && p.dS0)
-    store_cols<NB>(make_rsrc_u32(p.dS0 + (s * p.H + h) * p.K * p.V, sbytes), sat, (uint32_t)(p.V * 4), S);
+  float uw[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) uw[i] = 0.f;
+  each<CB>([&](int b, int t, int r, int row) {
+    W.t[b][t][r] *= eK[row];
+    uw[8 * b + 4 * t + r] = bt[row] * Er.t[b][t][r] * W.t[b][t][r];
+  });
+  Part<kIn> dOB[CB];
+  split_all(dOB, dO);
+  f3[1].load(x3.t, lane, j);
+  hold_lds();
+  f3[0].mma(W, dOB);
+  // dV = T^T (beta W)
+  Cols<CB> dV = zero_cols<CB>(), x;
+  Part<TP> B[CB];
+  each<CB>([&](int b, int t, int r, int row) { x.t[b][t][r] = W.t[b][t][r] * bt[row]; });
+  split_all(B, x);
+  f3[0].load(x3.m, lane, j);
+  hold_lds();
+  f3[1].mma(dV, B);
+  // Y = W - stril(D K K^T)^T dV
+  each<CB>([&](int b, int t, int r, int) { x.t[b][t][r] = -dV.t[b][t][r]; });
+  split_all(B, x);
+  ColTiles fq[2], fc[2];
+  fq[0].load(l.q, 0, lane, j);
+  fc[0].load(l.k, 0, lane, j);
+  hold_lds();
+  f3[0].mma(W, B);
+  float ye[16], dp[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) ye[i] = dp[i] = 0.f;
+  each<CB>([&](int b, int t, int r, int) {
+    ye[8 * b + 4 * t + r] = W.t[b][t][r] * Er.t[b][t][r];
+    dp[8 * b + 4 * t + r] = dV.t[b][t][r] * pred.t[b][t][r];
+  });
+  float* dots = p.dots + (sh * (p.VP / 16) + w.vb) * kDots;
+  const float sy = sum_rows16(ye, lane), sp = sum_rows16(dp, lane), sw = sum_rows16(uw, lane);
+  if (n < 8 * CB) {
+    const int row = 32 * (n / 8) + 8 * j + n % 8;
+    dots[C + row] = sy;
+    dots[2 * C + row] = sp;
+    dots[3 * C + row] = sw;
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
+  if (lane == 0) dots[4 * C] = dot;
+  store_cols<CB>(make_rsrc_u32(p.dV + sh * C * p.VP, (uint32_t)(C * p.VP * 4)), w.wat, w.wstride, dV);
+  store_out(head_rsrc(p.dv, w.seq.row0 + c * C, p.H, w.h, p.V, IO::es, w.rows(c)), w.vat, w.vstride, dV);
+  // dS0 = e^{G_C} dS1 + Q^T (scale e^G dO) - K^T (e^G dV)
+  Part<TP> BQ[CB];
+  each<CB>([&](int b, int t, int r, int row) {
+    dO.t[b][t][r] *= eG[row] * p.scale;
+    dV.t[b][t][r] *= -eG[row];
+  });
+  split_all(BQ, dO);
+  split_all(B, dV);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (b + 1 < NB) {
+      fq[(b + 1) & 1].load(l.q, b + 1, lane, j);
+      fc[(b + 1) & 1].load(l.k, b + 1, lane, j);
+    }
+    hold_lds();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) S.t[b][t] *= last;
+    fq[b & 1].mma(S.t[b], BQ);
+    fc[b & 1].mma(S.t[b], B);
+  }
+}
+
+__global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p) {
+  __shared__ __attribute__((aligned(16))) KeyRows l0;
+  __shared__ __attribute__((aligned(16))) RevTri x3;
+  const Walk w(p);
+  const KeyOffsets ko(p, w.tid);
+  Cols<NB> S = zero_cols<NB>();  // the adjoint of the state
+  if (p.dlast_S) S = load_cols<NB>(w.state(p.dlast_S, p), w.sat, (uint32_t)(p.V * 4));
+  const int64_t chunks = (w.seq.len + C - 1) / C;
+  for (int64_t c = chunks - 1; c >= 0; --c) {
+    const int64_t row0 = w.seq.row0 + c * C, slot = w.seq.slot0 + c, sh = slot * p.H + w.h;
+    const int rows = w.rows(c);
+    __syncthreads();
+    load_keys(l0, p, ko, slot, sh, row0, w.hk, rows, w.wave, w.lane);
+    load_tri<TP>(x3.p, p.P, sh, w.wave, w.lane);
+    load_tri<TP>(x3.t, p.T, sh, w.wave, w.lane);
+    load_tri<TP>(x3.m, p.M, sh, w.wave, w.lane);
+    RawCols d;
+    d.fetch(head_rsrc(p.do_, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
+    const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
+    const Cols<CB> Er = load_cols<CB>(rows_ws(p.E), w.wat, w.wstride);
+    const Cols<CB> pred = load_cols<CB>(rows_ws(p.pred), w.wat, w.wstride);
+    const Cols<NB> S0 = load_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride);
+    sync_loads();
+    if (w.on) rev_chunk(p, w, l0, x3, S, d.widen(), Er, pred, S0, c);
+  }
+  if (w.on && p.dS0) store_cols<NB>(w.state(p.dS0, p), w.sat, (uint32_t)(p.V * 4), S);
 }
 
 // ---- grad ----------------------------------------------------------------------------------
 
-constexpr int GP = Math::kGradParts;  // parts that the gradients of q and k are made of
+constexpr int GP = kOutParts;  // parts that the gradients of q and k are made of
 constexpr int kWavesGrad = KP == 256 ? 8 : 4;
 constexpr int kTilesGrad = KP / 16 / kWavesGrad > 0 ? KP / 16 / kWavesGrad : 1;  // 16-key tiles a wavefront
 constexpr int MT = C / 16;                                                      // 16-token tiles
-constexpr int VB = 64;                                                          // columns staged at a time
-constexpr int LDV = VB + Math::pad;
+constexpr int VB = MSM_IO_BF16 ? 64 : 32;                                       // columns staged at a time
+constexpr int LDV = VB + 8, LDT = C + 8;
 
 __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p) {
   constexpr int THREADS = 64 * kWavesGrad;
-  constexpr int kStage = (1 + 2 * TP) * C * LDV, kPair = 2 * GP * C * LDT;
-  __shared__ __attribute__((aligned(16))) E Ks[C * KP];
-  __shared__ __attribute__((aligned(16))) E Qs[C * KP];
+  constexpr int kStage = (kIn + 2 * TP) * C * LDV, kPair = 2 * GP * C * LDT;
+  __shared__ __attribute__((aligned(16))) uint16_t Ks[kIn * kRows];
+  __shared__ __attribute__((aligned(16))) uint16_t Qs[kIn * kRows];
   // first the staged columns of dO, dV and U, then the token-pair matrices X and Z + Z^T
-  __shared__ __attribute__((aligned(16))) TE buf[kStage > kPair ? kStage : kPair];
+  __shared__ __attribute__((aligned(16))) uint16_t buf[kStage > kPair ? kStage : kPair];
   __shared__ __attribute__((aligned(16))) float ev[3 * C];
   __shared__ double Gd[C];
   __shared__ float across[MT][C];  // sums of N_ij over a tile of rows i >= t and all j < t
@@ -612,14 +756,14 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   const ChunkRows ch = chunk_rows<C>(p, slot);
   if (ch.n == 0) return;
   const int64_t at = (ch.row0 * p.Hk + hk) * p.K;
-  stage_two<THREADS>(Ks, Qs, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, Math::es, ch.n),
-                     head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, Math::es, ch.n), (uint32_t)(p.Hk * p.K * Math::es),
-                     (int)p.K, p.vec_k, tid);
-  E* dOs = reinterpret_cast<E*>(buf);
-  TE* dVs = buf + C * LDV;
-  TE* Us = dVs + TP * C * LDV;
-  TE* Xs = buf;
-  TE* Zs = buf + GP * C * LDT;
+  const uint32_t stride = (uint32_t)(p.Hk * p.K * IO::es);
+  stage_rows<THREADS>(Ks, nullptr, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
+  stage_rows<THREADS>(Qs, nullptr, head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
+  uint16_t* dOs = buf;
+  uint16_t* dVs = buf + kIn * C * LDV;
+  uint16_t* Us = dVs + TP * C * LDV;
+  uint16_t* Xs = buf;
+  uint16_t* Zs = buf + GP * C * LDT;
   const int tile0 = wave * kTilesGrad;           // this wavefront's key tiles
   const bool keys = tile0 * 16 < KP;
   const bool pairs = wave < MT;                  // this wavefront's row of token pairs
@@ -642,60 +786,63 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
 #pragma unroll
       for (int t = 0; t < kTilesGrad; ++t) a1[m][t] = a2[m][t] = a3[m][t] = zero4();
     }
-    const auto rdo = head_rsrc(p.do_, ch.row0, p.H, h, p.V, Math::es, ch.n);
+    const auto rdo = head_rsrc(p.do_, ch.row0, p.H, h, p.V, IO::es, ch.n);
     const auto rdv = make_rsrc_u32(p.dV + sh * C * p.VP, (uint32_t)(C * p.VP * 4));
     const auto re = make_rsrc_u32(p.E + sh * C * p.VP, (uint32_t)(C * p.VP * 4));
-    for (int64_t v0 = 0; v0 < p.VP; v0 += VB) {
+    const auto rs0 = make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4));
+    const auto rs1 = make_rsrc_u32(p.dS + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4));
+    for (int v0 = 0; v0 < p.VP; v0 += VB) {
       __syncthreads();  // ev is there; the previous columns have been used
       for (int u = tid; u < C * VB / 8; u += THREADS) {
         const int row = u / (VB / 8), c = (u % (VB / 8)) * 8;
+        f32x4 o[2];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          dOs[row * LDV + c + i] = (E)IO::bload(rdo, v0 + c + i < p.V ? (uint32_t)(row * p.H * p.V + v0 + c + i) * Math::es : kOutside, 0);
+          o[i / 4][i % 4] = IO::widen(IO::bload(rdo, v0 + c + i < p.V ? (uint32_t)(row * p.H * p.V + v0 + c + i) * IO::es : kOutside, 0));
         const uint32_t w = v0 + c < p.VP ? (uint32_t)(row * p.VP + v0 + c) * 4 : kOutside;
-        const f32x4 a = __builtin_bit_cast(f32x4, bload16(rdv, w)), b = __builtin_bit_cast(f32x4, bload16(rdv, w + 16));
-        const f32x4 d = __builtin_bit_cast(f32x4, bload16(re, w)) * ev[2 * C + row];
-        const f32x4 e = __builtin_bit_cast(f32x4, bload16(re, w + 16)) * ev[2 * C + row];
-        Math::store_planes<TP>(dVs + row * LDV + c, C * LDV, a, b);
-        Math::store_planes<TP>(Us + row * LDV + c, C * LDV, d, e);
+        const f32x4 a = bload4(rdv, w), b = bload4(rdv, w + 16);
+        const f32x4 d = bload4(re, w) * ev[2 * C + row], e = bload4(re, w + 16) * ev[2 * C + row];
+        store_parts(dOs + row * LDV + c, C * LDV, split<kIn>(o[0], o[1]));
+        store_parts(dVs + row * LDV + c, C * LDV, split<TP>(a, b));
+        store_parts(Us + row * LDV + c, C * LDV, split<TP>(d, e));
       }
       __syncthreads();
 #pragma unroll
       for (int b = 0; b < VB / 32; ++b) {
         if (v0 + 32 * b >= p.VP) break;
         if (keys) {
-          Part<1> fo[MT];
+          Part<kIn> fo[MT];
           Part<GP> fv[MT], fu[MT];
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const int e = (16 * m + n) * LDV + 32 * b + 8 * j;
-            fo[m] = Math::load<1>(dOs + e, 0);
-            fv[m] = Math::load<GP>(dVs + e, C * LDV);
-            fu[m] = Math::load<GP>(Us + e, C * LDV);
+            fo[m] = load_ld<kIn>(dOs + e, C * LDV);
+            fv[m] = load_ld<GP>(dVs + e, C * LDV);
+            fu[m] = load_ld<GP>(Us + e, C * LDV);
           }
 #pragma unroll
           for (int t = 0; t < kTilesGrad; ++t) {
-            const int64_t i = (sh * KP + 16 * (tile0 + t) + n) * p.VP + v0 + 32 * b + 8 * j;
-            const auto s0 = Math::split<GP>(*reinterpret_cast<const f32x4*>(p.S + i), *reinterpret_cast<const f32x4*>(p.S + i + 4));
-            const auto s1 = Math::split<GP>(*reinterpret_cast<const f32x4*>(p.dS + i), *reinterpret_cast<const f32x4*>(p.dS + i + 4));
+            const uint32_t i = (uint32_t)((16 * (tile0 + t) + n) * p.VP + v0 + 32 * b + 8 * j) * 4;
+            const auto s0 = split<GP>(bload4(rs0, i), bload4(rs0, i + 16));
+            const auto s1 = split<GP>(bload4(rs1, i), bload4(rs1, i + 16));
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              Math::mma(a1[m][t], fo[m], s0);
-              Math::mma(a2[m][t], fv[m], s0);
-              Math::mma(a3[m][t], fu[m], s1);
+              mma(a1[m][t], fo[m], s0);
+              mma(a2[m][t], fv[m], s0);
+              mma(a3[m][t], fu[m], s1);
             }
           }
         }
         if (pairs) {
           const int e = (16 * wave + n) * LDV + 32 * b + 8 * j;
-          const auto fo = Math::load<1>(dOs + e, 0);
-          const auto fv = Math::load<TP>(dVs + e, C * LDV);
+          const auto fo = load_ld<kIn>(dOs + e, C * LDV);
+          const auto fv = load_ld<TP>(dVs + e, C * LDV);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (m > wave) continue;
-            const auto fu = Math::load<TP>(Us + (16 * m + n) * LDV + 32 * b + 8 * j, C * LDV);
-            Math::mma(X[m], fo, fu);
-            Math::mma(Z[m], fv, fu);
+            const auto fu = load_ld<TP>(Us + (16 * m + n) * LDV + 32 * b + 8 * j, C * LDV);
+            mma(X[m], fo, fu);
+            mma(Z[m], fv, fu);
           }
         }
       }
@@ -709,9 +856,9 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
         if (m <= wave) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const auto B = load_row<Math, UK, 1>(Ks, 16 * m + n, 32 * b + 8 * j, 0);
-            Math::mma(qk, load_row<Math, UK, 1>(Qs, 16 * wave + n, 32 * b + 8 * j, 0), B);
-            Math::mma(kk, load_row<Math, UK, 1>(Ks, 16 * wave + n, 32 * b + 8 * j, 0), B);
+            const auto B = load_row<UK, kIn>(Ks, 16 * m + n, 32 * b + 8 * j, kRows);
+            mma(qk, load_row<UK, kIn>(Qs, 16 * wave + n, 32 * b + 8 * j, kRows), B);
+            mma(kk, load_row<UK, kIn>(Ks, 16 * wave + n, 32 * b + 8 * j, kRows), B);
           }
         }
         float below = 0.f;
@@ -720,10 +867,10 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
           const int row = 16 * wave + 4 * j + r, c = 16 * m + n;
           const float D = c <= row ? exp_of(Gd[row] - Gd[c]) : 0.f;
           const float x = c <= row ? p.scale * D * X[m][r] : 0.f, z = c < row ? -D * Z[m][r] : 0.f;
-          Math::store1<GP>(Xs + row * LDT + c, C * LDT, x);
+          store_parts1<GP>(Xs + row * LDT + c, C * LDT, x);
           if (c <= row) {
-            Math::store1<GP>(Zs + row * LDT + c, C * LDT, z);
-            Math::store1<GP>(Zs + c * LDT + row, C * LDT, z);
+            store_parts1<GP>(Zs + row * LDT + c, C * LDT, z);
+            store_parts1<GP>(Zs + c * LDT + row, C * LDT, z);
           }
           // running sum of N along the row; a pair (row, c) lies across t = c + 1 and on
           float sum = c < row ? x * qk[r] + z * kk[r] : 0.f;
@@ -786,15 +933,15 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
       for (int b = 0; b < CB; ++b)
 #pragma unroll
         for (int t = 0; t < kTilesGrad; ++t) {
-          const auto kt = load_col<Math, UK, 1>(Ks, 32 * b + 8 * j, 16 * (tile0 + t), 4, lane, 0);
-          const auto qt = load_col<Math, UK, 1>(Qs, 32 * b + 8 * j, 16 * (tile0 + t), 4, lane, 0);
+          const auto kt = load_col<UK, kIn>(Ks, 32 * b + 8 * j, 16 * (tile0 + t), 4, lane, kRows);
+          const auto qt = load_col<UK, kIn>(Qs, 32 * b + 8 * j, 16 * (tile0 + t), 4, lane, kRows);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (m / 2 >= b)
-              Math::mma(dq[m][t], Math::load<GP>(Xs + (16 * m + n) * LDT + 32 * b + 8 * j, C * LDT), kt);
-            Math::mma(dk[m][t], Math::load<GP>(Zs + (16 * m + n) * LDT + 32 * b + 8 * j, C * LDT), kt);
+              mma(dq[m][t], load_ld<GP>(Xs + (16 * m + n) * LDT + 32 * b + 8 * j, C * LDT), kt);
+            mma(dk[m][t], load_ld<GP>(Zs + (16 * m + n) * LDT + 32 * b + 8 * j, C * LDT), kt);
             if (m / 2 <= b)
-              Math::mma(dk[m][t], Math::load_t<GP>(Xs + (32 * b + 8 * j) * LDT, LDT, C * LDT, lane, 16 * m, 4), qt);
+              mma(dk[m][t], load_col_ld<GP>(Xs + (32 * b + 8 * j) * LDT, LDT, 16 * m, lane, C * LDT), qt);
           }
         }
     }
@@ -809,8 +956,8 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
           const int row = 16 * m + 4 * j + r, c = 16 * (tile0 + t) + n;
           if (row < ch.n && c < p.K) {
             const int64_t i = at + row * p.Hk * p.K + c;
-            static_cast<E*>(p.dq)[i] = Math::narrow(dq[m][t][r]);
-            static_cast<E*>(p.dk)[i] = Math::narrow(dk[m][t][r]);
+            IO::store(p.dq, i, dq[m][t][r]);
+            IO::store(p.dk, i, dk[m][t][r]);
           }
         }
   }

@@ -12,13 +12,13 @@ namespace msm {
 
 constexpr int kDeltaMaxK = 256;  // key size a state may have (rows of S)
 
-// Tokens per chunk: 64, but 32 where two chunks of fp32 keys and queries of the largest padded
-// size would not fit the 160 KB of LDS.
+// Tokens per chunk: 64, but 32 where a chunk of fp32 keys and queries of the largest padded size,
+// in their three parts, would not fit the 160 KB of LDS.
 constexpr int delta_chunk(int io_bf16, int KP) { return (!io_bf16 && KP == 256) ? 32 : 64; }
 // Key size padded to a size the kernels are built for.
 constexpr int delta_padded_k(int64_t K) { return K <= 32 ? 32 : (K <= 64 ? 64 : (K <= 128 ? 128 : 256)); }
-// Planes a chunk matrix is stored in: fp32, or three bf16 planes whose sum is the fp32 value.
-constexpr int delta_planes(int io_bf16) { return io_bf16 ? 3 : 1; }
+// bf16 planes that q and k are kept in: as they are, or fp32 in three parts.
+constexpr int delta_in_planes(int io_bf16) { return io_bf16 ? 1 : 3; }
 
 struct DeltaArgs {
   const void* q;        // (tokens, Hk, K) I/O dtype
@@ -40,9 +40,10 @@ struct DeltaArgs {
   float* dS0;
   // workspace; sh = slot * H + head numbers the chunks
   float* vec;           // [sh][5 C]: e^G, e^(G_last - G), beta, G as doubles
-  void* T;              // [sh][planes][blocks]  inverse of the chunk's unit lower system
-  void* P;              // [sh][planes][blocks]  scale D tril(Q K^T)
-  void* M;              // [sh][planes][blocks]  D stril(K K^T)            (backward)
+  void* T;              // [sh][3 planes][blocks] inverse of the chunk's unit lower system
+  void* P;              // [sh][3 planes][blocks] scale D tril(Q K^T)
+  void* M;              // [sh][3 planes][blocks] D stril(K K^T)            (backward)
+  void* kq;             // [slot][Hk][2][planes][C][KP] k and q as LDS holds them, unless kq_direct
   float* S;             // [sh][KP][VP] state before the chunk          (backward)
   float* dS;            // [sh][KP][VP] adjoint of the state after it   (backward)
   float* E;             // [sh][C][VP] prediction errors                (backward)
@@ -56,6 +57,7 @@ struct DeltaArgs {
   int64_t Hk, H, K, V, VP;
   float scale;
   int32_t vec_k;        // rows of q and k can be read 16 bytes at a time
+  int32_t kq_direct;    // and they need no conversion
 };
 
 struct DeltaStepArgs {
