@@ -378,54 +378,53 @@ __device__ __forceinline__ void split_all(Part<N> (&B)[CB], const Cols<CB>& x) {
 constexpr int kPasses = C * UK / (64 * kWavesScan);  // of a plane of keys
 static_assert(C * UK % (64 * kWavesScan) == 0, "whole passes");
 
+// Passes of a wavefront over N planes of a chunk matrix; LDS holds whole rounds of all wavefronts.
+constexpr int tri_rounds(int n) { return (n * TriM::kPlane / 512 + kWavesScan - 1) / kWavesScan; }
+constexpr int tri_lds(int n) { return tri_rounds(n) * kWavesScan * 512; }
+
 struct KeyRows {  // LDS
   uint16_t k[kIn * kRows], q[kIn * kRows];
-  float ev[3 * C];  // e^G, e^(G_C - G), beta
+  float ev[256];  // e^G, e^(G_C - G), beta: 3 C floats
 };
+// The loads below have no branches (a walk's step is one block of code, whose products then cover
+// their address arithmetic): a chunk that is not there, `rows` = 0, has empty resources and
+// brings zeros.
 template <int N>
-__device__ __forceinline__ void load_tri(uint16_t* lds, const void* base, int64_t sh, int wave, int lane) {
-  const auto r = make_rsrc_u32(static_cast<const uint16_t*>(base) + sh * kTri, N * TriM::kPlane * 2);
+__device__ __forceinline__ void load_tri(uint16_t* lds, const void* base, int64_t sh, int rows, int wave, int lane) {
+  const auto r = make_rsrc_u32(static_cast<const uint16_t*>(base) + sh * kTri, rows > 0 ? N * TriM::kPlane * 2 : 0);
 #pragma unroll
-  for (int i = 0; i < (N * TriM::kPlane / 512 + kWavesScan - 1) / kWavesScan; ++i) {
+  for (int i = 0; i < tri_rounds(N); ++i) {
     const int pass = i * kWavesScan + wave;
-    if (pass < N * TriM::kPlane / 512) load_lds(r, lds + pass * 512, lane * 16, pass * 1024);
+    load_lds(r, lds + pass * 512, lane * 16 + pass * 1024, 0);
   }
 }
-// Offsets of this thread's units of keys in their rows, when they are loaded from q and k.
+// Offsets of this thread's units of keys in their rows, or in the planes in the workspace.
 struct KeyOffsets {
   uint32_t at[kPasses];
   __device__ __forceinline__ KeyOffsets(const DeltaArgs& p, int tid) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int u = tid + i * 64 * kWavesScan, row = u / UK, c = ((u % UK) ^ swizzle<UK>(row)) * 8;
-      at[i] = !p.kq_direct ? lane_offset(u) : (c < p.K ? (uint32_t)(row * p.Hk * p.K + c) * IO::es : kOutside);
+      at[i] = !p.kq_direct ? u * 16 : (c < p.K ? (uint32_t)(row * p.Hk * p.K + c) * IO::es : kOutside);
     }
   }
-  static __device__ __forceinline__ uint32_t lane_offset(int u) { return (uint32_t)u * 16; }
 };
 __device__ __forceinline__ void load_keys(KeyRows& l, const DeltaArgs& p, const KeyOffsets& o, int64_t slot, int64_t sh,
                                           int64_t row0, int64_t hk, int rows, int wave, int lane) {
-  if (p.kq_direct) {
-    const auto rk = head_rsrc(p.k, row0, p.Hk, hk, p.K, IO::es, rows);
-    const auto rq = head_rsrc(p.q, row0, p.Hk, hk, p.K, IO::es, rows);
+  const int64_t in_rows = (row0 * p.Hk + hk) * p.K * IO::es, in_ws = (slot * p.Hk + hk) * 2 * kIn * kRows * 2;
+  const char* k = p.kq_direct ? static_cast<const char*>(p.k) + in_rows : static_cast<const char*>(p.kq) + in_ws;
+  const char* q = p.kq_direct ? static_cast<const char*>(p.q) + in_rows : static_cast<const char*>(p.kq) + in_ws + kIn * kRows * 2;
+  const int64_t bytes = p.kq_direct ? ((rows - 1) * p.Hk + 1) * p.K * IO::es : kIn * kRows * 2;
+  const auto rk = make_rsrc(k, rows > 0 ? bytes : 0), rq = make_rsrc(q, rows > 0 ? bytes : 0);
+#pragma unroll
+  for (int n = 0; n < kIn; ++n)
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      load_lds(rk, l.k + (i * kWavesScan + wave) * 512, o.at[i], 0);
-      load_lds(rq, l.q + (i * kWavesScan + wave) * 512, o.at[i], 0);
+      load_lds(rk, l.k + n * kRows + (i * kWavesScan + wave) * 512, o.at[i] + n * kRows * 2, 0);
+      load_lds(rq, l.q + n * kRows + (i * kWavesScan + wave) * 512, o.at[i] + n * kRows * 2, 0);
     }
-  } else {
-    const auto r = make_rsrc_u32(static_cast<const uint16_t*>(p.kq) + (slot * p.Hk + hk) * 2 * kIn * kRows, 2 * kIn * kRows * 2);
-#pragma unroll
-    for (int n = 0; n < kIn; ++n)
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        load_lds(r, l.k + n * kRows + (i * kWavesScan + wave) * 512, o.at[i], n * kRows * 2);
-        load_lds(r, l.q + n * kRows + (i * kWavesScan + wave) * 512, o.at[i], (kIn + n) * kRows * 2);
-      }
-  }
-  // the first 3 C floats of vec are whole rows of 16-byte units; one wavefront loads them
-  if (wave == kWavesScan - 1 && lane < 3 * C / 4)
-    load_lds(make_rsrc_u32(p.vec + sh * kVec, 3 * C * 4), l.ev, lane * 16, 0);
+  // every wavefront brings the same values: cheaper than a branch
+  load_lds(make_rsrc_u32(p.vec + sh * kVec, rows > 0 ? 3 * C * 4 : 0), l.ev, lane * 16, 0);
 }
 
 // LDS of the walks: two chunks' worth where the 160 KB allow, so that the next chunk's loads run
@@ -435,8 +434,8 @@ template <bool BWD>
 struct ScanChunk {
   static constexpr int OP = BWD ? TP : kOutParts;
   KeyRows r;
-  uint16_t t[kTri];
-  uint16_t p[BWD ? 8 : OP * TriM::kPlane];
+  uint16_t t[tri_lds(TP)];
+  uint16_t p[BWD ? 8 : tri_lds(OP)];
 };
 struct Nothing {};
 
@@ -471,7 +470,11 @@ struct Walk {
     sat = col < p.V ? (8 * j * (uint32_t)p.V + col) * 4 : kOutside;  // states
     sbytes = (uint32_t)(p.K * p.V * 4);
   }
-  __device__ __forceinline__ int rows(int64_t c) const { return (int)(seq.len - c * C < C ? seq.len - c * C : C); }
+  // rows of a chunk, none past either end
+  __device__ __forceinline__ int rows(int64_t c) const {
+    const int64_t left = seq.len - c * C;
+    return c < 0 || left < 0 ? 0 : (int)(left < C ? left : C);
+  }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t state(const float* base, const DeltaArgs& p) const {
     return make_rsrc_u32(base + (s * p.H + h) * p.K * p.V, sbytes);
   }
@@ -535,7 +538,7 @@ __device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, co
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = i < 8 * CB ? O.t[(i / 8) % CB][(i / 4) % 2][i % 4] * dO.t[(i / 8) % CB][(i / 4) % 2][i % 4] : 0.f;
     const float sum = sum_rows16(x, lane);
-    if (n < 8 * CB) p.dots[(sh * (p.VP / 16) + w.vb) * kDots + 32 * (n / 8) + 8 * j + n % 8] = sum;
+    if (w.on && n < 8 * CB) p.dots[(sh * (p.VP / 16) + w.vb) * kDots + 32 * (n / 8) + 8 * j + n % 8] = sum;
   } else {
     Part<OP> UO[CB];
     split_all(UO, U);
@@ -570,8 +573,8 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
     const int64_t row0 = w.seq.row0 + c * C, slot = w.seq.slot0 + c, sh = slot * p.H + w.h;
     const int rows = w.rows(c);
     load_keys(l.r, p, ko, slot, sh, row0, w.hk, rows, w.wave, w.lane);
-    load_tri<TP>(l.t, p.T, sh, w.wave, w.lane);
-    if constexpr (!BWD) load_tri<ScanChunk<BWD>::OP>(l.p, p.P, sh, w.wave, w.lane);
+    load_tri<TP>(l.t, p.T, sh, rows, w.wave, w.lane);
+    if constexpr (!BWD) load_tri<ScanChunk<BWD>::OP>(l.p, p.P, sh, rows, w.wave, w.lane);
     v.fetch(head_rsrc(p.v, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
     if (BWD) d.fetch(head_rsrc(p.do_, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
   };
@@ -579,8 +582,8 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
     const auto step = [&](ScanChunk<BWD>& here, ScanChunk<BWD>& next, int64_t c) {
       sync_loads();  // `here` is loaded, and nothing reads `next` any more
       const Cols<CB> R = v.widen(), dO = d.widen();
-      if (c + 1 < chunks) fetch(next, c + 1);
-      if (w.on) scan_chunk<BWD>(p, w, here, S, R, dO, c);
+      fetch(next, c + 1);
+      scan_chunk<BWD>(p, w, here, S, R, dO, c);
     };
     if (chunks > 0) fetch(l0, 0);
     for (int64_t c = 0; c < chunks; c += 2) {
@@ -592,7 +595,7 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
       __syncthreads();
       fetch(l0, c);
       sync_loads();
-      if (w.on) scan_chunk<BWD>(p, w, l0, S, v.widen(), d.widen(), c);
+      scan_chunk<BWD>(p, w, l0, S, v.widen(), d.widen(), c);
     }
   }
   if (w.on && p.last_S) store_cols<NB>(w.state(p.last_S, p), w.sat, (uint32_t)(p.V * 4), S);
@@ -601,7 +604,7 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
 // ---- rev -----------------------------------------------------------------------------------
 
 struct RevTri {
-  uint16_t t[kTri], p[kTri], m[kTri];
+  uint16_t t[tri_lds(TP)], p[tri_lds(TP)], m[tri_lds(TP)];
 };
 
 __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, const KeyRows& l, const RevTri& x3,
@@ -671,7 +674,7 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
   });
   float* dots = p.dots + (sh * (p.VP / 16) + w.vb) * kDots;
   const float sy = sum_rows16(ye, lane), sp = sum_rows16(dp, lane), sw = sum_rows16(uw, lane);
-  if (n < 8 * CB) {
+  if (w.on && n < 8 * CB) {
     const int row = 32 * (n / 8) + 8 * j + n % 8;
     dots[C + row] = sy;
     dots[2 * C + row] = sp;
@@ -679,7 +682,7 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
   }
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
-  if (lane == 0) dots[4 * C] = dot;
+  if (w.on && lane == 0) dots[4 * C] = dot;
   store_cols<CB>(make_rsrc_u32(p.dV + sh * C * p.VP, (uint32_t)(C * p.VP * 4)), w.wat, w.wstride, dV);
   store_out(head_rsrc(p.dv, w.seq.row0 + c * C, p.H, w.h, p.V, IO::es, w.rows(c)), w.vat, w.vstride, dV);
   // dS0 = e^{G_C} dS1 + Q^T (scale e^G dO) - K^T (e^G dV)
@@ -717,9 +720,9 @@ __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p)
     const int rows = w.rows(c);
     __syncthreads();
     load_keys(l0, p, ko, slot, sh, row0, w.hk, rows, w.wave, w.lane);
-    load_tri<TP>(x3.p, p.P, sh, w.wave, w.lane);
-    load_tri<TP>(x3.t, p.T, sh, w.wave, w.lane);
-    load_tri<TP>(x3.m, p.M, sh, w.wave, w.lane);
+    load_tri<TP>(x3.p, p.P, sh, rows, w.wave, w.lane);
+    load_tri<TP>(x3.t, p.T, sh, rows, w.wave, w.lane);
+    load_tri<TP>(x3.m, p.M, sh, rows, w.wave, w.lane);
     RawCols d;
     d.fetch(head_rsrc(p.do_, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
     const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
@@ -727,7 +730,7 @@ __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p)
     const Cols<CB> pred = load_cols<CB>(rows_ws(p.pred), w.wat, w.wstride);
     const Cols<NB> S0 = load_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride);
     sync_loads();
-    if (w.on) rev_chunk(p, w, l0, x3, S, d.widen(), Er, pred, S0, c);
+    rev_chunk(p, w, l0, x3, S, d.widen(), Er, pred, S0, c);
   }
   if (w.on && p.dS0) store_cols<NB>(w.state(p.dS0, p), w.sat, (uint32_t)(p.V * 4), S);
 }
