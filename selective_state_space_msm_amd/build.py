@@ -18,7 +18,9 @@ LIB = os.path.join(PKG, "libmsm.so")
 # variant 0 plain, 1 fused extras, 2 fused extras with the zero-order hold -- all in parallel
 _PARTS = [("-DMSM_IO_BF16=%d" % io, "-DMSM_EXT=%d" % ext) for io in (0, 1) for ext in (0, 1, 2)]
 # the chunked gated delta rule: one build per I/O type and padded key size
-_DELTA = [("-DMSM_IO_BF16=%d" % io, "-DMSM_KP=%d" % kp) for io in (0, 1) for kp in (32, 64, 128, 256)]
+# (accumulators in ordinary registers: its kernels work on them between products, and each move
+# from the accumulator file would be one more vector instruction)
+_DELTA = [("-DMSM_IO_BF16=%d" % io, "-DMSM_KP=%d" % kp, "-mllvm", "-amdgpu-mfma-vgpr-form=1") for io in (0, 1) for kp in (32, 64, 128, 256)]
 SOURCES = ([("msm_api.cpp", ()), ("msm_launch.hip", ()), ("msm_bwd_wide.hip", ()),
             ("msm_step.hip", ()), ("msm_cfwd.hip", ()), ("msm_cbwd.hip", ())]
            + [("msm_fwd.hip", f) for f in _PARTS] + [("msm_bwd.hip", f) for f in _PARTS]
@@ -34,7 +36,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH, "-Xclang", "-t
 
 
 def _compile(src: str, flags) -> tuple[subprocess.Popen, str]:
-    tag = "".join(f.split("=")[-1] for f in flags)
+    tag = "".join(f.split("=")[-1] for f in flags if f.startswith("-D"))
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + (("." + tag) if tag else "") + ".o")
     cmd = [HIPCC, *COMMON, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
     return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), obj

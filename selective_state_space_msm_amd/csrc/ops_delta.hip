@@ -173,9 +173,10 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   const int64_t slot = blockIdx.x, h = blockIdx.y;
   const ChunkRows ch = chunk_rows<C>(p, slot);
   if (ch.n == 0) return;
-  const int64_t sh = slot * p.H + h, group = p.H / p.Hk, hk = h / group;
+  const uint32_t group = (uint32_t)p.H / (uint32_t)p.Hk;
+  const int64_t sh = slot * p.H + h, hk = uniform((int)((uint32_t)h / group));
   const uint32_t stride = (uint32_t)(p.Hk * p.K * IO::es);
-  uint16_t* ws = p.kq_direct || h % group != 0 ? nullptr : static_cast<uint16_t*>(p.kq) + (slot * p.Hk + hk) * 2 * kIn * kRows;
+  uint16_t* ws = p.kq_direct || h != hk * group ? nullptr : static_cast<uint16_t*>(p.kq) + (slot * p.Hk + hk) * 2 * kIn * kRows;
   stage_rows<256>(Ks, ws, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
   stage_rows<256>(Qs, ws ? ws + kIn * kRows : nullptr, head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride,
                   (int)p.K, p.vec_k, tid);
@@ -386,46 +387,85 @@ struct KeyRows {  // LDS
   uint16_t k[kIn * kRows], q[kIn * kRows];
   float ev[256];  // e^G, e^(G_C - G), beta: 3 C floats
 };
-// The loads below have no branches (a walk's step is one block of code, whose products then cover
-// their address arithmetic): a chunk that is not there, `rows` = 0, has empty resources and
-// brings zeros.
+// An array as a walk meets it: the address of the present chunk's part, the bytes to the next
+// one's, and the extent of a part of `rows` rows, rows * per_row + rest (0 rows: nothing, which
+// reads as zeros).  A walk's step is one block of code without branches, whose products then cover
+// its loads and their address arithmetic.
+struct Stream {
+  const char* at;
+  int64_t step;
+  int32_t per_row, rest;
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int rows) const {
+    return make_rsrc_u32(at, (uint32_t)uniform(rows > 0 ? rows * per_row + rest : 0));
+  }
+  // a whole chunk's part, whatever its rows
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t whole(int rows, uint32_t bytes) const {
+    return make_rsrc_u32(at, (uint32_t)uniform(rows > 0 ? (int)bytes : 0));
+  }
+  __device__ __forceinline__ void next(int dir) { at += dir > 0 ? step : -step; }
+};
+// One head of a token array (rows, heads, size), from row `row`.
+__device__ __forceinline__ Stream head_stream(const void* base, int64_t row, int64_t heads, int64_t h, int64_t size) {
+  const char* at = static_cast<const char*>(base) + ((row * heads + h) * size) * IO::es;
+  return Stream{reinterpret_cast<const char*>(uniform((int64_t)at)), uniform(C * heads * size * IO::es),
+                (int32_t)(heads * size * IO::es), (int32_t)(-(heads - 1) * size * IO::es)};
+}
+// Parts of `bytes` for every slot and head.
+__device__ __forceinline__ Stream slot_stream(const void* base, int64_t slot, int64_t heads, int64_t h, int64_t bytes) {
+  const char* at = static_cast<const char*>(base) + (slot * heads + h) * bytes;
+  return Stream{reinterpret_cast<const char*>(uniform((int64_t)at)), uniform(heads * bytes), 0, (int32_t)bytes};
+}
+
 template <int N>
-__device__ __forceinline__ void load_tri(uint16_t* lds, const void* base, int64_t sh, int rows, int wave, int lane) {
-  const auto r = make_rsrc_u32(static_cast<const uint16_t*>(base) + sh * kTri, rows > 0 ? N * TriM::kPlane * 2 : 0);
+__device__ __forceinline__ void load_tri(uint16_t* lds, const Stream& s, int rows, int wave, int lane) {
+  const auto r = s.whole(rows, N * TriM::kPlane * 2);
 #pragma unroll
   for (int i = 0; i < tri_rounds(N); ++i) {
     const int pass = i * kWavesScan + wave;
     load_lds(r, lds + pass * 512, lane * 16 + pass * 1024, 0);
   }
 }
-// Offsets of this thread's units of keys in their rows, or in the planes in the workspace.
-struct KeyOffsets {
-  uint32_t at[kPasses];
-  __device__ __forceinline__ KeyOffsets(const DeltaArgs& p, int tid) {
+
+// Keys, queries and row factors on their way into LDS: from q and k, or from their planes in the
+// workspace.
+struct Keys {
+  Stream k, q, ev;
+  uint32_t at[kPasses];  // offsets of this thread's units
+  __device__ __forceinline__ Keys(const DeltaArgs& p, int64_t row, int64_t slot, int64_t h, int64_t hk, int tid) {
+    if (p.kq_direct) {
+      k = head_stream(p.k, row, p.Hk, hk, p.K);
+      q = head_stream(p.q, row, p.Hk, hk, p.K);
+    } else {
+      k = slot_stream(p.kq, slot, p.Hk, hk, 2 * kIn * kRows * 2);
+      k.rest = kIn * kRows * 2;
+      q = k;
+      q.at += kIn * kRows * 2;
+    }
+    ev = slot_stream(p.vec, slot, p.H, h, kVec * 4);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int u = tid + i * 64 * kWavesScan, row = u / UK, c = ((u % UK) ^ swizzle<UK>(row)) * 8;
-      at[i] = !p.kq_direct ? u * 16 : (c < p.K ? (uint32_t)(row * p.Hk * p.K + c) * IO::es : kOutside);
+      const int u = tid + i * 64 * kWavesScan, row_ = u / UK, c = ((u % UK) ^ swizzle<UK>(row_)) * 8;
+      at[i] = !p.kq_direct ? u * 16 : (c < p.K ? (uint32_t)(row_ * p.Hk * p.K + c) * IO::es : kOutside);
     }
   }
+  __device__ __forceinline__ void load(KeyRows& l, int rows, int wave, int lane) const {
+    const auto rk = k.rsrc(rows), rq = q.rsrc(rows);
+#pragma unroll
+    for (int n = 0; n < kIn; ++n)
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        load_lds(rk, l.k + n * kRows + (i * kWavesScan + wave) * 512, at[i] + n * kRows * 2, 0);
+        load_lds(rq, l.q + n * kRows + (i * kWavesScan + wave) * 512, at[i] + n * kRows * 2, 0);
+      }
+    // every wavefront brings the same values: cheaper than a branch
+    load_lds(ev.whole(rows, 3 * C * 4), l.ev, lane * 16, 0);
+  }
+  __device__ __forceinline__ void next(int dir) {
+    k.next(dir);
+    q.next(dir);
+    ev.next(dir);
+  }
 };
-__device__ __forceinline__ void load_keys(KeyRows& l, const DeltaArgs& p, const KeyOffsets& o, int64_t slot, int64_t sh,
-                                          int64_t row0, int64_t hk, int rows, int wave, int lane) {
-  const int64_t in_rows = (row0 * p.Hk + hk) * p.K * IO::es, in_ws = (slot * p.Hk + hk) * 2 * kIn * kRows * 2;
-  const char* k = p.kq_direct ? static_cast<const char*>(p.k) + in_rows : static_cast<const char*>(p.kq) + in_ws;
-  const char* q = p.kq_direct ? static_cast<const char*>(p.q) + in_rows : static_cast<const char*>(p.kq) + in_ws + kIn * kRows * 2;
-  const int64_t bytes = p.kq_direct ? ((rows - 1) * p.Hk + 1) * p.K * IO::es : kIn * kRows * 2;
-  const auto rk = make_rsrc(k, rows > 0 ? bytes : 0), rq = make_rsrc(q, rows > 0 ? bytes : 0);
-#pragma unroll
-  for (int n = 0; n < kIn; ++n)
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      load_lds(rk, l.k + n * kRows + (i * kWavesScan + wave) * 512, o.at[i] + n * kRows * 2, 0);
-      load_lds(rq, l.q + n * kRows + (i * kWavesScan + wave) * 512, o.at[i] + n * kRows * 2, 0);
-    }
-  // every wavefront brings the same values: cheaper than a branch
-  load_lds(make_rsrc_u32(p.vec + sh * kVec, rows > 0 ? 3 * C * 4 : 0), l.ev, lane * 16, 0);
-}
 
 // LDS of the walks: two chunks' worth where the 160 KB allow, so that the next chunk's loads run
 // under the present one's products.
@@ -443,12 +483,25 @@ struct Nothing {};
 // read their left factors one step ahead, and without it the reads would sink to their uses.
 __device__ __forceinline__ void hold_lds() { __builtin_amdgcn_sched_barrier(0x1F); }
 
+// Asks for N times one MFMA followed by VALU other vector instructions, and a memory read every MEM
+// of them (0: none): an MFMA occupies the matrix unit for 16 cycles and the issue port for 4, so
+// up to three instructions fit under it, and memory reads issued in a row would wait for each
+// other.
+template <int N, int VALU, int MEM>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    if (MEM && i % (MEM ? MEM : 1) == 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+  }
+}
+
 // This wavefront's place in a walk.
 struct Walk {
-  int tid, wave, lane, n, j, vb, col;
+  int tid, wave, lane, n, j, vb, col, len, chunks;
   bool on;
-  int64_t s, h, hk;
-  SeqRows seq;
+  int64_t s, h, hk, row0, slot0;
   uint32_t vstride, wstride, vat, wat, sat, sbytes;
   __device__ __forceinline__ Walk(const DeltaArgs& p) {
     tid = threadIdx.x;
@@ -456,13 +509,19 @@ struct Walk {
     lane = tid & 63;
     n = lane & 15;
     j = lane >> 4;
-    s = blockIdx.x / p.H;
-    h = blockIdx.x % p.H;
-    hk = h / (p.H / p.Hk);
+    const uint32_t H = (uint32_t)p.H, group = H / (uint32_t)p.Hk;  // 32-bit: 64-bit division leaves the scalar unit
+    const int si = uniform((int)(blockIdx.x / H)), hi = uniform((int)(blockIdx.x - (uint32_t)si * H));
+    s = si;
+    h = hi;
+    hk = uniform((int)((uint32_t)hi / group));
     vb = blockIdx.y * kWavesScan + wave;
     col = vb * 16 + n;
     on = vb * 16 < p.VP;
-    seq = seq_rows<C>(p, s);
+    const SeqRows seq = seq_rows<C>(p, s);
+    len = (int)seq.len;
+    chunks = (len + C - 1) / C;
+    row0 = seq.row0;
+    slot0 = seq.slot0;
     vstride = (uint32_t)(p.H * p.V * IO::es);
     wstride = (uint32_t)(p.VP * 4);
     vat = col < p.V ? 8 * j * vstride + col * IO::es : kOutside;  // v, o, do, dv
@@ -471,28 +530,32 @@ struct Walk {
     sbytes = (uint32_t)(p.K * p.V * 4);
   }
   // rows of a chunk, none past either end
-  __device__ __forceinline__ int rows(int64_t c) const {
-    const int64_t left = seq.len - c * C;
-    return c < 0 || left < 0 ? 0 : (int)(left < C ? left : C);
+  __device__ __forceinline__ int rows(int c) const {
+    const int left = len - c * C, most = left < C ? left : C;
+    return c < 0 ? 0 : (most > 0 ? most : 0);
   }
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t state(const float* base, const DeltaArgs& p) const {
     return make_rsrc_u32(base + (s * p.H + h) * p.K * p.V, sbytes);
   }
 };
 
+// Arrays that a scan step writes, or none (forward or backward).
+struct ScanOut {
+  Stream o, S, pred, E;
+  float* dots;
+};
+
 template <bool BWD>
 __device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, const ScanChunk<BWD>& l, Cols<NB>& S,
-                                           Cols<CB> R, const Cols<CB>& dO, int64_t c) {
+                                           Cols<CB> R, const Cols<CB>& dO, const ScanOut& out, int rows) {
   constexpr int OP = ScanChunk<BWD>::OP;
   const int lane = w.lane, j = w.j, n = w.n;
-  const int64_t sh = (w.seq.slot0 + c) * p.H + w.h;
   const float* eG = l.r.ev + 8 * j;           // this lane's rows of the chunk's row factors
   const float* eK = l.r.ev + C + 8 * j;
   const float* bt = l.r.ev + 2 * C + 8 * j;
   const float last = l.r.ev[C - 1];           // decay over the whole chunk
-  const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
 
-  if (BWD) store_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride, S);
+  if (BWD) store_cols<NB>(out.S.rsrc(rows), w.wat, w.wstride, S);
   // products with the state: predictions K S and readouts Q S
   Cols<CB> KS = zero_cols<CB>(), O = zero_cols<CB>();
   RowTiles fk[2], fq[2];
@@ -513,6 +576,7 @@ __device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, co
     mma_tiles(tiles(KS), fk[b & 1].a, sb);
     mma_tiles(tiles(O), fq[b & 1].a, first<OP>(sb));
     if (b + 1 < NB) sb = split<TP>(S.t[(b + 1) % NB][0], S.t[(b + 1) % NB][1]);
+    interleave<2 * CB * (TP + OP), 3, 2>();
   }
   // errors of the chunk: E = T (V - e^G K S)
   each<CB>([&](int b, int t, int r, int row) {
@@ -521,7 +585,7 @@ __device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, co
     R.t[b][t][r] -= KS.t[b][t][r];
     O.t[b][t][r] *= x * p.scale;
   });
-  if (BWD) store_cols<CB>(rows_ws(p.pred), w.wat, w.wstride, KS);
+  if (BWD) store_cols<CB>(out.pred.rsrc(rows), w.wat, w.wstride, KS);
   Part<TP> B[CB];
   split_all(B, R);
   Cols<CB> U = zero_cols<CB>();
@@ -530,7 +594,7 @@ __device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, co
   fc[0].load(l.r.k, 0, lane, j);
   hold_lds();
   ft.mma(U, B);
-  if (BWD) store_cols<CB>(rows_ws(p.E), w.wat, w.wstride, U);
+  if (BWD) store_cols<CB>(out.E.rsrc(rows), w.wat, w.wstride, U);
   each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= bt[row]; });
   if constexpr (BWD) {
     // rows of dO . (scale e^G Q S0) over this wavefront's columns
@@ -538,12 +602,12 @@ __device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, co
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = i < 8 * CB ? O.t[(i / 8) % CB][(i / 4) % 2][i % 4] * dO.t[(i / 8) % CB][(i / 4) % 2][i % 4] : 0.f;
     const float sum = sum_rows16(x, lane);
-    if (w.on && n < 8 * CB) p.dots[(sh * (p.VP / 16) + w.vb) * kDots + 32 * (n / 8) + 8 * j + n % 8] = sum;
+    if (w.on && n < 8 * CB) out.dots[32 * (n / 8) + 8 * j + n % 8] = sum;
   } else {
     Part<OP> UO[CB];
     split_all(UO, U);
     fp.mma(O, UO);
-    store_out(head_rsrc(p.o, w.seq.row0 + c * C, p.H, w.h, p.V, IO::es, w.rows(c)), w.vat, w.vstride, O);
+    store_out(out.o.rsrc(rows), w.vat, w.vstride, O);
   }
   // state after the chunk
   each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= eK[row]; });
@@ -564,38 +628,61 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
   __shared__ __attribute__((aligned(16))) ScanChunk<BWD> l0;
   __shared__ __attribute__((aligned(16))) std::conditional_t<kTwo, ScanChunk<BWD>, Nothing> l1;
   const Walk w(p);
-  const KeyOffsets ko(p, w.tid);
   Cols<NB> S = zero_cols<NB>();
   if (p.S0) S = load_cols<NB>(w.state(p.S0, p), w.sat, (uint32_t)(p.V * 4));
-  const int64_t chunks = (w.seq.len + C - 1) / C;
+  Keys keys(p, w.row0, w.slot0, w.h, w.hk, w.tid);
+  Stream st = slot_stream(p.T, w.slot0, p.H, w.h, kTri * 2), sp = slot_stream(p.P, w.slot0, p.H, w.h, kTri * 2);
+  Stream sv = head_stream(p.v, w.row0, p.H, w.h, p.V), sd = head_stream(p.do_, w.row0, p.H, w.h, p.V);
+  ScanOut out;
+  out.o = head_stream(p.o, w.row0, p.H, w.h, p.V);
+  out.S = slot_stream(p.S, w.slot0, p.H, w.h, KP * p.VP * 4);
+  out.pred = slot_stream(p.pred, w.slot0, p.H, w.h, C * p.VP * 4);
+  out.E = slot_stream(p.E, w.slot0, p.H, w.h, C * p.VP * 4);
+  out.dots = p.dots + ((w.slot0 * p.H + w.h) * (p.VP / 16) + w.vb) * kDots;
+  const int64_t dots_step = p.H * (p.VP / 16) * kDots;
   RawCols v, d;
-  const auto fetch = [&](ScanChunk<BWD>& l, int64_t c) {
-    const int64_t row0 = w.seq.row0 + c * C, slot = w.seq.slot0 + c, sh = slot * p.H + w.h;
-    const int rows = w.rows(c);
-    load_keys(l.r, p, ko, slot, sh, row0, w.hk, rows, w.wave, w.lane);
-    load_tri<TP>(l.t, p.T, sh, rows, w.wave, w.lane);
-    if constexpr (!BWD) load_tri<ScanChunk<BWD>::OP>(l.p, p.P, sh, rows, w.wave, w.lane);
-    v.fetch(head_rsrc(p.v, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
-    if (BWD) d.fetch(head_rsrc(p.do_, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
+  const auto fetch = [&](ScanChunk<BWD>& l, int rows) {
+    keys.load(l.r, rows, w.wave, w.lane);
+    load_tri<TP>(l.t, st, rows, w.wave, w.lane);
+    if constexpr (!BWD) load_tri<ScanChunk<BWD>::OP>(l.p, sp, rows, w.wave, w.lane);
+    v.fetch(sv.rsrc(rows), w.vat, w.vstride);
+    if (BWD) d.fetch(sd.rsrc(rows), w.vat, w.vstride);
+    keys.next(1);
+    st.next(1);
+    sp.next(1);
+    sv.next(1);
+    sd.next(1);
+  };
+  const auto done = [&]() {
+    out.o.next(1);
+    out.S.next(1);
+    out.pred.next(1);
+    out.E.next(1);
+    out.dots += dots_step;
   };
   if constexpr (kTwo) {
-    const auto step = [&](ScanChunk<BWD>& here, ScanChunk<BWD>& next, int64_t c) {
+    const auto step = [&](ScanChunk<BWD>& here, ScanChunk<BWD>& next, int c) {
       sync_loads();  // `here` is loaded, and nothing reads `next` any more
       const Cols<CB> R = v.widen(), dO = d.widen();
-      fetch(next, c + 1);
-      scan_chunk<BWD>(p, w, here, S, R, dO, c);
+      fetch(next, w.rows(c + 1));
+      scan_chunk<BWD>(p, w, here, S, R, dO, out, w.rows(c));
+      done();
     };
-    if (chunks > 0) fetch(l0, 0);
-    for (int64_t c = 0; c < chunks; c += 2) {
+    fetch(l0, w.rows(0));
+    int c = 0;
+    for (; c + 1 < w.chunks; c += 2) {
       step(l0, l1, c);
-      if (c + 1 < chunks) step(l1, l0, c + 1);
+      step(l1, l0, c + 1);
     }
+    if (c < w.chunks) step(l0, l1, c);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // the last step's empty loads still write to LDS
   } else {
-    for (int64_t c = 0; c < chunks; ++c) {
-      __syncthreads();
-      fetch(l0, c);
+    for (int c = 0; c < w.chunks; ++c) {
+      sync_lds();
+      fetch(l0, w.rows(c));
       sync_loads();
-      scan_chunk<BWD>(p, w, l0, S, v.widen(), d.widen(), c);
+      scan_chunk<BWD>(p, w, l0, S, v.widen(), d.widen(), out, w.rows(c));
+      done();
     }
   }
   if (w.on && p.last_S) store_cols<NB>(w.state(p.last_S, p), w.sat, (uint32_t)(p.V * 4), S);
@@ -607,17 +694,21 @@ struct RevTri {
   uint16_t t[tri_lds(TP)], p[tri_lds(TP)], m[tri_lds(TP)];
 };
 
+struct RevOut {
+  Stream dv, dV, dS;
+  float* dots;
+};
+
 __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, const KeyRows& l, const RevTri& x3,
                                           Cols<NB>& S, Cols<CB> dO, const Cols<CB>& Er, const Cols<CB>& pred,
-                                          const Cols<NB>& S0, int64_t c) {
+                                          const Cols<NB>& S0, const RevOut& out, int rows) {
   const int lane = w.lane, j = w.j, n = w.n;
-  const int64_t sh = (w.seq.slot0 + c) * p.H + w.h;
   const float* eG = l.ev + 8 * j;
   const float* eK = l.ev + C + 8 * j;
   const float* bt = l.ev + 2 * C + 8 * j;
   const float last = l.ev[C - 1];
   // the adjoint after this chunk, kept for the gradients of q and k
-  store_cols<NB>(make_rsrc_u32(p.dS + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride, S);
+  store_cols<NB>(out.dS.rsrc(rows), w.wat, w.wstride, S);
   float dot = 0.f;
   each<NB>([&](int b, int t, int r, int) { dot = fmaf(S0.t[b][t][r], S.t[b][t][r], dot); });
   dot *= last;
@@ -672,7 +763,7 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
     ye[8 * b + 4 * t + r] = W.t[b][t][r] * Er.t[b][t][r];
     dp[8 * b + 4 * t + r] = dV.t[b][t][r] * pred.t[b][t][r];
   });
-  float* dots = p.dots + (sh * (p.VP / 16) + w.vb) * kDots;
+  float* dots = out.dots;
   const float sy = sum_rows16(ye, lane), sp = sum_rows16(dp, lane), sw = sum_rows16(uw, lane);
   if (w.on && n < 8 * CB) {
     const int row = 32 * (n / 8) + 8 * j + n % 8;
@@ -683,8 +774,8 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
   if (w.on && lane == 0) dots[4 * C] = dot;
-  store_cols<CB>(make_rsrc_u32(p.dV + sh * C * p.VP, (uint32_t)(C * p.VP * 4)), w.wat, w.wstride, dV);
-  store_out(head_rsrc(p.dv, w.seq.row0 + c * C, p.H, w.h, p.V, IO::es, w.rows(c)), w.vat, w.vstride, dV);
+  store_cols<CB>(out.dV.rsrc(rows), w.wat, w.wstride, dV);
+  store_out(out.dv.rsrc(rows), w.vat, w.vstride, dV);
   // dS0 = e^{G_C} dS1 + Q^T (scale e^G dO) - K^T (e^G dV)
   Part<TP> BQ[CB];
   each<CB>([&](int b, int t, int r, int row) {
@@ -711,26 +802,36 @@ __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p)
   __shared__ __attribute__((aligned(16))) KeyRows l0;
   __shared__ __attribute__((aligned(16))) RevTri x3;
   const Walk w(p);
-  const KeyOffsets ko(p, w.tid);
   Cols<NB> S = zero_cols<NB>();  // the adjoint of the state
   if (p.dlast_S) S = load_cols<NB>(w.state(p.dlast_S, p), w.sat, (uint32_t)(p.V * 4));
-  const int64_t chunks = (w.seq.len + C - 1) / C;
-  for (int64_t c = chunks - 1; c >= 0; --c) {
-    const int64_t row0 = w.seq.row0 + c * C, slot = w.seq.slot0 + c, sh = slot * p.H + w.h;
+  const int64_t end = w.chunks - 1, row = w.row0 + end * C, slot = w.slot0 + end;
+  Keys keys(p, row, slot, w.h, w.hk, w.tid);
+  Stream st = slot_stream(p.T, slot, p.H, w.h, kTri * 2), sp = slot_stream(p.P, slot, p.H, w.h, kTri * 2);
+  Stream sm = slot_stream(p.M, slot, p.H, w.h, kTri * 2), sd = head_stream(p.do_, row, p.H, w.h, p.V);
+  Stream sS = slot_stream(p.S, slot, p.H, w.h, KP * p.VP * 4);
+  Stream sE = slot_stream(p.E, slot, p.H, w.h, C * p.VP * 4), spred = slot_stream(p.pred, slot, p.H, w.h, C * p.VP * 4);
+  RevOut out;
+  out.dv = head_stream(p.dv, row, p.H, w.h, p.V);
+  out.dV = slot_stream(p.dV, slot, p.H, w.h, C * p.VP * 4);
+  out.dS = slot_stream(p.dS, slot, p.H, w.h, KP * p.VP * 4);
+  out.dots = p.dots + ((slot * p.H + w.h) * (p.VP / 16) + w.vb) * kDots;
+  for (int c = w.chunks - 1; c >= 0; --c) {
     const int rows = w.rows(c);
-    __syncthreads();
-    load_keys(l0, p, ko, slot, sh, row0, w.hk, rows, w.wave, w.lane);
-    load_tri<TP>(x3.p, p.P, sh, rows, w.wave, w.lane);
-    load_tri<TP>(x3.t, p.T, sh, rows, w.wave, w.lane);
-    load_tri<TP>(x3.m, p.M, sh, rows, w.wave, w.lane);
+    sync_lds();
+    keys.load(l0, rows, w.wave, w.lane);
+    load_tri<TP>(x3.p, sp, rows, w.wave, w.lane);
+    load_tri<TP>(x3.t, st, rows, w.wave, w.lane);
+    load_tri<TP>(x3.m, sm, rows, w.wave, w.lane);
     RawCols d;
-    d.fetch(head_rsrc(p.do_, row0, p.H, w.h, p.V, IO::es, rows), w.vat, w.vstride);
-    const auto rows_ws = [&](float* base) { return make_rsrc_u32(base + sh * C * p.VP, (uint32_t)(C * p.VP * 4)); };
-    const Cols<CB> Er = load_cols<CB>(rows_ws(p.E), w.wat, w.wstride);
-    const Cols<CB> pred = load_cols<CB>(rows_ws(p.pred), w.wat, w.wstride);
-    const Cols<NB> S0 = load_cols<NB>(make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride);
+    d.fetch(sd.rsrc(rows), w.vat, w.vstride);
+    const Cols<CB> Er = load_cols<CB>(sE.rsrc(rows), w.wat, w.wstride);
+    const Cols<CB> pred = load_cols<CB>(spred.rsrc(rows), w.wat, w.wstride);
+    const Cols<NB> S0 = load_cols<NB>(sS.rsrc(rows), w.wat, w.wstride);
     sync_loads();
-    rev_chunk(p, w, l0, x3, S, d.widen(), Er, pred, S0, c);
+    rev_chunk(p, w, l0, x3, S, d.widen(), Er, pred, S0, out, rows);
+    keys.next(-1);
+    for (Stream* x : {&st, &sp, &sm, &sd, &sS, &sE, &spred, &out.dv, &out.dV, &out.dS}) x->next(-1);
+    out.dots -= p.H * (p.VP / 16) * kDots;
   }
   if (w.on && p.dS0) store_cols<NB>(w.state(p.dS0, p), w.sat, (uint32_t)(p.V * 4), S);
 }
@@ -755,7 +856,7 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   __shared__ double Gd[C];
   __shared__ float across[MT][C];  // sums of N_ij over a tile of rows i >= t and all j < t
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
-  const int64_t slot = blockIdx.x, hk = blockIdx.y, group = p.H / p.Hk;
+  const int64_t slot = blockIdx.x, hk = blockIdx.y, group = (uint32_t)p.H / (uint32_t)p.Hk;
   const ChunkRows ch = chunk_rows<C>(p, slot);
   if (ch.n == 0) return;
   const int64_t at = (ch.row0 * p.Hk + hk) * p.K;

@@ -140,13 +140,32 @@ __device__ __forceinline__ Part<N> load_row(const uint16_t* lds, int row, int c,
   return a;
 }
 
+// The LDS address behind a pointer to shared memory: its lower half.  (A cast to the address space
+// compares the pointer with null first.)
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(3))) T* lds_address(const void* p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  return (__attribute__((address_space(3))) T*)(uint32_t)(uintptr_t)p;
+#else
+  return nullptr;
+#endif
+}
+
+// A value that all lanes share, in scalar registers: resources built from it need no loop over
+// the lanes' values.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 __device__ __forceinline__ bf16x8 read_tr(const uint16_t* lo, const uint16_t* hi) {
-  typedef __attribute__((address_space(3))) s16x4* lds4;
   struct {
     s16x4 lo, hi;
   } v;
-  v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(lo));
-  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(hi));
+  v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_address<s16x4>(lo));
+  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_address<s16x4>(hi));
   return __builtin_bit_cast(bf16x8, v);
 }
 // The same transposed: eight consecutive rows from row0 (a multiple of 8) of the column this lane
@@ -193,10 +212,11 @@ struct SeqRows {
 template <int C>
 __device__ __forceinline__ SeqRows seq_rows(const DeltaArgs& p, int64_t s) {
   if (!p.off) return SeqRows{s * p.L, p.L, s * p.NT};
+  // int32 arithmetic: offsets are below 2^31
   int64_t a = p.off[s], b = p.off[s + 1];
   a = a < 0 ? 0 : (a > p.tokens ? p.tokens : a);
   b = b < a ? a : (b > p.tokens ? p.tokens : b);
-  return SeqRows{a, b - a, a / C + s};
+  return SeqRows{uniform(a), uniform(b - a), uniform((int)((uint32_t)a / C)) + s};
 }
 
 // First row and number of rows of the chunk in a slot (0 rows: no chunk there).
@@ -209,7 +229,7 @@ template <int C>
 __device__ __forceinline__ ChunkRows chunk_rows(const DeltaArgs& p, int64_t slot) {
   int64_t s;
   if (!p.off) {
-    s = slot / p.NT;
+    s = uniform((int)((uint32_t)slot / (uint32_t)p.NT));
   } else {
     int64_t lo = 0, hi = p.nseq;  // the last sequence whose first slot is at or before this one
     while (hi - lo > 1) {
@@ -249,14 +269,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t head_rsrc(const void* base, in
 // One pass of a wavefront from memory into LDS, 64 units of 16 bytes, without registers between
 // (buffer_load ... lds); `lds` is the same for the whole wavefront.
 __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, soff, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_address<void>(lds), 16, off, soff, 0, 0);
 }
 
-// Barrier after which every wavefront's load_lds have landed: each waits for its own first (the
-// barrier by itself orders LDS accesses, not loads from memory).
+// Barriers of the walks.  A barrier by itself is no obstacle to the scheduler's moving loads from
+// memory into LDS across it, so both sides are closed.  After sync_loads every wavefront's
+// load_lds have landed: each waits for its own first.
+__device__ __forceinline__ void sync_lds() {
+  __builtin_amdgcn_sched_barrier(0);
+  __syncthreads();
+  __builtin_amdgcn_sched_barrier(0);
+}
 __device__ __forceinline__ void sync_loads() {
+  __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   __syncthreads();
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Chunk matrices (lower triangular, C x C) are kept as their 32 x 32 blocks on and below the
