@@ -69,12 +69,12 @@ __device__ __forceinline__ float exp_of(double x) { return exp2_fast((float)(x *
 // staying in wavefront j's registers as right factors.  Substitution in blocks keeps the error
 // of a triangular solve; products of powers of M would not.
 constexpr int LDM = C + 4;
-__device__ __forceinline__ void invert(const float* Ms, float* Ti, int wave, int lane) {
+__device__ __forceinline__ void invert(const MSM_LDS float* Ms, MSM_LDS float* Ti, int wave, int lane) {
   constexpr int B16 = C / 16;
   const int n = lane & 15, j = lane >> 4;
   if (wave < B16) {
     float x[16];
-    const float* M = Ms + (16 * wave) * LDM + 16 * wave;
+    const MSM_LDS float* M = Ms + (16 * wave) * LDM + 16 * wave;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == n ? 1.f : 0.f;
@@ -98,11 +98,11 @@ __device__ __forceinline__ void invert(const float* Ms, float* Ti, int wave, int
         f32x4 acc = zero4();
 #pragma unroll
         for (int e = 0; e < d; ++e) {
-          const f32x4 a = *reinterpret_cast<const f32x4*>(Ms + (16 * i + n) * LDM + 16 * (wave + e) + 4 * j);
+          const f32x4 a = *(const MSM_LDS f32x4*)(Ms + (16 * i + n) * LDM + 16 * (wave + e) + 4 * j);
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], t[e][r], acc, 0, 0, 0);
         }
-        const f32x4 a = *reinterpret_cast<const f32x4*>(Ti + (16 * i + n) * LDM + 16 * i + 4 * j);
+        const f32x4 a = *(const MSM_LDS f32x4*)(Ti + (16 * i + n) * LDM + 16 * i + 4 * j);
         t[d] = zero4();
 #pragma unroll
         for (int r = 0; r < 4; ++r) t[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(-a[r], acc[r], t[d], 0, 0, 0);
@@ -118,7 +118,7 @@ __device__ __forceinline__ void invert(const float* Ms, float* Ti, int wave, int
 // With `ws` the planes also go to memory, for kernels that then load them into LDS unchanged: fp32
 // inputs in their parts, and rows that cannot be read 16 bytes at a time.
 template <int THREADS>
-__device__ __forceinline__ void stage_rows(uint16_t* lds, uint16_t* ws, __amdgpu_buffer_rsrc_t r, uint32_t stride,
+__device__ __forceinline__ void stage_rows(lds_parts lds, uint16_t* ws, __amdgpu_buffer_rsrc_t r, uint32_t stride,
                                            int K, bool vec, int tid) {
   constexpr int N = C * UK / THREADS;
   static_assert(C * UK % THREADS == 0, "whole passes");
@@ -163,12 +163,15 @@ __device__ __forceinline__ void stage_rows(uint16_t* lds, uint16_t* ws, __amdgpu
 
 template <bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
-  __shared__ __attribute__((aligned(16))) uint16_t Ks[kIn * kRows];
-  __shared__ __attribute__((aligned(16))) uint16_t Qs[kIn * kRows];
-  __shared__ __attribute__((aligned(16))) float Ms[C * LDM];
-  __shared__ __attribute__((aligned(16))) float Ti[C * LDM];
+  __shared__ __attribute__((aligned(16))) uint16_t lds_k[kIn * kRows];
+  __shared__ __attribute__((aligned(16))) uint16_t lds_q[kIn * kRows];
+  __shared__ __attribute__((aligned(16))) float lds_m[C * LDM];
+  __shared__ __attribute__((aligned(16))) float lds_t[C * LDM];
   __shared__ double Gd[C];
   __shared__ float bt[C];
+  const lds_parts Ks = (lds_parts)lds_k, Qs = (lds_parts)lds_q;
+  MSM_LDS float* const Ms = (MSM_LDS float*)lds_m;
+  MSM_LDS float* const Ti = (MSM_LDS float*)lds_t;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
   const int64_t slot = blockIdx.x, h = blockIdx.y;
   const ChunkRows ch = chunk_rows<C>(p, slot);
@@ -240,8 +243,8 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
     if (c / 32 > row / 32) continue;
     f32x4 a = zero4(), b = zero4();
     if (c / 16 <= row / 16) {  // blocks above the diagonal were not written
-      a = *reinterpret_cast<const f32x4*>(Ti + row * LDM + c);
-      b = *reinterpret_cast<const f32x4*>(Ti + row * LDM + c + 4);
+      a = *(const MSM_LDS f32x4*)(Ti + row * LDM + c);
+      b = *(const MSM_LDS f32x4*)(Ti + row * LDM + c + 4);
     }
     store_parts(Tg + TriM::at(row, c), TriM::kPlane, split<TP>(a, b));
   }
@@ -316,7 +319,7 @@ __device__ __forceinline__ f32x4 (&tiles(Cols<CB>& c))[2 * CB] { return reinterp
 // Left factors of a product with keys or queries over 32 state rows: all tokens of the chunk.
 struct RowTiles {
   Part<kIn> a[2 * CB];
-  __device__ __forceinline__ void load(const uint16_t* lds, int b, int lane, int j) {
+  __device__ __forceinline__ void load(lds_cparts lds, int b, int lane, int j) {
 #pragma unroll
     for (int i = 0; i < 2 * CB; ++i) a[i] = load_row<UK, kIn>(lds, perm_row(i / 2, i % 2, lane), 32 * b + 8 * j, kRows);
   }
@@ -326,7 +329,7 @@ struct RowTiles {
 template <int NA, bool TRANS>
 struct TriTiles {
   Part<NA> a[CB][2 * CB];
-  __device__ __forceinline__ void load(const uint16_t* lds, int lane, int j) {
+  __device__ __forceinline__ void load(lds_cparts lds, int lane, int j) {
 #pragma unroll
     for (int b = 0; b < CB; ++b)
 #pragma unroll
@@ -356,7 +359,7 @@ struct TriTiles {
 // Left factors of a state update: 32 rows of K^T or Q^T over one block of tokens.
 struct ColTiles {
   Part<kIn> a[CB][2];
-  __device__ __forceinline__ void load(const uint16_t* lds, int b, int lane, int j) {
+  __device__ __forceinline__ void load(lds_cparts lds, int b, int lane, int j) {
 #pragma unroll
     for (int rb = 0; rb < CB; ++rb)
 #pragma unroll
@@ -398,9 +401,12 @@ struct Stream {
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int rows) const {
     return make_rsrc_u32(at, (uint32_t)uniform(rows > 0 ? rows * per_row + rest : 0));
   }
-  // a whole chunk's part, whatever its rows
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t whole(int rows, uint32_t bytes) const {
-    return make_rsrc_u32(at, (uint32_t)uniform(rows > 0 ? (int)bytes : 0));
+  // the same for load_lds, and for a whole chunk's part, whatever its rows
+  __device__ __forceinline__ u32x4 words(int rows) const {
+    return rsrc_words(at, (uint32_t)uniform(rows > 0 ? rows * per_row + rest : 0));
+  }
+  __device__ __forceinline__ u32x4 whole(int rows, uint32_t bytes) const {
+    return rsrc_words(at, (uint32_t)uniform(rows > 0 ? (int)bytes : 0));
   }
   __device__ __forceinline__ void next(int dir) { at += dir > 0 ? step : -step; }
 };
@@ -417,12 +423,12 @@ __device__ __forceinline__ Stream slot_stream(const void* base, int64_t slot, in
 }
 
 template <int N>
-__device__ __forceinline__ void load_tri(uint16_t* lds, const Stream& s, int rows, int wave, int lane) {
+__device__ __forceinline__ void load_tri(lds_parts lds, const Stream& s, int rows, int wave, int lane) {
   const auto r = s.whole(rows, N * TriM::kPlane * 2);
 #pragma unroll
   for (int i = 0; i < tri_rounds(N); ++i) {
     const int pass = i * kWavesScan + wave;
-    load_lds(r, lds + pass * 512, lane * 16 + pass * 1024, 0);
+    load_lds(r, lds + pass * 512, lane * 16 + pass * 1024);
   }
 }
 
@@ -448,17 +454,18 @@ struct Keys {
       at[i] = !p.kq_direct ? u * 16 : (c < p.K ? (uint32_t)(row_ * p.Hk * p.K + c) * IO::es : kOutside);
     }
   }
-  __device__ __forceinline__ void load(KeyRows& l, int rows, int wave, int lane) const {
-    const auto rk = k.rsrc(rows), rq = q.rsrc(rows);
+  // piece `part` of `parts`: the loads are issued between a step's products
+  __device__ __forceinline__ void load(MSM_LDS KeyRows& l, int rows, int wave, int lane, int part, int parts) const {
+    const u32x4 rk = k.words(rows), rq = q.words(rows);
 #pragma unroll
-    for (int n = 0; n < kIn; ++n)
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        load_lds(rk, l.k + n * kRows + (i * kWavesScan + wave) * 512, at[i] + n * kRows * 2, 0);
-        load_lds(rq, l.q + n * kRows + (i * kWavesScan + wave) * 512, at[i] + n * kRows * 2, 0);
-      }
+    for (int x = 0; x < kIn * kPasses; ++x) {
+      if (x * parts / (kIn * kPasses) != part) continue;
+      const int n = x / kPasses, i = x % kPasses;
+      load_lds(rk, l.k + n * kRows + (i * kWavesScan + wave) * 512, at[i] + n * kRows * 2);
+      load_lds(rq, l.q + n * kRows + (i * kWavesScan + wave) * 512, at[i] + n * kRows * 2);
+    }
     // every wavefront brings the same values: cheaper than a branch
-    load_lds(ev.whole(rows, 3 * C * 4), l.ev, lane * 16, 0);
+    if (part == 0) load_lds(ev.whole(rows, 3 * C * 4), (MSM_LDS void*)l.ev, lane * 16);
   }
   __device__ __forceinline__ void next(int dir) {
     k.next(dir);
@@ -483,17 +490,14 @@ struct Nothing {};
 // read their left factors one step ahead, and without it the reads would sink to their uses.
 __device__ __forceinline__ void hold_lds() { __builtin_amdgcn_sched_barrier(0x1F); }
 
-// Asks for N times one MFMA followed by VALU other vector instructions, and a memory read every MEM
-// of them (0: none): an MFMA occupies the matrix unit for 16 cycles and the issue port for 4, so
-// up to three instructions fit under it, and memory reads issued in a row would wait for each
-// other.
-template <int N, int VALU, int MEM>
+// Asks for N times one MFMA followed by VALU other vector instructions: an MFMA occupies the matrix
+// unit for 16 cycles and the issue port for 4, so up to three instructions fit under it.
+template <int N, int VALU>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-    if (MEM && i % (MEM ? MEM : 1) == 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
   }
 }
 
@@ -545,14 +549,15 @@ struct ScanOut {
   float* dots;
 };
 
-template <bool BWD>
-__device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, const ScanChunk<BWD>& l, Cols<NB>& S,
+// One chunk of a walk.  fetch(part) issues piece `part` of NB of the next chunk's loads.
+template <bool BWD, class F>
+__device__ __forceinline__ void scan_chunk(F fetch, const DeltaArgs& p, const Walk& w, const MSM_LDS ScanChunk<BWD>& l, Cols<NB>& S,
                                            Cols<CB> R, const Cols<CB>& dO, const ScanOut& out, int rows) {
   constexpr int OP = ScanChunk<BWD>::OP;
   const int lane = w.lane, j = w.j, n = w.n;
-  const float* eG = l.r.ev + 8 * j;           // this lane's rows of the chunk's row factors
-  const float* eK = l.r.ev + C + 8 * j;
-  const float* bt = l.r.ev + 2 * C + 8 * j;
+  const MSM_LDS float* eG = l.r.ev + 8 * j;           // this lane's rows of the chunk's row factors
+  const MSM_LDS float* eK = l.r.ev + C + 8 * j;
+  const MSM_LDS float* bt = l.r.ev + 2 * C + 8 * j;
   const float last = l.r.ev[C - 1];           // decay over the whole chunk
 
   if (BWD) store_cols<NB>(out.S.rsrc(rows), w.wat, w.wstride, S);
@@ -572,11 +577,12 @@ __device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, co
     } else {
       ft.load(l.t, lane, j);
     }
+    fetch(b);
     hold_lds();
     mma_tiles(tiles(KS), fk[b & 1].a, sb);
     mma_tiles(tiles(O), fq[b & 1].a, first<OP>(sb));
     if (b + 1 < NB) sb = split<TP>(S.t[(b + 1) % NB][0], S.t[(b + 1) % NB][1]);
-    interleave<2 * CB * (TP + OP), 3, 2>();
+    interleave<2 * CB * (TP + OP), 3>();
   }
   // errors of the chunk: E = T (V - e^G K S)
   each<CB>([&](int b, int t, int r, int row) {
@@ -625,8 +631,10 @@ __device__ __forceinline__ void scan_chunk(const DeltaArgs& p, const Walk& w, co
 template <bool BWD>
 __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p) {
   constexpr bool kTwo = 2 * sizeof(ScanChunk<BWD>) <= kLdsMost;
-  __shared__ __attribute__((aligned(16))) ScanChunk<BWD> l0;
-  __shared__ __attribute__((aligned(16))) std::conditional_t<kTwo, ScanChunk<BWD>, Nothing> l1;
+  __shared__ __attribute__((aligned(16))) ScanChunk<BWD> lds0;
+  __shared__ __attribute__((aligned(16))) std::conditional_t<kTwo, ScanChunk<BWD>, Nothing> lds1;
+  auto& l0 = (MSM_LDS ScanChunk<BWD>&)lds0;
+  auto& l1 = (MSM_LDS std::conditional_t<kTwo, ScanChunk<BWD>, Nothing>&)lds1;
   const Walk w(p);
   Cols<NB> S = zero_cols<NB>();
   if (p.S0) S = load_cols<NB>(w.state(p.S0, p), w.sat, (uint32_t)(p.V * 4));
@@ -641,17 +649,24 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
   out.dots = p.dots + ((w.slot0 * p.H + w.h) * (p.VP / 16) + w.vb) * kDots;
   const int64_t dots_step = p.H * (p.VP / 16) * kDots;
   RawCols v, d;
-  const auto fetch = [&](ScanChunk<BWD>& l, int rows) {
-    keys.load(l.r, rows, w.wave, w.lane);
-    load_tri<TP>(l.t, st, rows, w.wave, w.lane);
-    if constexpr (!BWD) load_tri<ScanChunk<BWD>::OP>(l.p, sp, rows, w.wave, w.lane);
-    v.fetch(sv.rsrc(rows), w.vat, w.vstride);
-    if (BWD) d.fetch(sd.rsrc(rows), w.vat, w.vstride);
-    keys.next(1);
-    st.next(1);
-    sp.next(1);
-    sv.next(1);
-    sd.next(1);
+  // the chunk that the streams stand at, in NB pieces
+  const auto fetch = [&](MSM_LDS ScanChunk<BWD>& l, int rows, int part) {
+    keys.load(l.r, rows, w.wave, w.lane, part, NB);
+    if (part == NB - 1) {
+      load_tri<TP>(l.t, st, rows, w.wave, w.lane);
+      if constexpr (!BWD) load_tri<ScanChunk<BWD>::OP>(l.p, sp, rows, w.wave, w.lane);
+      v.fetch(sv.rsrc(rows), w.vat, w.vstride);
+      if (BWD) d.fetch(sd.rsrc(rows), w.vat, w.vstride);
+      keys.next(1);
+      st.next(1);
+      sp.next(1);
+      sv.next(1);
+      sd.next(1);
+    }
+  };
+  const auto fetch_all = [&](MSM_LDS ScanChunk<BWD>& l, int rows) {
+#pragma unroll
+    for (int part = 0; part < NB; ++part) fetch(l, rows, part);
   };
   const auto done = [&]() {
     out.o.next(1);
@@ -661,14 +676,14 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
     out.dots += dots_step;
   };
   if constexpr (kTwo) {
-    const auto step = [&](ScanChunk<BWD>& here, ScanChunk<BWD>& next, int c) {
+    const auto step = [&](MSM_LDS ScanChunk<BWD>& here, MSM_LDS ScanChunk<BWD>& next, int c) {
       sync_loads();  // `here` is loaded, and nothing reads `next` any more
       const Cols<CB> R = v.widen(), dO = d.widen();
-      fetch(next, w.rows(c + 1));
-      scan_chunk<BWD>(p, w, here, S, R, dO, out, w.rows(c));
+      const int rows = w.rows(c + 1);
+      scan_chunk<BWD>([&](int part) { fetch(next, rows, part); }, p, w, here, S, R, dO, out, w.rows(c));
       done();
     };
-    fetch(l0, w.rows(0));
+    fetch_all(l0, w.rows(0));
     int c = 0;
     for (; c + 1 < w.chunks; c += 2) {
       step(l0, l1, c);
@@ -679,9 +694,9 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
   } else {
     for (int c = 0; c < w.chunks; ++c) {
       sync_lds();
-      fetch(l0, w.rows(c));
+      fetch_all(l0, w.rows(c));
       sync_loads();
-      scan_chunk<BWD>(p, w, l0, S, v.widen(), d.widen(), out, w.rows(c));
+      scan_chunk<BWD>([](int) {}, p, w, l0, S, v.widen(), d.widen(), out, w.rows(c));
       done();
     }
   }
@@ -699,13 +714,13 @@ struct RevOut {
   float* dots;
 };
 
-__device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, const KeyRows& l, const RevTri& x3,
+__device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, const MSM_LDS KeyRows& l, const MSM_LDS RevTri& x3,
                                           Cols<NB>& S, Cols<CB> dO, const Cols<CB>& Er, const Cols<CB>& pred,
                                           const Cols<NB>& S0, const RevOut& out, int rows) {
   const int lane = w.lane, j = w.j, n = w.n;
-  const float* eG = l.ev + 8 * j;
-  const float* eK = l.ev + C + 8 * j;
-  const float* bt = l.ev + 2 * C + 8 * j;
+  const MSM_LDS float* eG = l.ev + 8 * j;
+  const MSM_LDS float* eK = l.ev + C + 8 * j;
+  const MSM_LDS float* bt = l.ev + 2 * C + 8 * j;
   const float last = l.ev[C - 1];
   // the adjoint after this chunk, kept for the gradients of q and k
   store_cols<NB>(out.dS.rsrc(rows), w.wat, w.wstride, S);
@@ -799,8 +814,10 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
 }
 
 __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p) {
-  __shared__ __attribute__((aligned(16))) KeyRows l0;
-  __shared__ __attribute__((aligned(16))) RevTri x3;
+  __shared__ __attribute__((aligned(16))) KeyRows lds0;
+  __shared__ __attribute__((aligned(16))) RevTri lds1;
+  auto& l0 = (MSM_LDS KeyRows&)lds0;
+  auto& x3 = (MSM_LDS RevTri&)lds1;
   const Walk w(p);
   Cols<NB> S = zero_cols<NB>();  // the adjoint of the state
   if (p.dlast_S) S = load_cols<NB>(w.state(p.dlast_S, p), w.sat, (uint32_t)(p.V * 4));
@@ -818,7 +835,7 @@ __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p)
   for (int c = w.chunks - 1; c >= 0; --c) {
     const int rows = w.rows(c);
     sync_lds();
-    keys.load(l0, rows, w.wave, w.lane);
+    keys.load(l0, rows, w.wave, w.lane, 0, 1);
     load_tri<TP>(x3.p, sp, rows, w.wave, w.lane);
     load_tri<TP>(x3.t, st, rows, w.wave, w.lane);
     load_tri<TP>(x3.m, sm, rows, w.wave, w.lane);
@@ -848,13 +865,16 @@ constexpr int LDV = VB + 8, LDT = C + 8;
 __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p) {
   constexpr int THREADS = 64 * kWavesGrad;
   constexpr int kStage = (kIn + 2 * TP) * C * LDV, kPair = 2 * GP * C * LDT;
-  __shared__ __attribute__((aligned(16))) uint16_t Ks[kIn * kRows];
-  __shared__ __attribute__((aligned(16))) uint16_t Qs[kIn * kRows];
+  __shared__ __attribute__((aligned(16))) uint16_t lds_k[kIn * kRows];
+  __shared__ __attribute__((aligned(16))) uint16_t lds_q[kIn * kRows];
   // first the staged columns of dO, dV and U, then the token-pair matrices X and Z + Z^T
-  __shared__ __attribute__((aligned(16))) uint16_t buf[kStage > kPair ? kStage : kPair];
+  __shared__ __attribute__((aligned(16))) uint16_t lds_buf[kStage > kPair ? kStage : kPair];
   __shared__ __attribute__((aligned(16))) float ev[3 * C];
   __shared__ double Gd[C];
   __shared__ float across[MT][C];  // sums of N_ij over a tile of rows i >= t and all j < t
+  const lds_parts Ks = (lds_parts)lds_k, Qs = (lds_parts)lds_q, buf = (lds_parts)lds_buf;
+  const lds_parts dOs = buf, dVs = buf + kIn * C * LDV, Us = dVs + TP * C * LDV;
+  const lds_parts Xs = buf, Zs = buf + GP * C * LDT;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
   const int64_t slot = blockIdx.x, hk = blockIdx.y, group = (uint32_t)p.H / (uint32_t)p.Hk;
   const ChunkRows ch = chunk_rows<C>(p, slot);
@@ -863,11 +883,6 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   const uint32_t stride = (uint32_t)(p.Hk * p.K * IO::es);
   stage_rows<THREADS>(Ks, nullptr, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
   stage_rows<THREADS>(Qs, nullptr, head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
-  uint16_t* dOs = buf;
-  uint16_t* dVs = buf + kIn * C * LDV;
-  uint16_t* Us = dVs + TP * C * LDV;
-  uint16_t* Xs = buf;
-  uint16_t* Zs = buf + GP * C * LDT;
   const int tile0 = wave * kTilesGrad;           // this wavefront's key tiles
   const bool keys = tile0 * 16 < KP;
   const bool pairs = wave < MT;                  // this wavefront's row of token pairs

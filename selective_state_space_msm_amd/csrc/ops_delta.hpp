@@ -31,6 +31,12 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// Pointers to shared memory keep their address space: the compiler then knows which arrays a load
+// into LDS can touch, and need not wait for it before reading the others.
+#define MSM_LDS __attribute__((address_space(3)))
+typedef MSM_LDS uint16_t* lds_parts;
+typedef const MSM_LDS uint16_t* lds_cparts;
+
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
 // Upper halves of two words, the first one's in the low half.
@@ -73,12 +79,17 @@ __device__ __forceinline__ Part<N> first(const Part<NA>& a) {
   return o;
 }
 template <int N>
-__device__ __forceinline__ void store_parts(uint16_t* p, int plane, const Part<N>& s) {
+__device__ __forceinline__ void store_parts(lds_parts p, int plane, const Part<N>& s) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) *reinterpret_cast<bf16x8*>(p + n * plane) = s.p[n];
+  for (int n = 0; n < N; ++n) *(MSM_LDS bf16x8*)(p + n * plane) = s.p[n];
 }
 template <int N>
-__device__ __forceinline__ void store_parts1(uint16_t* p, int plane, float x) {
+__device__ __forceinline__ void store_parts(uint16_t* p, int plane, const Part<N>& s) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) *(bf16x8*)(p + n * plane) = s.p[n];
+}
+template <int N, class Ptr>
+__device__ __forceinline__ void store_parts1(Ptr p, int plane, float x) {
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const uint32_t u = __float_as_uint(x);
@@ -132,23 +143,12 @@ __device__ __forceinline__ int swizzle(int r) {
 
 // Left factor over 32 columns: eight consecutive elements from column c (a multiple of 8) of a row.
 template <int U, int N>
-__device__ __forceinline__ Part<N> load_row(const uint16_t* lds, int row, int c, int plane) {
-  const uint16_t* p = lds + row * U * 8 + ((c / 8) ^ swizzle<U>(row)) * 8;
+__device__ __forceinline__ Part<N> load_row(lds_cparts lds, int row, int c, int plane) {
+  const lds_cparts p = lds + row * U * 8 + ((c / 8) ^ swizzle<U>(row)) * 8;
   Part<N> a;
 #pragma unroll
-  for (int n = 0; n < N; ++n) a.p[n] = *reinterpret_cast<const bf16x8*>(p + n * plane);
+  for (int n = 0; n < N; ++n) a.p[n] = *(const MSM_LDS bf16x8*)(p + n * plane);
   return a;
-}
-
-// The LDS address behind a pointer to shared memory: its lower half.  (A cast to the address space
-// compares the pointer with null first.)
-template <typename T>
-__device__ __forceinline__ __attribute__((address_space(3))) T* lds_address(const void* p) {
-#ifdef __HIP_DEVICE_COMPILE__
-  return (__attribute__((address_space(3))) T*)(uint32_t)(uintptr_t)p;
-#else
-  return nullptr;
-#endif
 }
 
 // A value that all lanes share, in scalar registers: resources built from it need no loop over
@@ -160,12 +160,12 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-__device__ __forceinline__ bf16x8 read_tr(const uint16_t* lo, const uint16_t* hi) {
+__device__ __forceinline__ bf16x8 read_tr(lds_cparts lo, lds_cparts hi) {
   struct {
     s16x4 lo, hi;
   } v;
-  v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_address<s16x4>(lo));
-  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_address<s16x4>(hi));
+  v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MSM_LDS s16x4*)(lo));
+  v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MSM_LDS s16x4*)(hi));
   return __builtin_bit_cast(bf16x8, v);
 }
 // The same transposed: eight consecutive rows from row0 (a multiple of 8) of the column this lane
@@ -173,9 +173,9 @@ __device__ __forceinline__ bf16x8 read_tr(const uint16_t* lo, const uint16_t* hi
 // lanes of a group read a block of 4 rows x 16 columns, lane i row i / 4 and four consecutive
 // columns from chunk i % 4, and receive it transposed, lane i the four rows of column i.
 template <int U, int N>
-__device__ __forceinline__ Part<N> load_col(const uint16_t* lds, int row0, int c, int spread, int lane, int plane) {
+__device__ __forceinline__ Part<N> load_col(lds_cparts lds, int row0, int c, int spread, int lane, int plane) {
   const int i = lane & 15, row = row0 + (i >> 2), col = c + spread * (i & 3);
-  const uint16_t* p = lds + row * U * 8 + ((col / 8) ^ swizzle<U>(row)) * 8 + col % 8;
+  const lds_cparts p = lds + row * U * 8 + ((col / 8) ^ swizzle<U>(row)) * 8 + col % 8;
   Part<N> a;
 #pragma unroll
   for (int n = 0; n < N; ++n) a.p[n] = read_tr(p + n * plane, p + n * plane + 4 * U * 8);
@@ -183,19 +183,19 @@ __device__ __forceinline__ Part<N> load_col(const uint16_t* lds, int row0, int c
 }
 // Transposed from rows of `ld` elements.
 template <int N>
-__device__ __forceinline__ Part<N> load_col_ld(const uint16_t* row0, int ld, int c, int lane, int plane) {
+__device__ __forceinline__ Part<N> load_col_ld(lds_cparts row0, int ld, int c, int lane, int plane) {
   const int i = lane & 15;
-  const uint16_t* p = row0 + (i >> 2) * ld + c + 4 * (i & 3);
+  const lds_cparts p = row0 + (i >> 2) * ld + c + 4 * (i & 3);
   Part<N> a;
 #pragma unroll
   for (int n = 0; n < N; ++n) a.p[n] = read_tr(p + n * plane, p + n * plane + 4 * ld);
   return a;
 }
 template <int N>
-__device__ __forceinline__ Part<N> load_ld(const uint16_t* p, int plane) {
+__device__ __forceinline__ Part<N> load_ld(lds_cparts p, int plane) {
   Part<N> a;
 #pragma unroll
-  for (int n = 0; n < N; ++n) a.p[n] = *reinterpret_cast<const bf16x8*>(p + n * plane);
+  for (int n = 0; n < N; ++n) a.p[n] = *(const MSM_LDS bf16x8*)(p + n * plane);
   return a;
 }
 
@@ -267,9 +267,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t head_rsrc(const void* base, in
 }
 
 // One pass of a wavefront from memory into LDS, 64 units of 16 bytes, without registers between
-// (buffer_load ... lds); `lds` is the same for the whole wavefront.
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t off, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_address<void>(lds), 16, off, soff, 0, 0);
+// (buffer_load ... lds, at m0 plus 16 bytes a lane); `lds` is the same for the whole wavefront.
+// Written as assembly: before an LDS read that it cannot tell apart from the built-in's target
+// the compiler waits for the load, also where the target is the other buffer, and so for the
+// memory latency that the second buffer is there to hide.  It has no result register; sync_loads
+// waits for it by hand, and waits that the compiler counts for other loads only get longer.
+__device__ __forceinline__ void load_lds(u32x4 r, MSM_LDS void* lds, uint32_t off) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "m0");
+#endif
+}
+// The resource of make_rsrc_u32 in its four words.
+__device__ __forceinline__ u32x4 rsrc_words(const void* base, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)base;
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
 }
 
 // Barriers of the walks.  A barrier by itself is no obstacle to the scheduler's moving loads from
