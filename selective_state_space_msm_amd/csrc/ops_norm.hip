@@ -26,6 +26,9 @@ NormShape norm_shape(int64_t D, int per) {
 
 namespace {
 
+// Workgroups of the forward: eight for every CU, more than its registers hold at once.
+constexpr int64_t kNormGroups = 2048;
+
 // Sum over the T threads of a row, the same value in each of them.
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
@@ -103,52 +106,69 @@ __device__ __forceinline__ void load_param(const float* p, int64_t i, float othe
   for (int c = 0; c < VEC; ++c) x[c] = p ? p[i + c] : other;
 }
 
+// A workgroup walks several rows with its columns' weight and bias in registers: read again for
+// every row they would be four times the bytes of a bf16 row.  The next row's loads are issued
+// before the present one is reduced.
 template <typename IO, int VEC, int T, int NV>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormArgs p) {
   __shared__ float lds[8];
+  constexpr int RW = 256 / T;  // rows in flight
   const int t = threadIdx.x % T;
-  const int64_t row = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
-  if (T < 256 && row >= p.rows) return;  // whole groups of T lanes: no sum crosses groups
-  float x[NV][VEC];
-  float sum = 0.f;
+  const int64_t step = (int64_t)gridDim.x * RW;
+  int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / T;
+  if (row >= p.rows) return;  // whole groups of T lanes (for T = 256 the workgroup): no sum crosses groups
+  float w[NV][VEC], b[NV][VEC], next[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t c = ((int64_t)i * T + t) * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) x[i][e] = 0.f;
-    if (c < p.D) load_piece<IO, VEC>(p.x, row * p.D + c, x[i]);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) sum += x[i][e];
-  }
-  const float inv = 1.f / (float)p.D;
-  const float mean = row_sum<T>(sum, lds) * inv;
-  float sq = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = ((int64_t)i * T + t) * VEC;
-    if (c < p.D)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        x[i][e] -= mean;
-        sq = fmaf(x[i][e], x[i][e], sq);
-      }
-  }
-  const float rstd = 1.f / sqrtf(row_sum<T>(sq, lds) * inv + p.eps);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = ((int64_t)i * T + t) * VEC;
+    for (int e = 0; e < VEC; ++e) next[i][e] = w[i][e] = b[i][e] = 0.f;
     if (c < p.D) {
-      float w[VEC], b[VEC];
-      load_param<VEC>(p.weight, c, 1.f, w);
-      load_param<VEC>(p.bias, c, 0.f, b);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[i][e] = fmaf(x[i][e] * rstd, w[e], b[e]);
-      store_piece<IO, VEC>(p.y, row * p.D + c, x[i]);
+      load_param<VEC>(p.weight, c, 1.f, w[i]);
+      load_param<VEC>(p.bias, c, 0.f, b[i]);
+      load_piece<IO, VEC>(p.x, row * p.D + c, next[i]);
     }
   }
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
+  const float inv = 1.f / (float)p.D;
+  for (; row < p.rows; row += step) {
+    float x[NV][VEC];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = ((int64_t)i * T + t) * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        x[i][e] = next[i][e];
+        sum += x[i][e];
+      }
+      if (c < p.D && row + step < p.rows) load_piece<IO, VEC>(p.x, (row + step) * p.D + c, next[i]);
+    }
+    const float mean = row_sum<T>(sum, lds) * inv;
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = ((int64_t)i * T + t) * VEC;
+      if (c < p.D)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          x[i][e] -= mean;
+          sq = fmaf(x[i][e], x[i][e], sq);
+        }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<T>(sq, lds) * inv + p.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = ((int64_t)i * T + t) * VEC;
+      if (c < p.D) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[i][e] = fmaf(x[i][e] * rstd, w[i][e], b[i][e]);
+        store_piece<IO, VEC>(p.y, row * p.D + c, x[i]);
+      }
+    }
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
   }
 }
 
@@ -330,7 +350,8 @@ hipError_t join(const NormArgs& a, int64_t parts, hipStream_t s) {
 
 template <typename IO, int VEC, int T, int NV>
 hipError_t go_fwd(const NormArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.rows + 256 / T - 1) / (256 / T)));
+  const int64_t all = (a.rows + 256 / T - 1) / (256 / T);
+  const dim3 grid((unsigned)(all < kNormGroups ? all : kNormGroups));
   hipLaunchKernelGGL((norm_fwd_kernel<IO, VEC, T, NV>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }

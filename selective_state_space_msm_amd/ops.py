@@ -12,6 +12,7 @@ argument checks and marshalling only, every step in the library's HIP kernels.
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 __all__ = [
     "msm_delta_rule_fwd_workspace_bytes", "msm_delta_rule_bwd_workspace_bytes",
@@ -46,8 +47,38 @@ def declare(lib):
         getattr(lib, name).restype = ctypes.c_int
 
 
-from . import (MsmError, _check, _io_code, _Owned, _ptr, _stream_handle, _workspace,  # noqa: E402
-               load_library)
+from . import MsmError, _Owned, _workspace, load_library  # noqa: E402
+from . import _check as _explain  # noqa: E402
+from . import _io_code as _code  # noqa: E402
+
+
+# A small call's time is the time to make it: the checks below cost one comparison each while they
+# hold, addresses go to ctypes as plain numbers, and the current stream is asked for its handle
+# without an object around it.
+
+def _check(t, name, shape, dtype, device):
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _explain(t, name, shape, dtype, device)
+
+
+def _io_code(io):
+    import torch
+    if io is torch.bfloat16:
+        return 1
+    return 0 if io is torch.float32 else _code(io)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_handle(stream, device):
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    if device.type != "cuda":
+        raise ValueError("expected tensors on a GPU, got %s" % device)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def msm_delta_rule_fwd_workspace_bytes(Bt, L, Hk, H, K, V, io, packed=False) -> int:
@@ -269,27 +300,27 @@ def msm_grad_norm_workspace_bytes(count) -> int:
     return int(load_library().msm_grad_norm_workspace_bytes(count))
 
 
-def _tensor_list(tensors, what, like=None):
-    """Host arrays of addresses, element counts and dtypes of a list of contiguous tensors."""
+def _tensor_list(tensors, what):
+    """Host arrays of addresses, element counts and dtypes of a list of contiguous tensors on one
+    device."""
     import torch
-    n = len(tensors)
-    dev = tensors[0].device
-    for i, t in enumerate(tensors):
-        if t.device != dev:
-            raise ValueError("%s[%d] is on %s, expected %s" % (what, i, t.device, dev))
-        if not t.is_contiguous():
-            raise ValueError("%s[%d] must be contiguous" % (what, i))
-        if like is not None and (t.shape != like[i].shape or t.dtype != like[i].dtype):
-            raise ValueError("%s[%d] differs from its gradient in shape or dtype" % (what, i))
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors])
-    if like is not None:
-        return dev, ptrs, None, None
+    T = torch.Tensor
+    index = set(map(T.get_device, tensors))
+    if len(index) != 1:
+        raise ValueError("%s are on several devices" % what)
+    if not all(map(T.is_contiguous, tensors)):
+        i = [t.is_contiguous() for t in tensors].index(False)
+        raise ValueError("%s[%d] must be contiguous" % (what, i))
     code = {torch.float32: 0, torch.bfloat16: 1}
     try:
-        types = (ctypes.c_int32 * n)(*[code[t.dtype] for t in tensors])
+        types = [code[t.dtype] for t in tensors]
     except KeyError as e:
         raise ValueError("unsupported dtype %s in %s" % (e.args[0], what)) from None
-    return dev, ptrs, (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), types
+    return (array("Q", map(T.data_ptr, tensors)), array("q", map(T.numel, tensors)), array("i", types))
+
+
+def _address(a):
+    return None if a is None else a.buffer_info()[0]
 
 
 def msm_grad_norm(grads, *, workspace=None, stream=None):
@@ -301,11 +332,12 @@ def msm_grad_norm(grads, *, workspace=None, stream=None):
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
-    dev, ptrs, numel, types = _tensor_list(grads, "grads")
+    ptrs, numel, types = _tensor_list(grads, "grads")
+    dev = grads[0].device
     norm = own.empty((), torch.float32, dev)
     ws, wsb = _workspace(int(lib.msm_grad_norm_workspace_bytes(len(grads))), workspace, dev, own)
-    st = lib.msm_grad_norm(ptrs, numel, types, len(grads), _ptr(norm), _ptr(ws), wsb,
-                           _stream_handle(stream, dev))
+    st = lib.msm_grad_norm(_address(ptrs), _address(numel), _address(types), len(grads), _ptr(norm),
+                           _ptr(ws), wsb, _stream_handle(stream, dev))
     own.done()
     if st != 0:
         raise MsmError(st, "msm_grad_norm")
@@ -321,19 +353,23 @@ def msm_grad_clip(grads, max_norm, *, eps=1e-6, out=None, workspace=None, stream
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
-    dev, ptrs, numel, types = _tensor_list(grads, "grads")
+    ptrs, numel, types = _tensor_list(grads, "grads")
+    dev = grads[0].device
     optrs = None
     if out is not None:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out has %d tensors, expected %d" % (len(out), len(grads)))
-        odev, optrs, _, _ = _tensor_list(out, "out", like=grads)
-        if odev != dev:
-            raise ValueError("out is on %s, expected %s" % (odev, dev))
+        optrs, onumel, otypes = _tensor_list(out, "out")
+        if onumel != numel or otypes != types:
+            raise ValueError("a tensor of out differs from its gradient in size or dtype")
+        if out[0].device != dev:
+            raise ValueError("out is on %s, expected %s" % (out[0].device, dev))
     norm = own.empty((), torch.float32, dev)
     ws, wsb = _workspace(int(lib.msm_grad_norm_workspace_bytes(len(grads))), workspace, dev, own)
-    st = lib.msm_grad_clip(ptrs, optrs, numel, types, len(grads), float(max_norm), float(eps),
-                           _ptr(norm), _ptr(ws), wsb, _stream_handle(stream, dev))
+    st = lib.msm_grad_clip(_address(ptrs), _address(optrs), _address(numel), _address(types),
+                           len(grads), float(max_norm), float(eps), _ptr(norm), _ptr(ws), wsb,
+                           _stream_handle(stream, dev))
     own.done()
     if st != 0:
         raise MsmError(st, "msm_grad_clip")
