@@ -171,24 +171,24 @@ msm_status norm_check(int64_t rows, int64_t D, msm_dtype io) {
   return MSM_OK;
 }
 
-// Workgroups of the backward: each leaves 8 D bytes (32 D with rows of at most a wavefront) of
-// column sums, so few enough that they stay small beside the rows, and enough to fill the GPU.
+// Workgroups of the backward: each leaves 8 D bytes of column sums, so few enough that they stay
+// small beside the rows, and enough to fill the GPU.
 int64_t norm_groups(int64_t rows, const msm::NormShape& f) {
   if (f.NV == 0) return rows < 64 ? rows : 64;
-  const int64_t in_flight = 256 / f.T, g = ceil_div(rows, 4 * in_flight);
-  return g > 512 ? 512 : g;
+  const int64_t threads = msm::norm_threads(f.T, f.NV), in_flight = threads / f.T;
+  const int64_t g = ceil_div(rows, 2 * in_flight), most = f.T == 256 ? 256 : 512;
+  return g > most ? most : g;
 }
 
 size_t norm_bwd_bytes(int64_t rows, int64_t D, msm_dtype io) {
   // for either way of reading the rows (it depends on the arrays' alignment)
-  size_t most = 0;
+  int64_t most = 256;
   const int pers[2] = {1, io == MSM_BF16 ? 8 : 4};
   for (int per : pers) {
-    const msm::NormShape f = msm::norm_shape(D, per);
-    const size_t b = (size_t)norm_groups(rows, f) * (f.T == 256 ? 1 : 4) * 8 * (size_t)D;
-    if (b > most) most = b;
+    const int64_t g = norm_groups(rows, msm::norm_shape(D, per));
+    if (g > most) most = g;
   }
-  return align_up(most);
+  return align_up((size_t)most * 8 * (size_t)D);
 }
 
 // ---- clipping ----

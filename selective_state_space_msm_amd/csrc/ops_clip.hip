@@ -118,7 +118,7 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(const ClipBatch b, cons
             o[2 * q] = static_cast<__bf16>(__uint_as_float(w[q] << 16) * coef);
             o[2 * q + 1] = static_cast<__bf16>(__uint_as_float(w[q] & 0xffff0000u) * coef);
           }
-          *reinterpret_cast<bf16x8*>(y + i + 8 * threadIdx.x) = o;
+          __builtin_nontemporal_store(o, reinterpret_cast<bf16x8*>(y + i + 8 * threadIdx.x));
         }
       }
       for (i += threadIdx.x; i < n; i += 256)
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(const ClipBatch b, cons
       if ((((uintptr_t)x | (uintptr_t)y) & 15) == 0) {
         for (; i + 1024 <= n; i += 1024) {
           const f32x4 w = *reinterpret_cast<const f32x4*>(x + i + 4 * threadIdx.x);
-          *reinterpret_cast<f32x4*>(y + i + 4 * threadIdx.x) = w * coef;
+          __builtin_nontemporal_store(w * coef, reinterpret_cast<f32x4*>(y + i + 4 * threadIdx.x));
         }
       }
       for (i += threadIdx.x; i < n; i += 256) y[i] = x[i] * coef;

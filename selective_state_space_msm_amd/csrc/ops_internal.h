@@ -116,6 +116,11 @@ struct NormShape {
   int T, NV;
 };
 NormShape norm_shape(int64_t D, int per);
+// Threads of a backward workgroup: two wide rows side by side where the registers allow two
+// wavefronts a SIMD.  At 16384 x 4096 bf16, 256 workgroups of 512 threads take 81 us, 512 of 256
+// threads 84 us (1024: 105 us, their column sums are as many bytes as an eighth of the rows), and
+// 256 of 1024 threads 131 us, their barriers holding 16 wavefronts together.
+constexpr int norm_threads(int T, int NV) { return T == 256 && NV <= 4 ? 512 : 256; }
 hipError_t launch_norm_fwd(const NormArgs& a, int io_bf16, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, int io_bf16, hipStream_t s);
 

@@ -11,6 +11,8 @@
 // its columns and keeps their dw and db sums in registers over all rows of its workgroup; the
 // workgroups' sums are joined by a second kernel in a fixed order.  Longer rows are walked in
 // loops over memory.
+#include <type_traits>
+
 #include "ops_delta.hpp"
 
 namespace msm {
@@ -30,13 +32,14 @@ namespace {
 constexpr int64_t kNormGroups = 2048;
 
 // Sum over the T threads of a row, the same value in each of them.
+// With 256 threads the sum of each wavefront passes through `lds`, which the next sum must not be
+// (a later one may: a thread that writes there has passed the barrier in between).
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
   constexpr int W = T < 64 ? T : 64;
 #pragma unroll
   for (int m = W / 2; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
   if constexpr (T == 256) {
-    __syncthreads();  // the previous sum has been read
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
@@ -52,10 +55,9 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
     b += __shfl_xor(b, m, 64);
   }
   if constexpr (T == 256) {
-    __syncthreads();
     if ((threadIdx.x & 63) == 0) {
-      lds[threadIdx.x >> 6] = a;
-      lds[4 + (threadIdx.x >> 6)] = b;
+      lds[(threadIdx.x >> 6) & 3] = a;
+      lds[4 + ((threadIdx.x >> 6) & 3)] = b;
     }
     __syncthreads();
     a = (lds[0] + lds[1]) + (lds[2] + lds[3]);
@@ -63,24 +65,32 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
   }
 }
 
+// VEC elements between their load and their use.
 template <typename IO, int VEC>
-__device__ __forceinline__ void load_piece(const void* p, int64_t i, float (&x)[VEC]) {
-  using T = io<IO>;
-  if constexpr (VEC == 1) {
-    x[0] = T::widen(T::load(p, i));
-  } else if constexpr (T::es == 2) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      x[2 * c] = __uint_as_float(w[c] << 16);
-      x[2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
-    }
-  } else {
-    const f32x4 w = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = w[c];
+struct Piece {
+  std::conditional_t<VEC == 1, typename io<IO>::raw, u32x4> raw;
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (VEC == 1)
+      raw = io<IO>::load(p, i);
+    else
+      raw = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * io<IO>::es);
   }
-}
+  __device__ __forceinline__ void zero() { raw = {}; }
+  __device__ __forceinline__ void get(float (&x)[VEC]) const {
+    if constexpr (VEC == 1) {
+      x[0] = io<IO>::widen(raw);
+    } else if constexpr (io<IO>::es == 2) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        x[2 * c] = __uint_as_float(raw[c] << 16);
+        x[2 * c + 1] = __uint_as_float(raw[c] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = __uint_as_float(raw[c]);
+    }
+  }
+};
 template <typename IO, int VEC>
 __device__ __forceinline__ void store_piece(void* p, int64_t i, const float (&x)[VEC]) {
   using T = io<IO>;
@@ -117,16 +127,18 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormArgs p) {
   const int64_t step = (int64_t)gridDim.x * RW;
   int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / T;
   if (row >= p.rows) return;  // whole groups of T lanes (for T = 256 the workgroup): no sum crosses groups
-  float w[NV][VEC], b[NV][VEC], next[NV][VEC];
+  float w[NV][VEC], b[NV][VEC];
+  Piece<IO, VEC> next[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t c = ((int64_t)i * T + t) * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) next[i][e] = w[i][e] = b[i][e] = 0.f;
+    for (int e = 0; e < VEC; ++e) w[i][e] = b[i][e] = 0.f;
+    next[i].zero();
     if (c < p.D) {
       load_param<VEC>(p.weight, c, 1.f, w[i]);
       load_param<VEC>(p.bias, c, 0.f, b[i]);
-      load_piece<IO, VEC>(p.x, row * p.D + c, next[i]);
+      next[i].load(p.x, row * p.D + c);
     }
   }
   const float inv = 1.f / (float)p.D;
@@ -136,12 +148,10 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormArgs p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = ((int64_t)i * T + t) * VEC;
+      next[i].get(x[i]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        x[i][e] = next[i][e];
-        sum += x[i][e];
-      }
-      if (c < p.D && row + step < p.rows) load_piece<IO, VEC>(p.x, (row + step) * p.D + c, next[i]);
+      for (int e = 0; e < VEC; ++e) sum += x[i][e];
+      if (c < p.D && row + step < p.rows) next[i].load(p.x, (row + step) * p.D + c);
     }
     const float mean = row_sum<T>(sum, lds) * inv;
     float sq = 0.f;
@@ -155,7 +165,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormArgs p) {
           sq = fmaf(x[i][e], x[i][e], sq);
         }
     }
-    const float rstd = 1.f / sqrtf(row_sum<T>(sq, lds) * inv + p.eps);
+    const float rstd = 1.f / sqrtf(row_sum<T>(sq, lds + 4) * inv + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = ((int64_t)i * T + t) * VEC;
@@ -187,7 +197,7 @@ __global__ __launch_bounds__(256) void norm_fwd_loop_kernel(const NormArgs p) {
     const float d = T::widen(T::load(p.x, at + c)) - mean;
     sq = fmaf(d, d, sq);
   }
-  const float rstd = 1.f / sqrtf(row_sum<256>(sq, lds) * inv + p.eps);
+  const float rstd = 1.f / sqrtf(row_sum<256>(sq, lds + 4) * inv + p.eps);
   for (int64_t c = threadIdx.x; c < p.D; c += 256) {
     const float d = (T::widen(T::load(p.x, at + c)) - mean) * rstd;
     T::store(p.y, at + c, fmaf(d, p.weight ? p.weight[c] : 1.f, p.bias ? p.bias[c] : 0.f));
@@ -198,77 +208,109 @@ __global__ __launch_bounds__(256) void norm_fwd_loop_kernel(const NormArgs p) {
   }
 }
 
-template <typename IO, int VEC, int T, int NV>
-__global__ __launch_bounds__(256) void norm_bwd_kernel(const NormArgs p) {
-  __shared__ float lds[8];
-  constexpr int RW = 256 / T;  // rows in flight in the workgroup
+// BS threads, BS / T rows in flight.  The rows' pieces of x and dy are fetched one row ahead.  At
+// the end the workgroup joins its threads' column sums and leaves one pair of D sums.
+template <typename IO, int VEC, int T, int NV, int BS>
+__global__ __launch_bounds__(BS) void norm_bwd_kernel(const NormArgs p) {
+  constexpr int RW = BS / T;
+  constexpr int kGroup = T > 64 ? T : 64;  // threads whose column sums a wavefront (or row) has joined
+  constexpr int NG = BS / kGroup;
+  __shared__ float lds[2][T == 256 ? RW : 1][8];
+  int turn = 0;
+  __shared__ float cols[NG > 1 ? NG : 1][NG > 1 ? T * VEC : 1];
   const int t = threadIdx.x % T, rg = threadIdx.x / T;
   const float inv = 1.f / (float)p.D;
+  const int64_t step = (int64_t)gridDim.x * RW;
   float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+  Piece<IO, VEC> nx[NV], ny[NV];
+  int64_t row = (int64_t)blockIdx.x * RW + rg;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t c = ((int64_t)i * T + t) * VEC;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.f;
-    if (c < p.D) load_param<VEC>(p.weight, c, 1.f, w[i]);
+    nx[i].zero();
+    ny[i].zero();
+    if (c < p.D) {
+      load_param<VEC>(p.weight, c, 1.f, w[i]);
+      if (row < p.rows) {
+        nx[i].load(p.x, row * p.D + c);
+        ny[i].load(p.dy, row * p.D + c);
+      }
+    }
   }
-  for (int64_t row = (int64_t)blockIdx.x * RW + rg; row < p.rows; row += (int64_t)gridDim.x * RW) {
-    float x[NV][VEC], dy[NV][VEC];
-    const float mean = p.mean[row], rstd = p.rstd[row];
+  // every thread takes part in every pass (the sums of a 256-thread row meet at barriers); a row
+  // past the end adds nothing
+  for (int64_t first = (int64_t)blockIdx.x * RW; first < p.rows; first += step, row += step) {
+    const bool on = row < p.rows;
+    const float mean = on ? p.mean[row] : 0.f, rstd = on ? p.rstd[row] : 0.f;
+    float x[NV][VEC], u[NV][VEC];
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = ((int64_t)i * T + t) * VEC;
+      const bool in = on && c < p.D;
+      float dy[VEC];
+      nx[i].get(x[i]);
+      ny[i].get(dy);
+      if (c < p.D && row + step < p.rows) {
+        nx[i].load(p.x, (row + step) * p.D + c);
+        ny[i].load(p.dy, (row + step) * p.D + c);
+      }
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        x[i][e] = mean;
-        dy[i][e] = 0.f;
-      }
-      if (c < p.D) {
-        load_piece<IO, VEC>(p.x, row * p.D + c, x[i]);
-        load_piece<IO, VEC>(p.dy, row * p.D + c, dy[i]);
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        x[i][e] = (x[i][e] - mean) * rstd;
-        const float u = dy[i][e] * w[i][e];
-        a += u;
-        b = fmaf(u, x[i][e], b);
-        dw[i][e] = fmaf(dy[i][e], x[i][e], dw[i][e]);
-        db[i][e] += dy[i][e];
+        x[i][e] = in ? (x[i][e] - mean) * rstd : 0.f;
+        dy[e] = in ? dy[e] : 0.f;
+        u[i][e] = dy[e] * w[i][e];
+        a += u[i][e];
+        b = fmaf(u[i][e], x[i][e], b);
+        dw[i][e] = fmaf(dy[e], x[i][e], dw[i][e]);
+        db[i][e] += dy[e];
       }
     }
-    row_sum2<T>(a, b, lds);
+    row_sum2<T>(a, b, lds[turn][T == 256 ? rg : 0]);
+    turn ^= 1;
     a *= inv;
     b *= inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = ((int64_t)i * T + t) * VEC;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[i][e] = rstd * (fmaf(dy[i][e], w[i][e], -a) - x[i][e] * b);
-      if (c < p.D) store_piece<IO, VEC>(p.dx, row * p.D + c, x[i]);
+      for (int e = 0; e < VEC; ++e) x[i][e] = rstd * (u[i][e] - a - x[i][e] * b);
+      if (on && c < p.D) store_piece<IO, VEC>(p.dx, row * p.D + c, x[i]);
     }
   }
   if (!p.part) return;
-  // one pair of column sums a wavefront, or a workgroup when its rows are that wide
-  constexpr int PW = T == 256 ? 1 : 4;
-  float* part = p.part + ((int64_t)blockIdx.x * PW + (T == 256 ? 0 : threadIdx.x >> 6)) * 2 * p.D;
+  float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t c = ((int64_t)i * T + t) * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e)
+    for (int which = 0; which < 2; ++which) {
+      float(&v)[VEC] = which ? db[i] : dw[i];
 #pragma unroll
-      for (int m = T; m < 64; m *= 2) {
-        dw[i][e] += __shfl_xor(dw[i][e], m, 64);
-        db[i][e] += __shfl_xor(db[i][e], m, 64);
+      for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int m = T; m < 64; m *= 2) v[e] += __shfl_xor(v[e], m, 64);
+      if constexpr (NG > 1) {
+        __syncthreads();  // the last round has been read
+        if (T >= 64 || (threadIdx.x & 63) < T)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) cols[threadIdx.x / kGroup][t * VEC + e] = v[e];
+        __syncthreads();
+        for (int k = threadIdx.x; k < T * VEC; k += BS) {
+          float s = 0.f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) s += cols[g][k];
+          const int64_t c = (int64_t)i * T * VEC + k;
+          if (c < p.D) part[which * p.D + c] = s;
+        }
+      } else {
+        const int64_t c = ((int64_t)i * T + t) * VEC;
+        if (c < p.D)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) part[which * p.D + c + e] = v[e];
       }
-    if (c < p.D && (T >= 64 || (threadIdx.x & 63) < T))
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        part[c + e] = dw[i][e];
-        part[p.D + c + e] = db[i][e];
-      }
+    }
   }
 }
 
@@ -357,10 +399,11 @@ hipError_t go_fwd(const NormArgs& a, hipStream_t s) {
 }
 template <typename IO, int VEC, int T, int NV>
 hipError_t go_bwd(const NormArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((norm_bwd_kernel<IO, VEC, T, NV>), dim3((unsigned)a.groups), dim3(256), 0, s, a);
+  constexpr int BS = norm_threads(T, NV);
+  hipLaunchKernelGGL((norm_bwd_kernel<IO, VEC, T, NV, BS>), dim3((unsigned)a.groups), dim3(BS), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  return join(a, (int64_t)a.groups * (T == 256 ? 1 : 4), s);
+  return join(a, a.groups, s);
 }
 
 template <typename IO, int VEC, bool BWD>
