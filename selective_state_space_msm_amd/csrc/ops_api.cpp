@@ -318,6 +318,7 @@ msm_status msm_delta_rule_bwd(const void* q, const void* k, const void* v, const
   if (any_overlap(outs, 7, ins, 9)) return MSM_ERR_INVALID_ARG;
   DeltaArgs a = delta_args(s, l, io, q, k, v, g, beta, seq_offsets, S0, scale, workspace);
   a.do_ = do_;
+  a.vec_v = V * (int64_t)es % 16 == 0 && aligned(do_, 16);
   a.dlast_S = dlast_S;
   a.dq = dq;
   a.dk = dk;

@@ -856,8 +856,8 @@ __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p)
 // ---- grad ----------------------------------------------------------------------------------
 
 constexpr int GP = kOutParts;  // parts that the gradients of q and k are made of
-constexpr int kWavesGrad = KP == 256 ? 8 : 4;
-constexpr int kTilesGrad = KP / 16 / kWavesGrad > 0 ? KP / 16 / kWavesGrad : 1;  // 16-key tiles a wavefront
+constexpr int kWavesGrad = KP >= 128 ? 8 : 4;
+constexpr int kTilesGrad = KP == 256 ? 2 : 1;                                   // 16-key tiles a wavefront
 constexpr int MT = C / 16;                                                      // 16-token tiles
 constexpr int VB = MSM_IO_BF16 ? 64 : 32;                                       // columns staged at a time
 constexpr int LDV = VB + 8, LDT = C + 8;
@@ -895,60 +895,121 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
 
   for (int64_t gh = 0; gh < group; ++gh) {
     const int64_t h = hk * group + gh, sh = slot * p.H + h;
-    __syncthreads();
-    for (int i = tid; i < 3 * C; i += THREADS) ev[i] = p.vec[sh * kVec + i];
-    for (int i = tid; i < C; i += THREADS) Gd[i] = reinterpret_cast<const double*>(p.vec + sh * kVec + 3 * C)[i];
-    f32x4 a1[MT][kTilesGrad], a2[MT][kTilesGrad], a3[MT][kTilesGrad], X[MT], Z[MT];
+    const float evv = tid < 3 * C ? p.vec[sh * kVec + tid] : 0.f;
+    const double gv = tid < C ? reinterpret_cast<const double*>(p.vec + sh * kVec + 3 * C)[tid] : 0.0;
+    // sums over the columns for dbeta and dg: the last wavefront's, a token a lane
+    double db = 0, after = 0, before = 0, through = 0;
+    if (wave == kWavesGrad - 1 && lane < C) {
+      const float* dots = p.dots + sh * (p.VP / 16) * kDots;
+#pragma unroll 4
+      for (int b = 0; b < (int)(p.VP / 16); ++b, dots += kDots) {
+        after += (double)dots[lane] - (double)dots[2 * C + lane];
+        db += dots[C + lane];
+        before += dots[3 * C + lane];
+        through += dots[4 * C];
+      }
+    }
+    f32x4 a1[kTilesGrad][MT], a2[kTilesGrad][MT], a3[kTilesGrad][MT], X[MT], Z[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       X[m] = Z[m] = zero4();
 #pragma unroll
-      for (int t = 0; t < kTilesGrad; ++t) a1[m][t] = a2[m][t] = a3[m][t] = zero4();
+      for (int t = 0; t < kTilesGrad; ++t) a1[t][m] = a2[t][m] = a3[t][m] = zero4();
     }
     const auto rdo = head_rsrc(p.do_, ch.row0, p.H, h, p.V, IO::es, ch.n);
     const auto rdv = make_rsrc_u32(p.dV + sh * C * p.VP, (uint32_t)(C * p.VP * 4));
     const auto re = make_rsrc_u32(p.E + sh * C * p.VP, (uint32_t)(C * p.VP * 4));
     const auto rs0 = make_rsrc_u32(p.S + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4));
     const auto rs1 = make_rsrc_u32(p.dS + sh * KP * p.VP, (uint32_t)(KP * p.VP * 4));
+    // columns and states are fetched one step ahead; both come from memory, where a step's loads
+    // would take longer than its products
+    constexpr int kUnits = (C * VB / 8 + THREADS - 1) / THREADS;
+    f32x4 st[kUnits][6], ss[kTilesGrad][4];
+    const auto fetch_cols = [&](int v0) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = tid + i * THREADS, row = u / (VB / 8), c = v0 + (u % (VB / 8)) * 8;
+        const uint32_t o = (uint32_t)(row * p.H * p.V + c) * IO::es;
+        const bool in = C * VB / 8 % THREADS == 0 || row < C;
+        if (p.vec_v) {
+          st[i][0] = bload4(rdo, in && c < p.V ? o : kOutside);
+          if (!MSM_IO_BF16) st[i][1] = bload4(rdo, in && c + 4 < p.V ? o + 16 : kOutside);
+        } else {
+          uint32_t x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[e] = __builtin_bit_cast(uint32_t, IO::bload(rdo, in && c + e < p.V ? o + e * IO::es : kOutside, 0));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            st[i][0][e] = __uint_as_float(MSM_IO_BF16 ? x[2 * e] | (x[2 * e + 1] << 16) : x[e]);
+            st[i][1][e] = __uint_as_float(x[4 + e]);
+          }
+        }
+        const uint32_t w = in && c < p.VP ? (uint32_t)(row * p.VP + c) * 4 : kOutside;
+        st[i][2] = bload4(rdv, w);
+        st[i][3] = bload4(rdv, w + 16);
+        st[i][4] = bload4(re, w);
+        st[i][5] = bload4(re, w + 16);
+      }
+    };
+    const auto put_cols = [&]() {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = tid + i * THREADS, row = u / (VB / 8), c = (u % (VB / 8)) * 8;
+        if (C * VB / 8 % THREADS != 0 && row >= C) continue;
+        Part<kIn> o;
+        if constexpr (kIn == 1)
+          o.p[0] = __builtin_bit_cast(bf16x8, st[i][0]);
+        else
+          o = split<kIn>(st[i][0], st[i][1]);
+        const float beta = ev[2 * C + row];
+        store_parts(dOs + row * LDV + c, C * LDV, o);
+        store_parts(dVs + row * LDV + c, C * LDV, split<TP>(st[i][2], st[i][3]));
+        store_parts(Us + row * LDV + c, C * LDV, split<TP>(st[i][4] * beta, st[i][5] * beta));
+      }
+    };
+    const auto fetch_states = [&](int v) {
+#pragma unroll
+      for (int t = 0; t < kTilesGrad; ++t) {
+        const uint32_t i = keys && v < p.VP ? (uint32_t)((16 * (tile0 + t) + n) * p.VP + v + 8 * j) * 4 : kOutside;
+        ss[t][0] = bload4(rs0, i);
+        ss[t][1] = bload4(rs0, i + 16);
+        ss[t][2] = bload4(rs1, i);
+        ss[t][3] = bload4(rs1, i + 16);
+      }
+    };
+    fetch_cols(0);
+    fetch_states(0);
+    __syncthreads();  // the head before has been read
+    if (tid < 3 * C) ev[tid] = evv;
+    if (tid < C) Gd[tid] = gv;
     for (int v0 = 0; v0 < p.VP; v0 += VB) {
       __syncthreads();  // ev is there; the previous columns have been used
-      for (int u = tid; u < C * VB / 8; u += THREADS) {
-        const int row = u / (VB / 8), c = (u % (VB / 8)) * 8;
-        f32x4 o[2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          o[i / 4][i % 4] = IO::widen(IO::bload(rdo, v0 + c + i < p.V ? (uint32_t)(row * p.H * p.V + v0 + c + i) * IO::es : kOutside, 0));
-        const uint32_t w = v0 + c < p.VP ? (uint32_t)(row * p.VP + v0 + c) * 4 : kOutside;
-        const f32x4 a = bload4(rdv, w), b = bload4(rdv, w + 16);
-        const f32x4 d = bload4(re, w) * ev[2 * C + row], e = bload4(re, w + 16) * ev[2 * C + row];
-        store_parts(dOs + row * LDV + c, C * LDV, split<kIn>(o[0], o[1]));
-        store_parts(dVs + row * LDV + c, C * LDV, split<TP>(a, b));
-        store_parts(Us + row * LDV + c, C * LDV, split<TP>(d, e));
-      }
+      put_cols();
+      fetch_cols(v0 + VB);
       __syncthreads();
 #pragma unroll
       for (int b = 0; b < VB / 32; ++b) {
         if (v0 + 32 * b >= p.VP) break;
+        Part<GP> s0[kTilesGrad], s1[kTilesGrad];
+#pragma unroll
+        for (int t = 0; t < kTilesGrad; ++t) {
+          s0[t] = split<GP>(ss[t][0], ss[t][1]);
+          s1[t] = split<GP>(ss[t][2], ss[t][3]);
+        }
+        fetch_states(v0 + 32 * b + 32);
         if (keys) {
-          Part<kIn> fo[MT];
-          Part<GP> fv[MT], fu[MT];
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const int e = (16 * m + n) * LDV + 32 * b + 8 * j;
-            fo[m] = load_ld<kIn>(dOs + e, C * LDV);
-            fv[m] = load_ld<GP>(dVs + e, C * LDV);
-            fu[m] = load_ld<GP>(Us + e, C * LDV);
-          }
+            const auto fo = load_ld<kIn>(dOs + e, C * LDV);
+            const auto fv = load_ld<GP>(dVs + e, C * LDV);
+            const auto fu = load_ld<GP>(Us + e, C * LDV);
 #pragma unroll
-          for (int t = 0; t < kTilesGrad; ++t) {
-            const uint32_t i = (uint32_t)((16 * (tile0 + t) + n) * p.VP + v0 + 32 * b + 8 * j) * 4;
-            const auto s0 = split<GP>(bload4(rs0, i), bload4(rs0, i + 16));
-            const auto s1 = split<GP>(bload4(rs1, i), bload4(rs1, i + 16));
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma(a1[m][t], fo[m], s0);
-              mma(a2[m][t], fv[m], s0);
-              mma(a3[m][t], fu[m], s1);
+            for (int t = 0; t < kTilesGrad; ++t) {
+              mma(a1[t][m], fo, s0[t]);
+              mma(a2[t][m], fv, s0[t]);
+              mma(a3[t][m], fu, s1[t]);
             }
           }
         }
@@ -1007,33 +1068,25 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
       }
     }
     __syncthreads();
-    if (tid < C) {
-      // sums over the columns, then the running sums of the decay's gradient
-      const float* dots = p.dots + sh * (p.VP / 16) * kDots;
-      double db = 0, after = 0, before = 0, through = 0;
-      for (int64_t b = 0; b < p.VP / 16; ++b, dots += kDots) {
-        after += (double)dots[tid] - (double)dots[2 * C + tid];
-        db += dots[C + tid];
-        before += dots[3 * C + tid];
-        through += dots[4 * C];
-      }
+    if (wave == kWavesGrad - 1 && lane < C) {
+      // running sums of the decay's gradient
 #pragma unroll
       for (int m = 1; m < C; m *= 2) {
         const double dn = __shfl_down(after, m, 64), up = __shfl_up(before, m, 64);
-        if (tid + m < C) after += dn;
-        if (tid >= m) before += up;
+        if (lane + m < C) after += dn;
+        if (lane >= m) before += up;
       }
       double dg = after + through;
       const double up = __shfl_up(before, 1, 64);
-      if (tid > 0) {
+      if (lane > 0) {
         dg += up;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          if (16 * m + 15 >= tid) dg += across[m][tid - 1];
+          if (16 * m + 15 >= lane) dg += across[m][lane - 1];
       }
-      if (tid < ch.n) {
-        p.dg[(ch.row0 + tid) * p.H + h] = (float)dg;
-        p.dbeta[(ch.row0 + tid) * p.H + h] = (float)db;
+      if (lane < ch.n) {
+        p.dg[(ch.row0 + lane) * p.H + h] = (float)dg;
+        p.dbeta[(ch.row0 + lane) * p.H + h] = (float)db;
       }
     }
     if (keys) {
@@ -1044,8 +1097,8 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
           const float x = ev[16 * m + 4 * j + r], y = ev[C + 16 * m + 4 * j + r];
 #pragma unroll
           for (int t = 0; t < kTilesGrad; ++t) {
-            dq[m][t][r] = fmaf(x * p.scale, a1[m][t][r], dq[m][t][r]);
-            dk[m][t][r] += y * a3[m][t][r] - x * a2[m][t][r];
+            dq[m][t][r] = fmaf(x * p.scale, a1[t][m][r], dq[m][t][r]);
+            dk[m][t][r] += y * a3[t][m][r] - x * a2[t][m][r];
           }
         }
 #pragma unroll

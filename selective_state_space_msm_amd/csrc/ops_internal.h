@@ -58,6 +58,7 @@ struct DeltaArgs {
   float scale;
   int32_t vec_k;        // rows of q and k can be read 16 bytes at a time
   int32_t kq_direct;    // and they need no conversion
+  int32_t vec_v;        // rows of do can be read 16 bytes at a time
 };
 
 struct DeltaStepArgs {
