@@ -102,7 +102,7 @@ DeltaLayout delta_layout(const DeltaShape& s, msm_dtype io, bool bwd) {
     l.E = take(n * C * VP * 4);
     l.dV = take(n * C * VP * 4);
     l.pred = take(n * C * VP * 4);
-    l.dots = take(n * (VP / 16) * (4 * C + 4) * 4);
+    l.dots = take(n * (VP / 16) * 4 * C * 4);
   }
   l.total = at;
   return l;

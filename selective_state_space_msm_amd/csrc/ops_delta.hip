@@ -49,7 +49,7 @@ constexpr int kRows = C * KP;                   // elements of a plane of keys
 using TriM = Tri<C>;
 constexpr int kTri = TP * TriM::kPlane;         // elements of a chunk matrix
 constexpr int kVec = 5 * C;
-constexpr int kDots = 4 * C + 4;
+constexpr int kDots = 4 * C;
 constexpr int kWavesScan = 4;     // wavefronts of a scan workgroup, 16 columns each
 #if MSM_IO_BF16
 using IO = io<bf16_storage>;
@@ -714,9 +714,11 @@ struct RevOut {
   float* dots;
 };
 
-__device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, const MSM_LDS KeyRows& l, const MSM_LDS RevTri& x3,
+// p_used and tm_used are called when this wavefront has read P, and T and M, for the last time.
+template <class FP, class FT>
+__device__ __forceinline__ void rev_chunk(FP p_used, FT tm_used, const DeltaArgs& p, const Walk& w, const MSM_LDS KeyRows& l, const MSM_LDS RevTri& x3,
                                           Cols<NB>& S, Cols<CB> dO, const Cols<CB>& Er, const Cols<CB>& pred,
-                                          const Cols<NB>& S0, const RevOut& out, int rows) {
+                                          const RevOut& out, int rows) {
   const int lane = w.lane, j = w.j, n = w.n;
   const MSM_LDS float* eG = l.ev + 8 * j;
   const MSM_LDS float* eK = l.ev + C + 8 * j;
@@ -724,9 +726,6 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
   const float last = l.ev[C - 1];
   // the adjoint after this chunk, kept for the gradients of q and k
   store_cols<NB>(out.dS.rsrc(rows), w.wat, w.wstride, S);
-  float dot = 0.f;
-  each<NB>([&](int b, int t, int r, int) { dot = fmaf(S0.t[b][t][r], S.t[b][t][r], dot); });
-  dot *= last;
   // W = e^{G_C - G} (K dS) + P^T dO
   Cols<CB> W = zero_cols<CB>();
   RowTiles fk[2];
@@ -754,6 +753,7 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
   split_all(dOB, dO);
   f3[1].load(x3.t, lane, j);
   hold_lds();
+  p_used();
   f3[0].mma(W, dOB);
   // dV = T^T (beta W)
   Cols<CB> dV = zero_cols<CB>(), x;
@@ -770,6 +770,7 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
   fq[0].load(l.q, 0, lane, j);
   fc[0].load(l.k, 0, lane, j);
   hold_lds();
+  tm_used();
   f3[0].mma(W, B);
   float ye[16], dp[16];
 #pragma unroll
@@ -786,9 +787,6 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
     dots[2 * C + row] = sp;
     dots[3 * C + row] = sw;
   }
-#pragma unroll
-  for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
-  if (w.on && lane == 0) dots[4 * C] = dot;
   store_cols<CB>(out.dV.rsrc(rows), w.wat, w.wstride, dV);
   store_out(out.dv.rsrc(rows), w.vat, w.vstride, dV);
   // dS0 = e^{G_C} dS1 + Q^T (scale e^G dO) - K^T (e^G dV)
@@ -813,11 +811,16 @@ __device__ __forceinline__ void rev_chunk(const DeltaArgs& p, const Walk& w, con
   }
 }
 
+// The chunk matrices have one buffer each, filled again as soon as every wavefront has read it;
+// keys and queries have two where the LDS allows.
+template <bool kTwo>
 __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p) {
   __shared__ __attribute__((aligned(16))) KeyRows lds0;
-  __shared__ __attribute__((aligned(16))) RevTri lds1;
+  __shared__ __attribute__((aligned(16))) std::conditional_t<kTwo, KeyRows, Nothing> lds1;
+  __shared__ __attribute__((aligned(16))) RevTri lds_tri;
   auto& l0 = (MSM_LDS KeyRows&)lds0;
-  auto& x3 = (MSM_LDS RevTri&)lds1;
+  auto& l1 = (MSM_LDS std::conditional_t<kTwo, KeyRows, Nothing>&)lds1;
+  auto& x3 = (MSM_LDS RevTri&)lds_tri;
   const Walk w(p);
   Cols<NB> S = zero_cols<NB>();  // the adjoint of the state
   if (p.dlast_S) S = load_cols<NB>(w.state(p.dlast_S, p), w.sat, (uint32_t)(p.V * 4));
@@ -825,39 +828,87 @@ __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p)
   Keys keys(p, row, slot, w.h, w.hk, w.tid);
   Stream st = slot_stream(p.T, slot, p.H, w.h, kTri * 2), sp = slot_stream(p.P, slot, p.H, w.h, kTri * 2);
   Stream sm = slot_stream(p.M, slot, p.H, w.h, kTri * 2), sd = head_stream(p.do_, row, p.H, w.h, p.V);
-  Stream sS = slot_stream(p.S, slot, p.H, w.h, KP * p.VP * 4);
   Stream sE = slot_stream(p.E, slot, p.H, w.h, C * p.VP * 4), spred = slot_stream(p.pred, slot, p.H, w.h, C * p.VP * 4);
   RevOut out;
   out.dv = head_stream(p.dv, row, p.H, w.h, p.V);
   out.dV = slot_stream(p.dV, slot, p.H, w.h, C * p.VP * 4);
   out.dS = slot_stream(p.dS, slot, p.H, w.h, KP * p.VP * 4);
   out.dots = p.dots + ((slot * p.H + w.h) * (p.VP / 16) + w.vb) * kDots;
-  for (int c = w.chunks - 1; c >= 0; --c) {
-    const int rows = w.rows(c);
-    sync_lds();
-    keys.load(l0, rows, w.wave, w.lane, 0, 1);
+  RawCols d;
+  Cols<CB> Er, pred;
+  const auto fetch_keys = [&](auto& l, int rows) {
+    keys.load(l, rows, w.wave, w.lane, 0, 1);
+    keys.next(-1);
+  };
+  const auto fetch_cols = [&](int rows) {
+    d.fetch(sd.rsrc(rows), w.vat, w.vstride);
+    Er = load_cols<CB>(sE.rsrc(rows), w.wat, w.wstride);
+    pred = load_cols<CB>(spred.rsrc(rows), w.wat, w.wstride);
+    for (Stream* x : {&sd, &sE, &spred}) x->next(-1);
+  };
+  const auto fetch_p = [&](int rows) {
     load_tri<TP>(x3.p, sp, rows, w.wave, w.lane);
+    sp.next(-1);
+  };
+  const auto fetch_tm = [&](int rows) {
     load_tri<TP>(x3.t, st, rows, w.wave, w.lane);
     load_tri<TP>(x3.m, sm, rows, w.wave, w.lane);
-    RawCols d;
-    d.fetch(sd.rsrc(rows), w.vat, w.vstride);
-    const Cols<CB> Er = load_cols<CB>(sE.rsrc(rows), w.wat, w.wstride);
-    const Cols<CB> pred = load_cols<CB>(spred.rsrc(rows), w.wat, w.wstride);
-    const Cols<NB> S0 = load_cols<NB>(sS.rsrc(rows), w.wat, w.wstride);
-    sync_loads();
-    rev_chunk(p, w, l0, x3, S, d.widen(), Er, pred, S0, out, rows);
-    keys.next(-1);
-    for (Stream* x : {&st, &sp, &sm, &sd, &sS, &sE, &spred, &out.dv, &out.dV, &out.dS}) x->next(-1);
+    st.next(-1);
+    sm.next(-1);
+  };
+  const auto step = [&](auto& here, int c) {
+    const int rows = w.rows(c), before = w.rows(c - 1);
+    const Cols<CB> dO = d.widen(), E0 = Er, pred0 = pred;
+    fetch_cols(before);
+    rev_chunk(
+        [&] {
+          sync_lds();
+          fetch_p(before);
+        },
+        [&] {
+          sync_lds();
+          fetch_tm(before);
+        },
+        p, w, here, x3, S, dO, E0, pred0, out, rows);
+    for (Stream* x : {&out.dv, &out.dV, &out.dS}) x->next(-1);
     out.dots -= p.H * (p.VP / 16) * kDots;
+  };
+  fetch_cols(w.rows(w.chunks - 1));
+  fetch_p(w.rows(w.chunks - 1));
+  fetch_tm(w.rows(w.chunks - 1));
+  if constexpr (kTwo) {
+    fetch_keys(l0, w.rows(w.chunks - 1));
+    int c = w.chunks - 1;
+    for (; c > 0; c -= 2) {
+      sync_loads();
+      fetch_keys(l1, w.rows(c - 1));
+      step(l0, c);
+      sync_loads();
+      fetch_keys(l0, w.rows(c - 2));
+      step(l1, c - 1);
+    }
+    if (c == 0) {
+      sync_loads();
+      step(l0, c);
+    }
+  } else {
+    for (int c = w.chunks - 1; c >= 0; --c) {
+      sync_lds();
+      fetch_keys(l0, w.rows(c));
+      sync_loads();
+      step(l0, c);
+    }
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // empty loads past the first chunk still write to LDS
   if (w.on && p.dS0) store_cols<NB>(w.state(p.dS0, p), w.sat, (uint32_t)(p.V * 4), S);
 }
 
 // ---- grad ----------------------------------------------------------------------------------
 
 constexpr int GP = kOutParts;  // parts that the gradients of q and k are made of
-constexpr int kWavesGrad = KP >= 128 ? 8 : 4;
-constexpr int kTilesGrad = KP == 256 ? 2 : 1;                                   // 16-key tiles a wavefront
+// Wavefronts: two a SIMD hide each other's loads, but the fp32 parts of eight would not fit.
+constexpr int kWavesGrad = KP == 256 || (KP == 128 && MSM_IO_BF16) ? 8 : 4;
+constexpr int kTilesGrad = KP / 16 > kWavesGrad ? KP / 16 / kWavesGrad : 1;      // 16-key tiles a wavefront
 constexpr int MT = C / 16;                                                      // 16-token tiles
 constexpr int VB = MSM_IO_BF16 ? 64 : 32;                                       // columns staged at a time
 constexpr int LDV = VB + 8, LDT = C + 8;
@@ -871,6 +922,7 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   __shared__ __attribute__((aligned(16))) uint16_t lds_buf[kStage > kPair ? kStage : kPair];
   __shared__ __attribute__((aligned(16))) float ev[3 * C];
   __shared__ double Gd[C];
+  __shared__ float inner[kWavesGrad];  // <S0, dS1> over a wavefront's keys
   __shared__ float across[MT][C];  // sums of N_ij over a tile of rows i >= t and all j < t
   const lds_parts Ks = (lds_parts)lds_k, Qs = (lds_parts)lds_q, buf = (lds_parts)lds_buf;
   const lds_parts dOs = buf, dVs = buf + kIn * C * LDV, Us = dVs + TP * C * LDV;
@@ -898,7 +950,7 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
     const float evv = tid < 3 * C ? p.vec[sh * kVec + tid] : 0.f;
     const double gv = tid < C ? reinterpret_cast<const double*>(p.vec + sh * kVec + 3 * C)[tid] : 0.0;
     // sums over the columns for dbeta and dg: the last wavefront's, a token a lane
-    double db = 0, after = 0, before = 0, through = 0;
+    double db = 0, after = 0, before = 0;
     if (wave == kWavesGrad - 1 && lane < C) {
       const float* dots = p.dots + sh * (p.VP / 16) * kDots;
 #pragma unroll 4
@@ -906,7 +958,6 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
         after += (double)dots[lane] - (double)dots[2 * C + lane];
         db += dots[C + lane];
         before += dots[3 * C + lane];
-        through += dots[4 * C];
       }
     }
     f32x4 a1[kTilesGrad][MT], a2[kTilesGrad][MT], a3[kTilesGrad][MT], X[MT], Z[MT];
@@ -978,6 +1029,7 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
         ss[t][3] = bload4(rs1, i + 16);
       }
     };
+    float dot = 0.f;  // <S0, dS1>
     fetch_cols(0);
     fetch_states(0);
     __syncthreads();  // the head before has been read
@@ -996,6 +1048,8 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
         for (int t = 0; t < kTilesGrad; ++t) {
           s0[t] = split<GP>(ss[t][0], ss[t][1]);
           s1[t] = split<GP>(ss[t][2], ss[t][3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dot = fmaf(ss[t][0][i], ss[t][2][i], fmaf(ss[t][1][i], ss[t][3][i], dot));
         }
         fetch_states(v0 + 32 * b + 32);
         if (keys) {
@@ -1027,6 +1081,9 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
         }
       }
     }
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
+    if (lane == 0) inner[wave] = dot;
     __syncthreads();  // the staged columns have been used
     if (pairs) {
       float carry[4] = {0.f, 0.f, 0.f, 0.f};  // N's row sums over the tiles before
@@ -1076,7 +1133,10 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
         if (lane + m < C) after += dn;
         if (lane >= m) before += up;
       }
-      double dg = after + through;
+      double through = 0;
+#pragma unroll
+      for (int i = 0; i < kWavesGrad; ++i) through += inner[i];
+      double dg = after + through * ev[C - 1];
       const double up = __shfl_up(before, 1, 64);
       if (lane > 0) {
         dg += up;
@@ -1158,7 +1218,7 @@ hipError_t MSM_DELTA_NAME(bwd, MSM_IO_BF16, MSM_KP)(const DeltaArgs& a, hipStrea
   hipLaunchKernelGGL(scan_kernel<true>, scan_grid(a), dim3(64 * kWavesScan), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rev_kernel, scan_grid(a), dim3(64 * kWavesScan), 0, s, a);
+  hipLaunchKernelGGL(rev_kernel<2 * sizeof(KeyRows) + sizeof(RevTri) <= kLdsMost>, scan_grid(a), dim3(64 * kWavesScan), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(grad_kernel, dim3((unsigned)a.nslots, (unsigned)a.Hk), dim3(64 * kWavesGrad), 0, s, a);

@@ -49,7 +49,7 @@ struct DeltaArgs {
   float* E;             // [sh][C][VP] prediction errors                (backward)
   float* dV;            // [sh][C][VP] gradient of v                    (backward)
   float* pred;          // [sh][C][VP] what the state before the chunk predicts (backward)
-  float* dots;          // [sh][VP / 16][4 C + 4] row sums over 16 columns (backward)
+  float* dots;          // [sh][VP / 16][4 C] row sums over 16 columns (backward)
   int64_t tokens;       // rows of the token arrays
   int64_t nseq, L;      // uniform: nseq sequences of L tokens
   int64_t NT;           // uniform: chunks per sequence
