@@ -912,6 +912,7 @@ constexpr int kTilesGrad = KP / 16 > kWavesGrad ? KP / 16 / kWavesGrad : 1;     
 constexpr int MT = C / 16;                                                      // 16-token tiles
 constexpr int VB = MSM_IO_BF16 ? 64 : 32;                                       // columns staged at a time
 constexpr int LDV = VB + 8, LDT = C + 8;
+constexpr int PW = kWavesGrad >= 2 * MT ? 2 : 1, PT = MT / PW;  // wavefronts for a row of token pairs, tiles each
 
 __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p) {
   constexpr int THREADS = 64 * kWavesGrad;
@@ -923,6 +924,7 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   __shared__ __attribute__((aligned(16))) float ev[3 * C];
   __shared__ double Gd[C];
   __shared__ float inner[kWavesGrad];  // <S0, dS1> over a wavefront's keys
+  __shared__ float rowsum[MT][C];  // sums of N_ij over a tile of columns
   __shared__ float across[MT][C];  // sums of N_ij over a tile of rows i >= t and all j < t
   const lds_parts Ks = (lds_parts)lds_k, Qs = (lds_parts)lds_q, buf = (lds_parts)lds_buf;
   const lds_parts dOs = buf, dVs = buf + kIn * C * LDV, Us = dVs + TP * C * LDV;
@@ -937,7 +939,9 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   stage_rows<THREADS>(Qs, nullptr, head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
   const int tile0 = wave * kTilesGrad;           // this wavefront's key tiles
   const bool keys = tile0 * 16 < KP;
-  const bool pairs = wave < MT;                  // this wavefront's row of token pairs
+  // token pairs: 16-row tile `prow`, its 16-column tiles ppart, ppart + PW, ...
+  const int prow = wave % MT, ppart = wave / MT;
+  const bool pairs = ppart < PW;
 
   f32x4 dq[MT][kTilesGrad], dk[MT][kTilesGrad];
 #pragma unroll
@@ -960,10 +964,11 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
         before += dots[3 * C + lane];
       }
     }
-    f32x4 a1[kTilesGrad][MT], a2[kTilesGrad][MT], a3[kTilesGrad][MT], X[MT], Z[MT];
+    f32x4 a1[kTilesGrad][MT], a2[kTilesGrad][MT], a3[kTilesGrad][MT], X[PT], Z[PT];
+#pragma unroll
+    for (int m = 0; m < PT; ++m) X[m] = Z[m] = zero4();
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      X[m] = Z[m] = zero4();
 #pragma unroll
       for (int t = 0; t < kTilesGrad; ++t) a1[t][m] = a2[t][m] = a3[t][m] = zero4();
     }
@@ -1068,15 +1073,16 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
           }
         }
         if (pairs) {
-          const int e = (16 * wave + n) * LDV + 32 * b + 8 * j;
+          const int e = (16 * prow + n) * LDV + 32 * b + 8 * j;
           const auto fo = load_ld<kIn>(dOs + e, C * LDV);
           const auto fv = load_ld<TP>(dVs + e, C * LDV);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if (m > wave) continue;
+          for (int i = 0; i < PT; ++i) {
+            const int m = ppart + PW * i;
+            if (m > prow) continue;
             const auto fu = load_ld<TP>(Us + (16 * m + n) * LDV + 32 * b + 8 * j, C * LDV);
-            mma(X[m], fo, fu);
-            mma(Z[m], fv, fu);
+            mma(X[i], fo, fu);
+            mma(Z[i], fv, fu);
           }
         }
       }
@@ -1085,43 +1091,59 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
     for (int m = 1; m < 64; m *= 2) dot += __shfl_xor(dot, m, 64);
     if (lane == 0) inner[wave] = dot;
     __syncthreads();  // the staged columns have been used
+    float N[PT][4];  // running sums of N along the rows of a tile
     if (pairs) {
-      float carry[4] = {0.f, 0.f, 0.f, 0.f};  // N's row sums over the tiles before
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int i = 0; i < PT; ++i) {
+        const int m = ppart + PW * i;
         f32x4 qk = zero4(), kk = zero4();
-        if (m <= wave) {
+        if (m <= prow) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const auto B = load_row<UK, kIn>(Ks, 16 * m + n, 32 * b + 8 * j, kRows);
-            mma(qk, load_row<UK, kIn>(Qs, 16 * wave + n, 32 * b + 8 * j, kRows), B);
-            mma(kk, load_row<UK, kIn>(Ks, 16 * wave + n, 32 * b + 8 * j, kRows), B);
+            mma(qk, load_row<UK, kIn>(Qs, 16 * prow + n, 32 * b + 8 * j, kRows), B);
+            mma(kk, load_row<UK, kIn>(Ks, 16 * prow + n, 32 * b + 8 * j, kRows), B);
           }
         }
-        float below = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * wave + 4 * j + r, c = 16 * m + n;
+          const int row = 16 * prow + 4 * j + r, c = 16 * m + n;
           const float D = c <= row ? exp_of(Gd[row] - Gd[c]) : 0.f;
-          const float x = c <= row ? p.scale * D * X[m][r] : 0.f, z = c < row ? -D * Z[m][r] : 0.f;
+          const float x = c <= row ? p.scale * D * X[i][r] : 0.f, z = c < row ? -D * Z[i][r] : 0.f;
           store_parts1<GP>(Xs + row * LDT + c, C * LDT, x);
           if (c <= row) {
             store_parts1<GP>(Zs + row * LDT + c, C * LDT, z);
             store_parts1<GP>(Zs + c * LDT + row, C * LDT, z);
           }
-          // running sum of N along the row; a pair (row, c) lies across t = c + 1 and on
           float sum = c < row ? x * qk[r] + z * kk[r] : 0.f;
           sum += dpp<0x111>(sum);  // row_shr: from the lanes before in the group, zero past its start
           sum += dpp<0x112>(sum);
           sum += dpp<0x114>(sum);
           sum += dpp<0x118>(sum);
-          sum += carry[r];
-          carry[r] = __shfl(sum, lane | 15, 64);
-          if (c < row) below += sum;
+          N[i][r] = sum;
+          if (n == 15) rowsum[m][row] = sum;
+        }
+      }
+    }
+    __syncthreads();
+    if (pairs) {
+      // a pair (row, c) lies across t = c + 1 and on, up to t = row
+#pragma unroll
+      for (int i = 0; i < PT; ++i) {
+        const int m = ppart + PW * i;
+        float below = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * prow + 4 * j + r;
+          float sum = N[i][r];
+#pragma unroll
+          for (int k = 0; k < MT; ++k)
+            if (k < m) sum += rowsum[k][row];
+          if (16 * m + n < row) below += sum;
         }
         below += __shfl_xor(below, 16, 64);
         below += __shfl_xor(below, 32, 64);
-        if (j == 0) across[wave][16 * m + n] = below;
+        if (j == 0) across[prow][16 * m + n] = below;
       }
     }
     __syncthreads();
