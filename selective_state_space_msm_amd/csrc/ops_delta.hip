@@ -63,24 +63,25 @@ __device__ __forceinline__ float exp_of(double x) { return exp2_fast((float)(x *
 
 // ---- prep ----------------------------------------------------------------------------------
 
-// Inverse of the unit lower triangular I + Ms (C x C in LDS, entries below the diagonal) into
-// Ti.  Wavefront w inverts diagonal block w of 16 by forward substitution, a column per lane;
+// Inverse of the unit lower triangular I + Ms diag(beta) (Ms C x C in LDS, entries below the
+// diagonal) into Ti.  Wavefront w inverts diagonal block w of 16 by forward substitution, a column per lane;
 // block column j of the inverse then follows downwards, T_ij = -T_ii sum_k M_ik T_kj, its blocks
 // staying in wavefront j's registers as right factors.  Substitution in blocks keeps the error
 // of a triangular solve; products of powers of M would not.
 constexpr int LDM = C + 4;
-__device__ __forceinline__ void invert(const MSM_LDS float* Ms, MSM_LDS float* Ti, int wave, int lane) {
+__device__ __forceinline__ void invert(const MSM_LDS float* Ms, const MSM_LDS float* beta, MSM_LDS float* Ti, int wave, int lane) {
   constexpr int B16 = C / 16;
   const int n = lane & 15, j = lane >> 4;
   if (wave < B16) {
-    float x[16];
+    float x[16], bx[16];
     const MSM_LDS float* M = Ms + (16 * wave) * LDM + 16 * wave;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == n ? 1.f : 0.f;
 #pragma unroll
-      for (int k = 0; k < i; ++k) s = fmaf(-M[i * LDM + k], x[k], s);
+      for (int k = 0; k < i; ++k) s = fmaf(-M[i * LDM + k], bx[k], s);
       x[i] = s;
+      bx[i] = s * beta[16 * wave + i];
     }
     if (j == 0)
 #pragma unroll
@@ -88,9 +89,10 @@ __device__ __forceinline__ void invert(const MSM_LDS float* Ms, MSM_LDS float* T
   }
   __syncthreads();
   if (wave < B16) {
-    f32x4 t[B16];
+    f32x4 t, bt[B16];  // a block of the inverse, and those above it times beta
 #pragma unroll
-    for (int r = 0; r < 4; ++r) t[0][r] = Ti[(16 * wave + 4 * j + r) * LDM + 16 * wave + n];
+    for (int r = 0; r < 4; ++r)
+      bt[0][r] = Ti[(16 * wave + 4 * j + r) * LDM + 16 * wave + n] * beta[16 * wave + 4 * j + r];
 #pragma unroll
     for (int d = 1; d < B16; ++d) {
       const int i = wave + d;
@@ -100,14 +102,17 @@ __device__ __forceinline__ void invert(const MSM_LDS float* Ms, MSM_LDS float* T
         for (int e = 0; e < d; ++e) {
           const f32x4 a = *(const MSM_LDS f32x4*)(Ms + (16 * i + n) * LDM + 16 * (wave + e) + 4 * j);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], t[e][r], acc, 0, 0, 0);
+          for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], bt[e][r], acc, 0, 0, 0);
         }
         const f32x4 a = *(const MSM_LDS f32x4*)(Ti + (16 * i + n) * LDM + 16 * i + 4 * j);
-        t[d] = zero4();
+        t = zero4();
 #pragma unroll
-        for (int r = 0; r < 4; ++r) t[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(-a[r], acc[r], t[d], 0, 0, 0);
+        for (int r = 0; r < 4; ++r) t = __builtin_amdgcn_mfma_f32_16x16x4f32(-a[r], acc[r], t, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) Ti[(16 * i + 4 * j + r) * LDM + 16 * wave + n] = t[d][r];
+        for (int r = 0; r < 4; ++r) {
+          Ti[(16 * i + 4 * j + r) * LDM + 16 * wave + n] = t[r];
+          bt[d][r] = t[r] * beta[16 * i + 4 * j + r];
+        }
       }
     }
   }
@@ -161,17 +166,30 @@ __device__ __forceinline__ void stage_rows(lds_parts lds, uint16_t* ws, __amdgpu
   }
 }
 
+// A chunk matrix from LDS rows of LDM floats into its blocks, 16 bytes a plane and thread.
+__device__ __forceinline__ void write_tri(uint16_t* to, const MSM_LDS float* from, int tid) {
+  for (int u = tid; u < C * C / 8; u += 256) {
+    const int row = u / (C / 8), c = (u % (C / 8)) * 8;
+    if (c / 32 > row / 32) continue;
+    const f32x4 a = *(const MSM_LDS f32x4*)(from + row * LDM + c), b = *(const MSM_LDS f32x4*)(from + row * LDM + c + 4);
+    store_parts(to + TriM::at(row, c), TriM::kPlane, split<TP>(a, b));
+  }
+}
+
+// Bound by the latency of its steps (load, Gram products, inverse, store), so the LDS is kept small
+// for three workgroups a CU: the inverse and the outgoing matrices take the place of the keys and
+// queries once the Gram products are done.
 template <bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds_k[kIn * kRows];
-  __shared__ __attribute__((aligned(16))) uint16_t lds_q[kIn * kRows];
+  constexpr int kMat = C * LDM * 4, kKeys = 2 * kIn * kRows * 2, kMats = 2 * kMat;
+  __shared__ __attribute__((aligned(16))) char lds_kq[kKeys > kMats ? kKeys : kMats];
   __shared__ __attribute__((aligned(16))) float lds_m[C * LDM];
-  __shared__ __attribute__((aligned(16))) float lds_t[C * LDM];
   __shared__ double Gd[C];
   __shared__ float bt[C];
-  const lds_parts Ks = (lds_parts)lds_k, Qs = (lds_parts)lds_q;
+  const lds_parts Ks = (lds_parts)lds_kq, Qs = Ks + kIn * kRows;
   MSM_LDS float* const Ms = (MSM_LDS float*)lds_m;
-  MSM_LDS float* const Ti = (MSM_LDS float*)lds_t;
+  MSM_LDS float* const Ti = (MSM_LDS float*)lds_kq;
+  MSM_LDS float* const Pl = Ti + C * LDM;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
   const int64_t slot = blockIdx.x, h = blockIdx.y;
   const ChunkRows ch = chunk_rows<C>(p, slot);
@@ -180,19 +198,19 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   const int64_t sh = slot * p.H + h, hk = uniform((int)((uint32_t)h / group));
   const uint32_t stride = (uint32_t)(p.Hk * p.K * IO::es);
   uint16_t* ws = p.kq_direct || h != hk * group ? nullptr : static_cast<uint16_t*>(p.kq) + (slot * p.Hk + hk) * 2 * kIn * kRows;
+  float gl = 0.f, b = 0.f;
+  if (wave == 0 && lane < ch.n) {
+    gl = p.g[(ch.row0 + lane) * p.H + h];
+    b = p.beta[(ch.row0 + lane) * p.H + h];
+  }
   stage_rows<256>(Ks, ws, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
   stage_rows<256>(Qs, ws ? ws + kIn * kRows : nullptr, head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride,
                   (int)p.K, p.vec_k, tid);
   if (wave == 0) {
-    // running sum of the log decay in fp64: its differences keep fp32 accuracy
-    const bool on = lane < ch.n;
-    const int64_t i = (ch.row0 + lane) * p.H + h;
-    float gl = on ? p.g[i] : 0.f;
-    // exp(-1e4) is 0 already; below it the sum would lose the decays that follow (a decay of
-    // minus infinity, or of the lowest float, resets the state)
-    gl = gl < -1e4f ? -1e4f : gl;
-    double G = (double)gl;
-    const float b = on ? p.beta[i] : 0.f;
+    // running sum of the log decay in fp64: its differences keep fp32 accuracy.  exp(-1e4) is 0
+    // already; below it the sum would lose the decays that follow (a decay of minus infinity, or
+    // of the lowest float, resets the state)
+    double G = gl < -1e4f ? -1e4 : (double)gl;
 #pragma unroll
     for (int m = 1; m < C; m *= 2) {
       const double up = __shfl_up(G, m, 64);
@@ -210,44 +228,42 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
     }
   }
   __syncthreads();
-  // Gram tiles on and below the diagonal; 16 x 16, one wavefront each
-  uint16_t* Pg = static_cast<uint16_t*>(p.P) + sh * kTri;
-  uint16_t* Mg = BWD ? static_cast<uint16_t*>(p.M) + sh * kTri : nullptr;
-  for (int t = wave; t < (C / 16) * (C / 16); t += 4) {
-    const int mt = t / (C / 16), nt = t % (C / 16);
-    if (nt / 2 > mt / 2) continue;  // no block is kept there
-    f32x4 kk = zero4(), qk = zero4();
+  // Gram tiles of the kept blocks; 16 x 16, a wavefront's share of them in its registers
+  constexpr int B16 = C / 16, kTiles = B16 * B16 / 4;
+  f32x4 kk[kTiles], qk[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) {
+    const int t = 4 * i + wave, mt = t / B16, nt = t % B16;
+    kk[i] = qk[i] = zero4();
     if (nt <= mt) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const auto B = load_row<UK, kIn>(Ks, 16 * nt + n, 32 * b + 8 * j, kRows);
-        mma(kk, load_row<UK, kIn>(Ks, 16 * mt + n, 32 * b + 8 * j, kRows), B);
-        mma(qk, load_row<UK, kIn>(Qs, 16 * mt + n, 32 * b + 8 * j, kRows), B);
+        mma(kk[i], load_row<UK, kIn>(Ks, 16 * mt + n, 32 * b + 8 * j, kRows), B);
+        mma(qk[i], load_row<UK, kIn>(Qs, 16 * mt + n, 32 * b + 8 * j, kRows), B);
       }
     }
+  }
+  __syncthreads();  // keys and queries have been read
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) {
+    const int t = 4 * i + wave, mt = t / B16, nt = t % B16;
+    if (nt / 2 > mt / 2) continue;  // no block is kept there
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * mt + 4 * j + r, col = 16 * nt + n;
       const float D = col <= row ? exp_of(Gd[row] - Gd[col]) : 0.f;
-      const float m = col < row ? D * kk[r] : 0.f;
-      Ms[row * LDM + col] = m * bt[col];
-      store_parts1<TP>(Pg + TriM::at(row, col), TriM::kPlane, col <= row ? p.scale * D * qk[r] : 0.f);
-      if (BWD) store_parts1<TP>(Mg + TriM::at(row, col), TriM::kPlane, m);
+      const float m = col < row ? D * kk[i][r] : 0.f;
+      Ms[row * LDM + col] = m;
+      Pl[row * LDM + col] = col <= row ? p.scale * D * qk[i][r] : 0.f;
+      if (nt > mt) Ti[row * LDM + col] = 0.f;  // the inverse leaves blocks above the diagonal alone
     }
   }
   __syncthreads();
-  invert(Ms, Ti, wave, lane);
-  uint16_t* Tg = static_cast<uint16_t*>(p.T) + sh * kTri;
-  for (int u = tid; u < C * C / 8; u += 256) {
-    const int row = u / (C / 8), c = (u % (C / 8)) * 8;
-    if (c / 32 > row / 32) continue;
-    f32x4 a = zero4(), b = zero4();
-    if (c / 16 <= row / 16) {  // blocks above the diagonal were not written
-      a = *(const MSM_LDS f32x4*)(Ti + row * LDM + c);
-      b = *(const MSM_LDS f32x4*)(Ti + row * LDM + c + 4);
-    }
-    store_parts(Tg + TriM::at(row, c), TriM::kPlane, split<TP>(a, b));
-  }
+  write_tri(static_cast<uint16_t*>(p.P) + sh * kTri, Pl, tid);
+  if (BWD) write_tri(static_cast<uint16_t*>(p.M) + sh * kTri, Ms, tid);
+  invert(Ms, (const MSM_LDS float*)bt, Ti, wave, lane);
+  write_tri(static_cast<uint16_t*>(p.T) + sh * kTri, Ti, tid);
 }
 
 // ---- scan ----------------------------------------------------------------------------------
