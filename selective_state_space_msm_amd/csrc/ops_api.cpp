@@ -15,6 +15,7 @@ using msm::DeltaArgs;
 constexpr int64_t kLim = (int64_t)1 << 40;
 constexpr int64_t kGridX = ((int64_t)1 << 31) - 1;
 constexpr int64_t kGridY = 65535;
+constexpr int64_t kSegmentLeast = 8;   // chunks of a segment at least
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -45,9 +46,21 @@ bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 // ---- gated delta rule ----
 
 struct DeltaShape {
-  int64_t tokens, nseq, L, NT, nslots, Hk, H, K, V, VP;
-  int KP, C;
+  int64_t tokens, nseq, L, NT, nslots, nsegs, Hk, H, K, V, VP;
+  int KP, C, seg_len;
 };
+
+// Chunks of a segment, 0 for none.  Segments cost 2.4 times a walk's work, so they pay where whole
+// sequences would leave two thirds of the 256 CUs without a workgroup (Bt = 1, L = 65536, H = 16,
+// V = 128: 32 workgroups, 3.3 ms whole and 1.1 ms in segments); there are enough then for one a CU.
+// Packed sequences are seldom alike and the longest decides, so there half of the CUs is the bound.
+int delta_segment(const DeltaShape& s, bool packed) {
+  const int64_t blocks = s.H * ceil_div(s.VP, 64);  // workgroups of a sequence
+  if (s.nseq * blocks > (packed ? 128 : 80)) return 0;
+  int64_t len = ceil_div(s.nslots * blocks, 256);
+  if (len < kSegmentLeast) len = kSegmentLeast;
+  return s.nslots >= 3 * len * (packed ? 1 : s.nseq) ? (int)len : 0;
+}
 
 // Sizes of a call; packed: Bt sequences in L rows together.
 msm_status delta_shape(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K, int64_t V,
@@ -70,6 +83,9 @@ msm_status delta_shape(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K, 
   s->NT = packed ? 1 : ceil_div(L, s->C);
   s->nslots = packed ? L / s->C + Bt : Bt * s->NT;
   if (s->nslots > kGridX) return MSM_ERR_INVALID_ARG;
+  s->seg_len = delta_segment(*s, packed);
+  s->nsegs = s->seg_len == 0 ? 0 : (packed ? s->nslots / s->seg_len + Bt : Bt * s->NT / s->seg_len + Bt);
+  if (s->nsegs * H > kGridX) return MSM_ERR_INVALID_ARG;
   // the rows of a chunk are addressed with 32-bit byte offsets
   const int64_t es = io == MSM_BF16 ? 2 : 4, widest = Hk * K > H * V ? Hk * K : H * V;
   if (s->C * widest * es >= ((int64_t)1 << 31)) return MSM_ERR_UNSUPPORTED;
@@ -77,7 +93,7 @@ msm_status delta_shape(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K, 
 }
 
 struct DeltaLayout {
-  size_t vec, T, P, kq, M, S, dS, E, dV, pred, dots, total;
+  size_t vec, T, P, kq, segS, segF, M, S, dS, E, dV, pred, dots, total;
 };
 
 DeltaLayout delta_layout(const DeltaShape& s, msm_dtype io, bool bwd) {
@@ -95,6 +111,8 @@ DeltaLayout delta_layout(const DeltaShape& s, msm_dtype io, bool bwd) {
   l.T = take(mat);
   l.P = take(mat);
   l.kq = take((size_t)(s.nslots * s.Hk) * 2 * msm::delta_in_planes(io == MSM_BF16) * C * KP * 2);
+  l.segS = take((size_t)(s.nsegs * s.H) * KP * VP * 4);
+  l.segF = take((size_t)(s.nsegs * s.H) * KP * KP * 4);
   if (bwd) {
     l.M = take(mat);
     l.S = take(n * KP * VP * 4);
@@ -124,6 +142,10 @@ DeltaArgs delta_args(const DeltaShape& s, const DeltaLayout& l, msm_dtype io, co
   a.T = ws + l.T;
   a.P = ws + l.P;
   a.kq = ws + l.kq;
+  a.segS = reinterpret_cast<float*>(ws + l.segS);
+  a.segF = reinterpret_cast<float*>(ws + l.segF);
+  a.nsegs = s.nsegs;
+  a.seg_len = s.seg_len;
   a.M = ws + l.M;
   a.S = reinterpret_cast<float*>(ws + l.S);
   a.dS = reinterpret_cast<float*>(ws + l.dS);

@@ -520,7 +520,8 @@ __device__ __forceinline__ void interleave() {
 // This wavefront's place in a walk.
 struct Walk {
   int tid, wave, lane, n, j, vb, col, len, chunks;
-  bool on;
+  bool on, last;  // columns there are; the sequence's last segment
+  int64_t seg;    // segment and head: place of a segment's states
   int64_t s, h, hk, row0, slot0;
   uint32_t vstride, wstride, vat, wat, sat, sbytes;
   __device__ __forceinline__ Walk(const DeltaArgs& p) {
@@ -531,17 +532,19 @@ struct Walk {
     j = lane >> 4;
     const uint32_t H = (uint32_t)p.H, group = H / (uint32_t)p.Hk;  // 32-bit: 64-bit division leaves the scalar unit
     const int si = uniform((int)(blockIdx.x / H)), hi = uniform((int)(blockIdx.x - (uint32_t)si * H));
-    s = si;
+    seg = blockIdx.x;
     h = hi;
     hk = uniform((int)((uint32_t)hi / group));
     vb = blockIdx.y * kWavesScan + wave;
     col = vb * 16 + n;
     on = vb * 16 < p.VP;
-    const SeqRows seq = seq_rows<C>(p, s);
-    len = (int)seq.len;
+    const SegRows r = seg_rows<C>(p, si);
+    s = r.s;
+    len = (int)r.len;
     chunks = (len + C - 1) / C;
-    row0 = seq.row0;
-    slot0 = seq.slot0;
+    last = r.last;
+    row0 = r.row0;
+    slot0 = r.slot0;
     vstride = (uint32_t)(p.H * p.V * IO::es);
     wstride = (uint32_t)(p.VP * 4);
     vat = col < p.V ? 8 * j * vstride + col * IO::es : kOutside;  // v, o, do, dv
@@ -652,8 +655,12 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
   auto& l0 = (MSM_LDS ScanChunk<BWD>&)lds0;
   auto& l1 = (MSM_LDS std::conditional_t<kTwo, ScanChunk<BWD>, Nothing>&)lds1;
   const Walk w(p);
+  if (w.s < 0) return;  // no segment here
   Cols<NB> S = zero_cols<NB>();
-  if (p.S0) S = load_cols<NB>(w.state(p.S0, p), w.sat, (uint32_t)(p.V * 4));
+  if (p.seg_len > 0)
+    S = load_cols<NB>(make_rsrc_u32(p.segS + w.seg * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride);
+  else if (p.S0)
+    S = load_cols<NB>(w.state(p.S0, p), w.sat, (uint32_t)(p.V * 4));
   Keys keys(p, w.row0, w.slot0, w.h, w.hk, w.tid);
   Stream st = slot_stream(p.T, w.slot0, p.H, w.h, kTri * 2), sp = slot_stream(p.P, w.slot0, p.H, w.h, kTri * 2);
   Stream sv = head_stream(p.v, w.row0, p.H, w.h, p.V), sd = head_stream(p.do_, w.row0, p.H, w.h, p.V);
@@ -716,7 +723,159 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
       done();
     }
   }
-  if (w.on && p.last_S) store_cols<NB>(w.state(p.last_S, p), w.sat, (uint32_t)(p.V * 4), S);
+  if (w.on && w.last && p.last_S) store_cols<NB>(w.state(p.last_S, p), w.sat, (uint32_t)(p.V * 4), S);
+}
+
+// ---- segments ------------------------------------------------------------------------------
+//
+// A walk is sequential in the chunks, so few heads and sequences leave most of the GPU idle.  Then
+// sequences are cut into segments of seg_len chunks.  A segment maps the state affinely, S -> F S + G:
+// one walk over all segments at once finds G (from a zero state) and F (from the identity, with V
+// zero, as K more columns), a short second kernel runs through the segments' maps, and the walk
+// proper starts every segment from its state.  That is about 2.4 times the work.
+
+struct StateChunk {
+  uint16_t k[kIn * kRows];
+  float ev[256];
+  uint16_t t[tri_lds(TP)];
+};
+
+__global__ __launch_bounds__(64 * kWavesScan) void segment_kernel(const DeltaArgs p) {
+  __shared__ __attribute__((aligned(16))) StateChunk lds0;
+  __shared__ __attribute__((aligned(16))) StateChunk lds1;
+  auto& l0 = (MSM_LDS StateChunk&)lds0;
+  auto& l1 = (MSM_LDS StateChunk&)lds1;
+  const Walk w(p);
+  if (w.s < 0 || w.last) return;  // nobody starts from the last segment's state
+  const int lane = w.lane, j = w.j;
+  const int unit = w.col - (int)p.VP;  // column of the identity
+  Cols<NB> S;
+  each<NB>([&](int b, int t, int r, int row) { S.t[b][t][r] = row + 8 * j == unit ? 1.f : 0.f; });
+  Keys keys(p, w.row0, w.slot0, w.h, w.hk, w.tid);
+  Stream st = slot_stream(p.T, w.slot0, p.H, w.h, kTri * 2), sv = head_stream(p.v, w.row0, p.H, w.h, p.V);
+  RawCols v;
+  const auto fetch = [&](MSM_LDS StateChunk& l, int rows) {
+    const u32x4 rk = keys.k.words(rows);
+#pragma unroll
+    for (int x = 0; x < kIn * kPasses; ++x)
+      load_lds(rk, l.k + x / kPasses * kRows + (x % kPasses * kWavesScan + w.wave) * 512,
+               keys.at[x % kPasses] + x / kPasses * kRows * 2);
+    load_lds(keys.ev.whole(rows, 3 * C * 4), (MSM_LDS void*)l.ev, lane * 16);
+    load_tri<TP>(l.t, st, rows, w.wave, lane);
+    v.fetch(sv.rsrc(rows), w.vat, w.vstride);
+    keys.next(1);
+    st.next(1);
+    sv.next(1);
+  };
+  const auto step = [&](MSM_LDS StateChunk& l, MSM_LDS StateChunk& next, int c) {
+    sync_loads();
+    Cols<CB> R = v.widen(), KS = zero_cols<CB>(), U = zero_cols<CB>();
+    fetch(next, w.rows(c + 1));
+    const MSM_LDS float* eG = l.ev + 8 * j;
+    const MSM_LDS float* eK = l.ev + C + 8 * j;
+    const MSM_LDS float* bt = l.ev + 2 * C + 8 * j;
+    RowTiles fk[2];
+    TriTiles<TP, false> ft;
+    fk[0].load(l.k, 0, lane, j);
+    Part<TP> sb = split<TP>(S.t[0][0], S.t[0][1]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (b + 1 < NB)
+        fk[(b + 1) & 1].load(l.k, b + 1, lane, j);
+      else
+        ft.load(l.t, lane, j);
+      hold_lds();
+      mma_tiles(tiles(KS), fk[b & 1].a, sb);
+      if (b + 1 < NB) sb = split<TP>(S.t[(b + 1) % NB][0], S.t[(b + 1) % NB][1]);
+      interleave<2 * CB * TP, 3>();
+    }
+    each<CB>([&](int b, int t, int r, int row) { R.t[b][t][r] = fmaf(-eG[row], KS.t[b][t][r], R.t[b][t][r]); });
+    Part<TP> B[CB];
+    split_all(B, R);
+    ColTiles fc[2];
+    fc[0].load(l.k, 0, lane, j);
+    hold_lds();
+    ft.mma(U, B);
+    each<CB>([&](int b, int t, int r, int row) { U.t[b][t][r] *= bt[row] * eK[row]; });
+    split_all(B, U);
+    const float last = l.ev[C - 1];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (b + 1 < NB) fc[(b + 1) & 1].load(l.k, b + 1, lane, j);
+      hold_lds();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) S.t[b][t] *= last;
+      fc[b & 1].mma(S.t[b], B);
+    }
+  };
+  fetch(l0, w.rows(0));
+  int c = 0;
+  for (; c + 1 < w.chunks; c += 2) {
+    step(l0, l1, c);
+    step(l1, l0, c + 1);
+  }
+  if (c < w.chunks) step(l0, l1, c);
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  if (w.on)
+    store_cols<NB>(make_rsrc_u32(p.segS + w.seg * KP * p.VP, (uint32_t)(KP * p.VP * 4)), w.wat, w.wstride, S);
+  else if (unit < KP)
+    store_cols<NB>(make_rsrc_u32(p.segF + w.seg * KP * KP, (uint32_t)(KP * KP * 4)), (8 * j * KP + unit) * 4, KP * 4, S);
+}
+
+// Runs through a sequence's segments: every segment's G makes room for the state it starts from.
+// A workgroup has 16 columns, a wavefront 32 rows of them; the state passes between them through
+// LDS, and the next segment's map is fetched while the present one is applied.
+__global__ __launch_bounds__(64 * NB) void join_kernel(const DeltaArgs p) {
+  constexpr int LDJ = 17;
+  __shared__ float state[2][KP * LDJ];
+  const int rb = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 15, j = lane >> 4;
+  const uint32_t H = (uint32_t)p.H;
+  const int64_t s = uniform((int)(blockIdx.x / H)), h = uniform((int)(blockIdx.x % H));
+  const int col = blockIdx.y * 16 + n, row0 = 32 * rb + 8 * j;
+  const SeqSegs q = seq_segs<C>(p, s);
+  Cols<1> S = zero_cols<1>();
+  if (p.S0)
+    S = load_cols<1>(make_rsrc_u32(p.S0 + (s * p.H + h) * p.K * p.V, (uint32_t)(p.K * p.V * 4)),
+                     col < p.V ? (row0 * (uint32_t)p.V + col) * 4 : kOutside, (uint32_t)(p.V * 4));
+  const uint32_t at = (uint32_t)(row0 * p.VP + col) * 4, stride = (uint32_t)(p.VP * 4);
+  f32x4 F[NB][2][2];
+  const auto fetch = [&](int64_t g) {
+    const auto rf = make_rsrc_u32(p.segF + ((q.first + g) * p.H + h) * KP * KP, g + 1 < q.count ? (uint32_t)(KP * KP * 4) : 0u);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t i = (uint32_t)(perm_row(rb, t, lane) * KP + 32 * b + 8 * j) * 4;
+        F[b][t][0] = bload4(rf, i);
+        F[b][t][1] = bload4(rf, i + 16);
+      }
+  };
+  fetch(0);
+  for (int64_t g = 0; g < q.count; ++g) {
+    const auto rs = make_rsrc_u32(p.segS + ((q.first + g) * p.H + h) * KP * p.VP, (uint32_t)(KP * p.VP * 4));
+    const bool more = g + 1 < q.count;  // nobody starts from the last segment's end
+    Cols<1> next = zero_cols<1>();
+    if (more) next = load_cols<1>(rs, at, stride);
+    store_cols<1>(rs, at, stride, S);
+    if (!more) break;
+    float* lds = state[g & 1];
+    each<1>([&](int, int t, int r, int row) { lds[(row0 + row) * LDJ + n] = S.t[0][t][r]; });
+    Part<TP> f[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) f[b][t] = split<TP>(F[b][t][0], F[b][t][1]);
+    fetch(g + 1);
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      f32x4 x[2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i / 4][i % 4] = lds[(32 * b + 8 * j + i) * LDJ + n];
+      mma_tiles(next.t[0], f[b], split<TP>(x[0], x[1]));
+    }
+    S = next;
+  }
 }
 
 // ---- rev -----------------------------------------------------------------------------------
@@ -1233,30 +1392,44 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   }
 }
 
-dim3 scan_grid(const DeltaArgs& a) {
-  return dim3((unsigned)(a.nseq * a.H), (unsigned)((a.VP / 16 + kWavesScan - 1) / kWavesScan));
+dim3 scan_grid(int64_t walks, int64_t H, int64_t columns) {
+  return dim3((unsigned)(walks * H), (unsigned)((columns / 16 + kWavesScan - 1) / kWavesScan));
+}
+
+// The forward walk, in segments where the call is laid out for them.
+template <bool BWD>
+hipError_t walk(const DeltaArgs& a, hipStream_t s) {
+  const dim3 block(64 * kWavesScan);
+  if (a.seg_len > 0) {
+    hipLaunchKernelGGL(segment_kernel, scan_grid(a.nsegs, a.H, a.VP + KP), block, 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(a.nseq * a.H), (unsigned)(a.VP / 16)), dim3(64 * NB), 0, s, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(scan_kernel<BWD>, scan_grid(a.seg_len > 0 ? a.nsegs : a.nseq, a.H, a.VP), block, 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t MSM_DELTA_NAME(fwd, MSM_IO_BF16, MSM_KP)(const DeltaArgs& a, hipStream_t s) {
-  const dim3 chunks((unsigned)a.nslots, (unsigned)a.H);
-  hipLaunchKernelGGL(prep_kernel<false>, chunks, dim3(256), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(scan_kernel<false>, scan_grid(a), dim3(64 * kWavesScan), 0, s, a);
-  return hipGetLastError();
+  hipLaunchKernelGGL(prep_kernel<false>, dim3((unsigned)a.nslots, (unsigned)a.H), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? walk<false>(a, s) : e;
 }
 
 hipError_t MSM_DELTA_NAME(bwd, MSM_IO_BF16, MSM_KP)(const DeltaArgs& a, hipStream_t s) {
-  const dim3 chunks((unsigned)a.nslots, (unsigned)a.H);
-  hipLaunchKernelGGL(prep_kernel<true>, chunks, dim3(256), 0, s, a);
+  hipLaunchKernelGGL(prep_kernel<true>, dim3((unsigned)a.nslots, (unsigned)a.H), dim3(256), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(scan_kernel<true>, scan_grid(a), dim3(64 * kWavesScan), 0, s, a);
-  e = hipGetLastError();
+  e = walk<true>(a, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rev_kernel<2 * sizeof(KeyRows) + sizeof(RevTri) <= kLdsMost>, scan_grid(a), dim3(64 * kWavesScan), 0, s, a);
+  DeltaArgs whole = a;  // the walk back is not cut
+  whole.seg_len = 0;
+  hipLaunchKernelGGL(rev_kernel<2 * sizeof(KeyRows) + sizeof(RevTri) <= kLdsMost>, scan_grid(a.nseq, a.H, a.VP),
+                     dim3(64 * kWavesScan), 0, s, whole);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(grad_kernel, dim3((unsigned)a.nslots, (unsigned)a.Hk), dim3(64 * kWavesGrad), 0, s, a);

@@ -248,6 +248,49 @@ __device__ __forceinline__ ChunkRows chunk_rows(const DeltaArgs& p, int64_t slot
   return ChunkRows{r.row0 + at, (int)(left < C ? left : C)};
 }
 
+// Segments of a sequence: seg_len chunks each, numbered over all sequences as chunks are, sequence s
+// from floor(slot0 / seg_len) + s on.  Without segments (seg_len 0) a sequence is one.
+struct SeqSegs {
+  int64_t first, count;
+};
+template <int C>
+__device__ __forceinline__ SeqSegs seq_segs(const DeltaArgs& p, int64_t s) {
+  if (p.seg_len == 0) return SeqSegs{s, 1};
+  const SeqRows r = seq_rows<C>(p, s);
+  const uint32_t M = (uint32_t)p.seg_len, chunks = (uint32_t)((r.len + C - 1) / C);
+  const int count = uniform((int)((chunks + M - 1) / M));
+  const int first = uniform((int)((uint32_t)r.slot0 / M));
+  return SeqSegs{first + s, count < 1 ? 1 : count};
+}
+
+// Rows and first slot of a segment; s < 0 where there is none.
+struct SegRows {
+  int64_t s, row0, len, slot0;
+  bool last;
+};
+template <int C>
+__device__ __forceinline__ SegRows seg_rows(const DeltaArgs& p, int seg) {
+  int64_t s = seg, g = 0;
+  if (p.seg_len > 0) {
+    int lo = 0, hi = (int)p.nseq;  // the last sequence whose first segment is at or before this one
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (seq_segs<C>(p, mid).first <= seg)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    s = uniform(lo);
+  }
+  const SeqSegs q = seq_segs<C>(p, s);
+  const SeqRows r = seq_rows<C>(p, s);
+  g = seg - q.first;
+  if (g < 0 || g >= q.count) return SegRows{-1, 0, 0, 0, false};
+  if (p.seg_len == 0) return SegRows{s, r.row0, r.len, r.slot0, true};
+  const int64_t rows = (int64_t)p.seg_len * C, left = r.len - g * rows;
+  return SegRows{s, r.row0 + g * rows, left < rows ? left : rows, r.slot0 + g * p.seg_len, g + 1 == q.count};
+}
+
 // ---- memory ----
 constexpr uint32_t kOutside = 0x80000000u;  // an offset past any resource: reads zero, writes nothing
 

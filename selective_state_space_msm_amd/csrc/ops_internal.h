@@ -50,10 +50,14 @@ struct DeltaArgs {
   float* dV;            // [sh][C][VP] gradient of v                    (backward)
   float* pred;          // [sh][C][VP] what the state before the chunk predicts (backward)
   float* dots;          // [sh][VP / 16][4 C] row sums over 16 columns (backward)
+  float* segS;          // [segment][H][KP][VP] a segment's end state from zero, then its start
+  float* segF;          // [segment][H][KP][KP] its map of the state
   int64_t tokens;       // rows of the token arrays
   int64_t nseq, L;      // uniform: nseq sequences of L tokens
   int64_t NT;           // uniform: chunks per sequence
   int64_t nslots;
+  int64_t nsegs;        // segments at most
+  int32_t seg_len;      // chunks of a segment, 0: sequences are walked whole
   int64_t Hk, H, K, V, VP;
   float scale;
   int32_t vec_k;        // rows of q and k can be read 16 bytes at a time

@@ -327,3 +327,17 @@ def test_prefill_then_steps():
     ref = want(d, 64 ** -0.5, False)
     close(torch.stack(o, 1), ref["o"].reshape(2, 80, 4, 64)[:, 70:], "o")
     close(S, ref["S"], "S")
+
+
+# ---- sequences cut into segments ---------------------------------------------------------------
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,packed", [([2100], False), ([1600, 1600], False), ([1700, 0, 512, 1, 1900], True)])
+def test_segments(io, lens, packed):
+    """Few heads and long sequences: the walk is cut and joined."""
+    check(make(io, lens, 1, 2, 64, 40, seed=len(lens), packed=packed, g_scale=0.02))
+
+
+def test_segments_of_wide_heads():
+    check(make("bf16", [1800], 1, 1, 128, 80, seed=31, g_scale=0.01))
+    check(make("f32", [900], 1, 1, 200, 33, seed=32, g_scale=0.01))  # chunks of 32
