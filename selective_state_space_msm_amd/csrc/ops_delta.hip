@@ -166,13 +166,15 @@ __device__ __forceinline__ void stage_rows(lds_parts lds, uint16_t* ws, __amdgpu
   }
 }
 
-// A chunk matrix from LDS rows of LDM floats into its blocks, 16 bytes a plane and thread.
+// The first N parts of a chunk matrix from LDS rows of LDM floats into its blocks, 16 bytes a plane
+// and thread.
+template <int N>
 __device__ __forceinline__ void write_tri(uint16_t* to, const MSM_LDS float* from, int tid) {
   for (int u = tid; u < C * C / 8; u += 256) {
     const int row = u / (C / 8), c = (u % (C / 8)) * 8;
     if (c / 32 > row / 32) continue;
     const f32x4 a = *(const MSM_LDS f32x4*)(from + row * LDM + c), b = *(const MSM_LDS f32x4*)(from + row * LDM + c + 4);
-    store_parts(to + TriM::at(row, c), TriM::kPlane, split<TP>(a, b));
+    store_parts(to + TriM::at(row, c), TriM::kPlane, split<N>(a, b));
   }
 }
 
@@ -260,10 +262,10 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
     }
   }
   __syncthreads();
-  write_tri(static_cast<uint16_t*>(p.P) + sh * kTri, Pl, tid);
-  if (BWD) write_tri(static_cast<uint16_t*>(p.M) + sh * kTri, Ms, tid);
+  write_tri<BWD ? TP : kOutParts>(static_cast<uint16_t*>(p.P) + sh * kTri, Pl, tid);
+  if (BWD) write_tri<TP>(static_cast<uint16_t*>(p.M) + sh * kTri, Ms, tid);
   invert(Ms, (const MSM_LDS float*)bt, Ti, wave, lane);
-  write_tri(static_cast<uint16_t*>(p.T) + sh * kTri, Ti, tid);
+  write_tri<TP>(static_cast<uint16_t*>(p.T) + sh * kTri, Ti, tid);
 }
 
 // ---- scan ----------------------------------------------------------------------------------
