@@ -23,13 +23,18 @@
 // + <S1, dS1>, but its terms do not shrink with the decay and cancel: under strong decay it loses
 // two digits against this sum.)
 //
-// Four kernels, each built for one I/O type and padded key size (this file is compiled once
-// per pair):
-//   prep   one workgroup per chunk and head: decays, Gram matrices, the triangular inverse
-//   scan   one workgroup per sequence, head and 64 columns of V, chunk after chunk; S stays in
-//          registers, each wavefront owning all K rows of 16 columns
-//   rev    the same walk backwards for dS
-//   grad   one workgroup per chunk and key head: dQ, dK and the sums for dbeta and dg
+// The kernels, each built for one I/O type and padded key size (this file is compiled once per
+// pair):
+//   prep     one workgroup per chunk and head: decays, Gram matrices, the triangular inverse
+//   scan     one workgroup per sequence (or segment of one), head and 64 columns of V, chunk after
+//            chunk; the state stays in registers
+//   segment, join   the states that segments start from, where sequences are cut
+//   rev      the walk backwards for the adjoint of the state
+//   grad     one workgroup per chunk and key head: dQ, dK and the sums for dbeta and dg
+// The products run on the bf16 matrix unit over values cut into parts of 8 bits (ops_delta.hpp):
+// one part for a bf16 input, three for an fp32 value, which keeps its 24 bits, and two where the
+// result is rounded to bf16.  The card's fp32 matrix unit reaches 154 TFLOP/s, its bf16 unit 1240:
+// even the six products of three parts by three are faster there.
 #include <type_traits>
 
 #include "ops_delta.hpp"
@@ -180,7 +185,8 @@ __device__ __forceinline__ void write_tri(uint16_t* to, const MSM_LDS float* fro
 
 // Bound by the latency of its steps (load, Gram products, inverse, store), so the LDS is kept small
 // for three workgroups a CU: the inverse and the outgoing matrices take the place of the keys and
-// queries once the Gram products are done.
+// queries once the Gram products are done.  Bt=4 L=4096 H=32 K=128 bf16: 117 us, 262 MB written (the
+// chunk matrices in their parts); the same with 100 KB of LDS, one workgroup a CU: 170 us.
 template <bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   constexpr int kMat = C * LDM * 4, kKeys = 2 * kIn * kRows * 2, kMats = 2 * kMat;
@@ -649,6 +655,15 @@ __device__ __forceinline__ void scan_chunk(F fetch, const DeltaArgs& p, const Wa
   }
 }
 
+// A wavefront owns all rows of 16 columns of the state, 2 x NB tiles in its registers: the columns
+// are independent, so no state passes between wavefronts, and an accumulator's layout is that of a
+// right factor with its rows permuted, so a product's result is the next one's factor without a
+// trip through LDS.  Keys, queries and chunk matrices are left factors, shared by the four
+// wavefronts in LDS and loaded there a chunk ahead.  Sequential in the chunks, hence bound by a
+// chunk's chain of products (K S, T R, K^T U and the two of O) at one wavefront a SIMD: Bt=4 L=4096
+// H=32 K=V=128 bf16, 256 workgroups: 260-290 us for 64 chunks, 668 TFLOP/s of matrix products (54% of
+// what a large one reaches).  BWD stores what the backward needs and leaves O out: 295 us at
+// Bt=4 L=2048 H=16 fp32, where 128 workgroups leave half of the CUs idle.
 template <bool BWD>
 __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p) {
   constexpr bool kTwo = 2 * sizeof(ScanChunk<BWD>) <= kLdsMost;
@@ -734,7 +749,10 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
 // sequences are cut into segments of seg_len chunks.  A segment maps the state affinely, S -> F S + G:
 // one walk over all segments at once finds G (from a zero state) and F (from the identity, with V
 // zero, as K more columns), a short second kernel runs through the segments' maps, and the walk
-// proper starts every segment from its state.  That is about 2.4 times the work.
+// proper starts every segment from its state.  That is about 2.4 times the work, the segments' maps
+// at a higher rate than the walk's: Bt=1 L=65536 H=16 K=V=128 bf16 in 8 or 9 segments a head, 530 us
+// (940 TFLOP/s of matrix products, 76% of a large product's), 23 us, and 510 us for the walk, against
+// 3.3 ms for the walk of whole sequences.
 
 struct StateChunk {
   uint16_t k[kIn * kRows];
@@ -826,7 +844,8 @@ __global__ __launch_bounds__(64 * kWavesScan) void segment_kernel(const DeltaArg
 
 // Runs through a sequence's segments: every segment's G makes room for the state it starts from.
 // A workgroup has 16 columns, a wavefront 32 rows of them; the state passes between them through
-// LDS, and the next segment's map is fetched while the present one is applied.
+// LDS, and the next segment's map is fetched while the present one is applied.  Bound by the latency
+// of that fetch, 2.5 us a segment; one wavefront with all rows took 12 us.
 __global__ __launch_bounds__(64 * NB) void join_kernel(const DeltaArgs p) {
   constexpr int LDJ = 17;
   __shared__ float state[2][KP * LDJ];
@@ -988,8 +1007,11 @@ __device__ __forceinline__ void rev_chunk(FP p_used, FT tm_used, const DeltaArgs
   }
 }
 
-// The chunk matrices have one buffer each, filled again as soon as every wavefront has read it;
-// keys and queries have two where the LDS allows.
+// Split and layout as the scan's; per chunk it has six products where the scan has three (W from two,
+// dV, Y, dS0 from two) and three chunk matrices.  These have one buffer each in LDS, filled again as
+// soon as every wavefront has read it; keys and queries have two where the LDS allows.  Bound like the
+// scan: 325 us at Bt=4 L=2048 H=16 K=V=128 fp32 (128 workgroups), 490 us for 16384 packed tokens, H=16
+// bf16, the longest sequence's 72 chunks at 6.8 us.
 template <bool kTwo>
 __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p) {
   __shared__ __attribute__((aligned(16))) KeyRows lds0;
@@ -1091,6 +1113,14 @@ constexpr int VB = MSM_IO_BF16 ? 64 : 32;                                       
 constexpr int LDV = VB + 8, LDT = C + 8;
 constexpr int PW = kWavesGrad >= 2 * MT ? 2 : 1, PT = MT / PW;  // wavefronts for a row of token pairs, tiles each
 
+// All chunks at once.  A wavefront accumulates kTilesGrad tiles of 16 keys of dQ and dK over the value
+// heads that share them and, with others, the token pairs dO U^T and dV U^T; states and their adjoints
+// are read from memory straight into the factors' registers, once each, while columns of dO, dV and U
+// pass through LDS, all of them fetched one step ahead.  Bound by issue at two wavefronts a SIMD (4 to
+// 6 vector instructions a matrix one, most of them cutting fp32 values into parts) and its 256
+// registers: 366 us at Bt=4 L=2048 H=16 K=V=128 fp32 (388 TFLOP/s of matrix products), 510 us for
+// 16384 packed tokens, 8 key heads, H=16 bf16 (152 bytes spilled; 784 us with four wavefronts and
+// loads at their uses).
 __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p) {
   constexpr int THREADS = 64 * kWavesGrad;
   constexpr int kStage = (kIn + 2 * TP) * C * LDV, kPair = 2 * GP * C * LDT;

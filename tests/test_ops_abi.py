@@ -57,6 +57,18 @@ def test_delta_refusals(lib, bwd):
     assert call(S0=0x700000, **{"dS0" if bwd else "lS": 0x700000}) == INVALID
     assert call(off=0x10000010) == INVALID  # inside the workspace
 
+@pytest.mark.parametrize("bwd", [False, True])
+def test_delta_refuses_rows_past_32_bit_offsets(lib, bwd):
+    """64 rows of 2^18 x 32 fp32 values are 2^31 bytes, of bf16 ones half of that."""
+    q = lib.msm_delta_rule_bwd_workspace_bytes if bwd else lib.msm_delta_rule_fwd_workspace_bytes
+    wide = dict(Hk=1, H=32, K=16, V=1 << 18)
+    assert _delta(lib, bwd, **wide) == UNSUPPORTED
+    assert q(1, 8, 1, 32, 16, 1 << 18, 0, 0) == 0
+    assert q(1, 8, 1, 32, 16, 1 << 18, 0, 1) > 0
+    assert _delta(lib, bwd, V=(1 << 20) + 1) == INVALID
+    assert q(1, 8, 1, 65535, 16, 1 << 20, 0, 1) == 0
+
+
 
 def test_delta_workspace_queries(lib):
     for q in (lib.msm_delta_rule_fwd_workspace_bytes, lib.msm_delta_rule_bwd_workspace_bytes):
