@@ -124,52 +124,58 @@ __device__ __forceinline__ void invert(const MSM_LDS float* Ms, const MSM_LDS fl
   __syncthreads();
 }
 
-// Rows of keys or queries into swizzled LDS planes; rows and columns past the chunk's are zero.
-// With `ws` the planes also go to memory, for kernels that then load them into LDS unchanged: fp32
-// inputs in their parts, and rows that cannot be read 16 bytes at a time.
-template <int THREADS>
-__device__ __forceinline__ void stage_rows(lds_parts lds, uint16_t* ws, __amdgpu_buffer_rsrc_t r, uint32_t stride,
-                                           int K, bool vec, int tid) {
-  constexpr int N = C * UK / THREADS;
-  static_assert(C * UK % THREADS == 0, "whole passes");
+// KS columns from c0 of the chunk's rows of keys or queries, on their way into swizzled LDS planes;
+// rows and columns past the chunk's are zero.  With `ws` the planes also go to memory, for kernels
+// that then load them into LDS unchanged: fp32 inputs in their parts, and rows that cannot be read 16
+// bytes at a time.
+template <int THREADS, int KS>
+struct RawRows {
+  static constexpr int U = KS / 8, N = C * U / THREADS;
+  static_assert(C * U % THREADS == 0, "whole passes");
   f32x4 a[N][2];
+  static __device__ __forceinline__ int row(int u) { return u / U; }
+  static __device__ __forceinline__ int unit(int u) { return (u % U) ^ swizzle<U>(u / U); }
+  __device__ __forceinline__ void fetch(__amdgpu_buffer_rsrc_t r, uint32_t stride, int K, bool vec, int c0, int tid) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int u = tid + i * THREADS, row = u / UK, c = ((u % UK) ^ swizzle<UK>(row)) * 8;
-    const uint32_t at = row * stride + c * IO::es;
-    if (vec) {
-      a[i][0] = bload4(r, c < K ? at : kOutside);
-      if (!MSM_IO_BF16) a[i][1] = bload4(r, c + 4 < K ? at + 16 : kOutside);
-    } else {
-      uint32_t x[8];
+    for (int i = 0; i < N; ++i) {
+      const int u = tid + i * THREADS, c = c0 + unit(u) * 8;
+      const uint32_t at = row(u) * stride + c * IO::es;
+      if (vec) {
+        a[i][0] = bload4(r, c < K ? at : kOutside);
+        if (!MSM_IO_BF16) a[i][1] = bload4(r, c + 4 < K ? at + 16 : kOutside);
+      } else {
+        uint32_t x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const auto v = IO::bload(r, c + e < K ? at + e * IO::es : kOutside, 0);
-        x[e] = __builtin_bit_cast(uint32_t, v);
-      }
+        for (int e = 0; e < 8; ++e) {
+          const auto v = IO::bload(r, c + e < K ? at + e * IO::es : kOutside, 0);
+          x[e] = __builtin_bit_cast(uint32_t, v);
+        }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (MSM_IO_BF16) {
-          a[i][0][e] = __uint_as_float(x[2 * e] | (x[2 * e + 1] << 16));
-        } else {
-          a[i][0][e] = __uint_as_float(x[e]);
-          a[i][1][e] = __uint_as_float(x[4 + e]);
+        for (int e = 0; e < 4; ++e) {
+          if (MSM_IO_BF16) {
+            a[i][0][e] = __uint_as_float(x[2 * e] | (x[2 * e + 1] << 16));
+          } else {
+            a[i][0][e] = __uint_as_float(x[e]);
+            a[i][1][e] = __uint_as_float(x[4 + e]);
+          }
         }
       }
     }
   }
+  __device__ __forceinline__ void put(lds_parts lds, uint16_t* ws, int c0, int tid) const {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int u = tid + i * THREADS;
-    Part<kIn> s;
-    if constexpr (kIn == 1)
-      s.p[0] = __builtin_bit_cast(bf16x8, a[i][0]);
-    else
-      s = split<kIn>(a[i][0], a[i][1]);
-    store_parts(lds + u * 8, kRows, s);
-    if (ws) store_parts(ws + u * 8, kRows, s);
+    for (int i = 0; i < N; ++i) {
+      const int u = tid + i * THREADS;
+      Part<kIn> s;
+      if constexpr (kIn == 1)
+        s.p[0] = __builtin_bit_cast(bf16x8, a[i][0]);
+      else
+        s = split<kIn>(a[i][0], a[i][1]);
+      store_parts(lds + u * 8, C * KS, s);
+      if (ws) store_parts(ws + row(u) * KP + (((c0 / 8) + unit(u)) ^ swizzle<UK>(row(u))) * 8, kRows, s);
+    }
   }
-}
+};
 
 // The first N parts of a chunk matrix from LDS rows of LDM floats into its blocks, 16 bytes a plane
 // and thread.
@@ -183,18 +189,28 @@ __device__ __forceinline__ void write_tri(uint16_t* to, const MSM_LDS float* fro
   }
 }
 
-// Bound by the latency of its steps (load, Gram products, inverse, store), so the LDS is kept small
-// for three workgroups a CU: the inverse and the outgoing matrices take the place of the keys and
-// queries once the Gram products are done.  Bt=4 L=4096 H=32 K=128 bf16: 117 us, 262 MB written (the
-// chunk matrices in their parts); the same with 100 KB of LDS, one workgroup a CU: 170 us.
+// Key columns that prep stages at a time.
+constexpr int prep_columns() {
+  int ks = KP;
+  while (ks > 32 && 2 * kIn * C * ks * 2 > 36 * 1024) ks /= 2;
+  return ks;
+}
+
+// Bound by the latency of its steps (load, Gram products, inverse, store), so the LDS is kept to 53 KB
+// for three workgroups a CU: wide rows are staged some columns at a time, and the inverse and the
+// outgoing matrices take the place of the keys and queries once the Gram products are done.  Bt=4
+// L=4096 H=32 K=128 bf16: 117 us, 262 MB written (the chunk matrices in their parts); 170 us with
+// 100 KB, one workgroup a CU.  Bt=4 L=2048 H=16 K=128 fp32, backward: 93 us; 120 us with whole rows,
+// 117 KB.
 template <bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
-  constexpr int kMat = C * LDM * 4, kKeys = 2 * kIn * kRows * 2, kMats = 2 * kMat;
+  constexpr int KS = prep_columns();
+  constexpr int kMat = C * LDM * 4, kKeys = 2 * kIn * C * KS * 2, kMats = 2 * kMat;
   __shared__ __attribute__((aligned(16))) char lds_kq[kKeys > kMats ? kKeys : kMats];
   __shared__ __attribute__((aligned(16))) float lds_m[C * LDM];
   __shared__ double Gd[C];
   __shared__ float bt[C];
-  const lds_parts Ks = (lds_parts)lds_kq, Qs = Ks + kIn * kRows;
+  const lds_parts Ks = (lds_parts)lds_kq, Qs = Ks + kIn * C * KS;
   MSM_LDS float* const Ms = (MSM_LDS float*)lds_m;
   MSM_LDS float* const Ti = (MSM_LDS float*)lds_kq;
   MSM_LDS float* const Pl = Ti + C * LDM;
@@ -207,14 +223,44 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   const uint32_t stride = (uint32_t)(p.Hk * p.K * IO::es);
   uint16_t* ws = p.kq_direct || h != hk * group ? nullptr : static_cast<uint16_t*>(p.kq) + (slot * p.Hk + hk) * 2 * kIn * kRows;
   float gl = 0.f, b = 0.f;
-  if (wave == 0 && lane < ch.n) {
+  constexpr int B16 = C / 16, kTiles = B16 * B16 / 4;
+  constexpr int kLight = B16 - 1;  // the wavefront with the fewest Gram tiles takes the decays
+  if (wave == kLight && lane < ch.n) {
     gl = p.g[(ch.row0 + lane) * p.H + h];
     b = p.beta[(ch.row0 + lane) * p.H + h];
   }
-  stage_rows<256>(Ks, ws, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
-  stage_rows<256>(Qs, ws ? ws + kIn * kRows : nullptr, head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride,
-                  (int)p.K, p.vec_k, tid);
-  if (wave == 0) {
+  const auto rk = head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), rq = head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n);
+  RawRows<256, KS> kr, qr;
+  kr.fetch(rk, stride, (int)p.K, p.vec_k, 0, tid);
+  qr.fetch(rq, stride, (int)p.K, p.vec_k, 0, tid);
+  // Gram tiles of the kept blocks; 16 x 16, a wavefront's share of them in its registers
+  f32x4 kk[kTiles], qk[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) kk[i] = qk[i] = zero4();
+#pragma unroll 1
+  for (int c0 = 0; c0 < KP; c0 += KS) {
+    if (c0 > 0) __syncthreads();  // the columns before have been read
+    kr.put(Ks, ws, c0, tid);
+    qr.put(Qs, ws ? ws + kIn * kRows : nullptr, c0, tid);
+    if (c0 + KS < KP) {
+      kr.fetch(rk, stride, (int)p.K, p.vec_k, c0 + KS, tid);
+      qr.fetch(rq, stride, (int)p.K, p.vec_k, c0 + KS, tid);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const int t = 4 * i + wave, mt = t / B16, nt = t % B16;
+      if (nt <= mt) {
+#pragma unroll
+        for (int b = 0; b < KS / 32; ++b) {
+          const auto B = load_row<KS / 8, kIn>(Ks, 16 * nt + n, 32 * b + 8 * j, C * KS);
+          mma(kk[i], load_row<KS / 8, kIn>(Ks, 16 * mt + n, 32 * b + 8 * j, C * KS), B);
+          mma(qk[i], load_row<KS / 8, kIn>(Qs, 16 * mt + n, 32 * b + 8 * j, C * KS), B);
+        }
+      }
+    }
+  }
+  if (wave == kLight) {
     // running sum of the log decay in fp64: its differences keep fp32 accuracy.  exp(-1e4) is 0
     // already; below it the sum would lose the decays that follow (a decay of minus infinity, or
     // of the lowest float, resets the state)
@@ -233,23 +279,6 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
       vec[C + lane] = exp_of(last - G);
       vec[2 * C + lane] = b;
       reinterpret_cast<double*>(vec + 3 * C)[lane] = G;
-    }
-  }
-  __syncthreads();
-  // Gram tiles of the kept blocks; 16 x 16, a wavefront's share of them in its registers
-  constexpr int B16 = C / 16, kTiles = B16 * B16 / 4;
-  f32x4 kk[kTiles], qk[kTiles];
-#pragma unroll
-  for (int i = 0; i < kTiles; ++i) {
-    const int t = 4 * i + wave, mt = t / B16, nt = t % B16;
-    kk[i] = qk[i] = zero4();
-    if (nt <= mt) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const auto B = load_row<UK, kIn>(Ks, 16 * nt + n, 32 * b + 8 * j, kRows);
-        mma(kk[i], load_row<UK, kIn>(Ks, 16 * mt + n, 32 * b + 8 * j, kRows), B);
-        mma(qk[i], load_row<UK, kIn>(Qs, 16 * mt + n, 32 * b + 8 * j, kRows), B);
-      }
     }
   }
   __syncthreads();  // keys and queries have been read
@@ -1142,8 +1171,13 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   if (ch.n == 0) return;
   const int64_t at = (ch.row0 * p.Hk + hk) * p.K;
   const uint32_t stride = (uint32_t)(p.Hk * p.K * IO::es);
-  stage_rows<THREADS>(Ks, nullptr, head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
-  stage_rows<THREADS>(Qs, nullptr, head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, tid);
+  {
+    RawRows<THREADS, KP> kr, qr;
+    kr.fetch(head_rsrc(p.k, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, 0, tid);
+    qr.fetch(head_rsrc(p.q, ch.row0, p.Hk, hk, p.K, IO::es, ch.n), stride, (int)p.K, p.vec_k, 0, tid);
+    kr.put(Ks, nullptr, 0, tid);
+    qr.put(Qs, nullptr, 0, tid);
+  }
   const int tile0 = wave * kTilesGrad;           // this wavefront's key tiles
   const bool keys = tile0 * 16 < KP;
   // token pairs: 16-row tile `prow`, its 16-column tiles ppart, ppart + PW, ...
