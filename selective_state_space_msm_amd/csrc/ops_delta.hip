@@ -189,19 +189,20 @@ __device__ __forceinline__ void write_tri(uint16_t* to, const MSM_LDS float* fro
   }
 }
 
-// Key columns that prep stages at a time.
+// Key columns that prep stages at a time: 64 at least, so that their planes go to memory in whole
+// 128-byte lines (32 columns of fp32 keys of 128: 93 us and a slower scan after it, 313 us; 64: 88, 300).
 constexpr int prep_columns() {
   int ks = KP;
-  while (ks > 32 && 2 * kIn * C * ks * 2 > 36 * 1024) ks /= 2;
+  while (ks > 32 && 2 * kIn * C * ks * 2 > 50 * 1024) ks /= 2;
   return ks;
 }
 
 // Bound by the latency of its steps (load, Gram products, inverse, store), so the LDS is kept to 53 KB
-// for three workgroups a CU: wide rows are staged some columns at a time, and the inverse and the
-// outgoing matrices take the place of the keys and queries once the Gram products are done.  Bt=4
-// L=4096 H=32 K=128 bf16: 117 us, 262 MB written (the chunk matrices in their parts); 170 us with
-// 100 KB, one workgroup a CU.  Bt=4 L=2048 H=16 K=128 fp32, backward: 93 us; 120 us with whole rows,
-// 117 KB.
+// for three workgroups a CU (fp32 keys of 128: 67 KB for two): wide rows are staged some columns at a
+// time, and the inverse and the outgoing matrices take the place of the keys and queries once the
+// Gram products are done.  Bt=4 L=4096 H=32 K=128 bf16: 117 us, 262 MB written (the chunk matrices in
+// their parts); 170 us with 100 KB, one workgroup a CU.  Bt=4 L=2048 H=16 K=128 fp32, backward: 88 us;
+// 120 us with whole rows, 117 KB.
 template <bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
   constexpr int KS = prep_columns();
