@@ -315,10 +315,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t head_rsrc(const void* base, in
 // the compiler waits for the load, also where the target is the other buffer, and so for the
 // memory latency that the second buffer is there to hide.  It has no result register; sync_loads
 // waits for it by hand, and waits that the compiler counts for other loads only get longer.
+// The compiler does not look into it for wait states either, so it brings its own: a load needs 5
+// after a vector instruction's write of a scalar register that it reads (the resource's extent, often
+// a v_readfirstlane), 1 after m0's write.  The move to m0 is one of them and s_nop 3 the other four.
 __device__ __forceinline__ void load_lds(u32x4 r, MSM_LDS void* lds, uint32_t off) {
 #ifdef __HIP_DEVICE_COMPILE__
   const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "m0");
 #endif
 }
 // The resource of make_rsrc_u32 in its four words.
