@@ -316,10 +316,10 @@ msm_status msm_scan_complex_bwd(const void* x, const void* delta, const float* A
  * Requirements: Bt, L, Hk, H, K, V >= 1, H a multiple of Hk, K <= 256 and 64 rows of q or v (of
  * all heads) below 2^31 bytes (else MSM_ERR_UNSUPPORTED), V <= 2^20, H <= 65535, fewer than 2^31
  * tokens, scale finite.  Outputs must not overlap an input.  All sums are fp32; the products run
- * on bf16 matrix cores over values cut into parts that keep 24 bits (16 bits where the result is
- * rounded to bf16 anyway).  g of minus infinity forgets the state.  Tokens are taken in chunks of
- * 64 (32 for fp32 with K > 128) from a sequence's start: a NaN or an infinity in a token may reach
- * earlier outputs of its own chunk, and no other sequence. */
+ * on bf16 matrix cores over values cut into parts that keep 24 bits, whatever the io type.
+ * g of minus infinity forgets the state.  Tokens are taken in chunks of 64 (32 for fp32 with
+ * K > 128) from a sequence's start: a NaN or an infinity in a token may reach earlier outputs of
+ * its own chunk, and no other sequence. */
 size_t msm_delta_rule_fwd_workspace_bytes(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K,
                                           int64_t V, int32_t packed, msm_dtype io);
 msm_status msm_delta_rule_fwd(const void* q, const void* k, const void* v, const float* g,

@@ -32,8 +32,11 @@
 //   rev      the walk backwards for the adjoint of the state
 //   grad     one workgroup per chunk and key head: dQ, dK and the sums for dbeta and dg
 // The products run on the bf16 matrix unit over values cut into parts of 8 bits (ops_delta.hpp):
-// one part for a bf16 input, three for an fp32 value, which keeps its 24 bits, and two where the
-// result is rounded to bf16.  The card's fp32 matrix unit reaches 154 TFLOP/s, its bf16 unit 1240:
+// one part for a bf16 input and three for an fp32 value, which keeps its 24 bits, also where the
+// result is then rounded to bf16: two parts there, 16 bits, took 10% off the forward's time at Bt=4
+// L=4096 H=32 and 5% off the packed backward's, but moved about one result in 200 to its
+// bf16 neighbour.
+// The card's fp32 matrix unit reaches 154 TFLOP/s, its bf16 unit 1240:
 // even the six products of three parts by three are faster there.
 #include <type_traits>
 
@@ -49,7 +52,6 @@ constexpr int CB = C / 32;        // blocks of 32 tokens
 constexpr int UK = KP / 8;        // 16-byte units of a row of keys
 constexpr int kIn = MSM_IO_BF16 ? 1 : 3;        // parts of an input
 constexpr int TP = 3;                           // parts of an fp32 value
-constexpr int kOutParts = MSM_IO_BF16 ? 2 : 3;  // of what is rounded to the I/O type: 16 bits carry a bf16
 constexpr int kRows = C * KP;                   // elements of a plane of keys
 using TriM = Tri<C>;
 constexpr int kTri = TP * TriM::kPlane;         // elements of a chunk matrix
@@ -177,15 +179,14 @@ struct RawRows {
   }
 };
 
-// The first N parts of a chunk matrix from LDS rows of LDM floats into its blocks, 16 bytes a plane
-// and thread.
-template <int N>
+// The parts of a chunk matrix from LDS rows of LDM floats into its blocks, 16 bytes a plane and
+// thread.
 __device__ __forceinline__ void write_tri(uint16_t* to, const MSM_LDS float* from, int tid) {
   for (int u = tid; u < C * C / 8; u += 256) {
     const int row = u / (C / 8), c = (u % (C / 8)) * 8;
     if (c / 32 > row / 32) continue;
     const f32x4 a = *(const MSM_LDS f32x4*)(from + row * LDM + c), b = *(const MSM_LDS f32x4*)(from + row * LDM + c + 4);
-    store_parts(to + TriM::at(row, c), TriM::kPlane, split<N>(a, b));
+    store_parts(to + TriM::at(row, c), TriM::kPlane, split<TP>(a, b));
   }
 }
 
@@ -298,10 +299,10 @@ __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
     }
   }
   __syncthreads();
-  write_tri<BWD ? TP : kOutParts>(static_cast<uint16_t*>(p.P) + sh * kTri, Pl, tid);
-  if (BWD) write_tri<TP>(static_cast<uint16_t*>(p.M) + sh * kTri, Ms, tid);
+  write_tri(static_cast<uint16_t*>(p.P) + sh * kTri, Pl, tid);
+  if (BWD) write_tri(static_cast<uint16_t*>(p.M) + sh * kTri, Ms, tid);
   invert(Ms, (const MSM_LDS float*)bt, Ti, wave, lane);
-  write_tri<TP>(static_cast<uint16_t*>(p.T) + sh * kTri, Ti, tid);
+  write_tri(static_cast<uint16_t*>(p.T) + sh * kTri, Ti, tid);
 }
 
 // ---- scan ----------------------------------------------------------------------------------
@@ -533,10 +534,9 @@ struct Keys {
 constexpr size_t kLdsMost = 160 * 1024 - 512;
 template <bool BWD>
 struct ScanChunk {
-  static constexpr int OP = BWD ? TP : kOutParts;
   KeyRows r;
   uint16_t t[tri_lds(TP)];
-  uint16_t p[BWD ? 8 : tri_lds(OP)];
+  uint16_t p[BWD ? 8 : tri_lds(TP)];
 };
 struct Nothing {};
 
@@ -610,7 +610,6 @@ struct ScanOut {
 template <bool BWD, class F>
 __device__ __forceinline__ void scan_chunk(F fetch, const DeltaArgs& p, const Walk& w, const MSM_LDS ScanChunk<BWD>& l, Cols<NB>& S,
                                            Cols<CB> R, const Cols<CB>& dO, const ScanOut& out, int rows) {
-  constexpr int OP = ScanChunk<BWD>::OP;
   const int lane = w.lane, j = w.j, n = w.n;
   const MSM_LDS float* eG = l.r.ev + 8 * j;           // this lane's rows of the chunk's row factors
   const MSM_LDS float* eK = l.r.ev + C + 8 * j;
@@ -622,7 +621,7 @@ __device__ __forceinline__ void scan_chunk(F fetch, const DeltaArgs& p, const Wa
   Cols<CB> KS = zero_cols<CB>(), O = zero_cols<CB>();
   RowTiles fk[2], fq[2];
   TriTiles<TP, false> ft;
-  TriTiles<OP, false> fp;
+  TriTiles<TP, false> fp;
   fk[0].load(l.r.k, 0, lane, j);
   fq[0].load(l.r.q, 0, lane, j);
   Part<TP> sb = split<TP>(S.t[0][0], S.t[0][1]);
@@ -637,9 +636,9 @@ __device__ __forceinline__ void scan_chunk(F fetch, const DeltaArgs& p, const Wa
     fetch(b);
     hold_lds();
     mma_tiles(tiles(KS), fk[b & 1].a, sb);
-    mma_tiles(tiles(O), fq[b & 1].a, first<OP>(sb));
+    mma_tiles(tiles(O), fq[b & 1].a, sb);
     if (b + 1 < NB) sb = split<TP>(S.t[(b + 1) % NB][0], S.t[(b + 1) % NB][1]);
-    interleave<2 * CB * (TP + OP), 3>();
+    interleave<4 * CB * TP, 3>();
   }
   // errors of the chunk: E = T (V - e^G K S)
   each<CB>([&](int b, int t, int r, int row) {
@@ -667,9 +666,8 @@ __device__ __forceinline__ void scan_chunk(F fetch, const DeltaArgs& p, const Wa
     const float sum = sum_rows16(x, lane);
     if (w.on && n < 8 * CB) out.dots[32 * (n / 8) + 8 * j + n % 8] = sum;
   } else {
-    Part<OP> UO[CB];
-    split_all(UO, U);
-    fp.mma(O, UO);
+    split_all(B, U);
+    fp.mma(O, B);
     store_out(out.o.rsrc(rows), w.vat, w.vstride, O);
   }
   // state after the chunk
@@ -724,7 +722,7 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
     keys.load(l.r, rows, w.wave, w.lane, part, NB);
     if (part == NB - 1) {
       load_tri<TP>(l.t, st, rows, w.wave, w.lane);
-      if constexpr (!BWD) load_tri<ScanChunk<BWD>::OP>(l.p, sp, rows, w.wave, w.lane);
+      if constexpr (!BWD) load_tri<TP>(l.p, sp, rows, w.wave, w.lane);
       v.fetch(sv.rsrc(rows), w.vat, w.vstride);
       if (BWD) d.fetch(sd.rsrc(rows), w.vat, w.vstride);
       keys.next(1);
@@ -1134,7 +1132,6 @@ __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p)
 
 // ---- grad ----------------------------------------------------------------------------------
 
-constexpr int GP = kOutParts;  // parts that the gradients of q and k are made of
 // Wavefronts: two a SIMD hide each other's loads, but the fp32 parts of eight would not fit.
 constexpr int kWavesGrad = KP == 256 || (KP == 128 && MSM_IO_BF16) ? 8 : 4;
 constexpr int kTilesGrad = KP / 16 > kWavesGrad ? KP / 16 / kWavesGrad : 1;      // 16-key tiles a wavefront
@@ -1153,7 +1150,7 @@ constexpr int PW = kWavesGrad >= 2 * MT ? 2 : 1, PT = MT / PW;  // wavefronts fo
 // loads at their uses).
 __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p) {
   constexpr int THREADS = 64 * kWavesGrad;
-  constexpr int kStage = (kIn + 2 * TP) * C * LDV, kPair = 2 * GP * C * LDT;
+  constexpr int kStage = (kIn + 2 * TP) * C * LDV, kPair = 2 * TP * C * LDT;
   __shared__ __attribute__((aligned(16))) uint16_t lds_k[kIn * kRows];
   __shared__ __attribute__((aligned(16))) uint16_t lds_q[kIn * kRows];
   // first the staged columns of dO, dV and U, then the token-pair matrices X and Z + Z^T
@@ -1165,7 +1162,7 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
   __shared__ float across[MT][C];  // sums of N_ij over a tile of rows i >= t and all j < t
   const lds_parts Ks = (lds_parts)lds_k, Qs = (lds_parts)lds_q, buf = (lds_parts)lds_buf;
   const lds_parts dOs = buf, dVs = buf + kIn * C * LDV, Us = dVs + TP * C * LDV;
-  const lds_parts Xs = buf, Zs = buf + GP * C * LDT;
+  const lds_parts Xs = buf, Zs = buf + TP * C * LDT;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, j = lane >> 4;
   const int64_t slot = blockIdx.x, hk = blockIdx.y, group = (uint32_t)p.H / (uint32_t)p.Hk;
   const ChunkRows ch = chunk_rows<C>(p, slot);
@@ -1290,11 +1287,11 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
 #pragma unroll
       for (int b = 0; b < VB / 32; ++b) {
         if (v0 + 32 * b >= p.VP) break;
-        Part<GP> s0[kTilesGrad], s1[kTilesGrad];
+        Part<TP> s0[kTilesGrad], s1[kTilesGrad];
 #pragma unroll
         for (int t = 0; t < kTilesGrad; ++t) {
-          s0[t] = split<GP>(ss[t][0], ss[t][1]);
-          s1[t] = split<GP>(ss[t][2], ss[t][3]);
+          s0[t] = split<TP>(ss[t][0], ss[t][1]);
+          s1[t] = split<TP>(ss[t][2], ss[t][3]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dot = fmaf(ss[t][0][i], ss[t][2][i], fmaf(ss[t][1][i], ss[t][3][i], dot));
         }
@@ -1304,8 +1301,8 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
           for (int m = 0; m < MT; ++m) {
             const int e = (16 * m + n) * LDV + 32 * b + 8 * j;
             const auto fo = load_ld<kIn>(dOs + e, C * LDV);
-            const auto fv = load_ld<GP>(dVs + e, C * LDV);
-            const auto fu = load_ld<GP>(Us + e, C * LDV);
+            const auto fv = load_ld<TP>(dVs + e, C * LDV);
+            const auto fu = load_ld<TP>(Us + e, C * LDV);
 #pragma unroll
             for (int t = 0; t < kTilesGrad; ++t) {
               mma(a1[t][m], fo, s0[t]);
@@ -1352,10 +1349,10 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
           const int row = 16 * prow + 4 * j + r, c = 16 * m + n;
           const float D = c <= row ? exp_of(Gd[row] - Gd[c]) : 0.f;
           const float x = c <= row ? p.scale * D * X[i][r] : 0.f, z = c < row ? -D * Z[i][r] : 0.f;
-          store_parts1<GP>(Xs + row * LDT + c, C * LDT, x);
+          store_parts1<TP>(Xs + row * LDT + c, C * LDT, x);
           if (c <= row) {
-            store_parts1<GP>(Zs + row * LDT + c, C * LDT, z);
-            store_parts1<GP>(Zs + c * LDT + row, C * LDT, z);
+            store_parts1<TP>(Zs + row * LDT + c, C * LDT, z);
+            store_parts1<TP>(Zs + c * LDT + row, C * LDT, z);
           }
           float sum = c < row ? x * qk[r] + z * kk[r] : 0.f;
           sum += dpp<0x111>(sum);  // row_shr: from the lanes before in the group, zero past its start
@@ -1434,10 +1431,10 @@ __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (m / 2 >= b)
-              mma(dq[m][t], load_ld<GP>(Xs + (16 * m + n) * LDT + 32 * b + 8 * j, C * LDT), kt);
-            mma(dk[m][t], load_ld<GP>(Zs + (16 * m + n) * LDT + 32 * b + 8 * j, C * LDT), kt);
+              mma(dq[m][t], load_ld<TP>(Xs + (16 * m + n) * LDT + 32 * b + 8 * j, C * LDT), kt);
+            mma(dk[m][t], load_ld<TP>(Zs + (16 * m + n) * LDT + 32 * b + 8 * j, C * LDT), kt);
             if (m / 2 <= b)
-              mma(dk[m][t], load_col_ld<GP>(Xs + (32 * b + 8 * j) * LDT, LDT, 16 * m, lane, C * LDT), qt);
+              mma(dk[m][t], load_col_ld<TP>(Xs + (32 * b + 8 * j) * LDT, LDT, 16 * m, lane, C * LDT), qt);
           }
         }
     }

@@ -13,11 +13,12 @@
 // moves its right factors between lanes.
 //
 // Values are cut into bf16 parts by truncation, x = hi + mid + lo with 8 significant bits each:
-// three parts hold all 24 bits of an fp32 value, two parts 16, and a bf16 input is one part.  A
-// product of an NA-part and an NB-part factor keeps the terms whose places add up to less than
-// the larger count: an input times a three-part value is 3 MFMAs and two three-part values are
-// 6, to fp32 accuracy; the fp32 MFMA, 16 times slower per product, would take 2.7 times as
-// long as the 6.  Infinities leave NaN in the lower parts.
+// three parts hold all 24 bits of an fp32 value, and a bf16 input is one part.  A product of an
+// NA-part and an NB-part factor keeps the terms whose places add up to less than the larger
+// count: an input times a three-part value is 3 MFMAs, exact, and two three-part values are 6,
+// without what is below 2^-20 of a term (a sum of 64 products is off by 6e-8 of its size, an
+// fp32 sum by 1.5e-7); the fp32 MFMA, 16 times slower per product, would take 2.7 times as long
+// as the 6.  Infinities leave NaN in the lower parts.
 #pragma once
 
 #include "msm_device.hpp"
@@ -68,14 +69,6 @@ __device__ __forceinline__ Part<N> split(const f32x4& a, const f32x4& b) {
     }
     o.p[n] = __builtin_bit_cast(bf16x8, w);
   }
-  return o;
-}
-// The leading N parts.
-template <int N, int NA>
-__device__ __forceinline__ Part<N> first(const Part<NA>& a) {
-  Part<N> o;
-#pragma unroll
-  for (int n = 0; n < N; ++n) o.p[n] = a.p[n];
   return o;
 }
 template <int N>

@@ -341,3 +341,19 @@ def test_segments(io, lens, packed):
 def test_segments_of_wide_heads():
     check(make("bf16", [1800], 1, 1, 128, 80, seed=31, g_scale=0.01))
     check(make("f32", [900], 1, 1, 200, 33, seed=32, g_scale=0.01))  # chunks of 32
+
+
+# ---- bf16 results ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("Hk,H,K,V", [(2, 4, 64, 64), (1, 2, 128, 128), (1, 1, 256, 80)])
+def test_bf16_results_are_the_rounded_ones(Hk, H, K, V):
+    """bf16 I/O is rounded once, from fp32 accuracy.  A sum of 320 terms in fp32 is off by
+    e = 6e-8 sqrt(320) of its size; an error e x moves a value x to the neighbouring bf16, a step of at
+    most 2^-7 x away, with a probability of e x / step, so the 2-norm of the difference to the rounded
+    float64 results is at most sqrt(2^-7 e) of theirs."""
+    tol = (2.0 ** -7 * 6e-8 * 320 ** 0.5) ** 0.5
+    d = make("bf16", [200, 130], Hk, H, K, V, seed=40 + K, packed=True, g_scale=0.1)
+    got = dict(run_bwd(d), o=run_fwd(d)[0])
+    ref = dict(want(d, K ** -0.5, True), **want(d, K ** -0.5, False))
+    for n in ("o", "dq", "dk", "dv"):
+        close(got[n], ref[n].bfloat16().double(), n, tol)
