@@ -16,7 +16,7 @@ namespace msm {
 namespace {
 
 template <typename IO, int VEC, int LC, int RPT>
-__global__ __launch_bounds__(256) void delta_step_kernel(const DeltaStepArgs p) {
+__global__ __launch_bounds__(256) void delta_step_kernel(const DeltaStepArgs p, int64_t first) {
   using T = io<IO>;
   constexpr int RG = 256 / LC;          // rows of the tile in flight; row = rg + RG i
   __shared__ float ks[RG * RPT], qs[RG * RPT];
@@ -24,7 +24,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(const DeltaStepArgs p) 
   __shared__ float kq[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cl = tid % LC, rg = tid / LC;
-  const int64_t bh = blockIdx.x, b = bh / p.H, h = bh - b * p.H, hk = h / (p.H / p.Hk);
+  const int64_t bh = first + blockIdx.x, b = bh / p.H, h = bh - b * p.H, hk = h / (p.H / p.Hk);
   const int64_t col = ((int64_t)blockIdx.y * LC + cl) * VEC;
   const bool on = col < p.V;
   const int K = (int)p.K;
@@ -118,9 +118,16 @@ __global__ __launch_bounds__(256) void delta_step_kernel(const DeltaStepArgs p) 
 
 template <typename IO, int VEC, int LC, int RPT>
 hipError_t go(const DeltaStepArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.Bt * a.H), (unsigned)((a.V + LC * VEC - 1) / (LC * VEC)));
-  hipLaunchKernelGGL((delta_step_kernel<IO, VEC, LC, RPT>), grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  // 2^24 workgroups of 256 would be 2^32 threads, more than a dimension of a launch may have
+  constexpr int64_t kMost = (int64_t)1 << 23;
+  for (int64_t first = 0, all = a.Bt * a.H; first < all; first += kMost) {
+    const int64_t left = all - first;
+    const dim3 grid((unsigned)(left < kMost ? left : kMost), (unsigned)((a.V + LC * VEC - 1) / (LC * VEC)));
+    hipLaunchKernelGGL((delta_step_kernel<IO, VEC, LC, RPT>), grid, dim3(256), 0, s, a, first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename IO, int VEC>

@@ -317,6 +317,26 @@ def test_step(io, Bt, Hk, H, K, V, offset):
     close(t["S0"], ref["S"], "S")
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("Bt,H,V,offset", [((1 << 24) + 3, 1, 1, 0), ((1 << 23) + 1, 2, 2, 0),
+                                           (1, 1, 1 << 20, 0), (1, 1, 1 << 20, 1)])
+def test_step_of_many_sequences_or_columns(io, Bt, H, V, offset):
+    """More states than a launch of one workgroup each may have, and the widest state."""
+    import selective_state_space_msm_amd as msm
+    gen = torch.Generator("cuda").manual_seed(22)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    q, k, v = rnd(Bt, H, 1).to(DT[io]), rnd(Bt, H, 1).to(DT[io]), rnd(Bt, H, V).to(DT[io])
+    g, beta = -rnd(Bt, H).square(), torch.sigmoid(rnd(Bt, H))
+    S = torch.empty(Bt * H * V + offset, device="cuda")[offset:].view(Bt, H, 1, V).copy_(rnd(Bt, H, 1, V))
+    qw, kw, vw, Sw = (t.double() for t in (q, k, v, S))
+    Sw = g.double().exp()[..., None, None] * Sw
+    Sw = Sw + (kw * beta.double()[..., None] * (vw - kw * Sw[..., 0, :]))[..., None, :]
+    o = msm.msm_delta_rule_step(q, k, v, g, beta, S)
+    torch.cuda.synchronize()
+    close(o, (qw * Sw[..., 0, :]).cpu(), "o")
+    close(S, Sw.cpu(), "S")
+
+
 def test_prefill_then_steps():
     import selective_state_space_msm_amd as msm
     d = make("bf16", [80, 80], 2, 4, 64, 64, seed=21)
