@@ -315,8 +315,10 @@ msm_status msm_scan_complex_bwd(const void* x, const void* delta, const float* A
  * hold, but a token that no sequence covers leaves its output unwritten.
  * Requirements: Bt, L, Hk, H, K, V >= 1, H a multiple of Hk, K <= 256 and 64 rows of q or v (of
  * all heads) below 2^31 bytes (else MSM_ERR_UNSUPPORTED), V <= 2^20, H <= 65535, fewer than 2^31
- * tokens, scale finite.  Outputs must not overlap an input.  All sums are fp32; the products run
- * on bf16 matrix cores over values cut into parts that keep 24 bits, whatever the io type.
+ * tokens, scale finite; Bt H and the number of chunks (below) under 2^24, else MSM_ERR_UNSUPPORTED
+ * (one token at a time has no such bound).  Outputs must not overlap an input.  All sums are
+ * fp32; the products run on bf16 matrix cores over values cut into parts that keep 24 bits,
+ * whatever the io type.
  * g of minus infinity forgets the state.  Tokens are taken in chunks of 64 (32 for fp32 with
  * K > 128) from a sequence's start: a NaN or an infinity in a token may reach earlier outputs of
  * its own chunk, and no other sequence. */

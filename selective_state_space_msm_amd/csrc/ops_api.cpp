@@ -94,6 +94,18 @@ msm_status delta_shape(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K, 
   return MSM_OK;
 }
 
+// The same for whole sequences.  Their launches have a workgroup of 256 threads for every chunk, and
+// for every sequence (or segment) and head, in one dimension, which holds fewer than 2^32 threads;
+// past that a launch may run short without an error.
+constexpr int64_t kGroups256 = ((int64_t)1 << 24) - 1;
+msm_status delta_sequences(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K, int64_t V,
+                           msm_dtype io, bool packed, DeltaShape* s) {
+  const msm_status st = delta_shape(Bt, L, Hk, H, K, V, io, packed, s);
+  if (st != MSM_OK) return st;
+  const int64_t walks = s->nsegs > s->nseq ? s->nsegs : s->nseq;
+  return s->nslots > kGroups256 || walks * H > kGroups256 ? MSM_ERR_UNSUPPORTED : MSM_OK;
+}
+
 struct DeltaLayout {
   size_t vec, T, P, kq, segS, segF, M, S, dS, E, dV, pred, dots, total;
 };
@@ -281,14 +293,14 @@ extern "C" {
 size_t msm_delta_rule_fwd_workspace_bytes(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K,
                                           int64_t V, int32_t packed, msm_dtype io) {
   DeltaShape s;
-  if (delta_shape(Bt, L, Hk, H, K, V, io, packed != 0, &s) != MSM_OK) return 0;
+  if (delta_sequences(Bt, L, Hk, H, K, V, io, packed != 0, &s) != MSM_OK) return 0;
   return delta_layout(s, io, false).total;
 }
 
 size_t msm_delta_rule_bwd_workspace_bytes(int64_t Bt, int64_t L, int64_t Hk, int64_t H, int64_t K,
                                           int64_t V, int32_t packed, msm_dtype io) {
   DeltaShape s;
-  if (delta_shape(Bt, L, Hk, H, K, V, io, packed != 0, &s) != MSM_OK) return 0;
+  if (delta_sequences(Bt, L, Hk, H, K, V, io, packed != 0, &s) != MSM_OK) return 0;
   return delta_layout(s, io, true).total;
 }
 
@@ -298,7 +310,7 @@ msm_status msm_delta_rule_fwd(const void* q, const void* k, const void* v, const
                               int64_t K, int64_t V, float scale, msm_dtype io, void* workspace,
                               size_t workspace_bytes, void* stream) {
   DeltaShape s;
-  const msm_status st = delta_shape(Bt, L, Hk, H, K, V, io, seq_offsets != nullptr, &s);
+  const msm_status st = delta_sequences(Bt, L, Hk, H, K, V, io, seq_offsets != nullptr, &s);
   if (st != MSM_OK) return st;
   if (!q || !k || !v || !g || !beta || !o || !isfinite(scale)) return MSM_ERR_INVALID_ARG;
   const DeltaLayout l = delta_layout(s, io, false);
@@ -324,7 +336,7 @@ msm_status msm_delta_rule_bwd(const void* q, const void* k, const void* v, const
                               msm_dtype io, void* workspace, size_t workspace_bytes,
                               void* stream) {
   DeltaShape s;
-  const msm_status st = delta_shape(Bt, L, Hk, H, K, V, io, seq_offsets != nullptr, &s);
+  const msm_status st = delta_sequences(Bt, L, Hk, H, K, V, io, seq_offsets != nullptr, &s);
   if (st != MSM_OK) return st;
   if (!q || !k || !v || !g || !beta || !do_ || !dq || !dk || !dv || !dg || !dbeta || !isfinite(scale))
     return MSM_ERR_INVALID_ARG;

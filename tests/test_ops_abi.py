@@ -70,6 +70,26 @@ def test_delta_refuses_rows_past_32_bit_offsets(lib, bwd):
 
 
 
+@pytest.mark.parametrize("bwd", [False, True])
+def test_delta_refuses_launches_past_32_bits(lib, bwd):
+    """A launch has fewer than 2^32 threads: 2^24 workgroups of 256, one a chunk or a sequence and head."""
+    q = lib.msm_delta_rule_bwd_workspace_bytes if bwd else lib.msm_delta_rule_fwd_workspace_bytes
+    for sizes, packed in (((1 << 24, 1, 1, 1, 16, 16), 0), ((1 << 15, 1, 1, 512, 16, 16), 0),
+                          ((1 << 15, 4, 1, 512, 16, 16), 1), ((1, (1 << 30) + 64, 1, 1, 16, 16), 1)):
+        a = dict(zip(("Bt", "L", "Hk", "H", "K", "V"), sizes), wsb=1 << 62)
+        # arrays of such sizes do not overlap only if they are far apart
+        places = ["q", "k", "v", "g", "beta", "do", "o", "dq", "dk", "dv", "dg", "db", "ws"]
+        a.update({n: (i + 1) << 48 for i, n in enumerate(places)})
+        if packed:
+            a["off"] = 1 << 20
+        assert _delta(lib, bwd, **a) == UNSUPPORTED, sizes
+        assert q(*sizes, packed, 0) == 0
+    assert q((1 << 24) - 64, 1, 1, 1, 16, 16, 0, 0) > 0
+    step = [P((i + 1) << 40) for i in range(7)]
+    step[0] = None  # refused for this, not for its 2^24 states
+    assert lib.msm_delta_rule_step(*step, 1 << 24, 1, 1, 16, 16, ctypes.c_float(1), 0, None) == INVALID
+
+
 def test_delta_workspace_queries(lib):
     for q in (lib.msm_delta_rule_fwd_workspace_bytes, lib.msm_delta_rule_bwd_workspace_bytes):
         assert q(0, 8, 1, 1, 16, 16, 0, 0) == 0
