@@ -218,7 +218,7 @@ int64_t norm_groups(int64_t rows, const msm::NormShape& f) {
 
 size_t norm_bwd_bytes(int64_t rows, int64_t D, msm_dtype io) {
   // for either way of reading the rows (it depends on the arrays' alignment)
-  int64_t most = 256;
+  int64_t most = 1;
   const int pers[2] = {1, io == MSM_BF16 ? 8 : 4};
   for (int per : pers) {
     const int64_t g = norm_groups(rows, msm::norm_shape(D, per));

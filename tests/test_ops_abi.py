@@ -148,6 +148,13 @@ def test_norm_refusals(lib):
     assert lib.msm_layer_norm_bwd_workspace_bytes(0, 4, 0) == 0
 
 
+@pytest.mark.parametrize("io", [0, 1])
+@pytest.mark.parametrize("rows,D", [(1, 1 << 28), (3, 5001), (1, 4096), (7, 16)])
+def test_norm_workspace_of_few_rows(lib, rows, D, io):
+    """A pair of column sums for every workgroup, and no more workgroups than rows."""
+    assert lib.msm_layer_norm_bwd_workspace_bytes(rows, D, io) <= rows * 8 * D + 256
+
+
 def test_clip_refusals(lib):
     def call(clip=True, src=(0x100000, 0x200000), dst=None, n=(16, 16), t=(0, 1), count=2, norm=0x300000,
              ws=0x1000000, wsb=1 << 20, max_norm=1.0, eps=1e-6):
