@@ -383,8 +383,12 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const NormArgs p, int64_
   }
 }
 
+// Fewer columns a workgroup while that takes more of them to fill the GPU; for the widest rows a
+// thread a column, as D / 16 workgroups of 256 would pass the 2^32 threads of a launch.
 hipError_t join(const NormArgs& a, int64_t parts, hipStream_t s) {
-  if (a.D >= 4096)
+  if (a.D >= (1 << 22))
+    hipLaunchKernelGGL(norm_join_kernel<256>, dim3((unsigned)((a.D + 255) / 256)), dim3(256), 0, s, a, parts);
+  else if (a.D >= 4096)
     hipLaunchKernelGGL(norm_join_kernel<16>, dim3((unsigned)((a.D + 15) / 16)), dim3(256), 0, s, a, parts);
   else
     hipLaunchKernelGGL(norm_join_kernel<4>, dim3((unsigned)((a.D + 3) / 4)), dim3(256), 0, s, a, parts);

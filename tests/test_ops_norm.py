@@ -119,3 +119,19 @@ def test_repeated_and_on_another_stream(io):
     assert torch.equal(y, y2)
     for n in a:
         assert torch.equal(a[n], b[n]), n
+
+
+def test_column_gradients_of_very_wide_rows():
+    """2^28 columns: a workgroup for 16 of them would make 2^32 threads, more than a launch may have."""
+    import selective_state_space_msm_amd as msm
+    D = 1 << 28
+    x = torch.randn(1, D, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn(1, D, device="cuda", dtype=torch.bfloat16)
+    mean, rstd = torch.full((1,), 0.25, device="cuda"), torch.full((1,), 1.5, device="cuda")
+    nan = lambda: torch.full((D,), float("nan"), device="cuda")
+    out = {"dweight": nan(), "dbias": nan()}
+    d = msm.msm_layer_norm_bwd(x, dy, mean, rstd, torch.ones(D, device="cuda"), bias_grad=True, out=out)
+    assert torch.equal(d["dbias"], dy[0].float())
+    # one product of two roundings each
+    want = dy[0].float() * ((x[0].float() - 0.25) * 1.5)
+    assert bool(((d["dweight"] - want).abs() <= 2.0 ** -22 * want.abs()).all())
