@@ -183,29 +183,46 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormArgs p) {
   }
 }
 
-// Rows too long for the registers: three walks over the row, the later ones from cache.
+// Sum over a workgroup, the same value in each thread.  `lds` must not be the next sum's.
+__device__ __forceinline__ double wide_sum(double v, double* lds) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+// Workgroups of a walk over rows: 2^24 of 256 threads would be 2^32 threads, more than a launch has.
+constexpr int64_t kLoopGroups = (int64_t)1 << 20;
+
+// Rows too long for the registers, or too long to be held in pieces of one element: three walks over
+// a row, the later ones from cache.  A thread's own sum has up to D / 256 terms, 2^22 of them, so the
+// sums are fp64: in fp32 the roundings of equal terms all go one way (the mean of 2^22 times 1.1 was
+// off by 1e-4).
 template <typename IO>
 __global__ __launch_bounds__(256) void norm_fwd_loop_kernel(const NormArgs p) {
   using T = io<IO>;
-  __shared__ float lds[8];
-  const int64_t at = (int64_t)blockIdx.x * p.D;
-  float sum = 0.f;
-  for (int64_t c = threadIdx.x; c < p.D; c += 256) sum += T::widen(T::load(p.x, at + c));
-  const float inv = 1.f / (float)p.D;
-  const float mean = row_sum<256>(sum, lds) * inv;
-  float sq = 0.f;
-  for (int64_t c = threadIdx.x; c < p.D; c += 256) {
-    const float d = T::widen(T::load(p.x, at + c)) - mean;
-    sq = fmaf(d, d, sq);
-  }
-  const float rstd = 1.f / sqrtf(row_sum<256>(sq, lds + 4) * inv + p.eps);
-  for (int64_t c = threadIdx.x; c < p.D; c += 256) {
-    const float d = (T::widen(T::load(p.x, at + c)) - mean) * rstd;
-    T::store(p.y, at + c, fmaf(d, p.weight ? p.weight[c] : 1.f, p.bias ? p.bias[c] : 0.f));
-  }
-  if (threadIdx.x == 0) {
-    if (p.mean) p.mean[blockIdx.x] = mean;
-    if (p.rstd) p.rstd[blockIdx.x] = rstd;
+  __shared__ double lds[8];
+  const double inv = 1. / (double)p.D;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t at = row * p.D;
+    double sum = 0;
+    for (int64_t c = threadIdx.x; c < p.D; c += 256) sum += (double)T::widen(T::load(p.x, at + c));
+    const float mean = (float)(wide_sum(sum, lds) * inv);
+    double sq = 0;
+    for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+      const double d = T::widen(T::load(p.x, at + c)) - mean;
+      sq = fma(d, d, sq);
+    }
+    const float rstd = 1.f / sqrtf((float)(wide_sum(sq, lds + 4) * inv) + p.eps);
+    for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+      const float d = (T::widen(T::load(p.x, at + c)) - mean) * rstd;
+      T::store(p.y, at + c, fmaf(d, p.weight ? p.weight[c] : 1.f, p.bias ? p.bias[c] : 0.f));
+    }
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
   }
 }
 
@@ -318,40 +335,41 @@ __global__ __launch_bounds__(BS) void norm_bwd_kernel(const NormArgs p) {
 template <typename IO>
 __global__ __launch_bounds__(256) void norm_bwd_loop_kernel(const NormArgs p) {
   using T = io<IO>;
-  __shared__ float lds[8];
-  const float inv = 1.f / (float)p.D;
-  const int64_t at = (int64_t)blockIdx.x * p.D;
-  const float mean = p.mean[blockIdx.x], rstd = p.rstd[blockIdx.x];
-  float a = 0.f, b = 0.f;
-  for (int64_t c = threadIdx.x; c < p.D; c += 256) {
-    const float u = T::widen(T::load(p.dy, at + c)) * (p.weight ? p.weight[c] : 1.f);
-    a += u;
-    b = fmaf(u, (T::widen(T::load(p.x, at + c)) - mean) * rstd, b);
-  }
-  row_sum2<256>(a, b, lds);
-  a *= inv;
-  b *= inv;
-  for (int64_t c = threadIdx.x; c < p.D; c += 256) {
-    const float u = T::widen(T::load(p.dy, at + c)) * (p.weight ? p.weight[c] : 1.f);
-    const float xh = (T::widen(T::load(p.x, at + c)) - mean) * rstd;
-    T::store(p.dx, at + c, rstd * (u - a - xh * b));
+  __shared__ double lds[8];
+  const double inv = 1. / (double)p.D;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t at = row * p.D;
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    double sa = 0, sb = 0;  // fp64 as in the forward
+    for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+      const float u = T::widen(T::load(p.dy, at + c)) * (p.weight ? p.weight[c] : 1.f);
+      sa += (double)u;
+      sb = fma((double)u, (double)((T::widen(T::load(p.x, at + c)) - mean) * rstd), sb);
+    }
+    const float a = (float)(wide_sum(sa, lds) * inv), b = (float)(wide_sum(sb, lds + 4) * inv);
+    for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+      const float u = T::widen(T::load(p.dy, at + c)) * (p.weight ? p.weight[c] : 1.f);
+      const float xh = (T::widen(T::load(p.x, at + c)) - mean) * rstd;
+      T::store(p.dx, at + c, rstd * (u - a - xh * b));
+    }
   }
 }
 
-// Column sums of the rows of a group, for rows that the loop kernel walked: a thread per column.
+// Column sums of the rows of a group, for rows that the loop kernel walked: a thread per column, in
+// fp64 as a group may have millions of rows.
 template <typename IO>
 __global__ __launch_bounds__(256) void norm_cols_kernel(const NormArgs p) {
   using T = io<IO>;
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= p.D) return;
-  float dw = 0.f, db = 0.f;
+  double dw = 0, db = 0;
   for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
     const float dy = T::widen(T::load(p.dy, row * p.D + c));
-    dw = fmaf(dy, (T::widen(T::load(p.x, row * p.D + c)) - p.mean[row]) * p.rstd[row], dw);
-    db += dy;
+    dw = fma((double)dy, (double)((T::widen(T::load(p.x, row * p.D + c)) - p.mean[row]) * p.rstd[row]), dw);
+    db += (double)dy;
   }
-  p.part[(int64_t)blockIdx.y * 2 * p.D + c] = dw;
-  p.part[(int64_t)blockIdx.y * 2 * p.D + p.D + c] = db;
+  p.part[(int64_t)blockIdx.y * 2 * p.D + c] = (float)dw;
+  p.part[(int64_t)blockIdx.y * 2 * p.D + p.D + c] = (float)db;
 }
 
 // Joins the column sums of all parts in fp64: CL columns a workgroup, 256 / CL threads a column.
@@ -419,11 +437,12 @@ hipError_t pick(const NormArgs& a, hipStream_t s) {
   MSM_NORM(4, 1) MSM_NORM(4, 2) MSM_NORM(4, 4) MSM_NORM(16, 2) MSM_NORM(16, 4) MSM_NORM(64, 2)
   MSM_NORM(64, 4) MSM_NORM(256, 2) MSM_NORM(256, 4) MSM_NORM(256, 8) MSM_NORM(256, 16)
 #undef MSM_NORM
+  const dim3 grid((unsigned)(a.rows < kLoopGroups ? a.rows : kLoopGroups));
   if (!BWD) {
-    hipLaunchKernelGGL((norm_fwd_loop_kernel<IO>), dim3((unsigned)a.rows), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((norm_fwd_loop_kernel<IO>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((norm_bwd_loop_kernel<IO>), dim3((unsigned)a.rows), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((norm_bwd_loop_kernel<IO>), grid, dim3(256), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
   hipLaunchKernelGGL((norm_cols_kernel<IO>), dim3((unsigned)((a.D + 255) / 256), (unsigned)a.groups),

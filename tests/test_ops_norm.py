@@ -135,3 +135,39 @@ def test_column_gradients_of_very_wide_rows():
     # one product of two roundings each
     want = dy[0].float() * ((x[0].float() - 0.25) * 1.5)
     assert bool(((d["dweight"] - want).abs() <= 2.0 ** -22 * want.abs()).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_long_rows(io):
+    """Rows past the registers: a thread's own sum has thousands of terms.  For equal terms the
+    roundings of an fp32 sum all go one way; mean, variance and column sums must not drift with them."""
+    import selective_state_space_msm_amd as msm
+    D = (1 << 22) + 3
+    x = torch.full((2, D), 1.1, device="cuda").to(DT[io])
+    b = torch.randn(D, device="cuda")
+    y, mean, rstd = msm.msm_layer_norm_fwd(x, None, b, eps=1e-4, return_stats=True)
+    assert torch.equal(mean, x[:, 0].float())
+    assert torch.equal(y, b.to(DT[io]).expand(2, D))
+    assert torch.allclose(rstd, torch.full_like(rstd, 100.0), rtol=1e-6)
+    # u = 0.7 everywhere and xh = 0.5: dx = rstd (u - u - xh mean(u xh)) = -0.175 rstd
+    dy = torch.full((2, D), 0.7, device="cuda").to(DT[io])
+    mean, rstd = x[:, 0].float() - 0.5, torch.ones(2, device="cuda")
+    dx = msm.msm_layer_norm_bwd(x, dy, mean, rstd)["dx"]
+    want = -0.25 * dy.double()
+    tol = 1e-6 if io == "f32" else 2.0 ** -8
+    assert bool(((dx.double() - want).abs() <= tol * want.abs()).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_column_gradients_over_many_wide_rows(io):
+    import selective_state_space_msm_amd as msm
+    rows, D = 40000, 4097 if io == "bf16" else 16385
+    x = torch.full((rows, D), 1.1, device="cuda").to(DT[io])
+    dy = torch.full((rows, D), 0.7, device="cuda").to(DT[io])
+    mean, rstd = torch.full((rows,), 0.4, device="cuda"), torch.full((rows,), 1.3, device="cuda")
+    d = msm.msm_layer_norm_bwd(x, dy, mean, rstd, torch.ones(D, device="cuda"), bias_grad=True)
+    # a rounding of the sum and two of xh
+    db = rows * dy[0].double()
+    dw = db * ((x[0].float() - 0.4) * 1.3).double()
+    assert bool(((d["dbias"].double() - db).abs() <= 2.0 ** -22 * db).all())
+    assert bool(((d["dweight"].double() - dw).abs() <= 2.0 ** -22 * dw).all())
