@@ -510,10 +510,12 @@ msm_status msm_grad_clip(const void* const* grads, void* const* out, const int64
   double* part = static_cast<double*>(workspace);
   st = clip_sums(grads, numel, dtypes, count, plan, part, s);
   if (st != MSM_OK) return st;
+  const bool joined = plan.parts > msm::kClipPartials;  // too many for every launch to read
+  if (joined && msm::launch_clip_norm(part, plan.parts, norm, s) != hipSuccess) return MSM_ERR_LAUNCH;
   for (int64_t k = plan.batches - 1; k >= 0; --k) {  // the tensors read last first
     const int64_t i0 = k * msm::kClipTensors, left = count - i0;
     clip_batch(grads, out, numel, dtypes, i0, (int)(left < msm::kClipTensors ? left : msm::kClipTensors), &b);
-    const hipError_t e = msm::launch_clip_scale(b, part, plan.parts, k == 0 ? norm : nullptr, max_norm, eps, plan.groups, s);
+    const hipError_t e = msm::launch_clip_scale(b, joined ? nullptr : part, plan.parts, joined || k == 0 ? norm : nullptr, max_norm, eps, plan.groups, s);
     if (e != hipSuccess) return MSM_ERR_LAUNCH;
   }
   return MSM_OK;

@@ -7,8 +7,9 @@
 // chunks of kClipChunk elements; a workgroup walks chunks at a fixed stride and leaves one
 // partial sum.  Squares are summed in fp64: at HBM's rate its cost is hidden, it cannot overflow,
 // and the sum depends on no order.  The scaling kernel joins the partial sums itself, in a fixed
-// order (2048 of them come from L2 in about the time a launch takes), and walks the chunks from
-// the last to the first: the gradients that the norm read last are still in the last-level cache.
+// order (2048 of them come from L2 in about the time a launch takes; above 4096 tensors there are
+// more, and one launch joins them first: 2^18 tensors in 2048 launches took 128 ms with a join in
+// each), and walks the chunks from the last to the first: the gradients that the norm read last are still in the last-level cache.
 // 24 layers of 2048, 404 MB of bf16: 322 us for the 1.21 GB read twice and written once (3.8 TB/s; a
 // copy reaches 5.15), 330 us with twice the workgroups; small tensors are bound by the launches and the host's lists.
 #include "ops_delta.hpp"
@@ -113,8 +114,8 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(const ClipBatch b, cons
                                                          int64_t parts, float* norm,
                                                          float max_norm, float eps) {
   __shared__ double lds[4];
-  const float total = norm_of(part, parts, lds);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  const float total = part ? norm_of(part, parts, lds) : *norm;
+  if (part && norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   // a NaN norm makes the coefficient NaN, and with it every gradient
   const float c = max_norm / (total + eps), coef = c > 1.f ? 1.f : c;
   const uint32_t chunks = b.first[b.count];

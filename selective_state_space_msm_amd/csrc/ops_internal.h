@@ -146,6 +146,7 @@ struct ClipBatch {
 
 hipError_t launch_clip_sum(const ClipBatch& b, double* part, int groups, hipStream_t s);
 hipError_t launch_clip_norm(const double* part, int64_t parts, float* norm, hipStream_t s);
+// part null: `norm` holds the norm already; else it is joined from the parts, and written if non-null
 hipError_t launch_clip_scale(const ClipBatch& b, const double* part, int64_t parts, float* norm,
                              float max_norm, float eps, int groups, hipStream_t s);
 

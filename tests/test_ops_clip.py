@@ -117,3 +117,45 @@ def test_graph_replays():
         ref = [torch.empty_like(t) for t in g]
         assert float(msm.msm_grad_clip(g, 0.5, out=ref)) == n
         assert all(torch.equal(x, y) for x, y in zip(got, ref))
+
+
+def test_very_many_tensors():
+    """The join of the partial sums happens once, not again in every scaling launch: with as many
+    launches as the sums took, clipping takes about twice the norm's time.  (Joined in each of the
+    2048 launches here, clipping took over ten times as long.)"""
+    import ctypes
+    import selective_state_space_msm_amd as msm
+    lib = msm.load_library()
+    count = 1 << 18
+    src = torch.randn(count, device="cuda")
+    out = torch.empty_like(src)
+    P = ctypes.c_void_p
+    addresses = lambda t: (P * count)(*range(t.data_ptr(), t.data_ptr() + 4 * count, 4))
+    a, b = addresses(src), addresses(out)
+    n, kind = (ctypes.c_int64 * count)(*[1] * count), (ctypes.c_int32 * count)()
+    norm = torch.empty((), device="cuda")
+    ws = torch.empty(msm.msm_grad_norm_workspace_bytes(count), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream()
+    tail = (P(norm.data_ptr()), P(ws.data_ptr()), ws.numel(), P(stream.cuda_stream))
+
+    def seconds(f):
+        best = float("inf")
+        for _ in range(3):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda.synchronize()
+            start.record()
+            assert f() == 0
+            end.record()
+            torch.cuda.synchronize()
+            best = min(best, start.elapsed_time(end) * 1e-3)
+        return best
+
+    t_norm = seconds(lambda: lib.msm_grad_norm(a, n, kind, count, *tail))
+    want = float(src.double().norm())
+    assert abs(float(norm) - want) <= 1e-7 * want
+    f = ctypes.c_float
+    t_clip = seconds(lambda: lib.msm_grad_clip(a, b, n, kind, count, f(0.5 * want), f(0.0), *tail))
+    assert abs(float(norm) - want) <= 1e-7 * want
+    assert bool(((out - 0.5 * src).abs() <= 3e-7 * src.abs()).all())
+    print("norm %.4f s, clipping %.4f s" % (t_norm, t_clip))
+    assert t_clip <= 5 * t_norm, (t_clip, t_norm)
