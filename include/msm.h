@@ -371,7 +371,9 @@ msm_status msm_layer_norm_bwd(const void* x, const float* weight, const void* dy
 
 /* Global 2-norm over count tensors: grads[i] points to numel[i] contiguous elements of dtype
  * dtypes[i] (MSM_F32 or MSM_BF16, mixed freely; numel[i] may be 0).  The three arrays are HOST
- * memory, read during the call only.  norm: one fp32 value on the device.  count may be 0. */
+ * memory, read during the call only.  norm: one fp32 value on the device.  count may be 0.
+ * Neither norm nor the workspace may overlap a tensor or each other (MSM_ERR_INVALID_ARG; gradients
+ * may share memory here). */
 size_t msm_grad_norm_workspace_bytes(int64_t count);
 msm_status msm_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* dtypes,
                          int64_t count, float* norm, void* workspace, size_t workspace_bytes,
@@ -379,8 +381,11 @@ msm_status msm_grad_norm(const void* const* grads, const int64_t* numel, const i
 
 /* Clipping by the global norm: out[i] = grads[i] * min(1, max_norm / (norm + eps)); norm
  * receives the norm before clipping.  out NULL, or out[i] == grads[i], scales in place (and
- * writes nothing when the factor is 1); otherwise out[i] must not overlap a gradient.  A norm
- * that is NaN makes every gradient NaN; an infinite norm scales by 0.  max_norm >= 0, eps >= 0.
+ * writes nothing when the factor is 1).  What is written (an out[i], a gradient scaled in place,
+ * norm, the workspace) must not overlap anything else of the call, so a gradient is not scaled in
+ * place twice (MSM_ERR_INVALID_ARG; MSM_ERR_WORKSPACE if the host has no memory for the check of a
+ * long list).  A norm that is NaN makes every gradient NaN; an infinite norm scales by 0.
+ * max_norm >= 0, eps >= 0.
  * Workspace as msm_grad_norm. */
 msm_status msm_grad_clip(const void* const* grads, void* const* out, const int64_t* numel,
                          const int32_t* dtypes, int64_t count, float max_norm, float eps,

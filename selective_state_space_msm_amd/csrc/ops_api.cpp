@@ -3,6 +3,10 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include <hip/hip_runtime_api.h>
 
 #include "../../include/msm.h"
@@ -256,6 +260,46 @@ msm_status clip_check(const void* const* src, const int64_t* numel, const int32_
   return MSM_OK;
 }
 
+// Memory of a call: what it reads, or what it writes (and perhaps reads).
+struct Extent {
+  uintptr_t lo, hi;
+  bool written;
+};
+
+// Nothing that is written may overlap anything else: the gradients (apart from one that is scaled in
+// place, which is its own output), the outputs, the norm and the workspace, in the order of their
+// addresses.
+msm_status clip_overlaps(const void* const* src, void* const* dst, const int64_t* numel,
+                         const int32_t* dtypes, int64_t count, bool in_place, const float* norm,
+                         const void* workspace, size_t workspace_bytes) {
+  constexpr int64_t kHere = 514;  // of an ordinary call; longer lists go to the heap
+  Extent here[kHere];
+  const int64_t most = (dst ? 2 : 1) * count + 2;
+  std::unique_ptr<Extent[]> heap(most > kHere ? new (std::nothrow) Extent[most] : nullptr);
+  if (most > kHere && !heap) return MSM_ERR_WORKSPACE;
+  Extent* const e = most > kHere ? heap.get() : here;
+  int64_t n = 0;
+  const auto add = [&](const void* p, size_t bytes, bool written) {
+    if (bytes) e[n++] = Extent{(uintptr_t)p, (uintptr_t)p + bytes, written};
+  };
+  for (int64_t i = 0; i < count; ++i) {
+    const size_t bytes = (size_t)numel[i] * (dtypes[i] == MSM_BF16 ? 2 : 4);
+    const bool own = dst ? dst[i] == src[i] : in_place;
+    add(src[i], bytes, own);
+    if (dst && !own) add(dst[i], bytes, true);
+  }
+  add(norm, sizeof(float), true);
+  add(workspace, workspace_bytes, true);
+  std::sort(e, e + n, [](const Extent& a, const Extent& b) { return a.lo < b.lo; });
+  uintptr_t end = 0, end_written = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (e[i].lo < (e[i].written ? end : end_written)) return MSM_ERR_INVALID_ARG;
+    if (e[i].hi > end) end = e[i].hi;
+    if (e[i].written && e[i].hi > end_written) end_written = e[i].hi;
+  }
+  return MSM_OK;
+}
+
 // Tensors [i0, i0 + count) as a launch's table; false when their chunks outnumber 2^31.
 bool clip_batch(const void* const* src, void* const* dst, const int64_t* numel,
                 const int32_t* dtypes, int64_t i0, int count, msm::ClipBatch* b) {
@@ -469,6 +513,8 @@ msm_status msm_grad_norm(const void* const* grads, const int64_t* numel, const i
   const ClipPlan plan = clip_plan(count);
   if (!workspace || workspace_bytes < (size_t)plan.parts * sizeof(double)) return MSM_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return MSM_ERR_INVALID_ARG;
+  st = clip_overlaps(grads, nullptr, numel, dtypes, count, false, norm, workspace, plan.parts * sizeof(double));
+  if (st != MSM_OK) return st;
   msm::ClipBatch b;
   for (int64_t k = 0; k < plan.batches; ++k) {
     const int64_t i0 = k * msm::kClipTensors, left = count - i0;
@@ -492,14 +538,13 @@ msm_status msm_grad_clip(const void* const* grads, void* const* out, const int64
     for (int64_t i = 0; i < count; ++i) {
       const size_t es = dtypes[i] == MSM_BF16 ? 2 : 4;
       if (numel[i] > 0 && (!out[i] || !aligned(out[i], es))) return MSM_ERR_INVALID_ARG;
-      // an output is its own gradient's buffer or apart from it
-      if (out[i] != grads[i] && overlaps(rng(out[i], numel[i] * es), rng(grads[i], numel[i] * es)))
-        return MSM_ERR_INVALID_ARG;
     }
   }
   const ClipPlan plan = clip_plan(count);
   if (!workspace || workspace_bytes < (size_t)plan.parts * sizeof(double)) return MSM_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return MSM_ERR_INVALID_ARG;
+  st = clip_overlaps(grads, out, numel, dtypes, count, true, norm, workspace, plan.parts * sizeof(double));
+  if (st != MSM_OK) return st;
   msm::ClipBatch b;
   for (int64_t k = 0; k < plan.batches; ++k) {
     const int64_t i0 = k * msm::kClipTensors, left = count - i0;

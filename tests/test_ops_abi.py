@@ -185,6 +185,34 @@ def test_clip_refusals(lib):
     assert lib.msm_grad_norm(None, None, None, 1, P(1), P(16), 1 << 20, None) == INVALID
 
 
+def test_clip_refuses_overlaps(lib):
+    """Each of these would let a write reach what another part of the call reads or writes."""
+    def call(clip, src, dst=None, n=16, norm=0x300000, ws=0x1000000):
+        k = len(src)
+        a, d = (P * k)(*src), None if dst is None else (P * k)(*dst)
+        nn, tt = (ctypes.c_int64 * k)(*([n] * k)), (ctypes.c_int32 * k)()
+        if clip:
+            return lib.msm_grad_clip(a, d, nn, tt, k, ctypes.c_float(1), ctypes.c_float(0), P(norm), P(ws), 1 << 20, None)
+        return lib.msm_grad_norm(a, nn, tt, k, P(norm), P(ws), 1 << 20, None)
+
+    two = (0x100000, 0x200000)
+    assert call(True, two, dst=(0x200000, 0x400000)) == INVALID  # another gradient
+    assert call(True, two, dst=(0x400000, 0x100020)) == INVALID  # inside another gradient
+    assert call(True, two, dst=(0x100000, 0x100000)) == INVALID  # in place, and then again
+    assert call(True, two, dst=(0x400000, 0x400020)) == INVALID  # another output
+    assert call(True, two, dst=(0x400000, 0x300000)) == INVALID  # the norm
+    assert call(True, two, dst=(0x400000, 0x1000100)) == INVALID  # the workspace
+    assert call(True, (0x100000, 0x200000, 0x100000)) == INVALID  # one gradient twice, in place
+    assert call(True, (0x100000, 0x100020)) == INVALID            # two that share elements, in place
+    many = [0x40000000 + 0x100 * i for i in range(3000)]
+    assert call(True, many[::-1] + [many[1700]]) == INVALID
+    assert call(True, many, dst=[x + (1 << 40) for x in many[:-1]] + [many[7]]) == INVALID
+    for clip in (False, True):
+        assert call(clip, (0x100000, 0x300000 - 60)) == INVALID   # the norm in a gradient
+        assert call(clip, (0x100000, 0x1000000)) == INVALID       # the workspace in a gradient
+        assert call(clip, two, norm=0x1000008) == INVALID         # the norm in the workspace
+
+
 def test_python_refusals():
     """Shapes, dtypes and strides are refused before the library is called (CPU tensors serve)."""
     q, v = torch.zeros(1, 4, 1, 8), torch.zeros(1, 4, 2, 8)
