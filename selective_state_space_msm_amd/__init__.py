@@ -196,8 +196,18 @@ def _check(t, name, shape, dtype, device):
         raise ValueError("%s must be contiguous" % name)
 
 
+def _on_gpu(stream, device):
+    """Refuses tensors that are not on a GPU, or not on the given stream's: a kernel would fault on
+    their addresses."""
+    if device.type != "cuda":
+        raise ValueError("expected tensors on a GPU, got %s" % device)
+    if stream is not None and getattr(stream, "device", device) != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+
+
 def _stream_handle(stream, device):
     import torch
+    _on_gpu(stream, device)
     s = torch.cuda.current_stream(device) if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -230,6 +240,10 @@ def _workspace(nbytes, workspace, device, own):
         return None, 0
     if workspace is None:
         workspace = own.empty(nbytes, torch.uint8, device)
+    elif workspace.device != device:
+        raise ValueError("workspace is on %s, expected %s" % (workspace.device, device))
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if workspace.numel() * workspace.element_size() < nbytes:
         raise MsmError(3, "workspace")
     return workspace, workspace.numel() * workspace.element_size()

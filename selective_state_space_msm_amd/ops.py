@@ -47,7 +47,7 @@ def declare(lib):
         getattr(lib, name).restype = ctypes.c_int
 
 
-from . import MsmError, _Owned, _workspace, load_library  # noqa: E402
+from . import MsmError, _on_gpu, _Owned, _workspace, load_library  # noqa: E402
 from . import _check as _explain  # noqa: E402
 from . import _io_code as _code  # noqa: E402
 
@@ -74,10 +74,9 @@ def _ptr(t):
 
 def _stream_handle(stream, device):
     import torch
+    _on_gpu(stream, device)
     if stream is not None:
         return stream.cuda_stream
-    if device.type != "cuda":
-        raise ValueError("expected tensors on a GPU, got %s" % device)
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 

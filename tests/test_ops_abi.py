@@ -246,3 +246,45 @@ def test_python_refusals():
         msm.msm_grad_norm([torch.zeros(4, dtype=torch.float64)])
     with pytest.raises(ValueError, match="differs"):
         msm.msm_grad_clip([torch.zeros(4)], 1.0, out=[torch.zeros(5)])
+
+
+class _Stream:
+    """Enough of a stream for a call that must be refused before it uses one."""
+    cuda_stream = 0
+    device = torch.device("cuda", 0)
+
+
+def test_host_tensors_are_refused_on_a_given_stream():
+    q, v, g = torch.zeros(1, 4, 1, 8), torch.zeros(1, 4, 2, 8), torch.zeros(1, 4, 2)
+    x, m = torch.zeros(3, 8), torch.zeros(3)
+    s = _Stream()
+    outs = {n: torch.zeros(shape) for n, shape in (("dq", q.shape), ("dk", q.shape), ("dv", v.shape), ("dg", g.shape),
+                                                   ("dbeta", g.shape))}
+    calls = [
+        lambda: msm.msm_delta_rule_fwd(q, q, v, g, g, stream=s),
+        lambda: msm.msm_delta_rule_bwd(q, q, v, g, g, v, stream=s, out=outs),
+        lambda: msm.msm_delta_rule_step(q[0], q[0], v[0], g[0], g[0], torch.zeros(4, 2, 8, 8), stream=s),
+        lambda: msm.msm_layer_norm_fwd(x, stream=s),
+        lambda: msm.msm_layer_norm_bwd(x, x, m, m, stream=s),
+        lambda: msm.msm_grad_norm([x], stream=s),
+        lambda: msm.msm_grad_clip([x], 1.0, stream=s),
+        lambda: msm.msm_scan_fwd(torch.zeros(1, 4, 8), torch.zeros(1, 4, 8), torch.zeros(8, 4), torch.zeros(1, 4, 4),
+                                 torch.zeros(1, 4, 4), 0.9, 1.0, stream=s),
+    ]
+    for f in calls:
+        with pytest.raises(ValueError, match="on a GPU"):
+            f()
+
+
+def test_workspace_is_checked():
+    """As the other arguments are: where it lies and how (meta tensors stand for another device's)."""
+    from selective_state_space_msm_amd import _Owned, _workspace
+    own, cpu = _Owned(None), torch.device("cpu")
+    with pytest.raises(ValueError, match="workspace is on meta"):
+        _workspace(64, torch.empty(64, dtype=torch.uint8, device="meta"), cpu, own)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        _workspace(64, torch.zeros(128, dtype=torch.uint8)[::2], cpu, own)
+    with pytest.raises(msm.MsmError):
+        _workspace(64, torch.zeros(63, dtype=torch.uint8), cpu, own)
+    assert _workspace(64, torch.zeros(16), cpu, own)[1] == 64
+    assert _workspace(0, None, cpu, own) == (None, 0)
