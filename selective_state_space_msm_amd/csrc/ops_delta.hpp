@@ -314,7 +314,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t head_rsrc(const void* base, in
 __device__ __forceinline__ void load_lds(u32x4 r, MSM_LDS void* lds, uint32_t off) {
 #ifdef __HIP_DEVICE_COMPILE__
   const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)lds);
+  // m0 is named as changed; the compiler, which reserves it, warns that it would not save it, and need
+  // not: no kernel here has another use of it
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "m0");
+#pragma clang diagnostic pop
 #endif
 }
 // The resource of make_rsrc_u32 in its four words.

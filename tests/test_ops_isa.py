@@ -31,7 +31,7 @@ def assembly(source, flags, tmp_path):
     out = str(tmp_path / "out.s")
     r = subprocess.run([build.HIPCC, *build.COMMON, *flags, "-S", "--cuda-device-only", source, "-o", out],
                        capture_output=True, text=True)
-    assert r.returncode == 0, r.stdout + r.stderr
+    assert r.returncode == 0 and "warning:" not in r.stderr, r.stdout + r.stderr
     with open(out) as f:
         return f.read()
 
@@ -81,3 +81,12 @@ def test_walks(tmp_path):
     flags = build._DELTA[0]
     seen, short = short_waits(assembly(os.path.join(build.CSRC, "ops_delta.hip"), flags, tmp_path))
     assert seen > 10 and not short, short
+
+
+def test_loads_alone_use_m0(tmp_path):
+    """The loads change m0 behind the compiler's back, which is sound while nothing else has a use for it."""
+    text = assembly(os.path.join(build.CSRC, "ops_delta.hip"), build._DELTA[4], tmp_path)
+    seen, short = short_waits(text)
+    uses = [line for line in text.splitlines() if re.search(r"\bm0\b", line.split(";")[0])]
+    assert len(uses) == seen and all(re.match(r"\s*s_mov_b32 m0, ", u) for u in uses)
+    assert not short, short
