@@ -377,3 +377,59 @@ def test_bf16_results_are_the_rounded_ones(Hk, H, K, V):
     ref = dict(want(d, K ** -0.5, True), **want(d, K ** -0.5, False))
     for n in ("o", "dq", "dk", "dv"):
         close(got[n], ref[n].bfloat16().double(), n, tol)
+
+
+# ---- more of the builds and of the inputs ------------------------------------------------------
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,K,V", [([1700], 24, 40), ([1650, 1600], 100, 24), ([1700], 100, 130), ([1700], 140, 40)])
+def test_segments_of_every_build(io, lens, K, V):
+    """Keys padded to 32, 128 and 256; ragged last chunks, one and two sequences."""
+    check(make(io, lens, 1, 1, K, V, seed=50 + K, packed=len(lens) > 1, g_scale=0.02))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V", [(32, 32), (128, 64)])
+def test_write_strengths_up_to_two(io, K, V):
+    """beta in (0, 2): 1 - beta |k|^2 stays within -1 and 1, so a state still forgets, but a write is up
+    to twice as large: twice the fp32 bound."""
+    d = make(io, [150, 90], 1, 2, K, V, seed=60 + K, packed=True, g_scale=0.1)
+    d["beta"] = 2 * d["beta"]
+    check(d, tol=None if io == "bf16" else 2 * TOL[torch.float32])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["no_decay", "strong_decay", "beta_zero"])
+def test_extremes_of_wide_heads(io, kind):
+    d = make(io, [150], 1, 2, 128, 96, seed=61)
+    if kind == "no_decay":
+        d["g"].zero_()
+    elif kind == "strong_decay":
+        d["g"] = -60 * torch.rand(150, 2)
+    else:
+        d["beta"][20:90] = 0
+    check(d)
+
+
+def test_backward_of_alike_keys():
+    """One key throughout and full writes, as in the forward's test: the errors pass through the chunk's
+    system twice, once for e and once, transposed, for dv, each time up to 8 times as large."""
+    d = make("f32", [150], 1, 2, 32, 32, seed=8)
+    d["k"][:] = d["k"][:1]
+    d["beta"].fill_(1.0)
+    d["g"].zero_()
+    check(d, tol=64 * TOL[torch.float32])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_lowest_values_that_are_never_written(io):
+    """A value of the type's lowest at a token with beta = 0 and no adjoint changes nothing else."""
+    d = make(io, [100], 1, 2, 64, 32, seed=62)
+    d["beta"][40] = 0.0
+    clean = dict(d, v=d["v"].clone())
+    clean["v"][40] = 0.0
+    d["v"][40] = torch.finfo(DT[io]).min
+    o, S = run_fwd(d)
+    ref = want(clean, 64 ** -0.5, False)
+    close(o, ref["o"], "o")
+    close(S, ref["S"], "last_S")
