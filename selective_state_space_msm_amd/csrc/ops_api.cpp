@@ -54,9 +54,9 @@ struct DeltaShape {
   int KP, C, seg_len;
 };
 
-// Chunks of a segment, 0 for none.  Segments cost 2.4 times a walk's work, so they pay where whole
+// Chunks of a segment, 0 for none.  Segments cost 2.2 to 2.5 times a walk's work, so they pay where whole
 // sequences would leave two thirds of the 256 CUs without a workgroup (Bt = 1, L = 65536, H = 16,
-// V = 128: 32 workgroups, 3.3 ms whole and 1.1 ms in segments); there are enough then for one a CU.
+// V = 128: 32 workgroups, 3.8 ms whole and 1.03 ms in segments); there are enough then for one a CU.
 // Packed sequences are seldom alike and the longest decides, so there half of the CUs is the bound
 // (8191 fp32 tokens in 9 sequences, H = 6, V = 80: segments of 8 chunks 70 + 77 us, of 11, which leave
 // no second round of workgroups, 88 + 86 us).

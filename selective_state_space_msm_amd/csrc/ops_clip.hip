@@ -6,12 +6,13 @@
 // so nothing is copied to the device first and a launch can be captured.  Tensors are cut into
 // chunks of kClipChunk elements; a workgroup walks chunks at a fixed stride and leaves one
 // partial sum.  Squares are summed in fp64: at HBM's rate its cost is hidden, it cannot overflow,
-// and the sum depends on no order.  The scaling kernel joins the partial sums itself, in a fixed
+// and the order is fixed.  The scaling kernel joins the partial sums itself, in a fixed
 // order (2048 of them come from L2 in about the time a launch takes; above 4096 tensors there are
 // more, and one launch joins them first: 2^18 tensors in 2048 launches took 128 ms with a join in
 // each), and walks the chunks from the last to the first: the gradients that the norm read last are still in the last-level cache.
-// 24 layers of 2048, 404 MB of bf16: 322 us for the 1.21 GB read twice and written once (3.8 TB/s; a
-// copy reaches 5.15), 330 us with twice the workgroups; small tensors are bound by the launches and the host's lists.
+// 24 layers of 2048, 606 MB of bf16: 320 us for the 1.82 GB that are read twice and written once
+// (5.7 TB/s with the cache's part; a copy reaches 5.15; the norm alone 114 us, 5.3 TB/s), 330 us with
+// twice the workgroups; small tensors are bound by the launches and the host's lists.
 #include "ops_delta.hpp"
 
 namespace msm {

@@ -191,7 +191,7 @@ __device__ __forceinline__ void write_tri(uint16_t* to, const MSM_LDS float* fro
 }
 
 // Key columns that prep stages at a time: 64 at least, so that their planes go to memory in whole
-// 128-byte lines (32 columns of fp32 keys of 128: 93 us and a slower scan after it, 313 us; 64: 88, 300).
+// 128-byte lines (32 columns of fp32 keys of 128: 93 us and a slower scan after it, 313 us; 64: 90, 297).
 constexpr int prep_columns() {
   int ks = KP;
   while (ks > 32 && 2 * kIn * C * ks * 2 > 50 * 1024) ks /= 2;
@@ -201,8 +201,8 @@ constexpr int prep_columns() {
 // Bound by the latency of its steps (load, Gram products, inverse, store), so the LDS is kept to 53 KB
 // for three workgroups a CU (fp32 keys of 128: 67 KB for two): wide rows are staged some columns at a
 // time, and the inverse and the outgoing matrices take the place of the keys and queries once the
-// Gram products are done.  Bt=4 L=4096 H=32 K=128 bf16: 117 us, 262 MB written (the chunk matrices in
-// their parts); 170 us with 100 KB, one workgroup a CU.  Bt=4 L=2048 H=16 K=128 fp32, backward: 88 us;
+// Gram products are done.  Bt=4 L=4096 H=32 K=128 bf16: 112 us, 312 MB written (the chunk matrices in
+// their parts); 170 us with 100 KB, one workgroup a CU.  Bt=4 L=2048 H=16 K=128 fp32, backward: 90 us;
 // 120 us with whole rows, 117 KB.
 template <bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(const DeltaArgs p) {
@@ -689,8 +689,8 @@ __device__ __forceinline__ void scan_chunk(F fetch, const DeltaArgs& p, const Wa
 // trip through LDS.  Keys, queries and chunk matrices are left factors, shared by the four
 // wavefronts in LDS and loaded there a chunk ahead.  Sequential in the chunks, hence bound by a
 // chunk's chain of products (K S, T R, K^T U and the two of O) at one wavefront a SIMD: Bt=4 L=4096
-// H=32 K=V=128 bf16, 256 workgroups: 260-290 us for 64 chunks, 668 TFLOP/s of matrix products (54% of
-// what a large one reaches).  BWD stores what the backward needs and leaves O out: 295 us at
+// H=32 K=V=128 bf16, 256 workgroups: 271 us for 64 chunks, 855 TFLOP/s of matrix products (69% of
+// what a large one reaches).  BWD stores what the backward needs and leaves O out: 297 us at
 // Bt=4 L=2048 H=16 fp32, where 128 workgroups leave half of the CUs idle.
 template <bool BWD>
 __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p) {
@@ -777,10 +777,10 @@ __global__ __launch_bounds__(64 * kWavesScan) void scan_kernel(const DeltaArgs p
 // sequences are cut into segments of seg_len chunks.  A segment maps the state affinely, S -> F S + G:
 // one walk over all segments at once finds G (from a zero state) and F (from the identity, with V
 // zero, as K more columns), a short second kernel runs through the segments' maps, and the walk
-// proper starts every segment from its state.  That is about 2.4 times the work, the segments' maps
-// at a higher rate than the walk's: Bt=1 L=65536 H=16 K=V=128 bf16 in 8 or 9 segments a head, 530 us
-// (940 TFLOP/s of matrix products, 76% of a large product's), 23 us, and 510 us for the walk, against
-// 3.3 ms for the walk of whole sequences.
+// proper starts every segment from its state.  That is 2.2 to 2.5 times the work, the segments' maps
+// at a higher rate than the walk's: Bt=1 L=65536 H=16 K=V=128 bf16 in 8 or 9 segments a head, 476 us
+// (1040 TFLOP/s of matrix products, 84% of a large product's), 22 us, and 528 us for the walk, against
+// 3.8 ms for the walk of whole sequences.
 
 struct StateChunk {
   uint16_t k[kIn * kRows];
@@ -1038,8 +1038,8 @@ __device__ __forceinline__ void rev_chunk(FP p_used, FT tm_used, const DeltaArgs
 // Split and layout as the scan's; per chunk it has six products where the scan has three (W from two,
 // dV, Y, dS0 from two) and three chunk matrices.  These have one buffer each in LDS, filled again as
 // soon as every wavefront has read it; keys and queries have two where the LDS allows.  Bound like the
-// scan: 325 us at Bt=4 L=2048 H=16 K=V=128 fp32 (128 workgroups), 490 us for 16384 packed tokens, H=16
-// bf16, the longest sequence's 72 chunks at 6.8 us.
+// scan: 327 us at Bt=4 L=2048 H=16 K=V=128 fp32 (128 workgroups), 499 us for 16384 packed tokens, H=16
+// bf16, the longest sequence's 72 chunks at 6.9 us.
 template <bool kTwo>
 __global__ __launch_bounds__(64 * kWavesScan) void rev_kernel(const DeltaArgs p) {
   __shared__ __attribute__((aligned(16))) KeyRows lds0;
@@ -1143,11 +1143,11 @@ constexpr int PW = kWavesGrad >= 2 * MT ? 2 : 1, PT = MT / PW;  // wavefronts fo
 // All chunks at once.  A wavefront accumulates kTilesGrad tiles of 16 keys of dQ and dK over the value
 // heads that share them and, with others, the token pairs dO U^T and dV U^T; states and their adjoints
 // are read from memory straight into the factors' registers, once each, while columns of dO, dV and U
-// pass through LDS, all of them fetched one step ahead.  Bound by issue at two wavefronts a SIMD (4 to
-// 6 vector instructions a matrix one, most of them cutting fp32 values into parts) and its 256
-// registers: 366 us at Bt=4 L=2048 H=16 K=V=128 fp32 (388 TFLOP/s of matrix products), 510 us for
-// 16384 packed tokens, 8 key heads, H=16 bf16 (152 bytes spilled; 784 us with four wavefronts and
-// loads at their uses).
+// pass through LDS, all of them fetched one step ahead.  Bound by issue at one (fp32) or two (bf16)
+// wavefronts a SIMD, 4 vector instructions a matrix one, most of them cutting fp32 values into parts,
+// and by its 256 registers: 360 us at Bt=4 L=2048 H=16 K=V=128 fp32 (393 TFLOP/s of matrix products),
+// 578 us for 16384 packed tokens, 8 key heads, H=16 bf16 (336 TFLOP/s, 196 bytes spilled; with two
+// parts a factor 510 us, and 784 us then with four wavefronts and loads at their uses).
 __global__ __launch_bounds__(64 * kWavesGrad) void grad_kernel(const DeltaArgs p) {
   constexpr int THREADS = 64 * kWavesGrad;
   constexpr int kStage = (kIn + 2 * TP) * C * LDV, kPair = 2 * TP * C * LDT;

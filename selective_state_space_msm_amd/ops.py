@@ -345,7 +345,8 @@ def msm_grad_norm(grads, *, workspace=None, stream=None):
 
 def msm_grad_clip(grads, max_norm, *, eps=1e-6, out=None, workspace=None, stream=None):
     """Scales a list of gradients by min(1, max_norm / (norm + eps)), in place or into the tensors
-    of `out`.  Returns the norm before clipping, a float32 tensor without dimensions."""
+    of `out`.  What is written must not overlap anything else: in place, no tensor is listed twice.
+    Returns the norm before clipping, a float32 tensor without dimensions."""
     import torch
     lib = load_library()
     own = _Owned(stream)
