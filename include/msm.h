@@ -391,6 +391,81 @@ msm_status msm_grad_clip(const void* const* grads, void* const* out, const int64
                          const int32_t* dtypes, int64_t count, float max_norm, float eps,
                          float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Operators at a language model's ends and between its blocks: token embedding, the norms around
+ * a block with its gate and residual scale, cross entropy over a vocabulary.  The conventions
+ * above hold for them; arrays may begin at any address that is a multiple of their element's size.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Token embedding: y[t] = scale * table[ids[t]], ids (tokens,) int64, table (V, D) in table_io,
+ * y (tokens, D) in io (any combination of the two types).  An id outside [0, V) gives a row of
+ * zeros.  1 <= tokens, V < 2^31, 1 <= D <= 2^24, scale finite. */
+msm_status msm_embed_fwd(const int64_t* ids, const void* table, void* y, int64_t tokens, int64_t V,
+                         int64_t D, float scale, msm_dtype table_io, msm_dtype io, void* stream);
+
+/* Gradient of the table: dtable[v] = scale * sum of dy[t] over {t: ids[t] = v}, every row written
+ * (zeros for a row without a token).  Ids outside [0, V) take no part.  Tokens are sorted by id and
+ * added in the order of the batch: no atomics, the same result every time. */
+size_t msm_embed_bwd_workspace_bytes(int64_t tokens, int64_t V, int64_t D);
+msm_status msm_embed_bwd(const int64_t* ids, const void* dy, void* dtable, int64_t tokens,
+                         int64_t V, int64_t D, float scale, msm_dtype table_io, msm_dtype io,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norms after a block and before the next one, with the block's gate and residual scale, on
+ * rows of D elements; RMS(x) = x / sqrt(mean(x^2) + eps):
+ *     r_out = r + scale * post_weight * RMS(o) * silu(z)     (rounded to the io type)
+ *     y     = weight * RMS(r_out)
+ * r (the residual stream), o (the block's output), z (its gate), r_out, y: (rows, D) io; weight,
+ * post_weight: (D,) fp32, NULL meaning ones; rstd, post_rstd: (rows,) fp32, the reciprocal roots of
+ * the two norms, written when non-NULL.  z NULL: no gate.  o NULL: y = weight * RMS(r) alone, and
+ * post_weight, z, r_out and post_rstd are NULL.  r_out may be r itself (the stream is updated in
+ * place); no other overlap.  1 <= rows < 2^31, 1 <= D <= 2^30, scale finite, eps >= 0 and finite. */
+msm_status msm_block_norm_fwd(const void* r, const float* weight, const void* o,
+                              const float* post_weight, const void* z, void* r_out, void* y,
+                              float* rstd, float* post_rstd, int64_t rows, int64_t D, float scale,
+                              float eps, msm_dtype io, void* stream);
+
+/* Gradients of sum(dy * y) + sum(dr_out * r_out) (dr_out NULL: zero) from the forward's r_out and
+ * statistics: dr (also r_out's own), do, dz in the io type, dweight, dpost_weight (D,) fp32, each
+ * written when non-NULL.  Without o: r_out is r, and do, dz, dpost_weight and the block's inputs
+ * are NULL.  dz is given exactly when z is. */
+size_t msm_block_norm_bwd_workspace_bytes(int64_t rows, int64_t D, msm_dtype io);
+msm_status msm_block_norm_bwd(const void* r_out, const void* dy, const float* rstd,
+                              const float* weight, const void* o, const float* post_rstd,
+                              const float* post_weight, const void* z, const void* dr_out, void* dr,
+                              void* do_, void* dz, float* dweight, float* dpost_weight,
+                              int64_t rows, int64_t D, float scale, msm_dtype io, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Cross entropy of a linear layer over a vocabulary, without its logits in memory:
+ *     l[t][v] = scale * x[t] . weight[v],  lse[t] = log sum_v exp(l[t][v]),
+ *     loss[t] = lse[t] - l[t][targets[t]]
+ * x (T, D), weight (V, D) io; targets (T,) int64; loss, lse (T,) fp32, lse may be NULL.  A row whose
+ * target lies outside [0, V) is left out: its loss and lse are 0, whatever it holds (the other rows'
+ * results do not depend on it).  Logits, sums and statistics are fp32; fp32 inputs are multiplied in
+ * three bf16 parts that keep 24 bits.
+ * Requirements: T, V, D >= 1, T and V <= 2^22, D <= 2^16 (else MSM_ERR_UNSUPPORTED), scale finite.
+ * bf16 weights with D a multiple of 8 that begin at a multiple of 16 bytes are read where they are;
+ * others are copied a piece at a time into the workspace. */
+size_t msm_linear_cross_entropy_fwd_workspace_bytes(int64_t T, int64_t V, int64_t D, msm_dtype io);
+msm_status msm_linear_cross_entropy_fwd(const void* x, const void* weight, const int64_t* targets,
+                                        float* loss, float* lse, int64_t T, int64_t V, int64_t D,
+                                        float scale, msm_dtype io, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* Gradients of sum(dloss * loss) + sum(dlse * lse) (dlse NULL: zero) from the forward's lse:
+ *     g[t][v] = scale * ((dloss[t] + dlse[t]) exp(l[t][v] - lse[t]) - dloss[t] [v = targets[t]])
+ *     dx = g weight,  dweight = g^T x
+ * dx (T, D), dweight (V, D) io; dweight may be NULL.  A row that is left out has dx = 0 and adds
+ * nothing to dweight.  The vocabulary is taken in pieces, whose g (in bf16 for bf16 inputs, 24 bits
+ * for fp32 ones) is in the workspace; sums are fp32. */
+size_t msm_linear_cross_entropy_bwd_workspace_bytes(int64_t T, int64_t V, int64_t D, msm_dtype io);
+msm_status msm_linear_cross_entropy_bwd(const void* x, const void* weight, const int64_t* targets,
+                                        const float* lse, const float* dloss, const float* dlse,
+                                        void* dx, void* dweight, int64_t T, int64_t V, int64_t D,
+                                        float scale, msm_dtype io, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

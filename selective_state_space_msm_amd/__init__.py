@@ -16,7 +16,8 @@ fallback implementation.
                                    delta_softplus=True)        # also dz, ddelta_bias
 
 The operators of the block around the scan (gated delta rule, layer norm, gradient clipping) are
-in ``ops`` and are importable from here under their C names too.
+in ``ops``, those at a language model's ends and between its blocks (embedding, block norm, linear
+cross entropy) in ``lm``; all are importable from here under their C names too.
 """
 from __future__ import annotations
 
@@ -128,6 +129,7 @@ def load_library():
                                                     P]
     lib.msm_scan_complex_bwd.restype = ctypes.c_int
     ops.declare(lib)
+    lm.declare(lib)
     _lib = lib
     return lib
 
@@ -670,3 +672,13 @@ from .ops import *  # noqa: E402,F401,F403
 
 __all__ += ops.__all__
 EXPORTED_SYMBOLS += ops.SYMBOLS
+
+# ----------------------------------------------------------------------------------------------
+# operators at a language model's ends and between its blocks
+# ----------------------------------------------------------------------------------------------
+
+from . import lm  # noqa: E402
+from .lm import *  # noqa: E402,F401,F403
+
+__all__ += lm.__all__
+EXPORTED_SYMBOLS += lm.SYMBOLS

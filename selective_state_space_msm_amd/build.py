@@ -25,7 +25,8 @@ SOURCES = ([("msm_api.cpp", ()), ("msm_launch.hip", ()), ("msm_bwd_wide.hip", ()
             ("msm_step.hip", ()), ("msm_cfwd.hip", ()), ("msm_cbwd.hip", ())]
            + [("msm_fwd.hip", f) for f in _PARTS] + [("msm_bwd.hip", f) for f in _PARTS]
            + [("ops_api.cpp", ()), ("ops_delta_step.hip", ()), ("ops_norm.hip", ()),
-              ("ops_clip.hip", ())] + [("ops_delta.hip", f) for f in _DELTA])
+              ("ops_clip.hip", ()), ("lm_api.cpp", ()), ("lm_embed.hip", ()),
+              ("lm_block_norm.hip", ()), ("lm_xent.hip", ())] + [("ops_delta.hip", f) for f in _DELTA])
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

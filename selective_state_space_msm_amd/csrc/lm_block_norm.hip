@@ -1,0 +1,458 @@
+// The norms after a block and before the next one, fused with the block's gate, its residual
+// scale and the residual sum (gfx950), forward and backward.
+//   q = 1 / sqrt(mean(o^2) + eps),  oh = o q,  a = oh pw
+//   r' = r + scale a silu(z)                    (held in the I/O type; without o, r' = r)
+//   p = 1 / sqrt(mean(r'^2) + eps),  rh = r' p,  y = rh w
+//   u = dy w,        G  = dr' + p (u - rh mean(u rh)) = dr,          dw  = sum over rows of dy rh
+//   c = scale G silu(z),  v = c pw,  do = q (v - oh mean(v oh)),     dpw = sum over rows of c oh
+//   dz = scale G a silu'(z)
+//
+// Both passes are bound by HBM: o, z, r read and r', y written (forward), o, z, r', dy, dr' read
+// and dr, do, dz written (backward), each once.  A row lives in the registers of T threads, E
+// elements each, and the next row's loads are issued before the present one is reduced.  A piece
+// of a row is 16 bytes also where rows begin at odd addresses (the hardware takes unaligned
+// 16-byte accesses); only a row's last piece may be taken element by element.  The backward's
+// column sums stay in registers over the rows of a workgroup and are joined by a second kernel
+// in a fixed order.  Rows past the registers are walked in memory with fp64 sums.
+#include "lm_internal.h"
+#include "ops_internal.h"
+#include "ops_row.hpp"
+
+namespace msm {
+namespace {
+
+// Sum over the T threads of a row, the same value in each.  With more than a wavefront, `lds` must
+// not be the next sum's (the one after it may use it: a thread that writes there has passed the
+// barrier in between).
+template <int T>
+__device__ __forceinline__ float group_sum(float v, float* lds) {
+  constexpr int W = T < 64 ? T : 64;
+#pragma unroll
+  for (int m = W / 2; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) v += lds[i];
+  }
+  return v;
+}
+
+constexpr int block_threads(int T) { return T < 256 ? 256 : T; }
+constexpr int64_t kRowGroups = 2048;
+
+template <typename IO, int T, int E>
+__global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const BlockNormArgs p) {
+  constexpr int VEC = Chunk<IO>::VEC, NV = E / VEC, RW = block_threads(T) / T;
+  __shared__ float lds[2][T > 64 ? T / 64 : 1];
+  int turn = 0;
+  const int t = threadIdx.x % T;
+  const int64_t step = (int64_t)gridDim.x * RW;
+  int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / T;
+  if (row >= p.rows) return;  // whole rows leave: no sum crosses rows
+  float w[NV][VEC], pw[NV][VEC];
+  Chunk<IO> no[NV], nz[NV], nr[NV];
+  const bool block = p.o != nullptr, gate = p.z != nullptr;
+  const auto fetch = [&](int i, int64_t at) {
+    const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
+    if (n <= 0) return;
+    nr[i].load(p.r, at + c, n);
+    if (block) no[i].load(p.o, at + c, n);
+    if (gate) nz[i].load(p.z, at + c, n);
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = ((int64_t)i * T + t) * VEC;
+    nr[i].zero();
+    no[i].zero();
+    nz[i].zero();
+    fetch(i, row * p.D);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[i][e] = p.weight && c + e < p.D ? p.weight[c + e] : 1.f;
+      pw[i][e] = p.post_weight && c + e < p.D ? p.post_weight[c + e] : 1.f;
+    }
+  }
+  const float inv = 1.f / (float)p.D;
+  for (; row < p.rows; row += step) {
+    float x[NV][VEC], f[NV][VEC];
+    const int64_t at = row * p.D, next = (row + step) * p.D;
+    const bool more = row + step < p.rows;
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      nr[i].get(x[i]);
+      if (block) {
+        no[i].get(f[i]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) q = fmaf(f[i][e], f[i][e], q);
+        if (gate) {
+          float z[VEC];
+          nz[i].get(z);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) f[i][e] *= silu_f(z[e]);
+        }
+      }
+      if (more) fetch(i, next);
+    }
+    if (block) {
+      q = 1.f / sqrtf(group_sum<T>(q, lds[turn]) * inv + p.eps);
+      turn ^= 1;
+      const float qs = q * p.scale;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[i][e] = fmaf(f[i][e] * qs, pw[i][e], x[i][e]);
+        Chunk<IO> held;
+        held.set(x[i]);
+        held.get(x[i]);
+        if (n > 0) held.store(p.r_out, at + c, n);
+        // past the row's end the inputs are zero, but a gate of zero keeps them so
+      }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s = fmaf(x[i][e], x[i][e], s);
+    const float rstd = 1.f / sqrtf(group_sum<T>(s, lds[turn]) * inv + p.eps);
+    turn ^= 1;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[i][e] = x[i][e] * rstd * w[i][e];
+      Chunk<IO> out;
+      out.set(x[i]);
+      if (n > 0) out.store(p.y, at + c, n);
+    }
+    if (t == 0) {
+      if (p.rstd) p.rstd[row] = rstd;
+      if (p.post_rstd) p.post_rstd[row] = q;
+    }
+  }
+}
+
+template <typename IO, int T, int E>
+__global__ __launch_bounds__(block_threads(T)) void block_norm_bwd_kernel(const BlockNormArgs p) {
+  constexpr int VEC = Chunk<IO>::VEC, NV = E / VEC, BS = block_threads(T), RW = BS / T;
+  constexpr int kGroup = T > 64 ? T : 64, NG = BS / kGroup;
+  __shared__ float lds[2][T > 64 ? T / 64 : 1];
+  __shared__ float cols[NG > 1 ? NG : 1][NG > 1 ? T * VEC : 1];
+  int turn = 0;
+  const int t = threadIdx.x % T;
+  const float inv = 1.f / (float)p.D;
+  const int64_t step = (int64_t)gridDim.x * RW;
+  const bool block = p.o != nullptr, gate = p.z != nullptr, residual = p.dr_out != nullptr;
+  float w[NV][VEC], pw[NV][VEC], dw[NV][VEC], dpw[NV][VEC];
+  Chunk<IO> ny[NV], nr[NV], nd[NV], no[NV], nz[NV];
+  int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / T;
+  const auto fetch = [&](int i, int64_t at) {
+    const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
+    if (n <= 0) return;
+    ny[i].load(p.dy, at + c, n);
+    nr[i].load(p.r_out, at + c, n);
+    if (residual) nd[i].load(p.dr_out, at + c, n);
+    if (block) no[i].load(p.o, at + c, n);
+    if (gate) nz[i].load(p.z, at + c, n);
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = ((int64_t)i * T + t) * VEC;
+    ny[i].zero();
+    nr[i].zero();
+    nd[i].zero();
+    no[i].zero();
+    nz[i].zero();
+    if (row < p.rows) fetch(i, row * p.D);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[i][e] = p.weight && c + e < p.D ? p.weight[c + e] : 1.f;
+      pw[i][e] = p.post_weight && c + e < p.D ? p.post_weight[c + e] : 1.f;
+      dw[i][e] = dpw[i][e] = 0.f;
+    }
+  }
+  for (; row < p.rows; row += step) {  // whole rows leave: no sum crosses rows
+    const int64_t at = row * p.D, next = (row + step) * p.D;
+    const bool more = row + step < p.rows;
+    const float rstd = p.rstd[row], q = block ? p.post_rstd[row] : 0.f;
+    float u[NV][VEC], h[NV][VEC], g[NV][VEC], o[NV][VEC], z[NV][VEC];
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      ny[i].get(u[i]);
+      nr[i].get(h[i]);
+      nd[i].get(g[i]);
+      no[i].get(o[i]);
+      nz[i].get(z[i]);
+      if (more) fetch(i, next);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        h[i][e] *= rstd;
+        dw[i][e] = fmaf(u[i][e], h[i][e], dw[i][e]);
+        u[i][e] *= w[i][e];
+        a = fmaf(u[i][e], h[i][e], a);
+      }
+    }
+    a = group_sum<T>(a, lds[turn]) * inv;
+    turn ^= 1;
+    float b = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
+      Chunk<IO> out;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[i][e] = fmaf(rstd, u[i][e] - h[i][e] * a, g[i][e]);
+      out.set(g[i]);
+      if (n > 0) out.store(p.dr, at + c, n);
+      if (!block) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        o[i][e] *= q;
+        g[i][e] *= p.scale;
+      }
+      if (gate) {
+        float dz[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const Logistic l = logistic_f(z[i][e]);
+          dz[e] = g[i][e] * (o[i][e] * pw[i][e]) * (l.s * fmaf(z[i][e], l.sc, 1.f));
+          g[i][e] *= z[i][e] * l.s;
+        }
+        out.set(dz);
+        if (n > 0) out.store(p.dz, at + c, n);
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        dpw[i][e] = fmaf(g[i][e], o[i][e], dpw[i][e]);
+        g[i][e] *= pw[i][e];
+        b = fmaf(g[i][e], o[i][e], b);
+      }
+    }
+    if (!block) continue;
+    b = group_sum<T>(b, lds[turn]) * inv;
+    turn ^= 1;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
+      Chunk<IO> out;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[i][e] = q * (g[i][e] - o[i][e] * b);
+      out.set(g[i]);
+      if (n > 0) out.store(p.do_, at + c, n);
+    }
+  }
+  if (!p.part) return;
+  float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float(&v)[VEC] = which ? dpw[i] : dw[i];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int m = T; m < 64; m *= 2) v[e] += __shfl_xor(v[e], m, 64);
+      if constexpr (NG > 1) {
+        __syncthreads();  // the last round has been read
+        if (T >= 64 || (threadIdx.x & 63) < T)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) cols[threadIdx.x / kGroup][t * VEC + e] = v[e];
+        __syncthreads();
+        for (int k = threadIdx.x; k < T * VEC; k += BS) {
+          float s = 0.f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) s += cols[g][k];
+          const int64_t c = (int64_t)i * T * VEC + k;
+          if (c < p.D) part[which * p.D + c] = s;
+        }
+      } else {
+        const int64_t c = ((int64_t)i * T + t) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (c + e < p.D) part[which * p.D + c + e] = v[e];
+      }
+    }
+  }
+}
+
+// ---- rows past the registers: walks over memory, sums in fp64 as a thread's own may be long ----
+
+constexpr int64_t kLoopGroups = (int64_t)1 << 20;  // 2^24 workgroups of 256 would be 2^32 threads
+
+template <typename IO>
+__device__ __forceinline__ float at_of(const void* p, int64_t i) {
+  return io<IO>::widen(io<IO>::load(p, i));
+}
+
+template <typename IO>
+__global__ __launch_bounds__(256) void block_norm_fwd_loop_kernel(const BlockNormArgs p) {
+  __shared__ double lds[8];
+  const double inv = 1. / (double)p.D;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t at = row * p.D;
+    const void* r = p.r;
+    float q = 0.f;
+    double s = 0;
+    if (p.o) {
+      for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+        const double v = at_of<IO>(p.o, at + c);
+        s = fma(v, v, s);
+      }
+      q = 1.f / sqrtf((float)(wide_sum(s, lds) * inv) + p.eps);
+      s = 0;
+      for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+        float f = at_of<IO>(p.o, at + c) * (q * p.scale);
+        if (p.z) f *= silu_f(at_of<IO>(p.z, at + c));
+        io<IO>::store(p.r_out, at + c, fmaf(f, p.post_weight ? p.post_weight[c] : 1.f, at_of<IO>(p.r, at + c)));
+        const double v = at_of<IO>(p.r_out, at + c);
+        s = fma(v, v, s);
+      }
+      r = p.r_out;
+    } else {
+      for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+        const double v = at_of<IO>(p.r, at + c);
+        s = fma(v, v, s);
+      }
+    }
+    const float rstd = 1.f / sqrtf((float)(wide_sum(s, lds + 4) * inv) + p.eps);
+    for (int64_t c = threadIdx.x; c < p.D; c += 256)
+      io<IO>::store(p.y, at + c, at_of<IO>(r, at + c) * rstd * (p.weight ? p.weight[c] : 1.f));
+    if (threadIdx.x == 0) {
+      if (p.rstd) p.rstd[row] = rstd;
+      if (p.post_rstd) p.post_rstd[row] = q;
+    }
+    if (!p.o) __syncthreads();  // the one sum of a row: the next row's uses the same words
+  }
+}
+
+// G of an element, from the row's mean(u rh)
+template <typename IO>
+__device__ __forceinline__ float residual_grad(const BlockNormArgs& p, int64_t i, int64_t c, float rstd, float mean) {
+  const float h = at_of<IO>(p.r_out, i) * rstd, u = at_of<IO>(p.dy, i) * (p.weight ? p.weight[c] : 1.f);
+  return fmaf(rstd, u - h * mean, p.dr_out ? at_of<IO>(p.dr_out, i) : 0.f);
+}
+
+template <typename IO>
+__global__ __launch_bounds__(256) void block_norm_bwd_loop_kernel(const BlockNormArgs p) {
+  __shared__ double lds[8];
+  const double inv = 1. / (double)p.D;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t at = row * p.D;
+    const float rstd = p.rstd[row];
+    double s = 0;
+    for (int64_t c = threadIdx.x; c < p.D; c += 256)
+      s = fma((double)(at_of<IO>(p.dy, at + c) * (p.weight ? p.weight[c] : 1.f)), (double)(at_of<IO>(p.r_out, at + c) * rstd), s);
+    const float a = (float)(wide_sum(s, lds) * inv);
+    if (threadIdx.x == 0) p.row_mean[row] = a;
+    const float q = p.o ? p.post_rstd[row] : 0.f;
+    s = 0;
+    for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+      const float g = residual_grad<IO>(p, at + c, c, rstd, a);
+      if (!p.o) {
+        io<IO>::store(p.dr, at + c, g);
+        continue;
+      }
+      float f = p.scale * g;
+      const float oh = at_of<IO>(p.o, at + c) * q, pw = p.post_weight ? p.post_weight[c] : 1.f;
+      if (p.z) {
+        const float z = at_of<IO>(p.z, at + c);
+        const Logistic l = logistic_f(z);
+        io<IO>::store(p.dz, at + c, f * (oh * pw) * (l.s * fmaf(z, l.sc, 1.f)));
+        f *= z * l.s;
+      }
+      s = fma((double)(f * pw), (double)oh, s);
+    }
+    if (!p.o) {
+      __syncthreads();
+      continue;
+    }
+    const float b = (float)(wide_sum(s, lds + 4) * inv);
+    for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+      const float g = residual_grad<IO>(p, at + c, c, rstd, a);
+      float f = p.scale * g;
+      if (p.z) f *= silu_f(at_of<IO>(p.z, at + c));
+      const float oh = at_of<IO>(p.o, at + c) * q;
+      io<IO>::store(p.do_, at + c, q * (f * (p.post_weight ? p.post_weight[c] : 1.f) - oh * b));
+      io<IO>::store(p.dr, at + c, g);
+    }
+  }
+}
+
+template <typename IO>
+__global__ __launch_bounds__(256) void block_norm_cols_kernel(const BlockNormArgs p) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= p.D) return;
+  double dw = 0, dpw = 0;
+  for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
+    const int64_t i = row * p.D + c;
+    const float rstd = p.rstd[row];
+    dw = fma((double)at_of<IO>(p.dy, i), (double)(at_of<IO>(p.r_out, i) * rstd), dw);
+    if (p.o) {
+      float f = p.scale * residual_grad<IO>(p, i, c, rstd, p.row_mean[row]);
+      if (p.z) f *= silu_f(at_of<IO>(p.z, i));
+      dpw = fma((double)f, (double)(at_of<IO>(p.o, i) * p.post_rstd[row]), dpw);
+    }
+  }
+  p.part[(int64_t)blockIdx.y * 2 * p.D + c] = (float)dw;
+  p.part[(int64_t)blockIdx.y * 2 * p.D + p.D + c] = (float)dpw;
+}
+
+hipError_t join(const BlockNormArgs& a, hipStream_t s) {
+  NormArgs n{};
+  n.part = a.part;
+  n.D = a.D;
+  n.dweight = a.dweight;
+  n.dbias = a.dpost_weight;
+  return launch_norm_join(n, a.groups, s);
+}
+
+template <typename IO, int T, int E>
+hipError_t go(const BlockNormArgs& a, bool bwd, hipStream_t s) {
+  constexpr int BS = block_threads(T), RW = BS / T;
+  if (!bwd) {
+    const int64_t all = (a.rows + RW - 1) / RW;
+    hipLaunchKernelGGL((block_norm_fwd_kernel<IO, T, E>), dim3((unsigned)(all < kRowGroups ? all : kRowGroups)), dim3(BS), 0, s, a);
+    return hipGetLastError();
+  }
+  if constexpr (T < 1024 || E == 8) {
+    hipLaunchKernelGGL((block_norm_bwd_kernel<IO, T, E>), dim3((unsigned)a.groups), dim3(BS), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || !a.part ? e : join(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <typename IO>
+hipError_t pick(const BlockNormArgs& a, bool bwd, hipStream_t s) {
+  const BlockNormShape f = block_norm_shape(a.D, bwd);
+#define MSM_ROWS(TT, EE) \
+  if (f.T == TT && f.E == EE) return go<IO, TT, EE>(a, bwd, s);
+  MSM_ROWS(16, 8) MSM_ROWS(16, 16) MSM_ROWS(64, 8) MSM_ROWS(64, 16) MSM_ROWS(256, 8) MSM_ROWS(256, 16)
+  MSM_ROWS(1024, 8) MSM_ROWS(1024, 16)
+#undef MSM_ROWS
+  const dim3 grid((unsigned)(a.rows < kLoopGroups ? a.rows : kLoopGroups));
+  if (!bwd) {
+    hipLaunchKernelGGL((block_norm_fwd_loop_kernel<IO>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((block_norm_bwd_loop_kernel<IO>), grid, dim3(256), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.part) return e;
+  hipLaunchKernelGGL((block_norm_cols_kernel<IO>), dim3((unsigned)((a.D + 255) / 256), (unsigned)a.groups), dim3(256), 0, s, a);
+  e = hipGetLastError();
+  return e != hipSuccess ? e : join(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_block_norm_fwd(const BlockNormArgs& a, int io_bf16, hipStream_t s) {
+  return io_bf16 ? pick<bf16_storage>(a, false, s) : pick<float>(a, false, s);
+}
+hipError_t launch_block_norm_bwd(const BlockNormArgs& a, int io_bf16, hipStream_t s) {
+  return io_bf16 ? pick<bf16_storage>(a, true, s) : pick<float>(a, true, s);
+}
+
+}  // namespace msm

@@ -1,0 +1,452 @@
+// Token embedding (gfx950): y_t = scale table[id_t], and its gradient
+// dtable[v] = scale sum over {t: id_t = v} of dy_t.  Ids outside [0, V) give a row of zeros and take
+// no part in the gradient.
+//
+// The forward is a copy: bound by HBM (rows read, y written), or by the launch for a few tokens.
+//
+// The gradient reads dy once and writes dtable once, most of its rows zero.  Tokens are sorted by id
+// (stable, digits of up to 9 bits), so that a vocabulary row's places stand side by side in the order
+// of the batch, and every row is summed in that order without atomics.  A frequent token has
+// thousands of places (of log-uniform ids over 65536, the first has 6% of them): aligned runs of 32
+// places that belong to one row are summed beforehand, and runs of 32 such sums again, so that a row
+// adds at most 62 places, 62 sums of 32 and one sum per 1024 places (those in fp64).
+//
+// A sorting pass is two launches: every wavefront counts the digits of its own places, then each
+// workgroup finds its wavefronts' first positions from the counts of all (at most 256 wavefronts,
+// so there is no launch for a scan) and moves the places.  Ranks among 64 places come from ballots
+// over the digit's bits.  Up to 4096 places are sorted by one workgroup in LDS.
+#include "lm_internal.h"
+#include "ops_row.hpp"
+
+namespace msm {
+namespace {
+
+constexpr int kBins = 1 << kEmbedMostBits;
+constexpr int64_t kMostGroups = (int64_t)1 << 20;
+
+// ---- forward ----
+
+// A thread makes 16 bytes of y.
+template <typename TB, typename IO>
+__global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedArgs p, int64_t pieces) {
+  constexpr int VEC = Chunk<IO>::VEC, TV = Chunk<TB>::VEC;
+  const int64_t all = p.tokens * pieces;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / pieces, c = (i - t * pieces) * VEC, n = p.D - c;
+    const int64_t id = p.ids[t];
+    float x[VEC > TV ? VEC : TV];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+    if (id >= 0 && id < p.V) {
+      if constexpr (VEC >= TV) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += TV) {
+          Chunk<TB> r;
+          r.zero();
+          if (n > e) r.load(p.table, id * p.D + c + e, n - e);
+          r.get(x + e);
+        }
+      } else {  // 16 bytes of fp32 from 8 of bf16
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (e < n) x[e] = io<TB>::widen(io<TB>::load(p.table, id * p.D + c + e));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] *= p.scale;
+    Chunk<IO> out;
+    out.set(x);
+    out.store(p.y, t * p.D + c, n);
+  }
+}
+
+// ---- sorting ----
+
+__device__ __forceinline__ uint32_t key_of(const EmbedArgs& p, int64_t i) {
+  const int64_t id = p.ids[i];
+  return id >= 0 && id < p.V ? (uint32_t)id : (uint32_t)p.V;
+}
+
+// Lanes whose digit is this lane's, among the lanes that take part.
+__device__ __forceinline__ uint64_t same_digit(uint32_t digit, int bits, bool on) {
+  uint64_t same = __ballot(on);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t set = __ballot((digit >> b) & 1);
+    same &= (digit >> b) & 1 ? set : ~set;
+  }
+  return same;
+}
+
+// Counts of a wavefront's digits, in its own bins.
+__device__ __forceinline__ void count_digit(uint32_t* bins, uint32_t digit, int bits, bool on, int lane) {
+  const uint64_t same = same_digit(digit, bits, on);
+  if (on && (same & ((1ull << lane) - 1)) == 0) bins[digit] += __popcll(same);
+}
+// The place of this lane's digit, after which the wavefront's bins stand behind its places.
+__device__ __forceinline__ uint32_t take_place(uint32_t* bins, uint32_t digit, int bits, bool on, int lane) {
+  const uint64_t same = same_digit(digit, bits, on), below = same & ((1ull << lane) - 1);
+  const uint32_t first = on ? bins[digit] : 0;
+  if (on && below == 0) bins[digit] = first + __popcll(same);
+  return first + __popcll(below);
+}
+
+// A wavefront works alone on its bins: LDS answers its accesses in order, the compiler must not reorder them.
+__device__ __forceinline__ void wave_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+constexpr int kSortWaves = 8;
+
+// pass 0 reads the ids, later ones what the pass before left
+template <bool FIRST>
+__device__ __forceinline__ void place_of(const EmbedArgs& p, int pass, int64_t i, uint32_t* key, uint32_t* pos) {
+  if constexpr (FIRST) {
+    *key = key_of(p, i);
+    *pos = (uint32_t)i;
+  } else {
+    *key = p.key[(pass - 1) & 1][i];
+    *pos = p.pos[(pass - 1) & 1][i];
+  }
+}
+
+template <bool FIRST>
+__global__ __launch_bounds__(64 * kSortWaves) void embed_count_kernel(const EmbedArgs p, int pass) {
+  __shared__ uint32_t lds[kSortWaves][kBins];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = 1 << p.bits;
+  const int64_t w = (int64_t)blockIdx.x * kSortWaves + wave;
+  uint32_t* bins = lds[wave];
+  for (int b = lane; b < nb; b += 64) bins[b] = 0;
+  wave_order();
+  for (int64_t k = 0; k < p.per; k += 64) {
+    const int64_t i = w * p.per + k + lane;
+    const bool on = w < p.waves && i < p.tokens;
+    uint32_t key = 0, pos;
+    if (on) place_of<FIRST>(p, pass, i, &key, &pos);
+    count_digit(bins, (key >> (pass * p.bits)) & (nb - 1), p.bits, on, lane);
+    wave_order();
+  }
+  if (w < p.waves)
+    for (int b = lane; b < nb; b += 64) p.hist[w * nb + b] = bins[b];
+}
+
+// Exclusive sums of one value a thread over a workgroup of N threads, N <= 1024.
+template <int N>
+__device__ __forceinline__ uint32_t exclusive_sum(uint32_t v, uint32_t* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t s = v;
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) {
+    const uint32_t o = __shfl_up(s, m, 64);
+    if (lane >= m) s += o;
+  }
+  if (lane == 63) lds[wave] = s;
+  __syncthreads();
+  uint32_t before = 0;
+  for (int i = 0; i < wave; ++i) before += lds[i];
+  return before + s - v;
+}
+
+template <bool FIRST>
+__global__ __launch_bounds__(64 * kSortWaves) void embed_move_kernel(const EmbedArgs p, int pass) {
+  static_assert(64 * kSortWaves == kBins, "a thread for every bin");
+  __shared__ uint32_t lds[kSortWaves][kBins];
+  __shared__ uint32_t sums[kSortWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = 1 << p.bits, b = threadIdx.x;
+  const int64_t w0 = (int64_t)blockIdx.x * kSortWaves;
+  // this thread's bin: what stands before the workgroup's wavefronts, and in all
+  uint32_t before = 0, total = 0;
+  if (b < nb) {
+    int64_t w = 0;
+    for (; w + 8 <= p.waves; w += 8) {
+      uint32_t c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = p.hist[(w + j) * nb + b];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        before += w + j < w0 ? c[j] : 0;
+        total += c[j];
+      }
+    }
+    for (; w < p.waves; ++w) {
+      const uint32_t c = p.hist[w * nb + b];
+      before += w < w0 ? c : 0;
+      total += c;
+    }
+  }
+  uint32_t at = exclusive_sum<kBins>(total, sums) + before;
+  if (b < nb)
+    for (int j = 0; j < kSortWaves; ++j) {
+      lds[j][b] = at;
+      if (w0 + j < p.waves) at += p.hist[(w0 + j) * nb + b];
+    }
+  __syncthreads();
+  const int64_t w = w0 + wave;
+  if (w >= p.waves) return;
+  uint32_t* bins = lds[wave];
+  for (int64_t k = 0; k < p.per; k += 64) {
+    const int64_t i = w * p.per + k + lane;
+    const bool on = i < p.tokens;
+    uint32_t key = 0, pos = 0;
+    if (on) place_of<FIRST>(p, pass, i, &key, &pos);
+    const uint32_t to = take_place(bins, (key >> (pass * p.bits)) & (nb - 1), p.bits, on, lane);
+    wave_order();
+    if (on) {
+      p.key[pass & 1][to] = key;
+      p.pos[pass & 1][to] = pos;
+    }
+  }
+}
+
+// All passes in one workgroup, for up to kEmbedSmall places.
+constexpr int kSmallWaves = 16;
+__global__ __launch_bounds__(64 * kSmallWaves) void embed_sort_small_kernel(const EmbedArgs p) {
+  __shared__ uint32_t keys[2][kEmbedSmall];
+  __shared__ uint16_t places[2][kEmbedSmall];
+  __shared__ uint32_t lds[kSmallWaves][kBins];
+  __shared__ uint32_t sums[kSmallWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = 1 << p.bits, b = threadIdx.x;
+  const int n = (int)p.tokens, per = ((n + kSmallWaves * 64 - 1) / (kSmallWaves * 64)) * 64;
+  for (int i = threadIdx.x; i < n; i += 64 * kSmallWaves) {
+    keys[0][i] = key_of(p, i);
+    places[0][i] = (uint16_t)i;
+  }
+  uint32_t* bins = lds[wave];
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int from = pass & 1, shift = pass * p.bits;
+    for (int j = lane; j < nb; j += 64) bins[j] = 0;
+    __syncthreads();
+    for (int k = 0; k < per; k += 64) {
+      const int i = wave * per + k + lane;
+      const bool on = i < n;
+      count_digit(bins, ((on ? keys[from][i] : 0) >> shift) & (nb - 1), p.bits, on, lane);
+      wave_order();
+    }
+    __syncthreads();
+    uint32_t total = 0;
+    if (b < nb)
+      for (int j = 0; j < kSmallWaves; ++j) total += lds[j][b];
+    uint32_t at = exclusive_sum<64 * kSmallWaves>(total, sums);
+    if (b < nb)
+      for (int j = 0; j < kSmallWaves; ++j) {
+        const uint32_t c = lds[j][b];
+        lds[j][b] = at;
+        at += c;
+      }
+    __syncthreads();
+    for (int k = 0; k < per; k += 64) {
+      const int i = wave * per + k + lane;
+      const bool on = i < n;
+      const uint32_t key = on ? keys[from][i] : 0;
+      const uint32_t to = take_place(bins, (key >> shift) & (nb - 1), p.bits, on, lane);
+      wave_order();
+      if (on) {
+        keys[from ^ 1][to] = key;
+        places[from ^ 1][to] = places[from][i];
+      }
+    }
+    __syncthreads();
+  }
+  const int last = p.passes & 1, out = (p.passes - 1) & 1;
+  for (int i = threadIdx.x; i < n; i += 64 * kSmallWaves) {
+    p.key[out][i] = keys[last][i];
+    p.pos[out][i] = places[last][i];
+  }
+}
+
+// ---- sums ----
+
+// x += 16 bytes of the rows pos[i0 ... i1) of dy, eight of them in flight
+template <typename IO>
+__device__ __forceinline__ void add_places(const EmbedArgs& p, const uint32_t* pos, int64_t i0, int64_t i1, int64_t c,
+                                           float (&x)[Chunk<IO>::VEC]) {
+  constexpr int VEC = Chunk<IO>::VEC;
+  const int64_t n = p.D - c;
+  int64_t i = i0;
+  for (; i + 8 <= i1; i += 8) {
+    Chunk<IO> r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j].load(p.dy, (int64_t)pos[i + j] * p.D + c, n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float v[VEC];
+      r[j].get(v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] += v[e];
+    }
+  }
+  for (; i < i1; ++i) {
+    Chunk<IO> r;
+    r.load(p.dy, (int64_t)pos[i] * p.D + c, n);
+    float v[VEC];
+    r.get(v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] += v[e];
+  }
+}
+
+// Sums of the runs [32 k, 32 k + 32) of places that belong to one vocabulary row.
+template <typename IO>
+__global__ __launch_bounds__(256) void embed_run_kernel(const EmbedArgs p, int64_t runs, int64_t pieces) {
+  constexpr int VEC = Chunk<IO>::VEC;
+  const uint32_t *key = p.key[(p.passes - 1) & 1], *pos = p.pos[(p.passes - 1) & 1];
+  for (int64_t k = blockIdx.x; k < runs; k += gridDim.x) {
+    const int64_t i0 = k * kEmbedRun;
+    if (key[i0] != key[i0 + kEmbedRun - 1] || key[i0] >= p.V) continue;
+    for (int64_t q = threadIdx.x; q < pieces; q += 256) {
+      float x[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+      add_places<IO>(p, pos, i0, i0 + kEmbedRun, q * VEC, x);
+      const int64_t c = q * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (c + e < p.D) p.part[0][k * p.D + c + e] = x[e];
+    }
+  }
+}
+
+// The same over 32 runs of one vocabulary row.
+__global__ __launch_bounds__(256) void embed_run2_kernel(const EmbedArgs p, int64_t runs) {
+  const uint32_t* key = p.key[(p.passes - 1) & 1];
+  for (int64_t k = blockIdx.x; k < runs; k += gridDim.x) {
+    const int64_t i0 = k * kEmbedRun * kEmbedRun;
+    if (key[i0] != key[i0 + kEmbedRun * kEmbedRun - 1] || key[i0] >= p.V) continue;
+    for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+      float x = 0.f;
+#pragma unroll 8
+      for (int j = 0; j < kEmbedRun; ++j) x += p.part[0][(k * kEmbedRun + j) * p.D + c];
+      p.part[1][k * p.D + c] = x;
+    }
+  }
+}
+
+constexpr int kRowsOf = 16;  // vocabulary rows of a workgroup
+
+// x += sums j0 ... j1 of a level
+template <int VEC, typename F>
+__device__ __forceinline__ void add_sums(const float* part, int64_t j0, int64_t j1, int64_t D, int64_t c, F (&x)[VEC]) {
+#pragma unroll 4
+  for (int64_t j = j0; j < j1; ++j)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (c + e < D) x[e] += part[j * D + c + e];
+}
+
+template <typename TB, typename IO>
+__global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int64_t pieces) {
+  constexpr int VEC = Chunk<IO>::VEC, TV = Chunk<TB>::VEC;
+  __shared__ uint32_t first[kRowsOf + 1];
+  const uint32_t *key = p.key[(p.passes - 1) & 1], *pos = p.pos[(p.passes - 1) & 1];
+  const int64_t groups = (p.V + kRowsOf - 1) / kRowsOf;
+  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
+    const int64_t v0 = g * kRowsOf;
+    if (threadIdx.x <= kRowsOf) {  // the first place of a row, or of what comes after it
+      const int64_t v = v0 + threadIdx.x;
+      int64_t lo = 0, hi = p.tokens;
+      while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if ((int64_t)key[mid] < v)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      first[threadIdx.x] = (uint32_t)lo;
+    }
+    __syncthreads();
+    const int rows = (int)(p.V - v0 < kRowsOf ? p.V - v0 : kRowsOf);
+    for (int64_t k = threadIdx.x; k < rows * pieces; k += 256) {
+      const int64_t r = k / pieces, c = (k - r * pieces) * VEC, n = p.D - c;
+      const int64_t i0 = first[r], i1 = first[r + 1];
+      float x[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+      if (i1 - i0 < 2 * kEmbedRun) {
+        add_places<IO>(p, pos, i0, i1, c, x);
+      } else {
+        constexpr int R = kEmbedRun;
+        const int64_t j0 = (i0 + R - 1) / R, j1 = i1 / R;          // whole runs
+        const int64_t m0 = (j0 + R - 1) / R, m1 = j1 / R;          // whole runs of runs
+        add_places<IO>(p, pos, i0, j0 * R, c, x);
+        if (p.part[1] && m0 < m1) {
+          add_sums<VEC>(p.part[0], j0, m0 * R, p.D, c, x);
+          double wide[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) wide[e] = x[e];
+          add_sums<VEC>(p.part[1], m0, m1, p.D, c, wide);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) x[e] = (float)wide[e];
+          add_sums<VEC>(p.part[0], m1 * R, j1, p.D, c, x);
+        } else {
+          add_sums<VEC>(p.part[0], j0, j1, p.D, c, x);
+        }
+        add_places<IO>(p, pos, j1 * R, i1, c, x);
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] *= p.scale;
+      const int64_t at = (v0 + r) * p.D + c;
+      if constexpr (VEC >= TV) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += TV) {
+          Chunk<TB> out;
+          out.set(x + e);
+          if (n > e) out.store(p.dtable, at + e, n - e);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (e < n) io<TB>::store(p.dtable, at + e, x[e]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+unsigned groups_of(int64_t n) { return (unsigned)(n < 1 ? 1 : (n < kMostGroups ? n : kMostGroups)); }
+
+template <bool FIRST>
+hipError_t sort_pass(const EmbedArgs& a, int pass, hipStream_t s) {
+  const dim3 grid((unsigned)((a.waves + kSortWaves - 1) / kSortWaves)), block(64 * kSortWaves);
+  hipLaunchKernelGGL(embed_count_kernel<FIRST>, grid, block, 0, s, a, pass);
+  hipLaunchKernelGGL(embed_move_kernel<FIRST>, grid, block, 0, s, a, pass);
+  return hipGetLastError();
+}
+
+template <typename TB, typename IO>
+hipError_t fwd(const EmbedArgs& a, hipStream_t s) {
+  const int64_t pieces = (a.D + Chunk<IO>::VEC - 1) / Chunk<IO>::VEC;
+  hipLaunchKernelGGL((embed_fwd_kernel<TB, IO>), dim3(groups_of((a.tokens * pieces + 255) / 256)), dim3(256), 0, s, a, pieces);
+  return hipGetLastError();
+}
+
+template <typename TB, typename IO>
+hipError_t bwd(const EmbedArgs& a, hipStream_t s) {
+  const int64_t pieces = (a.D + Chunk<IO>::VEC - 1) / Chunk<IO>::VEC;
+  if (a.tokens <= kEmbedSmall) {
+    hipLaunchKernelGGL(embed_sort_small_kernel, dim3(1), dim3(64 * kSmallWaves), 0, s, a);
+  } else {
+    hipError_t e = sort_pass<true>(a, 0, s);
+    for (int pass = 1; pass < a.passes && e == hipSuccess; ++pass) e = sort_pass<false>(a, pass, s);
+    if (e != hipSuccess) return e;
+  }
+  if (a.tokens >= 2 * kEmbedRun) {
+    const int64_t runs = a.tokens / kEmbedRun;
+    hipLaunchKernelGGL((embed_run_kernel<IO>), dim3(groups_of(runs)), dim3(256), 0, s, a, runs, pieces);
+    if (a.part[1]) {
+      const int64_t runs2 = runs / kEmbedRun;
+      hipLaunchKernelGGL(embed_run2_kernel, dim3(groups_of(runs2)), dim3(256), 0, s, a, runs2);
+    }
+  }
+  hipLaunchKernelGGL((embed_rows_kernel<TB, IO>), dim3(groups_of((a.V + kRowsOf - 1) / kRowsOf)), dim3(256), 0, s, a, pieces);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_embed_fwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s) {
+  if (table_bf16) return io_bf16 ? fwd<bf16_storage, bf16_storage>(a, s) : fwd<bf16_storage, float>(a, s);
+  return io_bf16 ? fwd<float, bf16_storage>(a, s) : fwd<float, float>(a, s);
+}
+hipError_t launch_embed_bwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s) {
+  if (table_bf16) return io_bf16 ? bwd<bf16_storage, bf16_storage>(a, s) : bwd<bf16_storage, float>(a, s);
+  return io_bf16 ? bwd<float, bf16_storage>(a, s) : bwd<float, float>(a, s);
+}
+
+}  // namespace msm

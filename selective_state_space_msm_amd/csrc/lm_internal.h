@@ -1,0 +1,114 @@
+// Internal interface between the C-ABI layer (lm_api.cpp) and the kernels of the operators at a
+// language model's ends and between its blocks: embedding, block norm, linear cross entropy.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace msm {
+
+// ---- embedding ----
+
+struct EmbedArgs {
+  const int64_t* ids;  // (tokens,)
+  const void* table;   // (V, D) table type
+  void* y;             // (tokens, D) I/O type
+  const void* dy;      // backward
+  void* dtable;        // (V, D) table type
+  // workspace of the backward
+  uint32_t* key[2];    // (tokens,) ids, V for the positions without a token
+  uint32_t* pos[2];    // (tokens,) their positions
+  uint32_t* hist;      // [wavefronts][bins]
+  float* part[2];      // sums of 32 and of 1024 places of the sorted list, D each
+  int64_t tokens, V, D;
+  float scale;
+  int32_t waves, per;  // wavefronts of a sorting pass and their places (a multiple of 64)
+  int32_t bits;        // of a digit
+  int32_t passes;
+};
+
+constexpr int kEmbedMostBits = 9;      // of a digit: 512 bins
+constexpr int kEmbedSmall = 4096;      // places that one workgroup sorts in LDS
+constexpr int kEmbedRun = 32;          // places of a sum of the first level, and sums of the second
+hipError_t launch_embed_fwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s);
+hipError_t launch_embed_bwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s);
+
+// ---- block norm ----
+
+struct BlockNormArgs {
+  const void* r;             // (rows, D) I/O type
+  const void* o;             // or null
+  const void* z;             // or null
+  const float* weight;       // (D,) or null (ones)
+  const float* post_weight;  // (D,) or null (ones)
+  void* r_out;               // written by the forward when o is given, read by the backward
+  void* y;
+  float* rstd;
+  float* post_rstd;
+  const void* dy;            // backward
+  const void* dr_out;        // or null
+  void* dr;
+  void* do_;
+  void* dz;
+  float* dweight;
+  float* dpost_weight;
+  float* part;               // [groups][2][D] column sums, or null
+  float* row_mean;           // (rows,) of the first reduction, for rows past the registers
+  int64_t rows, D;
+  float scale, eps;
+  int32_t groups;
+};
+
+// T threads hold a row, E elements each; T = 0: the row is walked in memory.
+struct BlockNormShape {
+  int T, E;
+};
+constexpr BlockNormShape block_norm_shape(int64_t D, bool bwd) {
+  for (int T = 16; T <= 1024; T *= 4)
+    for (int E = 8; E <= (bwd && T == 1024 ? 8 : 16); E *= 2)
+      if (D <= (int64_t)T * E) return BlockNormShape{T, E};
+  return BlockNormShape{0, 0};
+}
+hipError_t launch_block_norm_fwd(const BlockNormArgs& a, int io_bf16, hipStream_t s);
+hipError_t launch_block_norm_bwd(const BlockNormArgs& a, int io_bf16, hipStream_t s);
+
+// ---- linear cross entropy ----
+
+// What a row that takes part needs in the epilogues.
+struct XentRow {
+  float lse, both, dloss;  // both: dloss + dlse
+  int32_t target;
+};
+
+struct XentArgs {
+  const void* x;           // (T, D) I/O type
+  const void* w;           // (V, D)
+  const int64_t* targets;  // (T,)
+  float* loss;             // (T,) forward
+  float* lse;              // (T,) written by the forward (may be null there), read by the backward
+  const float* dloss;      // (T,) backward
+  const float* dlse;       // (T,) or null
+  void* dx;                // (T, D)
+  void* dw;                // (V, D) or null
+  // workspace
+  int32_t* count;          // rows that take part
+  int32_t* map;            // (T,) their places in x
+  int32_t* inverse;        // (T,) and back, -1 for a row that is left out
+  XentRow* rows;           // (T,)
+  void* xp;                // [planes][T][DP] bf16 parts of the rows that take part
+  void* wp;                // [planes][piece][DP] the same of a piece of w, where w is not read directly
+  float* stat;             // forward: [tiles of the vocabulary][T][2] largest logit, sum of exponentials
+  float* at_target;        // forward: (T,) logit of the target
+  void* g;                 // backward: [planes][T][piece] gradient of a piece's logits
+  float* dx_sum;           // backward: [T][DQ]
+  int64_t T, V, D, DP, DQ, piece;
+  float scale;
+  int32_t planes;          // 1, or 3 for fp32
+  int32_t w_direct;
+  int32_t wide;            // tiles of 256 x 256, else of 128 x 128
+};
+hipError_t launch_xent_fwd(const XentArgs& a, int io_bf16, hipStream_t s);
+hipError_t launch_xent_bwd(const XentArgs& a, int io_bf16, hipStream_t s);
+
+}  // namespace msm

@@ -1,0 +1,552 @@
+// Cross entropy of a linear layer over a vocabulary, without keeping its logits (gfx950).
+//   l_tv = scale x_t . W_v,  lse_t = log sum_v exp(l_tv),  loss_t = lse_t - l_t,target(t)
+//   g_tv = scale ((dloss_t + dlse_t) exp(l_tv - lse_t) - dloss_t [v = target(t)])
+//   dx = g W,  dW = g^T x
+//
+// All of it is matrix products: 2 T V D operations forward, 6 T V D backward (the logits again, dx,
+// dW), on bf16 matrix cores.  The forward's tiles end in the largest logit and the sum of
+// exponentials of their columns; the backward takes the vocabulary in pieces, and a piece's g is all
+// of the logits that is ever in memory.
+//
+// One product kernel serves all three: C[m][n] = sum_k A[m][k] B[n][k], C tiles of 256 x 256 (or
+// 128 x 128), 64 values of k at a time through LDS, two buffers, the next step's loads issued before
+// the present step's products.  A and B are each either rows of k ("rows": k is contiguous in
+// memory) or k rows ("columns": m or n is contiguous), which is read transposed out of LDS.  m is
+// always the index that is contiguous in the result, as a lane's accumulators hold four consecutive
+// m of one n: logits are made as [v][t], so that the sums over v stay within a lane's registers but
+// for two exchanges; dx as [d][t] and dW as [d][v], stored four values at a time.
+//
+// bf16 inputs are multiplied as they are; g is rounded to bf16 for the products with W and x
+// (its relative error of 2^-9 is that of rounding the results, which it joins as a random error over
+// the summed terms).  fp32 values are cut into three bf16 parts, and the six products that matter are
+// summed (ops_delta.hpp), g too.  Rows without a target are left out of all products: the rows that
+// take part are gathered in front, and what the others hold is never multiplied.
+#include "lm_internal.h"
+#include "ops_row.hpp"
+
+namespace msm {
+namespace {
+
+// ---- rows that take part ----
+
+// Their places in order, by one workgroup.
+__global__ __launch_bounds__(1024) void xent_rows_kernel(const XentArgs p) {
+  __shared__ int sums[2][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int base = 0, turn = 0;
+  for (int64_t t0 = 0; t0 < p.T; t0 += 1024, turn ^= 1) {
+    const int64_t t = t0 + threadIdx.x;
+    const int64_t target = t < p.T ? p.targets[t] : -1;
+    const bool on = target >= 0 && target < p.V;
+    const uint64_t set = __ballot(on);
+    if (lane == 0) sums[turn][wave] = __popcll(set);
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = 0; i < 16; ++i) {
+      before += i < wave ? sums[turn][i] : 0;
+      all += sums[turn][i];
+    }
+    const int at = base + before + __popcll(set & ((1ull << lane) - 1));
+    if (t < p.T) p.inverse[t] = on ? at : -1;
+    if (on) {
+      XentRow r;
+      r.target = (int32_t)target;
+      r.lse = p.dloss ? p.lse[t] : 0.f;
+      r.dloss = p.dloss ? p.dloss[t] : 0.f;
+      r.both = r.dloss + (p.dlse ? p.dlse[t] : 0.f);
+      p.map[at] = (int32_t)t;
+      p.rows[at] = r;
+    }
+    base += all;
+  }
+  if (threadIdx.x == 0) *p.count = base;
+}
+
+// bf16 parts of rows, in rows of DP elements with zeros behind the D of the source; `map`: places
+// of the rows in the source, `count` of them (null: n rows as they come).
+template <typename IO>
+__global__ __launch_bounds__(256) void xent_pack_kernel(const void* src, const int32_t* map, const int32_t* count,
+                                                        int64_t n, int64_t D, int64_t DP, int64_t plane, uint16_t* dst) {
+  constexpr int P = io<IO>::es == 2 ? 1 : 3;
+  const int64_t chunks = DP / 8, all = (count ? (int64_t)*count : n) * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / chunks, c = (i - row * chunks) * 8, left = D - c;
+    const int64_t at = (map ? (int64_t)map[row] : row) * D + c;
+    constexpr int VEC = Chunk<IO>::VEC;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += VEC) {
+      Chunk<IO> r;
+      r.zero();
+      if (left > e) r.load(src, at + e, left - e);
+      r.get(x + e);
+    }
+    const Part<P> s = split<P>(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
+    store_parts(dst + row * DP + c, plane, s);
+  }
+}
+
+// ---- the product kernel ----
+
+enum class Fetch { kRows, kCols };
+enum class Ends { kStats, kGrad, kDx, kDw };
+
+constexpr int kStep = 64;  // k of a step
+
+struct ProductArgs {
+  const uint16_t *a, *b;
+  int64_t lda, ldb;        // elements between rows
+  int64_t plane_a, plane_b;
+  int32_t M, N, K;         // valid sizes
+  const int32_t* count_n;  // or null: fewer n
+  const int32_t* count_k;  // or null: fewer k
+  // ends
+  const XentRow* rows;
+  float scale;
+  int32_t v0;              // first vocabulary row of the piece
+  int32_t tile0;           // first tile of the vocabulary in stat
+  int64_t T;
+  float* stat;
+  float* at_target;
+  uint16_t* g;
+  int64_t ldg, plane_g;
+  float* dx_sum;
+  int64_t ld_dx;
+  int32_t first;           // of the pieces
+  void* dw;
+  int64_t ld_dw;
+};
+
+// Loads of a step of one operand by a wavefront: a tile of R rows of 64 k (128 bytes), or of 64 k
+// rows of R elements.  16-byte units are swizzled so that the reads below spread over all banks: unit
+// u of row r lies at u ^ (r % 8); transposed, the pair of units u of row k at u ^ swz(k).
+__device__ __forceinline__ int swz(int k) { return (k & 3) | ((k >> 1) & 4); }
+
+template <Fetch F, int R, int NW>
+struct Loader {
+  static constexpr int kLoads = R / 8 / NW;  // of 1024 bytes each, by a wavefront
+  uint32_t off[kLoads];
+  int c8;
+
+  // first: the tile's first row (kRows) or column (kCols), n: rows or columns there are
+  __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int32_t first, int32_t n) {
+    if constexpr (F == Fetch::kRows) {
+      c8 = ((lane & 7) ^ (lane >> 3)) * 8;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        off[i] = (uint32_t)(((wave * kLoads + i) * 8 + (lane >> 3)) * ld + c8) * 2;
+    } else {
+      constexpr int per = R / 8;       // lanes of a row
+      constexpr int rows = 64 / per;   // rows of a load
+      c8 = 0;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int k = (wave * kLoads + i) * rows + lane / per, s = lane % per;
+        const int col = (((s >> 1) ^ swz(k)) * 2 + (s & 1)) * 8;
+        off[i] = first + col < n ? (uint32_t)(k * ld + col) * 2 : kOutside;
+      }
+    }
+  }
+  // base: the operand's plane; rows (kRows) or columns (kCols) from `first` on, k from k0 on, K in all
+  __device__ __forceinline__ void issue(const uint16_t* base, int64_t ld, int32_t first, int32_t n, int32_t k0, int32_t K,
+                                        int wave, lds_parts to) const {
+    const int32_t left = (F == Fetch::kRows ? n - first : K - k0), most = F == Fetch::kRows ? R : kStep;
+    const int32_t rows = left < most ? left : most;
+    const uint16_t* at = F == Fetch::kRows ? base + (int64_t)first * ld + k0 : base + (int64_t)k0 * ld + first;
+    // the last row ends with the operand's own last element that a load may take
+    const int64_t bytes = rows <= 0 ? 0 : ((int64_t)rows * ld - (F == Fetch::kRows ? k0 : first)) * 2;
+    const u32x4 r = rsrc_words(at, (uint32_t)uniform((int)bytes));
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      uint32_t o = off[i];
+      if constexpr (F == Fetch::kRows) o = k0 + c8 < K ? o : kOutside;
+      load_lds(r, (MSM_LDS void*)(to + (wave * kLoads + i) * 512), o);
+    }
+  }
+};
+
+// A wavefront's factors of 16 rows each, for 32 of a step's k.
+template <Fetch F, int R>
+struct Reader {
+  int lane, first;  // first: the wavefront's first row in the tile
+  __device__ __forceinline__ bf16x8 read(lds_cparts tile, int i, int kk) const {
+    if constexpr (F == Fetch::kRows) {
+      const int row = first + i * 16 + (lane & 15);
+      return *(const MSM_LDS bf16x8*)(tile + row * 64 + (((lane >> 4) + 4 * kk) ^ (lane & 7)) * 8);
+    } else {
+      const int m = lane & 15, k = 32 * kk + 8 * (lane >> 4) + (m >> 2);
+      const lds_cparts p = tile + k * R + (((first / 16 + i) ^ swz(k)) * 16) + 4 * (m & 3);
+      return read_tr(p, p + 4 * R);
+    }
+  }
+};
+
+// The pairs of parts whose products matter, smallest first.
+__device__ __forceinline__ int2 part_pair(int i) {
+  return i == 0 ? int2{2, 0} : i == 1 ? int2{1, 1} : i == 2 ? int2{0, 2} : i == 3 ? int2{1, 0} : i == 4 ? int2{0, 1} : int2{0, 0};
+}
+
+// WM x WN wavefronts of MT x NT tiles of 16 x 16.
+template <typename IO, int WM, int WN, int MT, int NT, Fetch FA, Fetch FB, Ends END>
+__global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs p) {
+  constexpr int BM = WM * MT * 16, BN = WN * NT * 16, NW = WM * WN, P = io<IO>::es == 2 ? 1 : 3;
+  constexpr int kPairs = P == 1 ? 1 : 6, kA = BM * kStep, kB = BN * kStep;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * (kA + kB)];
+  const int N = p.count_n ? uniform(*p.count_n) : p.N, K = p.count_k ? uniform(*p.count_k) : p.K;
+  const int32_t m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
+  if (n0 >= N) return;
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), wm = wave % WM, wn = wave / WM;
+  const lds_parts tiles = (lds_parts)lds;
+  Loader<FA, BM, NW> la;
+  Loader<FB, BN, NW> lb;
+  la.init(wave, lane, p.lda, m0, p.M);
+  lb.init(wave, lane, p.ldb, n0, N);
+  const Reader<FA, BM> ra{lane, wm * MT * 16};
+  const Reader<FB, BN> rb{lane, wn * NT * 16};
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = zero4();
+  const int steps_k = (K + kStep - 1) / kStep, steps = kPairs * steps_k;
+  int pair = 0, k = 0;
+  const auto issue = [&](int buffer) {
+    const int2 ab = P == 1 ? int2{0, 0} : part_pair(pair);
+    const lds_parts to = tiles + buffer * (kA + kB);
+    la.issue(p.a + ab.x * p.plane_a, p.lda, m0, p.M, k * kStep, K, wave, to);
+    lb.issue(p.b + ab.y * p.plane_b, p.ldb, n0, N, k * kStep, K, wave, to + kA);
+    if (++k == steps_k) {
+      k = 0;
+      ++pair;
+    }
+  };
+  if (steps > 0) issue(0);
+  for (int s = 0; s < steps; ++s) {
+    sync_loads();
+    if (s + 1 < steps) issue((s + 1) & 1);
+    const lds_cparts ta = tiles + (s & 1) * (kA + kB), tb = ta + kA;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8 b[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) b[j] = rb.read(tb, j, kk);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const bf16x8 a = ra.read(ta, i, kk);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[j], acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+  // accumulator r of a lane: m = 4 (lane / 16) + r, n = lane % 16 of its tile
+  const int ml = m0 + wm * MT * 16 + 4 * (lane >> 4);
+  if constexpr (END == Ends::kStats) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int n = n0 + wn * NT * 16 + j * 16 + (lane & 15);
+      const int target = n < N ? p.rows[n].target - p.v0 : -1;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int m = ml + i * 16 + r;
+          const float l = acc[i][j][r] * p.scale;
+          if (m == target) p.at_target[n] = l;
+          acc[i][j][r] = m < p.M ? l : -INFINITY;
+          top = fmaxf(top, acc[i][j][r]);
+        }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float from = top == -INFINITY ? 0.f : top;  // nothing but minus infinity: a sum of 0
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum += exp2_fast((acc[i][j][r] - from) * kLog2e);
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      if (lane < 16 && n < N) {
+        float* to = p.stat + (((int64_t)p.tile0 + blockIdx.x * WM + wm) * p.T + n) * 2;
+        to[0] = top;
+        to[1] = sum;
+      }
+    }
+  } else if constexpr (END == Ends::kGrad) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int n = n0 + wn * NT * 16 + j * 16 + (lane & 15);
+      if (n >= N) continue;
+      const XentRow row = p.rows[n];
+      const int target = row.target - p.v0;
+      const float both = row.both * p.scale, minus = row.dloss * p.scale;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int m = ml + i * 16;
+        float g[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          g[r] = both * exp2_fast((acc[i][j][r] * p.scale - row.lse) * kLog2e);
+          g[r] -= m + r == target ? minus : 0.f;
+          g[r] = m + r < p.M ? g[r] : 0.f;  // the products' k behind the piece
+        }
+        uint16_t* to = p.g + n * p.ldg + m;
+        if constexpr (P == 1) {
+          typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<bf16x4*>(to) = bf16x4{(__bf16)g[0], (__bf16)g[1], (__bf16)g[2], (__bf16)g[3]};
+        } else {
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            uint2 w;
+            w.x = pack_hi(__float_as_uint(g[0]), __float_as_uint(g[1]));
+            w.y = pack_hi(__float_as_uint(g[2]), __float_as_uint(g[3]));
+            *reinterpret_cast<uint2*>(to + q * p.plane_g) = w;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) g[r] -= __uint_as_float(__float_as_uint(g[r]) & 0xffff0000u);
+          }
+        }
+      }
+    }
+  } else if constexpr (END == Ends::kDx) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int n = n0 + wn * NT * 16 + j * 16 + (lane & 15);
+      if (n >= N) continue;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int m = ml + i * 16;
+        if (m >= p.ld_dx) continue;
+        f32x4* to = reinterpret_cast<f32x4*>(p.dx_sum + n * p.ld_dx + m);
+        *to = p.first ? acc[i][j] : *to + acc[i][j];
+      }
+    }
+  } else {
+    const bool whole = p.ld_dw % 4 == 0 && ((uintptr_t)p.dw & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int n = n0 + wn * NT * 16 + j * 16 + (lane & 15);
+      if (n >= N) continue;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int m = ml + i * 16;
+        const int64_t to = ((int64_t)p.v0 + n) * p.ld_dw + m;
+        const f32x4 c = acc[i][j];
+        if (whole && m < p.M) {
+          if constexpr (P == 1) {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(p.dw) + to) = bf16x4{(__bf16)c[0], (__bf16)c[1], (__bf16)c[2], (__bf16)c[3]};
+          } else {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(p.dw) + to) = c;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (m + r < p.M) io<IO>::store(p.dw, to + r, c[r]);
+        }
+      }
+    }
+  }
+}
+
+// lse and loss of a row from its tiles' largest logits and sums: a wavefront a row.
+__global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs p, int64_t tiles) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < p.T; t += (int64_t)gridDim.x * 4) {
+    const int n = p.inverse[t];
+    float lse = 0.f, loss = 0.f;
+    if (n >= 0) {
+      float top = -INFINITY, sum = 0.f;
+      for (int64_t i = lane; i < tiles; i += 64) {
+        const float2 s = *reinterpret_cast<const float2*>(p.stat + (i * p.T + n) * 2);
+        const float m = fmaxf(top, s.x);
+        if (m != -INFINITY) sum = sum * exp2_fast((top - m) * kLog2e) + s.y * exp2_fast((s.x - m) * kLog2e);
+        else sum += s.y;  // 0, or NaN
+        top = m;
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const float m2 = __shfl_xor(top, d, 64), s2 = __shfl_xor(sum, d, 64);
+        const float m = fmaxf(top, m2);
+        if (m != -INFINITY) sum = sum * exp2_fast((top - m) * kLog2e) + s2 * exp2_fast((m2 - m) * kLog2e);
+        else sum += s2;
+        top = m;
+      }
+      lse = top + logf(sum);
+      loss = lse - p.at_target[n];
+    }
+    if (lane == 0) {
+      p.loss[t] = loss;
+      if (p.lse) p.lse[t] = lse;
+    }
+  }
+}
+
+// dx from the sums over all pieces; zero for the rows that are left out
+template <typename IO>
+__global__ __launch_bounds__(256) void xent_dx_kernel(const XentArgs p) {
+  constexpr int VEC = Chunk<IO>::VEC;
+  const int64_t pieces = (p.D + VEC - 1) / VEC, all = p.T * pieces;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / pieces, c = (i - t * pieces) * VEC;
+    const int n = p.inverse[t];
+    float x[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {
+      f32x4 v = zero4();
+      if (n >= 0 && c + e < p.DQ) v = *reinterpret_cast<const f32x4*>(p.dx_sum + n * p.DQ + c + e);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[e + r] = v[r];
+    }
+    Chunk<IO> out;
+    out.set(x);
+    out.store(p.dx, t * p.D + c, p.D - c);
+  }
+}
+
+constexpr int64_t kMostGroups = (int64_t)1 << 20;
+unsigned groups_of(int64_t n) { return (unsigned)(n < 1 ? 1 : (n < kMostGroups ? n : kMostGroups)); }
+
+template <typename IO, Fetch FA, Fetch FB, Ends END>
+hipError_t product(const ProductArgs& a, bool wide, hipStream_t s) {
+  const int b = wide ? 256 : 128;
+  const dim3 grid((unsigned)((a.M + b - 1) / b), (unsigned)((a.N + b - 1) / b));
+  if (wide)
+    hipLaunchKernelGGL((product_kernel<IO, 2, 4, 8, 4, FA, FB, END>), grid, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((product_kernel<IO, 2, 2, 4, 4, FA, FB, END>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t pack(const void* src, const int32_t* map, const int32_t* count, int64_t n, const XentArgs& a, int64_t plane,
+                void* dst, hipStream_t s) {
+  hipLaunchKernelGGL((xent_pack_kernel<IO>), dim3(groups_of((n * (a.DP / 8) + 255) / 256)), dim3(256), 0, s, src, map, count, n,
+                     a.D, a.DP, plane, static_cast<uint16_t*>(dst));
+  return hipGetLastError();
+}
+
+// The rows that take part, gathered, and the left side's operand of a piece.
+template <typename IO>
+hipError_t gather(const XentArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, s, a);
+  return pack<IO>(a.x, a.map, a.count, a.T, a, a.T * a.DP, a.xp, s);
+}
+template <typename IO>
+hipError_t weights(const XentArgs& a, int64_t v0, int64_t n, ProductArgs* g, hipStream_t s) {
+  const char* at = static_cast<const char*>(a.w) + v0 * a.D * io<IO>::es;
+  g->plane_a = 0;
+  if (a.w_direct) {
+    g->a = reinterpret_cast<const uint16_t*>(at);
+    g->lda = a.D;
+    return hipSuccess;
+  }
+  g->a = static_cast<const uint16_t*>(a.wp);
+  g->lda = a.DP;
+  g->plane_a = a.piece * a.DP;
+  return pack<IO>(at, nullptr, nullptr, n, a, a.piece * a.DP, a.wp, s);
+}
+
+template <typename IO>
+hipError_t fwd(const XentArgs& a, hipStream_t s) {
+  hipError_t e = gather<IO>(a, s);
+  const int64_t part = a.wide ? 128 : 64;  // vocabulary rows of a pair of sums
+  int64_t tiles = 0;
+  for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
+    const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
+    ProductArgs g{};
+    e = weights<IO>(a, v0, n, &g, s);
+    if (e != hipSuccess) break;
+    g.b = static_cast<const uint16_t*>(a.xp);
+    g.ldb = a.DP;
+    g.plane_b = a.T * a.DP;
+    g.M = (int32_t)n;
+    g.N = (int32_t)a.T;
+    g.K = (int32_t)a.D;
+    g.count_n = a.count;
+    g.rows = a.rows;
+    g.scale = a.scale;
+    g.v0 = (int32_t)v0;
+    g.tile0 = (int32_t)tiles;
+    g.T = a.T;
+    g.stat = a.stat;
+    g.at_target = a.at_target;
+    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kStats>(g, a.wide, s);
+    tiles += (n + 2 * part - 1) / (2 * part) * 2;
+  }
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(xent_join_kernel, dim3(groups_of((a.T + 3) / 4)), dim3(256), 0, s, a, tiles);
+  return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t bwd(const XentArgs& a, hipStream_t s) {
+  hipError_t e = gather<IO>(a, s);
+  for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
+    const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
+    ProductArgs g{};
+    e = weights<IO>(a, v0, n, &g, s);
+    if (e != hipSuccess) break;
+    const uint16_t* w = g.a;
+    const int64_t ldw = g.lda, plane_w = g.plane_a;
+    g.b = static_cast<const uint16_t*>(a.xp);
+    g.ldb = a.DP;
+    g.plane_b = a.T * a.DP;
+    g.M = (int32_t)n;
+    g.N = (int32_t)a.T;
+    g.K = (int32_t)a.D;
+    g.count_n = a.count;
+    g.rows = a.rows;
+    g.scale = a.scale;
+    g.v0 = (int32_t)v0;
+    g.g = static_cast<uint16_t*>(a.g);
+    g.ldg = a.piece;
+    g.plane_g = a.T * a.piece;
+    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kGrad>(g, a.wide, s);
+    if (e != hipSuccess) break;
+    ProductArgs x{};
+    x.a = w;
+    x.lda = ldw;
+    x.plane_a = plane_w;
+    x.b = static_cast<const uint16_t*>(a.g);
+    x.ldb = a.piece;
+    x.plane_b = a.T * a.piece;
+    x.M = (int32_t)a.D;
+    x.N = (int32_t)a.T;
+    x.K = (int32_t)n;
+    x.count_n = a.count;
+    x.dx_sum = a.dx_sum;
+    x.ld_dx = a.DQ;
+    x.first = v0 == 0;
+    e = product<IO, Fetch::kCols, Fetch::kRows, Ends::kDx>(x, a.wide, s);
+    if (e != hipSuccess || !a.dw) continue;
+    ProductArgs d{};
+    d.a = static_cast<const uint16_t*>(a.xp);
+    d.lda = a.DP;
+    d.plane_a = a.T * a.DP;
+    d.b = static_cast<const uint16_t*>(a.g);
+    d.ldb = a.piece;
+    d.plane_b = a.T * a.piece;
+    d.M = (int32_t)a.D;
+    d.N = (int32_t)n;
+    d.K = (int32_t)a.T;
+    d.count_k = a.count;
+    d.v0 = (int32_t)v0;
+    d.dw = a.dw;
+    d.ld_dw = a.D;
+    e = product<IO, Fetch::kCols, Fetch::kCols, Ends::kDw>(d, a.wide, s);
+  }
+  if (e != hipSuccess) return e;
+  const int64_t pieces = (a.D * io<IO>::es + 15) / 16;
+  hipLaunchKernelGGL((xent_dx_kernel<IO>), dim3(groups_of((a.T * pieces + 255) / 256)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_xent_fwd(const XentArgs& a, int io_bf16, hipStream_t s) {
+  return io_bf16 ? fwd<bf16_storage>(a, s) : fwd<float>(a, s);
+}
+hipError_t launch_xent_bwd(const XentArgs& a, int io_bf16, hipStream_t s) {
+  return io_bf16 ? bwd<bf16_storage>(a, s) : bwd<float>(a, s);
+}
+
+}  // namespace msm

@@ -128,6 +128,8 @@ NormShape norm_shape(int64_t D, int per);
 constexpr int norm_threads(int T, int NV) { return T == 256 && NV <= 4 ? 512 : 256; }
 hipError_t launch_norm_fwd(const NormArgs& a, int io_bf16, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, int io_bf16, hipStream_t s);
+// dweight and dbias (either may be null) from `parts` pairs of column sums at `part`
+hipError_t launch_norm_join(const NormArgs& a, int64_t parts, hipStream_t s);
 
 // ---- gradient norm and clipping ----
 

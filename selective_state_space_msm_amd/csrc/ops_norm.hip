@@ -12,9 +12,7 @@
 // workgroups' sums are joined by a second kernel in a fixed order.  Longer rows are walked in
 // loops over memory.  16384 x 4096 bf16: forward 56 us (4.8 TB/s), backward 81 us with its join
 // (5.0 TB/s); a copy reaches 5.15 TB/s.
-#include <type_traits>
-
-#include "ops_delta.hpp"
+#include "ops_row.hpp"
 
 namespace msm {
 
@@ -31,91 +29,6 @@ namespace {
 
 // Workgroups of the forward: eight for every CU, more than its registers hold at once.
 constexpr int64_t kNormGroups = 2048;
-
-// Sum over the T threads of a row, the same value in each of them.
-// With 256 threads the sum of each wavefront passes through `lds`, which the next sum must not be
-// (a later one may: a thread that writes there has passed the barrier in between).
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float* lds) {
-  constexpr int W = T < 64 ? T : 64;
-#pragma unroll
-  for (int m = W / 2; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
-  if constexpr (T == 256) {
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
-  }
-  return v;
-}
-template <int T>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float* lds) {
-  constexpr int W = T < 64 ? T : 64;
-#pragma unroll
-  for (int m = W / 2; m > 0; m >>= 1) {
-    a += __shfl_xor(a, m, 64);
-    b += __shfl_xor(b, m, 64);
-  }
-  if constexpr (T == 256) {
-    if ((threadIdx.x & 63) == 0) {
-      lds[(threadIdx.x >> 6) & 3] = a;
-      lds[4 + ((threadIdx.x >> 6) & 3)] = b;
-    }
-    __syncthreads();
-    a = (lds[0] + lds[1]) + (lds[2] + lds[3]);
-    b = (lds[4] + lds[5]) + (lds[6] + lds[7]);
-  }
-}
-
-// VEC elements between their load and their use.
-template <typename IO, int VEC>
-struct Piece {
-  std::conditional_t<VEC == 1, typename io<IO>::raw, u32x4> raw;
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    if constexpr (VEC == 1)
-      raw = io<IO>::load(p, i);
-    else
-      raw = *reinterpret_cast<const u32x4*>(static_cast<const char*>(p) + i * io<IO>::es);
-  }
-  __device__ __forceinline__ void zero() { raw = {}; }
-  __device__ __forceinline__ void get(float (&x)[VEC]) const {
-    if constexpr (VEC == 1) {
-      x[0] = io<IO>::widen(raw);
-    } else if constexpr (io<IO>::es == 2) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        x[2 * c] = __uint_as_float(raw[c] << 16);
-        x[2 * c + 1] = __uint_as_float(raw[c] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = __uint_as_float(raw[c]);
-    }
-  }
-};
-template <typename IO, int VEC>
-__device__ __forceinline__ void store_piece(void* p, int64_t i, const float (&x)[VEC]) {
-  using T = io<IO>;
-  if constexpr (VEC == 1) {
-    T::store(p, i, x[0]);
-  } else if constexpr (T::es == 2) {
-    u32x4 w;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t lo = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x[2 * c]));
-      const uint32_t hi = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x[2 * c + 1]));
-      w[c] = lo | (hi << 16);
-    }
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = w;
-  } else {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = f32x4{x[0], x[1], x[2], x[3]};
-  }
-}
-// fp32 parameters of a piece (vector loads: their address is a multiple of VEC elements)
-template <int VEC>
-__device__ __forceinline__ void load_param(const float* p, int64_t i, float other, float (&x)[VEC]) {
-#pragma unroll
-  for (int c = 0; c < VEC; ++c) x[c] = p ? p[i + c] : other;
-}
 
 // A workgroup walks several rows with its columns' weight and bias in registers: read again for
 // every row they would be four times the bytes of a bf16 row.  The next row's loads are issued
@@ -181,15 +94,6 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const NormArgs p) {
       if (p.rstd) p.rstd[row] = rstd;
     }
   }
-}
-
-// Sum over a workgroup, the same value in each thread.  `lds` must not be the next sum's.
-__device__ __forceinline__ double wide_sum(double v, double* lds) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
 // Workgroups of a walk over rows: 2^24 of 256 threads would be 2^32 threads, more than a launch has.
@@ -401,9 +305,11 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const NormArgs p, int64_
   }
 }
 
+}  // namespace
+
 // Fewer columns a workgroup while that takes more of them to fill the GPU; for the widest rows a
 // thread a column, as D / 16 workgroups of 256 would pass the 2^32 threads of a launch.
-hipError_t join(const NormArgs& a, int64_t parts, hipStream_t s) {
+hipError_t launch_norm_join(const NormArgs& a, int64_t parts, hipStream_t s) {
   if (a.D >= (1 << 22))
     hipLaunchKernelGGL(norm_join_kernel<256>, dim3((unsigned)((a.D + 255) / 256)), dim3(256), 0, s, a, parts);
   else if (a.D >= 4096)
@@ -412,6 +318,8 @@ hipError_t join(const NormArgs& a, int64_t parts, hipStream_t s) {
     hipLaunchKernelGGL(norm_join_kernel<4>, dim3((unsigned)((a.D + 3) / 4)), dim3(256), 0, s, a, parts);
   return hipGetLastError();
 }
+
+namespace {
 
 template <typename IO, int VEC, int T, int NV>
 hipError_t go_fwd(const NormArgs& a, hipStream_t s) {
@@ -426,7 +334,7 @@ hipError_t go_bwd(const NormArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((norm_bwd_kernel<IO, VEC, T, NV, BS>), dim3((unsigned)a.groups), dim3(BS), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.part) return e;
-  return join(a, a.groups, s);
+  return launch_norm_join(a, a.groups, s);
 }
 
 template <typename IO, int VEC, bool BWD>
@@ -449,7 +357,7 @@ hipError_t pick(const NormArgs& a, hipStream_t s) {
                      dim3(256), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return join(a, a.groups, s);
+  return launch_norm_join(a, a.groups, s);
 }
 
 }  // namespace
