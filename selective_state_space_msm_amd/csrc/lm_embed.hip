@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedArgs p, int64
   constexpr int VEC = Chunk<IO>::VEC, TV = Chunk<TB>::VEC;
   const int64_t all = p.tokens * pieces;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / pieces, c = (i - t * pieces) * VEC, n = p.D - c;
+    const int64_t t = quotient(i, pieces), c = (i - t * pieces) * VEC, n = p.D - c;
     const int64_t id = p.ids[t];
     float x[VEC > TV ? VEC : TV];
 #pragma unroll
@@ -94,6 +94,7 @@ __device__ __forceinline__ uint32_t take_place(uint32_t* bins, uint32_t digit, i
 __device__ __forceinline__ void wave_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 constexpr int kSortWaves = 8;
+constexpr int kAhead = 4;  // loads of 64 places in flight
 
 // pass 0 reads the ids, later ones what the pass before left
 template <bool FIRST>
@@ -115,13 +116,21 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_count_kernel(const Embe
   uint32_t* bins = lds[wave];
   for (int b = lane; b < nb; b += 64) bins[b] = 0;
   wave_order();
-  for (int64_t k = 0; k < p.per; k += 64) {
-    const int64_t i = w * p.per + k + lane;
-    const bool on = w < p.waves && i < p.tokens;
-    uint32_t key = 0, pos;
-    if (on) place_of<FIRST>(p, pass, i, &key, &pos);
-    count_digit(bins, (key >> (pass * p.bits)) & (nb - 1), p.bits, on, lane);
-    wave_order();
+  for (int64_t k = 0; k < p.per; k += 64 * kAhead) {
+    uint32_t key[kAhead], pos;
+    bool on[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t i = w * p.per + k + 64 * j + lane;
+      on[j] = w < p.waves && k + 64 * j < p.per && i < p.tokens;
+      key[j] = 0;
+      if (on[j]) place_of<FIRST>(p, pass, i, &key[j], &pos);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      count_digit(bins, (key[j] >> (pass * p.bits)) & (nb - 1), p.bits, on[j], lane);
+      wave_order();
+    }
   }
   if (w < p.waves)
     for (int b = lane; b < nb; b += 64) p.hist[w * nb + b] = bins[b];
@@ -155,12 +164,12 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_move_kernel(const Embed
   uint32_t before = 0, total = 0;
   if (b < nb) {
     int64_t w = 0;
-    for (; w + 8 <= p.waves; w += 8) {
-      uint32_t c[8];
+    for (; w + 32 <= p.waves; w += 32) {
+      uint32_t c[32];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) c[j] = p.hist[(w + j) * nb + b];
+      for (int j = 0; j < 32; ++j) c[j] = p.hist[(w + j) * nb + b];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 32; ++j) {
         before += w + j < w0 ? c[j] : 0;
         total += c[j];
       }
@@ -181,16 +190,24 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_move_kernel(const Embed
   const int64_t w = w0 + wave;
   if (w >= p.waves) return;
   uint32_t* bins = lds[wave];
-  for (int64_t k = 0; k < p.per; k += 64) {
-    const int64_t i = w * p.per + k + lane;
-    const bool on = i < p.tokens;
-    uint32_t key = 0, pos = 0;
-    if (on) place_of<FIRST>(p, pass, i, &key, &pos);
-    const uint32_t to = take_place(bins, (key >> (pass * p.bits)) & (nb - 1), p.bits, on, lane);
-    wave_order();
-    if (on) {
-      p.key[pass & 1][to] = key;
-      p.pos[pass & 1][to] = pos;
+  for (int64_t k = 0; k < p.per; k += 64 * kAhead) {
+    uint32_t key[kAhead], pos[kAhead];
+    bool on[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t i = w * p.per + k + 64 * j + lane;
+      on[j] = k + 64 * j < p.per && i < p.tokens;
+      key[j] = pos[j] = 0;
+      if (on[j]) place_of<FIRST>(p, pass, i, &key[j], &pos[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const uint32_t to = take_place(bins, (key[j] >> (pass * p.bits)) & (nb - 1), p.bits, on[j], lane);
+      wave_order();
+      if (on[j]) {
+        p.key[pass & 1][to] = key[j];
+        p.pos[pass & 1][to] = pos[j];
+      }
     }
   }
 }
@@ -318,7 +335,8 @@ __global__ __launch_bounds__(256) void embed_run2_kernel(const EmbedArgs p, int6
   }
 }
 
-constexpr int kRowsOf = 16;  // vocabulary rows of a workgroup
+constexpr int kRowsOf = 8;  // vocabulary rows of a workgroup
+constexpr int kBusy = 8;     // a row of more places has a workgroup of its own
 
 // x += sums j0 ... j1 of a level
 template <int VEC, typename F>
@@ -330,72 +348,159 @@ __device__ __forceinline__ void add_sums(const float* part, int64_t j0, int64_t 
       if (c + e < D) x[e] += part[j * D + c + e];
 }
 
+// The first of the places lo ... hi whose key is v or more, found by a wavefront: 64 probes a round.
+__device__ __forceinline__ int64_t first_place(const uint32_t* key, int64_t lo, int64_t hi, int64_t v) {
+  const int lane = threadIdx.x & 63;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 63) / 64, at = lo + lane * step;
+    const int below = __popcll(__ballot(at < hi && (int64_t)key[at < hi ? at : lo] < v));
+    if (below == 0) return lo;
+    const int64_t end = lo + below * step;
+    lo += (below - 1) * step + 1;
+    hi = end < hi ? end : hi;
+  }
+  return lo;
+}
+
+// first[r]: the first place of row v0 + r or of what comes after it, r = 0 ... kRowsOf, by a workgroup.
+// Its barriers close what was read of `first` before; `ends` holds two words, `near` the positions of
+// the first 256 places.
+__device__ __forceinline__ void first_places(const uint32_t* key, const uint32_t* pos, int64_t tokens, int64_t v0, uint32_t* first,
+                                             uint32_t* ends, uint32_t* near) {
+  const int wave = threadIdx.x >> 6;
+  __syncthreads();
+  if (wave < 2) {
+    const int64_t e = first_place(key, 0, tokens, v0 + wave * kRowsOf);
+    if ((threadIdx.x & 63) == 0) ends[wave] = (uint32_t)e;
+  }
+  __syncthreads();
+  const int64_t lo = ends[0], hi = ends[1], n = hi - lo;
+  if (threadIdx.x < n) near[threadIdx.x] = pos[lo + threadIdx.x];
+  if (n < 256) {
+    const int t = threadIdx.x;
+    if (t <= n) {  // place t ends the rows before its own, n ends them all
+      const int64_t from = t == 0 ? 0 : (int64_t)key[lo + t - 1] - v0 + 1;
+      const int64_t to = t == n ? kRowsOf : (int64_t)key[lo + t] - v0;
+      for (int64_t r = from; r <= to; ++r) first[r] = (uint32_t)(lo + t);
+    }
+  } else {
+    for (int r = wave; r <= kRowsOf; r += 4) {
+      const int64_t e = first_place(key, lo, hi, v0 + r);
+      if ((threadIdx.x & 63) == 0) first[r] = (uint32_t)e;
+    }
+  }
+  __syncthreads();
+}
+
+template <typename TB, int VEC>
+__device__ __forceinline__ void store_row(const EmbedArgs& p, int64_t v, int64_t c, float (&x)[VEC]) {
+  constexpr int TV = Chunk<TB>::VEC;
+  const int64_t at = v * p.D + c, n = p.D - c;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] *= p.scale;
+  if constexpr (VEC >= TV) {
+#pragma unroll
+    for (int e = 0; e < VEC; e += TV) {
+      Chunk<TB> out;
+      out.set(x + e);
+      if (n > e) out.store(p.dtable, at + e, n - e);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (e < n) io<TB>::store(p.dtable, at + e, x[e]);
+  }
+}
+
+// All rows.  The first `busy` workgroups each look at one place in kBusy: a row of more places holds at
+// least one of these, and the workgroup of the first of them has the row.  The others take kRowsOf rows
+// each, most of them empty: one batch of loads a row.  (With the busy rows among the others, the
+// workgroup of the first rows took 16 of them one after another: 500 us of 543 for 16384 tokens of 65536,
+// D = 2048, bf16.)
 template <typename TB, typename IO>
-__global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int64_t pieces) {
-  constexpr int VEC = Chunk<IO>::VEC, TV = Chunk<TB>::VEC;
-  __shared__ uint32_t first[kRowsOf + 1];
+__global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int64_t pieces, int64_t busy) {
+  constexpr int VEC = Chunk<IO>::VEC;
+  __shared__ uint32_t first[kRowsOf + 1], ends[2], near[256];
   const uint32_t *key = p.key[(p.passes - 1) & 1], *pos = p.pos[(p.passes - 1) & 1];
   const int64_t groups = (p.V + kRowsOf - 1) / kRowsOf;
-  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-    const int64_t v0 = g * kRowsOf;
-    if (threadIdx.x <= kRowsOf) {  // the first place of a row, or of what comes after it
-      const int64_t v = v0 + threadIdx.x;
-      int64_t lo = 0, hi = p.tokens;
-      while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if ((int64_t)key[mid] < v)
-          lo = mid + 1;
-        else
-          hi = mid;
+  for (int64_t g = blockIdx.x; g < busy + groups; g += gridDim.x) {
+    if (g < busy) {
+      const int64_t at = g * kBusy, v = key[at];
+      if (v >= p.V) continue;
+      // the row's workgroup is an earlier one
+      if (at >= kBusy && key[at - kBusy] == v) continue;
+      __syncthreads();
+      if (threadIdx.x < 128) {
+        const int64_t e = first_place(key, 0, p.tokens, v + (threadIdx.x >> 6));
+        if ((threadIdx.x & 63) == 0) ends[threadIdx.x >> 6] = (uint32_t)e;
       }
-      first[threadIdx.x] = (uint32_t)lo;
+      __syncthreads();
+      const int64_t i0 = ends[0], i1 = ends[1];
+      if (i1 - i0 <= kBusy) continue;
+      for (int64_t q = threadIdx.x; q < pieces; q += 256) {
+        const int64_t c = q * VEC;
+        float x[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+        if (i1 - i0 < 2 * kEmbedRun) {
+          add_places<IO>(p, pos, i0, i1, c, x);
+        } else {
+          constexpr int R = kEmbedRun;
+          const int64_t j0 = (i0 + R - 1) / R, j1 = i1 / R;  // whole runs
+          const int64_t m0 = (j0 + R - 1) / R, m1 = j1 / R;  // whole runs of runs
+          add_places<IO>(p, pos, i0, j0 * R, c, x);
+          if (p.part[1] && m0 < m1) {
+            add_sums<VEC>(p.part[0], j0, m0 * R, p.D, c, x);
+            double wide[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) wide[e] = x[e];
+            add_sums<VEC>(p.part[1], m0, m1, p.D, c, wide);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[e] = (float)wide[e];
+            add_sums<VEC>(p.part[0], m1 * R, j1, p.D, c, x);
+          } else {
+            add_sums<VEC>(p.part[0], j0, j1, p.D, c, x);
+          }
+          add_places<IO>(p, pos, j1 * R, i1, c, x);
+        }
+        store_row<TB, VEC>(p, v, c, x);
+      }
+      continue;
     }
-    __syncthreads();
+    const int64_t v0 = (g - busy) * kRowsOf;
+    first_places(key, pos, p.tokens, v0, first, ends, near);
     const int rows = (int)(p.V - v0 < kRowsOf ? p.V - v0 : kRowsOf);
-    for (int64_t k = threadIdx.x; k < rows * pieces; k += 256) {
-      const int64_t r = k / pieces, c = (k - r * pieces) * VEC, n = p.D - c;
-      const int64_t i0 = first[r], i1 = first[r + 1];
+    const uint32_t all = rows * (uint32_t)pieces;  // 32 bits: D is at most 2^24
+    for (uint32_t k = threadIdx.x; k < all; k += 256) {
+      const uint32_t r = k / (uint32_t)pieces;
+      const int64_t c = (int64_t)(k - r * (uint32_t)pieces) * VEC, n = p.D - c;
+      const int64_t i0 = first[r];
+      const int count = (int)(first[r + 1] - i0);
+      if (count > kBusy) continue;
       float x[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) x[e] = 0.f;
-      if (i1 - i0 < 2 * kEmbedRun) {
-        add_places<IO>(p, pos, i0, i1, c, x);
-      } else {
-        constexpr int R = kEmbedRun;
-        const int64_t j0 = (i0 + R - 1) / R, j1 = i1 / R;          // whole runs
-        const int64_t m0 = (j0 + R - 1) / R, m1 = j1 / R;          // whole runs of runs
-        add_places<IO>(p, pos, i0, j0 * R, c, x);
-        if (p.part[1] && m0 < m1) {
-          add_sums<VEC>(p.part[0], j0, m0 * R, p.D, c, x);
-          double wide[VEC];
+      if (count > 0) {
+        Chunk<IO> in[kBusy];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) wide[e] = x[e];
-          add_sums<VEC>(p.part[1], m0, m1, p.D, c, wide);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) x[e] = (float)wide[e];
-          add_sums<VEC>(p.part[0], m1 * R, j1, p.D, c, x);
-        } else {
-          add_sums<VEC>(p.part[0], j0, j1, p.D, c, x);
+        for (int j = 0; j < kBusy; ++j) {
+          in[j].zero();
+          if (j < count) {
+            const int64_t k = i0 + j - ends[0];
+            in[j].load(p.dy, (int64_t)(k < 256 ? near[k] : pos[i0 + j]) * p.D + c, n);
+          }
         }
-        add_places<IO>(p, pos, j1 * R, i1, c, x);
-      }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] *= p.scale;
-      const int64_t at = (v0 + r) * p.D + c;
-      if constexpr (VEC >= TV) {
+        for (int j = 0; j < kBusy; ++j) {
+          float v[VEC];
+          in[j].get(v);
+          if (j < count)
 #pragma unroll
-        for (int e = 0; e < VEC; e += TV) {
-          Chunk<TB> out;
-          out.set(x + e);
-          if (n > e) out.store(p.dtable, at + e, n - e);
+            for (int e = 0; e < VEC; ++e) x[e] += v[e];
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (e < n) io<TB>::store(p.dtable, at + e, x[e]);
       }
+      store_row<TB, VEC>(p, v0 + r, c, x);
     }
-    __syncthreads();
   }
 }
 
@@ -434,7 +539,8 @@ hipError_t bwd(const EmbedArgs& a, hipStream_t s) {
       hipLaunchKernelGGL(embed_run2_kernel, dim3(groups_of(runs2)), dim3(256), 0, s, a, runs2);
     }
   }
-  hipLaunchKernelGGL((embed_rows_kernel<TB, IO>), dim3(groups_of((a.V + kRowsOf - 1) / kRowsOf)), dim3(256), 0, s, a, pieces);
+  const int64_t busy = a.tokens > kBusy ? (a.tokens + kBusy - 1) / kBusy : 0;
+  hipLaunchKernelGGL((embed_rows_kernel<TB, IO>), dim3(groups_of(busy + (a.V + kRowsOf - 1) / kRowsOf)), dim3(256), 0, s, a, pieces, busy);
   return hipGetLastError();
 }
 

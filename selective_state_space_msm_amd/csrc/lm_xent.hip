@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(const void* src, const i
   constexpr int P = io<IO>::es == 2 ? 1 : 3;
   const int64_t chunks = DP / 8, all = (count ? (int64_t)*count : n) * chunks;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / chunks, c = (i - row * chunks) * 8, left = D - c;
+    const int64_t row = quotient(i, chunks), c = (i - row * chunks) * 8, left = D - c;
     const int64_t at = (map ? (int64_t)map[row] : row) * D + c;
     constexpr int VEC = Chunk<IO>::VEC;
     float x[8];
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(256) void xent_dx_kernel(const XentArgs p) {
   constexpr int VEC = Chunk<IO>::VEC;
   const int64_t pieces = (p.D + VEC - 1) / VEC, all = p.T * pieces;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / pieces, c = (i - t * pieces) * VEC;
+    const int64_t t = quotient(i, pieces), c = (i - t * pieces) * VEC;
     const int n = p.inverse[t];
     float x[VEC];
 #pragma unroll

@@ -101,6 +101,11 @@ __device__ __forceinline__ double wide_sum(double v, double* lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where both are that small (a quarter of the instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // 16 bytes of a row that may begin at any element's address (the hardware takes unaligned 16-byte
 // accesses).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
