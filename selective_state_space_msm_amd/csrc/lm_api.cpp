@@ -96,9 +96,9 @@ BlockNormLayout block_norm_layout(int64_t rows, int64_t D) {
 // ---- linear cross entropy ----
 
 struct XentLayout {
-  size_t count, map, inverse, rows, xp, wp, stat, at_target, g, dx_sum, total;
+  size_t count, map, inverse, rows, xp, wp, stat, at_target, g, dx_sum, rest, total;
   int64_t DP, DQ, piece, piece_packed;
-  int planes;
+  int planes, splits;
   bool direct, wide;
 };
 
@@ -109,7 +109,7 @@ constexpr size_t kXentUnaligned = (size_t)16 << 20;   // bytes of weights packed
 msm_status xent_check(int64_t T, int64_t V, int64_t D, msm_dtype io) {
   if (!known(io)) return MSM_ERR_UNSUPPORTED;
   if (T < 1 || V < 1 || D < 1) return MSM_ERR_INVALID_ARG;
-  if (T > kXentMost || V > kXentMost || D > ((int64_t)1 << 16)) return MSM_ERR_UNSUPPORTED;
+  if (T > kXentMost || V > kXentMost || D > ((int64_t)1 << 16) || T * V > ((int64_t)1 << 39)) return MSM_ERR_UNSUPPORTED;
   return MSM_OK;
 }
 
@@ -120,13 +120,22 @@ int64_t rows_of(size_t bytes, size_t row, int64_t V) {
   return n < all ? n : all;
 }
 
+// The product of dx sums over the vocabulary and has few tiles where T and D are small: its sum is
+// split until the tiles fill the GPU or a split has fewer than 8 steps of 64.
+int xent_splits(int64_t T, int64_t D, int64_t piece) {
+  const int64_t b = msm::xent_wide(D, T) ? 256 : 128, slots = b == 256 ? 256 : 512;
+  int64_t n = slots / (ceil_div(D, b) * ceil_div(T, b));
+  if (n > piece / 512) n = piece / 512;
+  return (int)(n < 1 ? 1 : (n > 32 ? 32 : n));
+}
+
 XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) {
   XentLayout l{};
   l.planes = io == MSM_BF16 ? 1 : 3;
   l.DP = ceil_div(D, 64) * 64;
   l.DQ = ceil_div(D, 4) * 4;
   l.direct = io == MSM_BF16 && D % 8 == 0;  // if the weights are aligned, too
-  l.wide = ceil_div(T, 256) * ceil_div(V, 256) >= 256 && T > 128;
+  l.wide = msm::xent_wide(V, T);
   const size_t row_w = (size_t)l.DP * 2 * l.planes, row_g = (size_t)T * 2 * l.planes;
   l.piece = bwd ? rows_of(kXentPiece, row_g, V) : ceil_div(V, 256) * 256;
   l.piece_packed = rows_of(l.direct ? kXentUnaligned : kXentPiece, row_w, V);
@@ -141,7 +150,9 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) 
   l.wp = take((size_t)l.piece_packed * row_w);
   if (bwd) {
     l.g = take((size_t)l.piece * row_g);
-    l.dx_sum = take((size_t)T * l.DQ * 4);
+    l.splits = xent_splits(T, D, l.piece_packed);
+    l.dx_sum = take((size_t)l.splits * T * l.DQ * 4);
+    l.rest = take((size_t)T * 4);
   } else {
     l.stat = take((size_t)(ceil_div(V, 64) + 4) * T * 8);
     l.at_target = take((size_t)T * 4);
@@ -167,6 +178,8 @@ msm::XentArgs xent_args(const XentLayout& l, const void* x, const void* w, const
   a.at_target = reinterpret_cast<float*>(ws + l.at_target);
   a.g = ws + l.g;
   a.dx_sum = reinterpret_cast<float*>(ws + l.dx_sum);
+  a.rest = reinterpret_cast<float*>(ws + l.rest);
+  a.splits = l.splits;
   a.T = T;
   a.V = V;
   a.D = D;

@@ -101,13 +101,21 @@ struct XentArgs {
   float* stat;             // forward: [tiles of the vocabulary][T][2] largest logit, sum of exponentials
   float* at_target;        // forward: (T,) logit of the target
   void* g;                 // backward: [planes][T][piece] gradient of a piece's logits
-  float* dx_sum;           // backward: [T][DQ]
+  float* dx_sum;           // backward: [splits][T][DQ]
+  float* rest;             // backward, bf16: (T,) what the target's g lost to its rounding
   int64_t T, V, D, DP, DQ, piece;
   float scale;
   int32_t planes;          // 1, or 3 for fp32
   int32_t w_direct;
-  int32_t wide;            // tiles of 256 x 256, else of 128 x 128
+  int32_t wide;            // the forward's tiles: 256 x 256, else 128 x 128
+  int32_t splits;          // of the vocabulary's pieces in the product of dx
 };
+// Tiles of 256 x 256 or of 128 x 128 for an M x N product: rounds of the 256 CUs (one workgroup a CU, or
+// two of the small tiles), a small tile taking a quarter of a large one's work at 0.8 of its rate.
+constexpr bool xent_wide(int64_t M, int64_t N) {
+  const int64_t large = ((M + 255) / 256) * ((N + 255) / 256), small = ((M + 127) / 128) * ((N + 127) / 128);
+  return (large + 255) / 256 * 8 <= (small + 511) / 512 * 5;
+}
 hipError_t launch_xent_fwd(const XentArgs& a, int io_bf16, hipStream_t s);
 hipError_t launch_xent_bwd(const XentArgs& a, int io_bf16, hipStream_t s);
 

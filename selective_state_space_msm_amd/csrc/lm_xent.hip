@@ -111,8 +111,10 @@ struct ProductArgs {
   uint16_t* g;
   int64_t ldg, plane_g;
   float* dx_sum;
-  int64_t ld_dx;
+  int64_t ld_dx, plane_dx;
   int32_t first;           // of the pieces
+  int32_t splits;          // of k, over gridDim.z
+  float* rest;             // what the target's g lost to bf16
   void* dw;
   int64_t ld_dw;
 };
@@ -186,6 +188,27 @@ __device__ __forceinline__ int2 part_pair(int i) {
   return i == 0 ? int2{2, 0} : i == 1 ? int2{1, 1} : i == 2 ? int2{0, 2} : i == 3 ? int2{1, 0} : i == 4 ? int2{0, 1} : int2{0, 0};
 }
 
+// Where a workgroup's tile is.  Workgroups go round the 8 XCDs one by one, so number i of an XCD is i * 8
+// + XCD; an XCD takes blocks of 8 x 4 tiles, whose operands its L2 shares, and the XCDs stand rm x 8 / rm
+// side by side, moved on by one from round to round of n, so that a last block of m is not always the same
+// XCDs'.  (All m of one n after another, as the grid counts, the forward reads the whole of W for every 256
+// tokens, 8.6 GB for 8192 of 65536, D = 2048: 2.09 ms there, 1.93 in blocks.)  Small tiles, of which there
+// are few, are taken as they come: blocks leave XCDs idle (160 for 110 us at 513 x 10007 x 1000).
+struct Place {
+  int m, n;
+};
+__host__ __device__ inline int xcds_m(int tm, int tn, bool wide) {
+  if (!wide || tm * (int64_t)tn < 256) return 0;
+  return tm <= 8 ? 1 : (tn <= 4 ? 8 : (tn <= 8 ? 4 : 2));
+}
+__device__ __forceinline__ Place place_of(int tm, int tn, bool wide) {
+  const int rm = xcds_m(tm, tn, wide), at = blockIdx.y * gridDim.x + blockIdx.x;
+  if (rm == 0) return Place{at % tm, at / tm};
+  const int rounds_m = (tm + 8 * rm - 1) / (8 * rm), round = blockIdx.y, round_n = round / rounds_m;
+  const int xcd = (blockIdx.x + round_n) % 8, i = blockIdx.x / 8;
+  return Place{((round % rounds_m) * rm + xcd % rm) * 8 + i % 8, (round_n * (8 / rm) + xcd / rm) * 4 + i / 8};
+}
+
 // WM x WN wavefronts of MT x NT tiles of 16 x 16.
 template <typename IO, int WM, int WN, int MT, int NT, Fetch FA, Fetch FB, Ends END>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs p) {
@@ -193,8 +216,9 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   constexpr int kPairs = P == 1 ? 1 : 6, kA = BM * kStep, kB = BN * kStep;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * (kA + kB)];
   const int N = p.count_n ? uniform(*p.count_n) : p.N, K = p.count_k ? uniform(*p.count_k) : p.K;
-  const int32_t m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
-  if (n0 >= N) return;
+  const Place at = place_of((p.M + BM - 1) / BM, (N + BN - 1) / BN, BM == 256);
+  const int32_t m0 = at.m * BM, n0 = at.n * BN;
+  if (m0 >= p.M || n0 >= N) return;  // fewer rows than the grid was made for among these
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), wm = wave % WM, wn = wave / WM;
   const lds_parts tiles = (lds_parts)lds;
   Loader<FA, BM, NW> la;
@@ -208,15 +232,21 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = zero4();
-  const int steps_k = (K + kStep - 1) / kStep, steps = kPairs * steps_k;
-  int pair = 0, k = 0;
+  int k_first = 0, k_end = (K + kStep - 1) / kStep;
+  if constexpr (END == Ends::kDx) {
+    const int all = k_end, z = blockIdx.z;
+    k_first = (int)((int64_t)all * z / p.splits);
+    k_end = (int)((int64_t)all * (z + 1) / p.splits);
+  }
+  const int steps = kPairs * (k_end - k_first);
+  int pair = 0, k = k_first;
   const auto issue = [&](int buffer) {
     const int2 ab = P == 1 ? int2{0, 0} : part_pair(pair);
     const lds_parts to = tiles + buffer * (kA + kB);
     la.issue(p.a + ab.x * p.plane_a, p.lda, m0, p.M, k * kStep, K, wave, to);
     lb.issue(p.b + ab.y * p.plane_b, p.ldb, n0, N, k * kStep, K, wave, to + kA);
-    if (++k == steps_k) {
-      k = 0;
+    if (++k == k_end) {
+      k = k_first;
       ++pair;
     }
   };
@@ -240,68 +270,98 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   }
   // accumulator r of a lane: m = 4 (lane / 16) + r, n = lane % 16 of its tile
   const int ml = m0 + wm * MT * 16 + 4 * (lane >> 4);
+  // the tile's rows of C end inside it, or one of the wavefront's columns has its target there: seldom, so
+  // the ordinary way asks nothing of a value
+  const bool ends = m0 + BM > p.M;
   if constexpr (END == Ends::kStats) {
+    const float to2 = p.scale * kLog2e;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int n = n0 + wn * NT * 16 + j * 16 + (lane & 15);
-      const int target = n < N ? p.rows[n].target - p.v0 : -1;
+      const int target = n < N ? p.rows[n].target - p.v0 - m0 : -1;
+      if (__any(target >= 0 && target < BM)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (ml - m0 + i * 16 + r == target) p.at_target[n] = acc[i][j][r] * p.scale;
+      }
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int m = ml + i * 16 + r;
-          const float l = acc[i][j][r] * p.scale;
-          if (m == target) p.at_target[n] = l;
-          acc[i][j][r] = m < p.M ? l : -INFINITY;
-          top = fmaxf(top, acc[i][j][r]);
-        }
+        for (int r = 0; r < 4; ++r) acc[i][j][r] *= to2;
+      if (ends) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = ml + i * 16 + r < p.M ? acc[i][j][r] : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float from = top == -INFINITY ? 0.f : top;  // nothing but minus infinity: a sum of 0
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sum += exp2_fast((acc[i][j][r] - from) * kLog2e);
+        for (int r = 0; r < 4; ++r) sum += exp2_fast(acc[i][j][r] - from);
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);
       if (lane < 16 && n < N) {
-        float* to = p.stat + (((int64_t)p.tile0 + blockIdx.x * WM + wm) * p.T + n) * 2;
-        to[0] = top;
+        float* to = p.stat + (((int64_t)p.tile0 + at.m * WM + wm) * p.T + n) * 2;
+        to[0] = top;  // in units of log 2
         to[1] = sum;
       }
     }
   } else if constexpr (END == Ends::kGrad) {
+    const float to2 = p.scale * kLog2e;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int n = n0 + wn * NT * 16 + j * 16 + (lane & 15);
+      XentRow row{0.f, 0.f, 0.f, -1};
+      if (n < N) row = p.rows[n];
+      const int target = row.target - p.v0 - m0;
+      const float both = row.both * p.scale, lse2 = row.lse * kLog2e;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = both * exp2_fast(fmaf(acc[i][j][r], to2, -lse2));
+      if (__any(target >= 0 && target < BM)) {
+        const float minus = row.dloss * p.scale;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (ml - m0 + i * 16 + r == target) {
+              acc[i][j][r] -= minus;
+              if constexpr (P == 1) p.rest[n] = acc[i][j][r] - (float)(__bf16)acc[i][j][r];
+            }
+      }
+      if (ends) {  // the products' k behind the piece
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = ml + i * 16 + r < p.M ? acc[i][j][r] : 0.f;
+      }
       if (n >= N) continue;
-      const XentRow row = p.rows[n];
-      const int target = row.target - p.v0;
-      const float both = row.both * p.scale, minus = row.dloss * p.scale;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int m = ml + i * 16;
-        float g[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          g[r] = both * exp2_fast((acc[i][j][r] * p.scale - row.lse) * kLog2e);
-          g[r] -= m + r == target ? minus : 0.f;
-          g[r] = m + r < p.M ? g[r] : 0.f;  // the products' k behind the piece
-        }
-        uint16_t* to = p.g + n * p.ldg + m;
+        uint16_t* to = p.g + n * p.ldg + ml + i * 16;
         if constexpr (P == 1) {
           typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<bf16x4*>(to) = bf16x4{(__bf16)g[0], (__bf16)g[1], (__bf16)g[2], (__bf16)g[3]};
+          *reinterpret_cast<bf16x4*>(to) = bf16x4{(__bf16)acc[i][j][0], (__bf16)acc[i][j][1], (__bf16)acc[i][j][2], (__bf16)acc[i][j][3]};
         } else {
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
             uint2 w;
-            w.x = pack_hi(__float_as_uint(g[0]), __float_as_uint(g[1]));
-            w.y = pack_hi(__float_as_uint(g[2]), __float_as_uint(g[3]));
+            w.x = pack_hi(__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1]));
+            w.y = pack_hi(__float_as_uint(acc[i][j][2]), __float_as_uint(acc[i][j][3]));
             *reinterpret_cast<uint2*>(to + q * p.plane_g) = w;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) g[r] -= __uint_as_float(__float_as_uint(g[r]) & 0xffff0000u);
+            for (int r = 0; r < 4; ++r) acc[i][j][r] -= __uint_as_float(__float_as_uint(acc[i][j][r]) & 0xffff0000u);
           }
         }
       }
@@ -315,7 +375,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
       for (int i = 0; i < MT; ++i) {
         const int m = ml + i * 16;
         if (m >= p.ld_dx) continue;
-        f32x4* to = reinterpret_cast<f32x4*>(p.dx_sum + n * p.ld_dx + m);
+        f32x4* to = reinterpret_cast<f32x4*>(p.dx_sum + blockIdx.z * p.plane_dx + n * p.ld_dx + m);
         *to = p.first ? acc[i][j] : *to + acc[i][j];
       }
     }
@@ -358,7 +418,7 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs p, int64_
       for (int64_t i = lane; i < tiles; i += 64) {
         const float2 s = *reinterpret_cast<const float2*>(p.stat + (i * p.T + n) * 2);
         const float m = fmaxf(top, s.x);
-        if (m != -INFINITY) sum = sum * exp2_fast((top - m) * kLog2e) + s.y * exp2_fast((s.x - m) * kLog2e);
+        if (m != -INFINITY) sum = sum * exp2_fast(top - m) + s.y * exp2_fast(s.x - m);
         else sum += s.y;  // 0, or NaN
         top = m;
       }
@@ -366,11 +426,11 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs p, int64_
       for (int d = 1; d < 64; d *= 2) {
         const float m2 = __shfl_xor(top, d, 64), s2 = __shfl_xor(sum, d, 64);
         const float m = fmaxf(top, m2);
-        if (m != -INFINITY) sum = sum * exp2_fast((top - m) * kLog2e) + s2 * exp2_fast((m2 - m) * kLog2e);
+        if (m != -INFINITY) sum = sum * exp2_fast(top - m) + s2 * exp2_fast(m2 - m);
         else sum += s2;
         top = m;
       }
-      lse = top + logf(sum);
+      lse = (top + log2f(sum)) * kLn2;
       loss = lse - p.at_target[n];
     }
     if (lane == 0) {
@@ -380,7 +440,10 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs p, int64_
   }
 }
 
-// dx from the sums over all pieces; zero for the rows that are left out
+// dx from the sums over all pieces, of every split; zero for the rows that are left out.  With bf16 g,
+// what the target's g lost to its rounding is made up for here: it is most of a row's g as a rule, and
+// its rounding alone had dx off by 1.65 times the rounding of the result (2.8e-3 for 1.7e-3 of its size;
+// 8192 tokens of 65536, D = 2048).
 template <typename IO>
 __global__ __launch_bounds__(256) void xent_dx_kernel(const XentArgs p) {
   constexpr int VEC = Chunk<IO>::VEC;
@@ -392,9 +455,25 @@ __global__ __launch_bounds__(256) void xent_dx_kernel(const XentArgs p) {
 #pragma unroll
     for (int e = 0; e < VEC; e += 4) {
       f32x4 v = zero4();
-      if (n >= 0 && c + e < p.DQ) v = *reinterpret_cast<const f32x4*>(p.dx_sum + n * p.DQ + c + e);
+      if (n >= 0 && c + e < p.DQ) {
+        const float* from = p.dx_sum + n * p.DQ + c + e;
+        v = *reinterpret_cast<const f32x4*>(from);
+        for (int z = 1; z < p.splits; ++z) v += *reinterpret_cast<const f32x4*>(from + z * (p.T * p.DQ));
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[e + r] = v[r];
+    }
+    if constexpr (io<IO>::es == 2) {
+      if (n >= 0) {
+        const float rest = p.rest[n];
+        float w[VEC];
+        Chunk<IO> r;
+        r.load(p.w, p.rows[n].target * p.D + c, p.D - c);
+        r.get(w);
+        if (rest != 0.f)  // nor is a weight multiplied that may be infinite
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) x[e] = fmaf(rest, w[e], x[e]);
+      }
     }
     Chunk<IO> out;
     out.set(x);
@@ -407,8 +486,9 @@ unsigned groups_of(int64_t n) { return (unsigned)(n < 1 ? 1 : (n < kMostGroups ?
 
 template <typename IO, Fetch FA, Fetch FB, Ends END>
 hipError_t product(const ProductArgs& a, bool wide, hipStream_t s) {
-  const int b = wide ? 256 : 128;
-  const dim3 grid((unsigned)((a.M + b - 1) / b), (unsigned)((a.N + b - 1) / b));
+  const int b = wide ? 256 : 128, tm = (a.M + b - 1) / b, tn = (a.N + b - 1) / b, rm = xcds_m(tm, tn, wide);
+  const int64_t all = (int64_t)tm * tn, rounds = rm == 0 ? 1 : (int64_t)((tm + 8 * rm - 1) / (8 * rm)) * ((tn + 32 / rm - 1) / (32 / rm));
+  const dim3 grid(rm == 0 ? (unsigned)all : 256u, (unsigned)rounds, END == Ends::kDx ? (unsigned)a.splits : 1u);
   if (wide)
     hipLaunchKernelGGL((product_kernel<IO, 2, 4, 8, 4, FA, FB, END>), grid, dim3(512), 0, s, a);
   else
@@ -500,7 +580,8 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     g.g = static_cast<uint16_t*>(a.g);
     g.ldg = a.piece;
     g.plane_g = a.T * a.piece;
-    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kGrad>(g, a.wide, s);
+    g.rest = a.rest;
+    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kGrad>(g, xent_wide(n, a.T), s);
     if (e != hipSuccess) break;
     ProductArgs x{};
     x.a = w;
@@ -515,8 +596,10 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     x.count_n = a.count;
     x.dx_sum = a.dx_sum;
     x.ld_dx = a.DQ;
+    x.plane_dx = a.T * a.DQ;
+    x.splits = a.splits;
     x.first = v0 == 0;
-    e = product<IO, Fetch::kCols, Fetch::kRows, Ends::kDx>(x, a.wide, s);
+    e = product<IO, Fetch::kCols, Fetch::kRows, Ends::kDx>(x, xent_wide(a.D, a.T), s);
     if (e != hipSuccess || !a.dw) continue;
     ProductArgs d{};
     d.a = static_cast<const uint16_t*>(a.xp);
@@ -532,7 +615,7 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     d.v0 = (int32_t)v0;
     d.dw = a.dw;
     d.ld_dw = a.D;
-    e = product<IO, Fetch::kCols, Fetch::kCols, Ends::kDw>(d, a.wide, s);
+    e = product<IO, Fetch::kCols, Fetch::kCols, Ends::kDw>(d, xent_wide(a.D, n), s);
   }
   if (e != hipSuccess) return e;
   const int64_t pieces = (a.D * io<IO>::es + 15) / 16;
