@@ -149,21 +149,22 @@ struct Loader {
       }
     }
   }
-  // base: the operand's plane; rows (kRows) or columns (kCols) from `first` on, k from k0 on, K in all
-  __device__ __forceinline__ void issue(const uint16_t* base, int64_t ld, int32_t first, int32_t n, int32_t k0, int32_t K,
-                                        int wave, lds_parts to) const {
+  // What a step's loads need.  base: the operand's plane; rows (kRows) or columns (kCols) from `first`
+  // on, k from k0 on, K in all.
+  struct Step {
+    u32x4 rsrc;
+    uint32_t outside;  // of this lane's k
+  };
+  __device__ __forceinline__ Step step(const uint16_t* base, int64_t ld, int32_t first, int32_t n, int32_t k0, int32_t K) const {
     const int32_t left = (F == Fetch::kRows ? n - first : K - k0), most = F == Fetch::kRows ? R : kStep;
     const int32_t rows = left < most ? left : most;
     const uint16_t* at = F == Fetch::kRows ? base + (int64_t)first * ld + k0 : base + (int64_t)k0 * ld + first;
     // the last row ends with the operand's own last element that a load may take
     const int64_t bytes = rows <= 0 ? 0 : ((int64_t)rows * ld - (F == Fetch::kRows ? k0 : first)) * 2;
-    const u32x4 r = rsrc_words(at, (uint32_t)uniform((int)bytes));
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      uint32_t o = off[i];
-      if constexpr (F == Fetch::kRows) o = k0 + c8 < K ? o : kOutside;
-      load_lds(r, (MSM_LDS void*)(to + (wave * kLoads + i) * 512), o);
-    }
+    return Step{rsrc_words((const void*)uniform((int64_t)(uintptr_t)at), (uint32_t)uniform((int)bytes)), F == Fetch::kRows && k0 + c8 >= K ? kOutside : 0u};
+  }
+  __device__ __forceinline__ void load(const Step& s, int i, int wave, lds_parts to) const {
+    load_lds(s.rsrc, (MSM_LDS void*)(to + (wave * kLoads + i) * 512), off[i] | s.outside);
   }
 };
 
@@ -240,34 +241,57 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   }
   const int steps = kPairs * (k_end - k_first);
   int pair = 0, k = k_first;
-  const auto issue = [&](int buffer) {
-    const int2 ab = P == 1 ? int2{0, 0} : part_pair(pair);
-    const lds_parts to = tiles + buffer * (kA + kB);
-    la.issue(p.a + ab.x * p.plane_a, p.lda, m0, p.M, k * kStep, K, wave, to);
-    lb.issue(p.b + ab.y * p.plane_b, p.ldb, n0, N, k * kStep, K, wave, to + kA);
+  using LA = Loader<FA, BM, NW>;
+  using LB = Loader<FB, BN, NW>;
+  constexpr int kLoads = LA::kLoads + LB::kLoads;
+  typename LA::Step sa;
+  typename LB::Step sb;
+  // describes the step to be loaded next; nothing is loaded behind the last
+  const auto next = [&](bool there) {
+    sa = la.step(p.a + (P == 1 ? 0 : part_pair(pair).x * p.plane_a), p.lda, m0, there ? p.M : m0, k * kStep, FA == Fetch::kRows || there ? K : 0);
+    sb = lb.step(p.b + (P == 1 ? 0 : part_pair(pair).y * p.plane_b), p.ldb, n0, there ? N : n0, k * kStep, FB == Fetch::kRows || there ? K : 0);
     if (++k == k_end) {
       k = k_first;
       ++pair;
     }
   };
-  if (steps > 0) issue(0);
+  const auto load = [&](int j, lds_parts to) {
+    if (j < LA::kLoads)
+      la.load(sa, j, wave, to);
+    else
+      lb.load(sb, j - LA::kLoads, wave, to + kA);
+  };
+  if (steps > 0) {
+    next(true);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) load(j, tiles);
+  }
+  // The next step's loads go out one by one between the products: all of them right behind the barrier
+  // hold the wavefronts up for as long as the CU takes to accept 64 KB of them, half a step (forward
+  // at 8192 tokens of 65536, D = 2048: 1833 us, one by one 1710).  Factors are read one tile of rows ahead.
   for (int s = 0; s < steps; ++s) {
     sync_loads();
-    if (s + 1 < steps) issue((s + 1) & 1);
+    next(s + 1 < steps);
+    const lds_parts to = tiles + ((s + 1) & 1) * (kA + kB);
     const lds_cparts ta = tiles + (s & 1) * (kA + kB), tb = ta + kA;
+    bf16x8 b[2][NT], a[2];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 b[NT];
+    for (int j = 0; j < NT; ++j) b[0][j] = rb.read(tb, j, 0);
+    a[0] = ra.read(ta, 0, 0);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) b[j] = rb.read(tb, j, kk);
+    for (int it = 0; it < 2 * MT; ++it) {
+      const int kk = it / MT, i = it % MT;
+      if (it + 1 < 2 * MT) a[(it + 1) & 1] = ra.read(ta, (it + 1) % MT, (it + 1) / MT);
+      if (kk == 0 && i >= MT - NT) b[1][i - (MT - NT)] = rb.read(tb, i - (MT - NT), 1);
+      if (it < kLoads) load(it, to);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const bf16x8 a = ra.read(ta, i, kk);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[j], acc[i][j], 0, 0, 0);
-      }
+      for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[it & 1], b[kk][j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+  // the last step's loads, of nothing, still write zeros: not into LDS that is another workgroup's by then
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   // accumulator r of a lane: m = 4 (lane / 16) + r, n = lane % 16 of its tile
   const int ml = m0 + wm * MT * 16 + 4 * (lane >> 4);
   // the tile's rows of C end inside it, or one of the wavefront's columns has its target there: seldom, so
