@@ -99,7 +99,7 @@ struct XentLayout {
   size_t count, map, inverse, rows, xp, wp, stat, at_target, g, dx_sum, rest, total;
   int64_t DP, DQ, piece, piece_packed;
   int planes, splits;
-  bool direct, wide;
+  bool direct, wide, few;
 };
 
 constexpr int64_t kXentMost = (int64_t)1 << 22;
@@ -142,6 +142,14 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) 
   if (l.piece_packed > l.piece) l.piece_packed = l.piece;
   if (!l.direct) l.piece = l.piece_packed;
   Take take;
+  if (!bwd && T <= msm::kXentFew) {
+    l.xp = take((size_t)ceil_div(D, 32) * ceil_div(T, 16) * 1024 * l.planes);
+    l.stat = take((size_t)msm::kXentFewGroups * T * 8);
+    l.at_target = take((size_t)T * 4);
+    l.few = true;
+    l.total = take.at;
+    return l;
+  }
   l.count = take(4);
   l.map = take((size_t)T * 4);
   l.inverse = take((size_t)T * 4);
@@ -170,7 +178,7 @@ msm::XentArgs xent_args(const XentLayout& l, const void* x, const void* w, const
   a.targets = targets;
   a.count = reinterpret_cast<int32_t*>(ws + l.count);
   a.map = reinterpret_cast<int32_t*>(ws + l.map);
-  a.inverse = reinterpret_cast<int32_t*>(ws + l.inverse);
+  a.inverse = l.few ? nullptr : reinterpret_cast<int32_t*>(ws + l.inverse);
   a.rows = reinterpret_cast<msm::XentRow*>(ws + l.rows);
   a.xp = ws + l.xp;
   a.wp = ws + l.wp;

@@ -94,7 +94,7 @@ struct XentArgs {
   // workspace
   int32_t* count;          // rows that take part
   int32_t* map;            // (T,) their places in x
-  int32_t* inverse;        // (T,) and back, -1 for a row that is left out
+  int32_t* inverse;        // (T,) and back, -1 for a row that is left out; null: rows as they come
   XentRow* rows;           // (T,)
   void* xp;                // [planes][T][DP] bf16 parts of the rows that take part
   void* wp;                // [planes][piece][DP] the same of a piece of w, where w is not read directly
@@ -110,6 +110,8 @@ struct XentArgs {
   int32_t wide;            // the forward's tiles: 256 x 256, else 128 x 128
   int32_t splits;          // of the vocabulary's pieces in the product of dx
 };
+constexpr int kXentFew = 32;         // rows that the forward takes without tiles
+constexpr int kXentFewGroups = 256;  // workgroups it takes them with at most: one a CU
 // Tiles of 256 x 256 or of 128 x 128 for an M x N product: rounds of the 256 CUs (one workgroup a CU, or
 // two of the small tiles), a small tile taking a quarter of a large one's work at 0.8 of its rate.
 constexpr bool xent_wide(int64_t M, int64_t N) {

@@ -431,34 +431,222 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   }
 }
 
-// lse and loss of a row from its tiles' largest logits and sums: a wavefront a row.
+// ---- few rows ----
+// Log-probabilities of up to 32 tokens: the weights are read once, from memory into registers in the
+// matrix cores' layout (lane l: row l % 16, eight k from 8 (l / 16) on).  The tokens are brought into that
+// order beforehand, 1 KB for 32 k of 16 tokens: read as they are, 16 rows a power of two apart at the same k,
+// they come from one channel of L2 (16 tokens of 65536, D = 4096, bf16: 145 us).  Bound by HBM.  A workgroup
+// takes 16 vocabulary rows at a time and its wavefronts a part of k each.
+constexpr int kFewWaves = 16;  // of a workgroup
+constexpr int kFewHeld = 8;    // pieces of 32 k that a wavefront holds
+
+// Joins the largest logit (in units of log 2) and the sum of exponentials of another set of columns.
+__device__ __forceinline__ void join_sums(float& top, float& sum, float top2, float sum2) {
+  const float m = fmaxf(top, top2);
+  if (m != -INFINITY)
+    sum = sum * exp2_fast(top - m) + sum2 * exp2_fast(top2 - m);
+  else
+    sum += sum2;  // 0, or NaN
+  top = m;
+}
+
+// Eight values, in the parts that are multiplied; the first n belong to the row, the others are zero.
+template <typename IO>
+struct Eight {
+  static constexpr int P = io<IO>::es == 2 ? 1 : 3;
+  Chunk<IO> raw[8 / Chunk<IO>::VEC];
+  __device__ __forceinline__ void load(const void* p, int64_t at, int64_t n) {
+#pragma unroll
+    for (int i = 0; i < 8 / Chunk<IO>::VEC; ++i) {
+      const int64_t left = n - i * Chunk<IO>::VEC;
+      raw[i].zero();
+      if (left > 0) raw[i].load(p, at + i * Chunk<IO>::VEC, left);
+    }
+  }
+  __device__ __forceinline__ Part<P> parts() const {
+    if constexpr (P == 1) {
+      Part<1> r;
+      r.p[0] = __builtin_bit_cast(bf16x8, raw[0].raw);
+      return r;
+    } else {
+      return split<3>(__builtin_bit_cast(f32x4, raw[0].raw), __builtin_bit_cast(f32x4, raw[1].raw));
+    }
+  }
+};
+
+// xp: [part][32 k][16 tokens] of 64 lanes' eight values; zeros behind the rows' ends and the last token.
+template <typename IO>
+__global__ __launch_bounds__(256) void xent_few_pack_kernel(const XentArgs p, int pieces, int groups) {
+  const int i = blockIdx.x * 256 + threadIdx.x, lane = i & 63, j = (i >> 6) % groups, c = (i >> 6) / groups;
+  if (c >= pieces) return;
+  const int64_t t = j * 16 + (lane & 15), k = c * 32 + 8 * (lane >> 4);
+  Eight<IO> x;
+  x.load(p.x, (t < p.T ? t : 0) * p.D + k, t < p.T ? p.D - k : 0);
+  store_parts(static_cast<uint16_t*>(p.xp) + (int64_t)i * 8, pieces * groups * 512, x.parts());
+}
+
+// A barrier for what passes through LDS alone: loads from memory stay in flight over it.
+__device__ __forceinline__ void sync_lds_only() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// HOLD: a wavefront's pieces of k, at most kFewHeld, have their tokens in registers throughout (x is p.x),
+// and a tile's weights are loaded during the tile before; else the tokens are read again for every tile, in
+// the matrix cores' order (x is p.xp).  16 tokens of 65536, D = 4096, bf16: 93 and 116 us.
+// (fp32 tokens in three parts do not fit the registers: 16 of 65536, D = 4096, 250 us, 4.3 TB/s.)
+template <typename IO, int NT, bool HOLD>
+__global__ __launch_bounds__(64 * kFewWaves) void xent_few_kernel(const XentArgs p, int tiles) {
+  constexpr int kAhead = HOLD ? kFewHeld : kFewHeld / (NT * (io<IO>::es / 2));  // what the registers hold
+  constexpr int P = Eight<IO>::P;
+  __shared__ f32x4 sums[2][kFewWaves][NT][64];
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  const int k8 = 8 * (lane >> 4);
+  // this wavefront's pieces of 32 k
+  const int pieces = (int)((p.D + 31) / 32), whole = (int)(p.D / 32);
+  const int each = (pieces + kFewWaves - 1) / kFewWaves, c0 = wave * each, c1 = c0 + each < pieces ? c0 + each : pieces;
+  const bf16x8* const xs = static_cast<const bf16x8*>(p.xp) + lane;
+  // the first threads join the parts, each one value of every tile: token t, row 4 g + r of the tile
+  const int cell = threadIdx.x, t = cell / 256 * 16 + (cell & 15), g = (cell >> 4) & 3, r = (cell >> 6) & 3;
+  const bool joins = cell < NT * 256 && t < p.T;
+  const int64_t target = joins ? p.targets[t] : -1;
+  float top = -INFINITY, sum = 0.f;
+  int turn = 0;
+  Eight<IO> w[kAhead];
+  Part<P> x[kAhead][NT];
+  const auto fetch = [&](int c, int tile) {  // kAhead pieces of a tile's rows
+    const int64_t row = (int64_t)tile * 16 + (lane & 15), w_at = (row < p.V ? row : p.V - 1) * p.D + k8;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (c + u < c1 && c + u < whole) w[u].load(p.w, w_at + (int64_t)(c + u) * 32, 8);
+      else if (c + u < c1) w[u].load(p.w, w_at + (int64_t)(c + u) * 32, p.D - (int64_t)(c + u) * 32 - k8);
+      if constexpr (!HOLD)
+        if (c + u < c1)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int q = 0; q < P; ++q) x[u][j].p[q] = xs[((q * pieces + c + u) * NT + j) * 64];
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all loads in flight first: by itself the compiler keeps two or three
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int64_t k = (int64_t)(c0 + u) * 32 + k8, token = j * 16 + (lane & 15);
+        Eight<IO> v;
+        v.load(p.x, (token < p.T ? token : 0) * p.D + k, c0 + u < c1 && token < p.T ? p.D - k : 0);
+        x[u][j] = v.parts();
+      }
+    if ((int)blockIdx.x < tiles) fetch(c0, blockIdx.x);
+  }
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    f32x4 acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = zero4();
+    for (int c = c0; c < c1; c += kAhead) {
+      if constexpr (!HOLD) fetch(c, tile);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (c + u < c1) {
+          const Part<P> a = w[u].parts();
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma(acc[j], a, x[u][j]);
+        }
+    }
+    if constexpr (HOLD) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (tile + (int)gridDim.x < tiles) fetch(c0, tile + gridDim.x);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sums[turn][wave][j][lane] = acc[j];
+    sync_lds_only();  // and what was read two tiles ago may be written
+    if (joins) {
+      float l = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFewWaves; ++i) l += sums[turn][i][cell / 256][g * 16 + (cell & 15)][r];
+      const int64_t v = (int64_t)tile * 16 + 4 * g + r;
+      if (v < p.V) {
+        if (v == target) p.at_target[t] = l * p.scale;
+        l *= p.scale * kLog2e;
+        join_sums(top, sum, l, l == l ? 1.f : l);
+      }
+    }
+  }
+  __syncthreads();
+  // one pair of sums a token from its 16 threads
+  float* all = reinterpret_cast<float*>(sums);
+  if (joins) {
+    all[(t * 16 + g * 4 + r) * 2] = top;
+    all[(t * 16 + g * 4 + r) * 2 + 1] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x < p.T) {
+    top = -INFINITY;
+    sum = 0.f;
+    for (int i = 0; i < 16; ++i) join_sums(top, sum, all[(threadIdx.x * 16 + i) * 2], all[(threadIdx.x * 16 + i) * 2 + 1]);
+    float* to = p.stat + ((int64_t)blockIdx.x * p.T + threadIdx.x) * 2;
+    to[0] = top;
+    to[1] = sum;
+  }
+}
+
+template <typename IO, int NT>
+hipError_t few(const XentArgs& a, hipStream_t s) {
+  const int pieces = (int)((a.D + 31) / 32), tiles = (int)((a.V + 15) / 16);
+  const int groups = tiles < kXentFewGroups ? tiles : kXentFewGroups;
+  if constexpr (io<IO>::es == 2) {
+    if (pieces <= kFewWaves * kFewHeld) {
+      hipLaunchKernelGGL((xent_few_kernel<IO, NT, true>), dim3(groups), dim3(64 * kFewWaves), 0, s, a, tiles);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((xent_few_pack_kernel<IO>), dim3((pieces * NT + 3) / 4), dim3(256), 0, s, a, pieces, NT);
+  hipLaunchKernelGGL((xent_few_kernel<IO, NT, false>), dim3(groups), dim3(64 * kFewWaves), 0, s, a, tiles);
+  return hipGetLastError();
+}
+
+// lse and loss of a row from its tiles' largest logits and sums, by W wavefronts of a workgroup of 4: one
+// for many rows, four for few (16 rows of 1024 tiles: 9.5 us by one, 4.8 by four).
+template <int W>
 __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs p, int64_t tiles) {
-  const int lane = threadIdx.x & 63;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < p.T; t += (int64_t)gridDim.x * 4) {
-    const int n = p.inverse[t];
-    float lse = 0.f, loss = 0.f;
+  __shared__ float others[2][4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = threadIdx.x % (64 * W);
+  for (int64_t t = (int64_t)blockIdx.x * (4 / W) + wave / W; t < p.T; t += (int64_t)gridDim.x * (4 / W)) {
+    int64_t n = t;
+    if (p.inverse)
+      n = p.inverse[t];
+    else if (p.targets[t] < 0 || p.targets[t] >= p.V)
+      n = -1;
+    float top = -INFINITY, sum = 0.f;
     if (n >= 0) {
-      float top = -INFINITY, sum = 0.f;
-      for (int64_t i = lane; i < tiles; i += 64) {
+#pragma unroll 4
+      for (int64_t i = part; i < tiles; i += 64 * W) {
         const float2 s = *reinterpret_cast<const float2*>(p.stat + (i * p.T + n) * 2);
-        const float m = fmaxf(top, s.x);
-        if (m != -INFINITY) sum = sum * exp2_fast(top - m) + s.y * exp2_fast(s.x - m);
-        else sum += s.y;  // 0, or NaN
-        top = m;
+        join_sums(top, sum, s.x, s.y);
       }
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
-        const float m2 = __shfl_xor(top, d, 64), s2 = __shfl_xor(sum, d, 64);
-        const float m = fmaxf(top, m2);
-        if (m != -INFINITY) sum = sum * exp2_fast(top - m) + s2 * exp2_fast(m2 - m);
-        else sum += s2;
-        top = m;
+        const float top2 = __shfl_xor(top, d, 64), sum2 = __shfl_xor(sum, d, 64);
+        join_sums(top, sum, top2, sum2);
       }
-      lse = (top + log2f(sum)) * kLn2;
-      loss = lse - p.at_target[n];
     }
-    if (lane == 0) {
-      p.loss[t] = loss;
+    if constexpr (W > 1) {
+      __syncthreads();  // the row before has been read
+      if (lane == 0) {
+        others[0][wave] = top;
+        others[1][wave] = sum;
+      }
+      __syncthreads();
+      for (int i = 1; i < W; ++i)
+        if (wave == 0) join_sums(top, sum, others[0][i], others[1][i]);
+    }
+    if (part == 0) {
+      const float lse = n < 0 ? 0.f : (top + log2f(sum)) * kLn2;
+      p.loss[t] = n < 0 ? 0.f : lse - p.at_target[n];
       if (p.lse) p.lse[t] = lse;
     }
   }
@@ -549,8 +737,22 @@ hipError_t weights(const XentArgs& a, int64_t v0, int64_t n, ProductArgs* g, hip
   return pack<IO>(at, nullptr, nullptr, n, a, a.piece * a.DP, a.wp, s);
 }
 
+// lse and loss
+hipError_t join(const XentArgs& a, int64_t tiles, hipStream_t s) {
+  if (a.T <= 512)
+    hipLaunchKernelGGL(xent_join_kernel<4>, dim3(groups_of(a.T)), dim3(256), 0, s, a, tiles);
+  else
+    hipLaunchKernelGGL(xent_join_kernel<1>, dim3(groups_of((a.T + 3) / 4)), dim3(256), 0, s, a, tiles);
+  return hipGetLastError();
+}
+
 template <typename IO>
 hipError_t fwd(const XentArgs& a, hipStream_t s) {
+  if (a.T <= kXentFew) {
+    const hipError_t e = a.T <= 16 ? few<IO, 1>(a, s) : few<IO, 2>(a, s);
+    const int64_t groups = (a.V + 15) / 16;
+    return e != hipSuccess ? e : join(a, groups < kXentFewGroups ? groups : kXentFewGroups, s);
+  }
   hipError_t e = gather<IO>(a, s);
   const int64_t part = a.wide ? 128 : 64;  // vocabulary rows of a pair of sums
   int64_t tiles = 0;
@@ -576,9 +778,7 @@ hipError_t fwd(const XentArgs& a, hipStream_t s) {
     e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kStats>(g, a.wide, s);
     tiles += (n + 2 * part - 1) / (2 * part) * 2;
   }
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(xent_join_kernel, dim3(groups_of((a.T + 3) / 4)), dim3(256), 0, s, a, tiles);
-  return hipGetLastError();
+  return e != hipSuccess ? e : join(a, tiles, s);
 }
 
 template <typename IO>
