@@ -121,10 +121,13 @@ int64_t rows_of(size_t bytes, size_t row, int64_t V) {
 }
 
 // The product of dx sums over the vocabulary and has few tiles where T and D are small: its sum is
-// split until the tiles fill the GPU or a split has fewer than 8 steps of 64.
-int xent_splits(int64_t T, int64_t D, int64_t piece) {
-  const int64_t b = msm::xent_wide(D, T) ? 256 : 128, slots = b == 256 ? 256 : 512;
-  int64_t n = slots / (ceil_div(D, b) * ceil_div(T, b));
+// split until the tiles fill the GPU twice (rows without a target leave tiles without work) or a split
+// has fewer than 8 steps of 64.
+int xent_splits(int64_t T, int64_t D, int64_t piece, int planes) {
+  const int64_t b = msm::xent_wide(D, T, planes) ? 256 : 128, slots = b == 256 || planes > 1 ? 256 : 512;
+  const int64_t tiles = ceil_div(D, b) * ceil_div(T, b);
+  if (tiles > slots * 3 / 4) return 1;
+  int64_t n = 2 * slots / tiles;
   if (n > piece / 512) n = piece / 512;
   return (int)(n < 1 ? 1 : (n > 32 ? 32 : n));
 }
@@ -135,7 +138,7 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) 
   l.DP = ceil_div(D, 64) * 64;
   l.DQ = ceil_div(D, 4) * 4;
   l.direct = io == MSM_BF16 && D % 8 == 0;  // if the weights are aligned, too
-  l.wide = msm::xent_wide(V, T);
+  l.wide = msm::xent_wide(V, T, l.planes);
   const size_t row_w = (size_t)l.DP * 2 * l.planes, row_g = (size_t)T * 2 * l.planes;
   l.piece = bwd ? rows_of(kXentPiece, row_g, V) : ceil_div(V, 256) * 256;
   l.piece_packed = rows_of(l.direct ? kXentUnaligned : kXentPiece, row_w, V);
@@ -158,7 +161,7 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) 
   l.wp = take((size_t)l.piece_packed * row_w);
   if (bwd) {
     l.g = take((size_t)l.piece * row_g);
-    l.splits = xent_splits(T, D, l.piece_packed);
+    l.splits = xent_splits(T, D, l.piece_packed, l.planes);
     l.dx_sum = take((size_t)l.splits * T * l.DQ * 4);
     l.rest = take((size_t)T * 4);
   } else {

@@ -39,6 +39,11 @@ __device__ __forceinline__ float group_sum(float v, float* lds) {
   return v;
 }
 
+// 1 / sqrt(sum / D + eps), rounded once: what a row's statistic is off by, the whole row is.
+__device__ __forceinline__ float rstd_of(double sum, double inv, float eps) {
+  return (float)(1. / sqrt(sum * inv + (double)eps));
+}
+
 constexpr int block_threads(int T) { return T < 256 ? 256 : T; }
 constexpr int64_t kRowGroups = 2048;
 
@@ -74,7 +79,7 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const 
       pw[i][e] = p.post_weight && c + e < p.D ? p.post_weight[c + e] : 1.f;
     }
   }
-  const float inv = 1.f / (float)p.D;
+  const double inv = 1. / (double)p.D;
   for (; row < p.rows; row += step) {
     float x[NV][VEC], f[NV][VEC];
     const int64_t at = row * p.D, next = (row + step) * p.D;
@@ -97,7 +102,7 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const 
       if (more) fetch(i, next);
     }
     if (block) {
-      q = 1.f / sqrtf(group_sum<T>(q, lds[turn]) * inv + p.eps);
+      q = rstd_of(group_sum<T>(q, lds[turn]), inv, p.eps);
       turn ^= 1;
       const float qs = q * p.scale;
 #pragma unroll
@@ -117,7 +122,7 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const 
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s = fmaf(x[i][e], x[i][e], s);
-    const float rstd = 1.f / sqrtf(group_sum<T>(s, lds[turn]) * inv + p.eps);
+    const float rstd = rstd_of(group_sum<T>(s, lds[turn]), inv, p.eps);
     turn ^= 1;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -301,7 +306,7 @@ __global__ __launch_bounds__(256) void block_norm_fwd_loop_kernel(const BlockNor
         const double v = at_of<IO>(p.o, at + c);
         s = fma(v, v, s);
       }
-      q = 1.f / sqrtf((float)(wide_sum(s, lds) * inv) + p.eps);
+      q = rstd_of(wide_sum(s, lds), inv, p.eps);
       s = 0;
       for (int64_t c = threadIdx.x; c < p.D; c += 256) {
         float f = at_of<IO>(p.o, at + c) * (q * p.scale);
@@ -317,7 +322,7 @@ __global__ __launch_bounds__(256) void block_norm_fwd_loop_kernel(const BlockNor
         s = fma(v, v, s);
       }
     }
-    const float rstd = 1.f / sqrtf((float)(wide_sum(s, lds + 4) * inv) + p.eps);
+    const float rstd = rstd_of(wide_sum(s, lds + 4), inv, p.eps);
     for (int64_t c = threadIdx.x; c < p.D; c += 256)
       io<IO>::store(p.y, at + c, at_of<IO>(r, at + c) * rstd * (p.weight ? p.weight[c] : 1.f));
     if (threadIdx.x == 0) {

@@ -113,8 +113,10 @@ struct XentArgs {
 constexpr int kXentFew = 32;         // rows that the forward takes without tiles
 constexpr int kXentFewGroups = 256;  // workgroups it takes them with at most: one a CU
 // Tiles of 256 x 256 or of 128 x 128 for an M x N product: rounds of the 256 CUs (one workgroup a CU, or
-// two of the small tiles), a small tile taking a quarter of a large one's work at 0.8 of its rate.
-constexpr bool xent_wide(int64_t M, int64_t N) {
+// two of the small tiles), a small tile taking a quarter of a large one's work at 0.8 of its rate.  Three
+// planes of an fp32 tile fill the LDS at 128 x 128.
+constexpr bool xent_wide(int64_t M, int64_t N, int planes) {
+  if (planes > 1) return false;
   const int64_t large = ((M + 255) / 256) * ((N + 255) / 256), small = ((M + 127) / 128) * ((N + 127) / 128);
   return (large + 255) / 256 * 8 <= (small + 511) / 512 * 5;
 }

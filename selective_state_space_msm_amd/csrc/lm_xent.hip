@@ -91,8 +91,6 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(const void* src, const i
 enum class Fetch { kRows, kCols };
 enum class Ends { kStats, kGrad, kDx, kDw };
 
-constexpr int kStep = 64;  // k of a step
-
 struct ProductArgs {
   const uint16_t *a, *b;
   int64_t lda, ldb;        // elements between rows
@@ -119,27 +117,33 @@ struct ProductArgs {
   int64_t ld_dw;
 };
 
-// Loads of a step of one operand by a wavefront: a tile of R rows of 64 k (128 bytes), or of 64 k
-// rows of R elements.  16-byte units are swizzled so that the reads below spread over all banks: unit
-// u of row r lies at u ^ (r % 8); transposed, the pair of units u of row k at u ^ swz(k).
+// A step's tile of an operand, of one plane: R rows of KS k (64 or 32: 128 or 64 bytes), or KS k rows of R
+// elements.  16-byte units are swizzled so that the reads below spread over all banks: unit u of row r lies
+// at u ^ swz_row(r); transposed, the pair of units u of row k at u ^ swz(k).
+template <int KS>
+__device__ __forceinline__ int swz_row(int r) {
+  if constexpr (KS == 64) return r & 7;
+  return ((r >> 2) & 1) | (((r >> 1) ^ (r >> 3)) & 1) << 1;
+}
 __device__ __forceinline__ int swz(int k) { return (k & 3) | ((k >> 1) & 4); }
 
-template <Fetch F, int R, int NW>
+// Its loads by a wavefront.
+template <Fetch F, int R, int NW, int KS>
 struct Loader {
-  static constexpr int kLoads = R / 8 / NW;  // of 1024 bytes each, by a wavefront
+  static constexpr int kLoads = R * KS / 512 / NW;  // of 1024 bytes each
   uint32_t off[kLoads];
   int c8;
 
   // first: the tile's first row (kRows) or column (kCols), n: rows or columns there are
   __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int32_t first, int32_t n) {
     if constexpr (F == Fetch::kRows) {
-      c8 = ((lane & 7) ^ (lane >> 3)) * 8;
+      constexpr int per = KS / 8, rows = 64 / per;  // lanes of a row, rows of a load
+      c8 = ((lane % per) ^ swz_row<KS>(lane / per)) * 8;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
-        off[i] = (uint32_t)(((wave * kLoads + i) * 8 + (lane >> 3)) * ld + c8) * 2;
+        off[i] = (uint32_t)(((wave * kLoads + i) * rows + lane / per) * ld + c8) * 2;
     } else {
-      constexpr int per = R / 8;       // lanes of a row
-      constexpr int rows = 64 / per;   // rows of a load
+      constexpr int per = R / 8, rows = 64 / per;
       c8 = 0;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -150,32 +154,34 @@ struct Loader {
     }
   }
   // What a step's loads need.  base: the operand's plane; rows (kRows) or columns (kCols) from `first`
-  // on, k from k0 on, K in all.
+  // on, k from k0 on, K in all; nothing is loaded where there is no step.
   struct Step {
     u32x4 rsrc;
     uint32_t outside;  // of this lane's k
   };
-  __device__ __forceinline__ Step step(const uint16_t* base, int64_t ld, int32_t first, int32_t n, int32_t k0, int32_t K) const {
-    const int32_t left = (F == Fetch::kRows ? n - first : K - k0), most = F == Fetch::kRows ? R : kStep;
+  __device__ __forceinline__ Step step(const uint16_t* base, int64_t ld, int32_t first, int32_t n, int32_t k0, int32_t K,
+                                       bool there) const {
+    const int32_t left = (F == Fetch::kRows ? n - first : K - k0), most = F == Fetch::kRows ? R : KS;
     const int32_t rows = left < most ? left : most;
     const uint16_t* at = F == Fetch::kRows ? base + (int64_t)first * ld + k0 : base + (int64_t)k0 * ld + first;
     // the last row ends with the operand's own last element that a load may take
-    const int64_t bytes = rows <= 0 ? 0 : ((int64_t)rows * ld - (F == Fetch::kRows ? k0 : first)) * 2;
-    return Step{rsrc_words((const void*)uniform((int64_t)(uintptr_t)at), (uint32_t)uniform((int)bytes)), F == Fetch::kRows && k0 + c8 >= K ? kOutside : 0u};
+    const int64_t bytes = rows <= 0 || !there ? 0 : ((int64_t)rows * ld - (F == Fetch::kRows ? k0 : first)) * 2;
+    return Step{rsrc_words((const void*)uniform((int64_t)(uintptr_t)at), (uint32_t)uniform((int)bytes)),
+                F == Fetch::kRows && k0 + c8 >= K ? kOutside : 0u};
   }
   __device__ __forceinline__ void load(const Step& s, int i, int wave, lds_parts to) const {
     load_lds(s.rsrc, (MSM_LDS void*)(to + (wave * kLoads + i) * 512), off[i] | s.outside);
   }
 };
 
-// A wavefront's factors of 16 rows each, for 32 of a step's k.
-template <Fetch F, int R>
+// A wavefront's factors of 16 rows each, for the 32 k number kk of a step.
+template <Fetch F, int R, int KS>
 struct Reader {
   int lane, first;  // first: the wavefront's first row in the tile
   __device__ __forceinline__ bf16x8 read(lds_cparts tile, int i, int kk) const {
     if constexpr (F == Fetch::kRows) {
       const int row = first + i * 16 + (lane & 15);
-      return *(const MSM_LDS bf16x8*)(tile + row * 64 + (((lane >> 4) + 4 * kk) ^ (lane & 7)) * 8);
+      return *(const MSM_LDS bf16x8*)(tile + row * KS + (((lane >> 4) + 4 * kk) ^ swz_row<KS>(lane & 15)) * 8);
     } else {
       const int m = lane & 15, k = 32 * kk + 8 * (lane >> 4) + (m >> 2);
       const lds_cparts p = tile + k * R + (((first / 16 + i) ^ swz(k)) * 16) + 4 * (m & 3);
@@ -184,27 +190,40 @@ struct Reader {
   }
 };
 
-// The pairs of parts whose products matter, smallest first.
-__device__ __forceinline__ int2 part_pair(int i) {
-  return i == 0 ? int2{2, 0} : i == 1 ? int2{1, 1} : i == 2 ? int2{0, 2} : i == 3 ? int2{1, 0} : i == 4 ? int2{0, 1} : int2{0, 0};
+// Waits until all but the last N loads of each wavefront have landed.
+template <int N>
+__device__ __forceinline__ void sync_but() {
+  static_assert(N < 64, "vmcnt has 6 bits");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+  __syncthreads();
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Where a workgroup's tile is.  Workgroups go round the 8 XCDs one by one, so number i of an XCD is i * 8
 // + XCD; an XCD takes blocks of 8 x 4 tiles, whose operands its L2 shares, and the XCDs stand rm x 8 / rm
 // side by side, moved on by one from round to round of n, so that a last block of m is not always the same
 // XCDs'.  (All m of one n after another, as the grid counts, the forward reads the whole of W for every 256
-// tokens, 8.6 GB for 8192 of 65536, D = 2048: 2.09 ms there, 1.93 in blocks.)  Small tiles, of which there
-// are few, are taken as they come: blocks leave XCDs idle (160 for 110 us at 513 x 10007 x 1000).
+// tokens, 8.6 GB for 8192 of 65536, D = 2048: 2.09 ms there, 1.93 in blocks.)  Few tiles would leave XCDs
+// without a block: there an XCD takes whole rows or columns of tiles, of the side that has more, where these
+// go round the XCDs evenly enough (the logits of an fp32
+// backward at 1999 tokens of 10007, D = 513: 94 and 91 us).
 struct Place {
   int m, n;
 };
 __host__ __device__ inline int xcds_m(int tm, int tn, bool wide) {
-  if (!wide || tm * (int64_t)tn < 256) return 0;
+  if (tm * (int64_t)tn < (wide ? 256 : 2048)) return 0;
   return tm <= 8 ? 1 : (tn <= 4 ? 8 : (tn <= 8 ? 4 : 2));
 }
 __device__ __forceinline__ Place place_of(int tm, int tn, bool wide) {
   const int rm = xcds_m(tm, tn, wide), at = blockIdx.y * gridDim.x + blockIdx.x;
-  if (rm == 0) return Place{at % tm, at / tm};
+  if (rm == 0) {
+    const bool by_m = tm >= tn;
+    const int large = by_m ? tm : tn, small = by_m ? tn : tm;
+    if ((large + 7) / 8 * 64 > large * 9) return Place{at % tm, at / tm};
+    const int i = at / 8, l = i / small * 8 + at % 8, r = i % small;
+    return by_m ? Place{l, r} : Place{r, l};
+  }
   const int rounds_m = (tm + 8 * rm - 1) / (8 * rm), round = blockIdx.y, round_n = round / rounds_m;
   const int xcd = (blockIdx.x + round_n) % 8, i = blockIdx.x / 8;
   return Place{((round % rounds_m) * rm + xcd % rm) * 8 + i % 8, (round_n * (8 / rm) + xcd / rm) * 4 + i / 8};
@@ -214,81 +233,139 @@ __device__ __forceinline__ Place place_of(int tm, int tn, bool wide) {
 template <typename IO, int WM, int WN, int MT, int NT, Fetch FA, Fetch FB, Ends END>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs p) {
   constexpr int BM = WM * MT * 16, BN = WN * NT * 16, NW = WM * WN, P = io<IO>::es == 2 ? 1 : 3;
-  constexpr int kPairs = P == 1 ? 1 : 6, kA = BM * kStep, kB = BN * kStep;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * (kA + kB)];
+  constexpr int KS = P == 1 ? 64 : 32, kStages = P == 1 ? 2 : 3, kA = BM * KS, kB = BN * KS;
+  using LA = Loader<FA, BM, NW, KS>;
+  using LB = Loader<FB, BN, NW, KS>;
+  constexpr int kLoads = LA::kLoads + LB::kLoads;  // of a plane
+  __shared__ __attribute__((aligned(16))) uint16_t lds[kStages * P * (kA + kB)];
   const int N = p.count_n ? uniform(*p.count_n) : p.N, K = p.count_k ? uniform(*p.count_k) : p.K;
   const Place at = place_of((p.M + BM - 1) / BM, (N + BN - 1) / BN, BM == 256);
   const int32_t m0 = at.m * BM, n0 = at.n * BN;
   if (m0 >= p.M || n0 >= N) return;  // fewer rows than the grid was made for among these
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), wm = wave % WM, wn = wave / WM;
   const lds_parts tiles = (lds_parts)lds;
-  Loader<FA, BM, NW> la;
-  Loader<FB, BN, NW> lb;
+  LA la;
+  LB lb;
   la.init(wave, lane, p.lda, m0, p.M);
   lb.init(wave, lane, p.ldb, n0, N);
-  const Reader<FA, BM> ra{lane, wm * MT * 16};
-  const Reader<FB, BN> rb{lane, wn * NT * 16};
+  const Reader<FA, BM, KS> ra{lane, wm * MT * 16};
+  const Reader<FB, BN, KS> rb{lane, wn * NT * 16};
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = zero4();
-  int k_first = 0, k_end = (K + kStep - 1) / kStep;
+  int k_first = 0, k_end = (K + KS - 1) / KS;
   if constexpr (END == Ends::kDx) {
     const int all = k_end, z = blockIdx.z;
     k_first = (int)((int64_t)all * z / p.splits);
     k_end = (int)((int64_t)all * (z + 1) / p.splits);
   }
-  const int steps = kPairs * (k_end - k_first);
-  int pair = 0, k = k_first;
-  using LA = Loader<FA, BM, NW>;
-  using LB = Loader<FB, BN, NW>;
-  constexpr int kLoads = LA::kLoads + LB::kLoads;
-  typename LA::Step sa;
-  typename LB::Step sb;
-  // describes the step to be loaded next; nothing is loaded behind the last
-  const auto next = [&](bool there) {
-    sa = la.step(p.a + (P == 1 ? 0 : part_pair(pair).x * p.plane_a), p.lda, m0, there ? p.M : m0, k * kStep, FA == Fetch::kRows || there ? K : 0);
-    sb = lb.step(p.b + (P == 1 ? 0 : part_pair(pair).y * p.plane_b), p.ldb, n0, there ? N : n0, k * kStep, FB == Fetch::kRows || there ? K : 0);
-    if (++k == k_end) {
-      k = k_first;
-      ++pair;
+  const int steps = k_end - k_first;
+  typename LA::Step sa[P];
+  typename LB::Step sb[P];
+  int k = k_first, at_send = 0;  // the step to be loaded next, and its stage
+  lds_parts to = tiles;
+  const auto next = [&] {
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      sa[q] = la.step(p.a + q * p.plane_a, p.lda, m0, p.M, k * KS, K, k < k_end);
+      sb[q] = lb.step(p.b + q * p.plane_b, p.ldb, n0, N, k * KS, K, k < k_end);
     }
+    to = tiles + at_send * P * (kA + kB);
+    at_send = at_send + 1 == kStages ? 0 : at_send + 1;
+    ++k;
   };
-  const auto load = [&](int j, lds_parts to) {
+  const auto load = [&](int i) {
+    const int q = i / kLoads, j = i % kLoads;
+    const lds_parts plane = to + q * (kA + kB);
     if (j < LA::kLoads)
-      la.load(sa, j, wave, to);
+      la.load(sa[q], j, wave, plane);
     else
-      lb.load(sb, j - LA::kLoads, wave, to + kA);
+      lb.load(sb[q], j - LA::kLoads, wave, plane + kA);
   };
   if (steps > 0) {
-    next(true);
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) load(j, tiles);
-  }
-  // The next step's loads go out one by one between the products: all of them right behind the barrier
-  // hold the wavefronts up for as long as the CU takes to accept 64 KB of them, half a step (forward
-  // at 8192 tokens of 65536, D = 2048: 1833 us, one by one 1710).  Factors are read one tile of rows ahead.
-  for (int s = 0; s < steps; ++s) {
-    sync_loads();
-    next(s + 1 < steps);
-    const lds_parts to = tiles + ((s + 1) & 1) * (kA + kB);
-    const lds_cparts ta = tiles + (s & 1) * (kA + kB), tb = ta + kA;
-    bf16x8 b[2][NT], a[2];
+    for (int s = 0; s < (P == 1 ? 1 : kStages); ++s) {
+      next();
 #pragma unroll
-    for (int j = 0; j < NT; ++j) b[0][j] = rb.read(tb, j, 0);
-    a[0] = ra.read(ta, 0, 0);
-#pragma unroll
-    for (int it = 0; it < 2 * MT; ++it) {
-      const int kk = it / MT, i = it % MT;
-      if (it + 1 < 2 * MT) a[(it + 1) & 1] = ra.read(ta, (it + 1) % MT, (it + 1) / MT);
-      if (kk == 0 && i >= MT - NT) b[1][i - (MT - NT)] = rb.read(tb, i - (MT - NT), 1);
-      if (it < kLoads) load(it, to);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[it & 1], b[kk][j], acc[i][j], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < P * kLoads; ++i) load(i);
     }
+  }
+  // Loads go out one by one between the products: all of them right behind the barrier hold the wavefronts
+  // up for as long as the CU takes to accept them, 64 KB half a step (bf16 forward at 8192 tokens of 65536,
+  // D = 2048: 1833 us, one by one 1710).
+  if constexpr (P == 1) {
+    // two stages: a step's loads during the step before; factors are read one tile of rows ahead
+    for (int s = 0; s < steps; ++s) {
+      sync_loads();
+      next();
+      const lds_cparts ta = tiles + (s & 1) * (kA + kB), tb = ta + kA;
+      bf16x8 b[2][NT], a[2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) b[0][j] = rb.read(tb, j, 0);
+      a[0] = ra.read(ta, 0, 0);
+#pragma unroll
+      for (int it = 0; it < 2 * MT; ++it) {
+        const int kk = it / MT, i = it % MT;
+        if (it + 1 < 2 * MT) a[(it + 1) & 1] = ra.read(ta, (it + 1) % MT, (it + 1) / MT);
+        if (kk == 0 && i >= MT - NT) b[1][i - (MT - NT)] = rb.read(tb, i - (MT - NT), 1);
+        if (it < kLoads) load(it);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[it & 1], b[kk][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  } else {
+    // Three planes a step, each loaded once for the six products of parts (three loads of an operand where
+    // six products of one plane each take six).  A step's factors are read during the products of the step
+    // before, into the other set of registers: at the barrier before step s those of s are in registers,
+    // s + 1 has landed, s + 2 may be on its way, and s + 3 goes where s was.
+    struct Factors {
+      bf16x8 a[3][MT], b[3][NT];
+    } f0, f1;
+    int at_read = 0;
+    constexpr int kReads = 3 * (MT + NT);
+    const auto read = [&](Factors& f, int i) {
+      const lds_cparts st = tiles + at_read * P * (kA + kB) + i / (MT + NT) * (kA + kB);
+      const int j = i % (MT + NT);
+      if (j < MT)
+        f.a[i / (MT + NT)][j] = ra.read(st, j, 0);
+      else
+        f.b[i / (MT + NT)][j - MT] = rb.read(st + kA, j - MT, 0);
+    };
+    constexpr int pairs[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};  // smallest first
+    const auto step = [&](const Factors& now, Factors& then) {
+      sync_but<P * kLoads>();
+      next();
+      at_read = at_read + 1 == kStages ? 0 : at_read + 1;
+#pragma unroll
+      for (int q = 0; q < 6; ++q) {
+#pragma unroll
+        for (int i = q * kReads / 6; i < (q + 1) * kReads / 6; ++i) read(then, i);
+#pragma unroll
+        for (int i = q * P * kLoads / 6; i < (q + 1) * P * kLoads / 6; ++i) load(i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.a[pairs[q][0]][i], now.b[pairs[q][1]][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    if (steps > 0) {
+      sync_but<(kStages - 1) * P * kLoads>();
+#pragma unroll
+      for (int i = 0; i < kReads; ++i) read(f0, i);
+    }
+    int s = 0;
+    for (; s + 1 < steps; s += 2) {
+      step(f0, f1);
+      step(f1, f0);
+    }
+    if (s < steps) step(f0, f1);
   }
   // the last step's loads, of nothing, still write zeros: not into LDS that is another workgroup's by then
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
@@ -699,12 +776,16 @@ unsigned groups_of(int64_t n) { return (unsigned)(n < 1 ? 1 : (n < kMostGroups ?
 template <typename IO, Fetch FA, Fetch FB, Ends END>
 hipError_t product(const ProductArgs& a, bool wide, hipStream_t s) {
   const int b = wide ? 256 : 128, tm = (a.M + b - 1) / b, tn = (a.N + b - 1) / b, rm = xcds_m(tm, tn, wide);
-  const int64_t all = (int64_t)tm * tn, rounds = rm == 0 ? 1 : (int64_t)((tm + 8 * rm - 1) / (8 * rm)) * ((tn + 32 / rm - 1) / (32 / rm));
+  const int64_t all = (int64_t)((tm + 7) / 8 * 8) * ((tn + 7) / 8 * 8), rounds = rm == 0 ? 1 : (int64_t)((tm + 8 * rm - 1) / (8 * rm)) * ((tn + 32 / rm - 1) / (32 / rm));
   const dim3 grid(rm == 0 ? (unsigned)all : 256u, (unsigned)rounds, END == Ends::kDx ? (unsigned)a.splits : 1u);
-  if (wide)
-    hipLaunchKernelGGL((product_kernel<IO, 2, 4, 8, 4, FA, FB, END>), grid, dim3(512), 0, s, a);
-  else
-    hipLaunchKernelGGL((product_kernel<IO, 2, 2, 4, 4, FA, FB, END>), grid, dim3(256), 0, s, a);
+  if constexpr (io<IO>::es == 4) {
+    hipLaunchKernelGGL((product_kernel<IO, 2, 4, 4, 2, FA, FB, END>), grid, dim3(512), 0, s, a);
+  } else {
+    if (wide)
+      hipLaunchKernelGGL((product_kernel<IO, 2, 4, 8, 4, FA, FB, END>), grid, dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((product_kernel<IO, 2, 2, 4, 4, FA, FB, END>), grid, dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
@@ -805,7 +886,7 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     g.ldg = a.piece;
     g.plane_g = a.T * a.piece;
     g.rest = a.rest;
-    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kGrad>(g, xent_wide(n, a.T), s);
+    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kGrad>(g, xent_wide(n, a.T, a.planes), s);
     if (e != hipSuccess) break;
     ProductArgs x{};
     x.a = w;
@@ -823,7 +904,7 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     x.plane_dx = a.T * a.DQ;
     x.splits = a.splits;
     x.first = v0 == 0;
-    e = product<IO, Fetch::kCols, Fetch::kRows, Ends::kDx>(x, xent_wide(a.D, a.T), s);
+    e = product<IO, Fetch::kCols, Fetch::kRows, Ends::kDx>(x, xent_wide(a.D, a.T, a.planes), s);
     if (e != hipSuccess || !a.dw) continue;
     ProductArgs d{};
     d.a = static_cast<const uint16_t*>(a.xp);
@@ -839,7 +920,7 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     d.v0 = (int32_t)v0;
     d.dw = a.dw;
     d.ld_dw = a.D;
-    e = product<IO, Fetch::kCols, Fetch::kCols, Ends::kDw>(d, xent_wide(a.D, n), s);
+    e = product<IO, Fetch::kCols, Fetch::kCols, Ends::kDw>(d, xent_wide(a.D, n, a.planes), s);
   }
   if (e != hipSuccess) return e;
   const int64_t pieces = (a.D * io<IO>::es + 15) / 16;
