@@ -99,7 +99,8 @@ struct XentLayout {
   size_t count, map, inverse, rows, xp, wp, stat, at_target, g, dx_sum, rest, total;
   int64_t DP, DQ, piece, piece_packed;
   int planes, splits;
-  bool direct, wide, few;
+  bool direct, few;
+  int tile;
 };
 
 constexpr int64_t kXentMost = (int64_t)1 << 22;
@@ -124,7 +125,7 @@ int64_t rows_of(size_t bytes, size_t row, int64_t V) {
 // split until the tiles fill the GPU twice (rows without a target leave tiles without work) or a split
 // has fewer than 8 steps of 64.
 int xent_splits(int64_t T, int64_t D, int64_t piece, int planes) {
-  const int64_t b = msm::xent_wide(D, T, planes) ? 256 : 128, slots = b == 256 || planes > 1 ? 256 : 512;
+  const int64_t b = msm::xent_tile(D, T, piece, planes), slots = b == 256 || (planes > 1 && b == 128) ? 256 : 512;
   const int64_t tiles = ceil_div(D, b) * ceil_div(T, b);
   if (tiles > slots * 3 / 4) return 1;
   int64_t n = 2 * slots / tiles;
@@ -138,7 +139,6 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) 
   l.DP = ceil_div(D, 64) * 64;
   l.DQ = ceil_div(D, 4) * 4;
   l.direct = io == MSM_BF16 && D % 8 == 0;  // if the weights are aligned, too
-  l.wide = msm::xent_wide(V, T, l.planes);
   const size_t row_w = (size_t)l.DP * 2 * l.planes, row_g = (size_t)T * 2 * l.planes;
   l.piece = bwd ? rows_of(kXentPiece, row_g, V) : ceil_div(V, 256) * 256;
   l.piece_packed = rows_of(l.direct ? kXentUnaligned : kXentPiece, row_w, V);
@@ -161,11 +161,11 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) 
   l.wp = take((size_t)l.piece_packed * row_w);
   if (bwd) {
     l.g = take((size_t)l.piece * row_g);
-    l.splits = xent_splits(T, D, l.piece_packed, l.planes);
+    l.splits = xent_splits(T, D, l.piece, l.planes);
     l.dx_sum = take((size_t)l.splits * T * l.DQ * 4);
     l.rest = take((size_t)T * 4);
   } else {
-    l.stat = take((size_t)(ceil_div(V, 64) + 4) * T * 8);
+    l.stat = take((size_t)(ceil_div(V, 32) + 4) * T * 8);
     l.at_target = take((size_t)T * 4);
   }
   l.total = take.at;
@@ -198,9 +198,9 @@ msm::XentArgs xent_args(const XentLayout& l, const void* x, const void* w, const
   a.DQ = l.DQ;
   a.w_direct = l.direct && aligned(w, 16);
   a.piece = a.w_direct ? l.piece : l.piece_packed;
+  a.tile = msm::xent_tile(a.piece < V ? a.piece : V, T, D, l.planes);
   a.scale = scale;
   a.planes = l.planes;
-  a.wide = l.wide;
   return a;
 }
 

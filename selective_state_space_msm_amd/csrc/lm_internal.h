@@ -107,18 +107,21 @@ struct XentArgs {
   float scale;
   int32_t planes;          // 1, or 3 for fp32
   int32_t w_direct;
-  int32_t wide;            // the forward's tiles: 256 x 256, else 128 x 128
+  int32_t tile;            // side of the forward's tiles
   int32_t splits;          // of the vocabulary's pieces in the product of dx
 };
 constexpr int kXentFew = 32;         // rows that the forward takes without tiles
 constexpr int kXentFewGroups = 256;  // workgroups it takes them with at most: one a CU
-// Tiles of 256 x 256 or of 128 x 128 for an M x N product: rounds of the 256 CUs (one workgroup a CU, or
-// two of the small tiles), a small tile taking a quarter of a large one's work at 0.8 of its rate.  Three
-// planes of an fp32 tile fill the LDS at 128 x 128.
-constexpr bool xent_wide(int64_t M, int64_t N, int planes) {
-  if (planes > 1) return false;
+// Side of the tiles of an M x N product over K.  256 or 128 by rounds of the 256 CUs (one workgroup a CU, or
+// two of the smaller tiles), a small tile taking a quarter of a large one's work at 0.8 of its rate; not 256
+// where the tiles' ends are the work (64 tokens, 7178 x 6656: dW in TILE_K).  64 where 128 leaves CUs idle:
+// its five stages hide what two of 128 wait for (64 tokens of 7178, D = 6656: logits TILE_64).  Three planes
+// of an fp32 tile fill the LDS at 128.
+constexpr int xent_tile(int64_t M, int64_t N, int64_t K, int planes) {
   const int64_t large = ((M + 255) / 256) * ((N + 255) / 256), small = ((M + 127) / 128) * ((N + 127) / 128);
-  return (large + 255) / 256 * 8 <= (small + 511) / 512 * 5;
+  if (planes > 1) return small >= 192 ? 128 : 64;
+  if (K > 512 && (large + 255) / 256 * 8 <= (small + 511) / 512 * 5) return 256;
+  return small >= 384 ? 128 : 64;
 }
 hipError_t launch_xent_fwd(const XentArgs& a, int io_bf16, hipStream_t s);
 hipError_t launch_xent_bwd(const XentArgs& a, int io_bf16, hipStream_t s);

@@ -8,9 +8,9 @@
 // exponentials of their columns; the backward takes the vocabulary in pieces, and a piece's g is all
 // of the logits that is ever in memory.
 //
-// One product kernel serves all three: C[m][n] = sum_k A[m][k] B[n][k], C tiles of 256 x 256 (or
-// 128 x 128), 64 values of k at a time through LDS, two buffers, the next step's loads issued before
-// the present step's products.  A and B are each either rows of k ("rows": k is contiguous in
+// One product kernel serves all three: C[m][n] = sum_k A[m][k] B[n][k], C tiles of 256 x 256 (128 x 128
+// and 64 x 64 where these are few), 64 values of k at a time through LDS, the loads of a later step
+// issued between the present step's products.  A and B are each either rows of k ("rows": k is contiguous in
 // memory) or k rows ("columns": m or n is contiguous), which is read transposed out of LDS.  m is
 // always the index that is contiguous in the result, as a lane's accumulators hold four consecutive
 // m of one n: logits are made as [v][t], so that the sums over v stay within a lane's registers but
@@ -119,13 +119,17 @@ struct ProductArgs {
 
 // A step's tile of an operand, of one plane: R rows of KS k (64 or 32: 128 or 64 bytes), or KS k rows of R
 // elements.  16-byte units are swizzled so that the reads below spread over all banks: unit u of row r lies
-// at u ^ swz_row(r); transposed, the pair of units u of row k at u ^ swz(k).
+// at u ^ swz_row(r); transposed, the pair of units u of row k at u ^ swz<R>(k).
 template <int KS>
 __device__ __forceinline__ int swz_row(int r) {
   if constexpr (KS == 64) return r & 7;
   return ((r >> 2) & 1) | (((r >> 1) ^ (r >> 3)) & 1) << 1;
 }
-__device__ __forceinline__ int swz(int k) { return (k & 3) | ((k >> 1) & 4); }
+template <int R>
+__device__ __forceinline__ int swz(int k) {
+  if constexpr (R >= 128) return (k & 3) | ((k >> 1) & 4);
+  return ((k >> 1) & 1) | ((k >> 2) & 2);  // rows of 128 bytes: four pairs of units
+}
 
 // Its loads by a wavefront.
 template <Fetch F, int R, int NW, int KS>
@@ -148,7 +152,7 @@ struct Loader {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int k = (wave * kLoads + i) * rows + lane / per, s = lane % per;
-        const int col = (((s >> 1) ^ swz(k)) * 2 + (s & 1)) * 8;
+        const int col = (((s >> 1) ^ swz<R>(k)) * 2 + (s & 1)) * 8;
         off[i] = first + col < n ? (uint32_t)(k * ld + col) * 2 : kOutside;
       }
     }
@@ -184,7 +188,7 @@ struct Reader {
       return *(const MSM_LDS bf16x8*)(tile + row * KS + (((lane >> 4) + 4 * kk) ^ swz_row<KS>(lane & 15)) * 8);
     } else {
       const int m = lane & 15, k = 32 * kk + 8 * (lane >> 4) + (m >> 2);
-      const lds_cparts p = tile + k * R + (((first / 16 + i) ^ swz(k)) * 16) + 4 * (m & 3);
+      const lds_cparts p = tile + k * R + (((first / 16 + i) ^ swz<R>(k)) * 16) + 4 * (m & 3);
       return read_tr(p, p + 4 * R);
     }
   }
@@ -229,15 +233,15 @@ __device__ __forceinline__ Place place_of(int tm, int tn, bool wide) {
   return Place{((round % rounds_m) * rm + xcd % rm) * 8 + i % 8, (round_n * (8 / rm) + xcd / rm) * 4 + i / 8};
 }
 
-// WM x WN wavefronts of MT x NT tiles of 16 x 16.
-template <typename IO, int WM, int WN, int MT, int NT, Fetch FA, Fetch FB, Ends END>
+// WM x WN wavefronts of MT x NT tiles of 16 x 16; S stages of a step each in LDS.
+template <typename IO, int WM, int WN, int MT, int NT, int S, Fetch FA, Fetch FB, Ends END>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs p) {
   constexpr int BM = WM * MT * 16, BN = WN * NT * 16, NW = WM * WN, P = io<IO>::es == 2 ? 1 : 3;
-  constexpr int KS = P == 1 ? 64 : 32, kStages = P == 1 ? 2 : 3, kA = BM * KS, kB = BN * KS;
+  constexpr int KS = P == 1 ? 64 : 32, kA = BM * KS, kB = BN * KS;
   using LA = Loader<FA, BM, NW, KS>;
   using LB = Loader<FB, BN, NW, KS>;
   constexpr int kLoads = LA::kLoads + LB::kLoads;  // of a plane
-  __shared__ __attribute__((aligned(16))) uint16_t lds[kStages * P * (kA + kB)];
+  __shared__ __attribute__((aligned(16))) uint16_t lds[S * P * (kA + kB)];
   const int N = p.count_n ? uniform(*p.count_n) : p.N, K = p.count_k ? uniform(*p.count_k) : p.K;
   const Place at = place_of((p.M + BM - 1) / BM, (N + BN - 1) / BN, BM == 256);
   const int32_t m0 = at.m * BM, n0 = at.n * BN;
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
       sb[q] = lb.step(p.b + q * p.plane_b, p.ldb, n0, N, k * KS, K, k < k_end);
     }
     to = tiles + at_send * P * (kA + kB);
-    at_send = at_send + 1 == kStages ? 0 : at_send + 1;
+    at_send = at_send + 1 == S ? 0 : at_send + 1;
     ++k;
   };
   const auto load = [&](int i) {
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   };
   if (steps > 0) {
 #pragma unroll
-    for (int s = 0; s < (P == 1 ? 1 : kStages); ++s) {
+    for (int s = 0; s < (P == 1 ? S - 1 : S); ++s) {
       next();
 #pragma unroll
       for (int i = 0; i < P * kLoads; ++i) load(i);
@@ -296,11 +300,14 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   // up for as long as the CU takes to accept them, 64 KB half a step (bf16 forward at 8192 tokens of 65536,
   // D = 2048: 1833 us, one by one 1710).
   if constexpr (P == 1) {
-    // two stages: a step's loads during the step before; factors are read one tile of rows ahead
+    // the loads of S - 1 steps ahead; factors are read one tile of rows ahead
+    static_assert(kLoads <= 2 * MT, "a load between the products of each tile of rows");
+    int stage = 0;
     for (int s = 0; s < steps; ++s) {
-      sync_loads();
+      sync_but<(S - 2) * kLoads>();
       next();
-      const lds_cparts ta = tiles + (s & 1) * (kA + kB), tb = ta + kA;
+      const lds_cparts ta = tiles + stage * (kA + kB), tb = ta + kA;
+      stage = stage + 1 == S ? 0 : stage + 1;
       bf16x8 b[2][NT], a[2];
 #pragma unroll
       for (int j = 0; j < NT; ++j) b[0][j] = rb.read(tb, j, 0);
@@ -322,6 +329,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     // six products of one plane each take six).  A step's factors are read during the products of the step
     // before, into the other set of registers: at the barrier before step s those of s are in registers,
     // s + 1 has landed, s + 2 may be on its way, and s + 3 goes where s was.
+    static_assert(S == 3, "the stages in use and on their way");
     struct Factors {
       bf16x8 a[3][MT], b[3][NT];
     } f0, f1;
@@ -339,7 +347,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     const auto step = [&](const Factors& now, Factors& then) {
       sync_but<P * kLoads>();
       next();
-      at_read = at_read + 1 == kStages ? 0 : at_read + 1;
+      at_read = at_read + 1 == S ? 0 : at_read + 1;
 #pragma unroll
       for (int q = 0; q < 6; ++q) {
 #pragma unroll
@@ -356,7 +364,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
       }
     };
     if (steps > 0) {
-      sync_but<(kStages - 1) * P * kLoads>();
+      sync_but<(S - 1) * P * kLoads>();
 #pragma unroll
       for (int i = 0; i < kReads; ++i) read(f0, i);
     }
@@ -774,17 +782,22 @@ constexpr int64_t kMostGroups = (int64_t)1 << 20;
 unsigned groups_of(int64_t n) { return (unsigned)(n < 1 ? 1 : (n < kMostGroups ? n : kMostGroups)); }
 
 template <typename IO, Fetch FA, Fetch FB, Ends END>
-hipError_t product(const ProductArgs& a, bool wide, hipStream_t s) {
-  const int b = wide ? 256 : 128, tm = (a.M + b - 1) / b, tn = (a.N + b - 1) / b, rm = xcds_m(tm, tn, wide);
+hipError_t product(const ProductArgs& a, int tile, hipStream_t s) {
+  const int b = tile, tm = (a.M + b - 1) / b, tn = (a.N + b - 1) / b, rm = xcds_m(tm, tn, tile == 256);
   const int64_t all = (int64_t)((tm + 7) / 8 * 8) * ((tn + 7) / 8 * 8), rounds = rm == 0 ? 1 : (int64_t)((tm + 8 * rm - 1) / (8 * rm)) * ((tn + 32 / rm - 1) / (32 / rm));
   const dim3 grid(rm == 0 ? (unsigned)all : 256u, (unsigned)rounds, END == Ends::kDx ? (unsigned)a.splits : 1u);
   if constexpr (io<IO>::es == 4) {
-    hipLaunchKernelGGL((product_kernel<IO, 2, 4, 4, 2, FA, FB, END>), grid, dim3(512), 0, s, a);
-  } else {
-    if (wide)
-      hipLaunchKernelGGL((product_kernel<IO, 2, 4, 8, 4, FA, FB, END>), grid, dim3(512), 0, s, a);
+    if (tile == 128)
+      hipLaunchKernelGGL((product_kernel<IO, 2, 4, 4, 2, 3, FA, FB, END>), grid, dim3(512), 0, s, a);
     else
-      hipLaunchKernelGGL((product_kernel<IO, 2, 2, 4, 4, FA, FB, END>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((product_kernel<IO, 2, 2, 2, 2, 3, FA, FB, END>), grid, dim3(256), 0, s, a);
+  } else {
+    if (tile == 256)
+      hipLaunchKernelGGL((product_kernel<IO, 2, 4, 8, 4, 2, FA, FB, END>), grid, dim3(512), 0, s, a);
+    else if (tile == 128)
+      hipLaunchKernelGGL((product_kernel<IO, 2, 2, 4, 4, 2, FA, FB, END>), grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((product_kernel<IO, 2, 2, 2, 2, 5, FA, FB, END>), grid, dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }
@@ -835,7 +848,7 @@ hipError_t fwd(const XentArgs& a, hipStream_t s) {
     return e != hipSuccess ? e : join(a, groups < kXentFewGroups ? groups : kXentFewGroups, s);
   }
   hipError_t e = gather<IO>(a, s);
-  const int64_t part = a.wide ? 128 : 64;  // vocabulary rows of a pair of sums
+  const int64_t part = a.tile / 2;  // vocabulary rows of a pair of sums
   int64_t tiles = 0;
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
     const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
@@ -856,7 +869,7 @@ hipError_t fwd(const XentArgs& a, hipStream_t s) {
     g.T = a.T;
     g.stat = a.stat;
     g.at_target = a.at_target;
-    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kStats>(g, a.wide, s);
+    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kStats>(g, a.tile, s);
     tiles += (n + 2 * part - 1) / (2 * part) * 2;
   }
   return e != hipSuccess ? e : join(a, tiles, s);
@@ -886,7 +899,7 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     g.ldg = a.piece;
     g.plane_g = a.T * a.piece;
     g.rest = a.rest;
-    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kGrad>(g, xent_wide(n, a.T, a.planes), s);
+    e = product<IO, Fetch::kRows, Fetch::kRows, Ends::kGrad>(g, xent_tile(n, a.T, a.D, a.planes), s);
     if (e != hipSuccess) break;
     ProductArgs x{};
     x.a = w;
@@ -904,7 +917,7 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     x.plane_dx = a.T * a.DQ;
     x.splits = a.splits;
     x.first = v0 == 0;
-    e = product<IO, Fetch::kCols, Fetch::kRows, Ends::kDx>(x, xent_wide(a.D, a.T, a.planes), s);
+    e = product<IO, Fetch::kCols, Fetch::kRows, Ends::kDx>(x, xent_tile(a.D, a.T, n, a.planes), s);
     if (e != hipSuccess || !a.dw) continue;
     ProductArgs d{};
     d.a = static_cast<const uint16_t*>(a.xp);
@@ -920,7 +933,7 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     d.v0 = (int32_t)v0;
     d.dw = a.dw;
     d.ld_dw = a.D;
-    e = product<IO, Fetch::kCols, Fetch::kCols, Ends::kDw>(d, xent_wide(a.D, n, a.planes), s);
+    e = product<IO, Fetch::kCols, Fetch::kCols, Ends::kDw>(d, xent_tile(a.D, n, a.T, a.planes), s);
   }
   if (e != hipSuccess) return e;
   const int64_t pieces = (a.D * io<IO>::es + 15) / 16;

@@ -34,14 +34,14 @@ def ulp(n):
 
 
 def inside(got, want, tol, what):
-    got = got.detach().double().cpu().reshape(want.shape)
+    got = got.detach().double().to(want.device).reshape(want.shape)
     assert torch.isfinite(got).all(), what
     err = (got - want).abs()
     log("  %s: %.2g of its bound" % (what, float((err / (tol + 1e-300)).max())))
     assert bool((err <= tol).all()), (what, float(err.max()), float((err / (tol + 1e-300)).max()))
 
 
-def check(io, T, V, D, ignored=0.2, scale=0.9, penalty=True, offset=0, spread=2.0, lead=None, weight_grad=True):
+def check(io, T, V, D, ignored=0.2, scale=0.9, penalty=True, offset=0, spread=2.0, lead=None, weight_grad=True, on="cpu"):
     import selective_state_space_msm_amd as msm
     gen = torch.Generator().manual_seed(T * 7 + V * 3 + D)
     x, w, t = inputs(io, T, V, D, ignored, gen, spread)
@@ -52,7 +52,7 @@ def check(io, T, V, D, ignored=0.2, scale=0.9, penalty=True, offset=0, spread=2.
     loss, lse = msm.msm_linear_cross_entropy_fwd(gx, gw, gt, scale, return_lse=True)
     assert loss.shape == gt.shape == lse.shape
     s = float(torch.tensor(scale))
-    xd, wd = x.double(), w.double()
+    xd, wd, t = x.double().to(on), w.double().to(on), t.to(on)
     rloss, rlse, logits = lm_ref.xent_fwd(xd, wd, t, s)
     # a logit: a sum of D products, each rounding at most 2^-24 of the sum of their sizes; fp32
     # products leave out less than 2^-20 of a term and are summed in six rounds; scaling rounds once
@@ -65,7 +65,7 @@ def check(io, T, V, D, ignored=0.2, scale=0.9, penalty=True, offset=0, spread=2.
     dlse = torch.where(live, dlse, 0.0)
     inside(lse, rlse, dlse, "lse")
     inside(loss, rloss, 2 * dlse, "loss")
-    dloss, dp = torch.randn(T, generator=gen), (0.3 * torch.randn(T, generator=gen) if penalty else None)
+    dloss, dp = torch.randn(T, generator=gen).to(on), (0.3 * torch.randn(T, generator=gen).to(on) if penalty else None)
     gl = rlse.float()
     shape = (lambda a: a) if not lead else (lambda a: a.view(lead))
     d = msm.msm_linear_cross_entropy_bwd(gx, gw, gt, shape(gl.cuda()), shape(dloss.cuda()), scale,
@@ -110,6 +110,13 @@ def test_sizes(io, T, V, D):
 @pytest.mark.parametrize("T,V,D", [(513, 32801, 72), (1030, 13000, 264)])
 def test_many_tiles(io, T, V, D):
     check(io, T, V, D)
+
+
+@pytest.mark.parametrize("io,T,V,D", [("bf16", 2048, 8200, 584), ("bf16", 2056, 1030, 8192), ("bf16", 1030, 2056, 8200),
+                                      ("bf16", 900, 3001, 1032), ("f32", 1800, 1700, 100), ("f32", 300, 6000, 1030)])
+def test_tiles_of_every_size(io, T, V, D):
+    """Logits, dx and dweight in tiles of 256 each once, and in tiles of 128 and 64; the float64 products on the GPU."""
+    check(io, T, V, D, on="cuda")
 
 
 @pytest.mark.parametrize("T", [1, 2, 5, 16, 17, 31, 32, 33, 48, 64, 65])
