@@ -274,59 +274,114 @@ __global__ __launch_bounds__(64 * kSmallWaves) void embed_sort_small_kernel(cons
 template <typename IO>
 __device__ __forceinline__ void add_places(const EmbedArgs& p, const uint32_t* pos, int64_t i0, int64_t i1, int64_t c,
                                            float (&x)[Chunk<IO>::VEC]) {
-  constexpr int VEC = Chunk<IO>::VEC;
+  constexpr int VEC = Chunk<IO>::VEC, N = 8;
   const int64_t n = p.D - c;
-  int64_t i = i0;
-  for (; i + 8 <= i1; i += 8) {
-    Chunk<IO> r[8];
+  for (int64_t i = i0; i < i1; i += N) {
+    Chunk<IO> r[N];
+    uint32_t at[N];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j].load(p.dy, (int64_t)pos[i + j] * p.D + c, n);
+    for (int j = 0; j < N; ++j) at[j] = i + j < i1 ? pos[i + j] : 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < N; ++j) {
+      r[j].zero();
+      if (i + j < i1) r[j].load(p.dy, (int64_t)at[j] * p.D + c, n);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
       float v[VEC];
       r[j].get(v);
+      if (i + j < i1)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] += v[e];
+        for (int e = 0; e < VEC; ++e) x[e] += v[e];
     }
   }
-  for (; i < i1; ++i) {
-    Chunk<IO> r;
-    r.load(p.dy, (int64_t)pos[i] * p.D + c, n);
-    float v[VEC];
-    r.get(v);
+}
+
+// x += sums j0 ... j1 of a level, four in flight
+template <int VEC, typename F>
+__device__ __forceinline__ void add_sums(const float* part, int64_t j0, int64_t j1, int64_t D, int64_t c, F (&x)[VEC]) {
+  constexpr int N = 4;
+  for (int64_t j = j0; j < j1; j += N) {
+    Chunk<float> r[N][VEC / 4];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] += v[e];
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC / 4; ++e) {
+        r[k][e].zero();
+        if (j + k < j1 && c + 4 * e < D) r[k][e].load(part, (j + k) * D + c + 4 * e, D - c - 4 * e);
+      }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (j + k < j1)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] += __uint_as_float(r[k][e / 4].raw[e % 4]);
   }
+}
+
+// Threads of a workgroup over 16-byte pieces of a row, blockIdx.y the 256 of them: where there are few,
+// `parts` threads share a piece, and what each has summed is joined in their order.
+struct Share {
+  int part, parts;
+  int64_t q;  // the piece
+  bool on;
+};
+__device__ __forceinline__ Share share_of(int64_t pieces) {
+  const int64_t left = pieces - (int64_t)blockIdx.y * 256;
+  const int here = (int)(left < 256 ? left : 256), t = threadIdx.x;
+  const int parts = here > 128 ? 1 : (256 / here < 32 ? 256 / here : 32);
+  return Share{t / here, parts, (int64_t)blockIdx.y * 256 + t % here, t < here * parts};
+}
+// Share number `part` of a list
+__device__ __forceinline__ int64_t cut(int64_t a, int64_t b, const Share& s, int part) {
+  return a + (b - a) * part / s.parts;
+}
+// x of the first thread of each piece: the sum of all its threads'.  `lds` holds 256 VEC floats; its barriers
+// are for the whole workgroup.
+template <int VEC>
+__device__ __forceinline__ void join_shares(const Share& s, int64_t pieces, float (&x)[VEC], float* lds) {
+  if (s.parts == 1) return;
+  const int64_t left = pieces - (int64_t)blockIdx.y * 256;
+  const int here = (int)(left < 256 ? left : 256);
+  __syncthreads();  // the join before has been read
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) lds[threadIdx.x * VEC + e] = x[e];
+  __syncthreads();
+  if (s.on && s.part == 0)
+    for (int k = 1; k < s.parts; ++k)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] += lds[(threadIdx.x + k * here) * VEC + e];
 }
 
 // Sums of the runs [32 k, 32 k + 32) of places that belong to one vocabulary row.
 template <typename IO>
 __global__ __launch_bounds__(256) void embed_run_kernel(const EmbedArgs p, int64_t runs, int64_t pieces) {
   constexpr int VEC = Chunk<IO>::VEC;
+  __shared__ float lds[256 * VEC];
   const uint32_t *key = p.key[(p.passes - 1) & 1], *pos = p.pos[(p.passes - 1) & 1];
+  const Share s = share_of(pieces);
+  const int64_t c = s.q * VEC;
   for (int64_t k = blockIdx.x; k < runs; k += gridDim.x) {
-    const int64_t i0 = k * kEmbedRun;
-    if (key[i0] != key[i0 + kEmbedRun - 1] || key[i0] >= p.V) continue;
-    for (int64_t q = threadIdx.x; q < pieces; q += 256) {
-      float x[VEC];
+    const int64_t i0 = k * kEmbedRun, i1 = i0 + kEmbedRun;
+    if (key[i0] != key[i1 - 1] || key[i0] >= p.V) continue;
+    float x[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
-      add_places<IO>(p, pos, i0, i0 + kEmbedRun, q * VEC, x);
-      const int64_t c = q * VEC;
+    for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+    if (s.on) add_places<IO>(p, pos, cut(i0, i1, s, s.part), cut(i0, i1, s, s.part + 1), c, x);
+    join_shares<VEC>(s, pieces, x, lds);
+    if (s.on && s.part == 0)
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
         if (c + e < p.D) p.part[0][k * p.D + c + e] = x[e];
-    }
   }
 }
 
-// The same over 32 runs of one vocabulary row.
+// The same over 32 runs of one vocabulary row, a thread a column.
 __global__ __launch_bounds__(256) void embed_run2_kernel(const EmbedArgs p, int64_t runs) {
   const uint32_t* key = p.key[(p.passes - 1) & 1];
   for (int64_t k = blockIdx.x; k < runs; k += gridDim.x) {
     const int64_t i0 = k * kEmbedRun * kEmbedRun;
     if (key[i0] != key[i0 + kEmbedRun * kEmbedRun - 1] || key[i0] >= p.V) continue;
-    for (int64_t c = threadIdx.x; c < p.D; c += 256) {
+    for (int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x; c < p.D; c += gridDim.y * 256) {
       float x = 0.f;
 #pragma unroll 8
       for (int j = 0; j < kEmbedRun; ++j) x += p.part[0][(k * kEmbedRun + j) * p.D + c];
@@ -335,18 +390,10 @@ __global__ __launch_bounds__(256) void embed_run2_kernel(const EmbedArgs p, int6
   }
 }
 
-constexpr int kRowsOf = 8;  // vocabulary rows of a workgroup
-constexpr int kBusy = 8;     // a row of more places has a workgroup of its own
-
-// x += sums j0 ... j1 of a level
-template <int VEC, typename F>
-__device__ __forceinline__ void add_sums(const float* part, int64_t j0, int64_t j1, int64_t D, int64_t c, F (&x)[VEC]) {
-#pragma unroll 4
-  for (int64_t j = j0; j < j1; ++j)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (c + e < D) x[e] += part[j * D + c + e];
-}
+constexpr int kBusy = 8;      // a row of more places has a workgroup of its own
+constexpr int kMostRows = 64;
+// Vocabulary rows of a workgroup: more where a row has few pieces.
+__host__ __device__ constexpr int rows_of(int64_t pieces) { return pieces <= 32 ? kMostRows : 8; }
 
 // The first of the places lo ... hi whose key is v or more, found by a wavefront: 64 probes a round.
 __device__ __forceinline__ int64_t first_place(const uint32_t* key, int64_t lo, int64_t hi, int64_t v) {
@@ -362,15 +409,15 @@ __device__ __forceinline__ int64_t first_place(const uint32_t* key, int64_t lo, 
   return lo;
 }
 
-// first[r]: the first place of row v0 + r or of what comes after it, r = 0 ... kRowsOf, by a workgroup.
+// first[r]: the first place of row v0 + r or of what comes after it, r = 0 ... rows, by a workgroup.
 // Its barriers close what was read of `first` before; `ends` holds two words, `near` the positions of
 // the first 256 places.
-__device__ __forceinline__ void first_places(const uint32_t* key, const uint32_t* pos, int64_t tokens, int64_t v0, uint32_t* first,
-                                             uint32_t* ends, uint32_t* near) {
+__device__ __forceinline__ void first_places(const uint32_t* key, const uint32_t* pos, int64_t tokens, int64_t v0, int rows,
+                                             uint32_t* first, uint32_t* ends, uint32_t* near) {
   const int wave = threadIdx.x >> 6;
   __syncthreads();
   if (wave < 2) {
-    const int64_t e = first_place(key, 0, tokens, v0 + wave * kRowsOf);
+    const int64_t e = first_place(key, 0, tokens, v0 + wave * rows);
     if ((threadIdx.x & 63) == 0) ends[wave] = (uint32_t)e;
   }
   __syncthreads();
@@ -380,13 +427,20 @@ __device__ __forceinline__ void first_places(const uint32_t* key, const uint32_t
     const int t = threadIdx.x;
     if (t <= n) {  // place t ends the rows before its own, n ends them all
       const int64_t from = t == 0 ? 0 : (int64_t)key[lo + t - 1] - v0 + 1;
-      const int64_t to = t == n ? kRowsOf : (int64_t)key[lo + t] - v0;
+      const int64_t to = t == n ? rows : (int64_t)key[lo + t] - v0;
       for (int64_t r = from; r <= to; ++r) first[r] = (uint32_t)(lo + t);
     }
   } else {
-    for (int r = wave; r <= kRowsOf; r += 4) {
-      const int64_t e = first_place(key, lo, hi, v0 + r);
-      if ((threadIdx.x & 63) == 0) first[r] = (uint32_t)e;
+    for (int r = threadIdx.x; r <= rows; r += 256) {
+      int64_t a = lo, b = hi;
+      while (a < b) {
+        const int64_t mid = (a + b) / 2;
+        if ((int64_t)key[mid] < v0 + r)
+          a = mid + 1;
+        else
+          b = mid;
+      }
+      first[r] = (uint32_t)a;
     }
   }
   __syncthreads();
@@ -413,16 +467,18 @@ __device__ __forceinline__ void store_row(const EmbedArgs& p, int64_t v, int64_t
 }
 
 // All rows.  The first `busy` workgroups each look at one place in kBusy: a row of more places holds at
-// least one of these, and the workgroup of the first of them has the row.  The others take kRowsOf rows
-// each, most of them empty: one batch of loads a row.  (With the busy rows among the others, the
-// workgroup of the first rows took 16 of them one after another: 500 us of 543 for 16384 tokens of 65536,
-// D = 2048, bf16.)
+// least one of these, and the workgroup of the first of them has the row.  The others take some rows each,
+// most of them empty: one batch of loads a row.  (With the busy rows among the others, the workgroup of the
+// first rows took 16 of them one after another: 500 us of 543 for 16384 tokens of 65536, D = 2048, bf16.)
 template <typename TB, typename IO>
 __global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int64_t pieces, int64_t busy) {
   constexpr int VEC = Chunk<IO>::VEC;
-  __shared__ uint32_t first[kRowsOf + 1], ends[2], near[256];
+  __shared__ uint32_t first[kMostRows + 1], ends[2], near[256];
+  __shared__ float lds[256 * VEC];
   const uint32_t *key = p.key[(p.passes - 1) & 1], *pos = p.pos[(p.passes - 1) & 1];
-  const int64_t groups = (p.V + kRowsOf - 1) / kRowsOf;
+  const int each = rows_of(pieces);
+  const int64_t groups = (p.V + each - 1) / each;
+  const Share s = share_of(pieces);
   for (int64_t g = blockIdx.x; g < busy + groups; g += gridDim.x) {
     if (g < busy) {
       const int64_t at = g * kBusy, v = key[at];
@@ -435,45 +491,50 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int6
         if ((threadIdx.x & 63) == 0) ends[threadIdx.x >> 6] = (uint32_t)e;
       }
       __syncthreads();
-      const int64_t i0 = ends[0], i1 = ends[1];
+      const int64_t i0 = ends[0], i1 = ends[1], c = s.q * VEC;
       if (i1 - i0 <= kBusy) continue;
-      for (int64_t q = threadIdx.x; q < pieces; q += 256) {
-        const int64_t c = q * VEC;
-        float x[VEC];
+      float x[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] = 0.f;
-        if (i1 - i0 < 2 * kEmbedRun) {
-          add_places<IO>(p, pos, i0, i1, c, x);
+      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+      const auto places = [&](int64_t a, int64_t b) { add_places<IO>(p, pos, cut(a, b, s, s.part), cut(a, b, s, s.part + 1), c, x); };
+      const auto sums = [&](const float* part, int64_t a, int64_t b, auto& y) {
+        add_sums<VEC>(part, cut(a, b, s, s.part), cut(a, b, s, s.part + 1), p.D, c, y);
+      };
+      if (!s.on) {
+      } else if (i1 - i0 < 2 * kEmbedRun) {
+        places(i0, i1);
+      } else {
+        constexpr int R = kEmbedRun;
+        const int64_t j0 = (i0 + R - 1) / R, j1 = i1 / R;  // whole runs
+        const int64_t m0 = (j0 + R - 1) / R, m1 = j1 / R;  // whole runs of runs
+        places(i0, j0 * R);
+        if (p.part[1] && m0 < m1) {
+          sums(p.part[0], j0, m0 * R, x);
+          double wide[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) wide[e] = x[e];
+          sums(p.part[1], m0, m1, wide);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) x[e] = (float)wide[e];
+          sums(p.part[0], m1 * R, j1, x);
         } else {
-          constexpr int R = kEmbedRun;
-          const int64_t j0 = (i0 + R - 1) / R, j1 = i1 / R;  // whole runs
-          const int64_t m0 = (j0 + R - 1) / R, m1 = j1 / R;  // whole runs of runs
-          add_places<IO>(p, pos, i0, j0 * R, c, x);
-          if (p.part[1] && m0 < m1) {
-            add_sums<VEC>(p.part[0], j0, m0 * R, p.D, c, x);
-            double wide[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) wide[e] = x[e];
-            add_sums<VEC>(p.part[1], m0, m1, p.D, c, wide);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[e] = (float)wide[e];
-            add_sums<VEC>(p.part[0], m1 * R, j1, p.D, c, x);
-          } else {
-            add_sums<VEC>(p.part[0], j0, j1, p.D, c, x);
-          }
-          add_places<IO>(p, pos, j1 * R, i1, c, x);
+          sums(p.part[0], j0, j1, x);
         }
-        store_row<TB, VEC>(p, v, c, x);
+        places(j1 * R, i1);
       }
+      join_shares<VEC>(s, pieces, x, lds);
+      if (s.on && s.part == 0) store_row<TB, VEC>(p, v, c, x);
       continue;
     }
-    const int64_t v0 = (g - busy) * kRowsOf;
-    first_places(key, pos, p.tokens, v0, first, ends, near);
-    const int rows = (int)(p.V - v0 < kRowsOf ? p.V - v0 : kRowsOf);
-    const uint32_t all = rows * (uint32_t)pieces;  // 32 bits: D is at most 2^24
+    const int64_t v0 = (g - busy) * each;
+    first_places(key, pos, p.tokens, v0, each, first, ends, near);
+    const int rows = (int)(p.V - v0 < each ? p.V - v0 : each);
+    // this workgroup's pieces of the rows, in 32 bits
+    const int64_t q0 = (int64_t)blockIdx.y * 256;
+    const uint32_t here = (uint32_t)(pieces - q0 < 256 ? pieces - q0 : 256), all = rows * here;
     for (uint32_t k = threadIdx.x; k < all; k += 256) {
-      const uint32_t r = k / (uint32_t)pieces;
-      const int64_t c = (int64_t)(k - r * (uint32_t)pieces) * VEC, n = p.D - c;
+      const uint32_t r = k / here;
+      const int64_t c = (q0 + (k - r * here)) * VEC, n = p.D - c;
       const int64_t i0 = first[r];
       const int count = (int)(first[r + 1] - i0);
       if (count > kBusy) continue;
@@ -486,8 +547,8 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int6
         for (int j = 0; j < kBusy; ++j) {
           in[j].zero();
           if (j < count) {
-            const int64_t k = i0 + j - ends[0];
-            in[j].load(p.dy, (int64_t)(k < 256 ? near[k] : pos[i0 + j]) * p.D + c, n);
+            const int64_t at = i0 + j - ends[0];
+            in[j].load(p.dy, (int64_t)(at < 256 ? near[at] : pos[i0 + j]) * p.D + c, n);
           }
         }
 #pragma unroll
@@ -523,7 +584,8 @@ hipError_t fwd(const EmbedArgs& a, hipStream_t s) {
 
 template <typename TB, typename IO>
 hipError_t bwd(const EmbedArgs& a, hipStream_t s) {
-  const int64_t pieces = (a.D + Chunk<IO>::VEC - 1) / Chunk<IO>::VEC;
+  const int64_t pieces = (a.D + Chunk<IO>::VEC - 1) / Chunk<IO>::VEC, each = rows_of(pieces);
+  const unsigned slices = (unsigned)((pieces + 255) / 256);
   if (a.tokens <= kEmbedSmall) {
     hipLaunchKernelGGL(embed_sort_small_kernel, dim3(1), dim3(64 * kSmallWaves), 0, s, a);
   } else {
@@ -533,14 +595,14 @@ hipError_t bwd(const EmbedArgs& a, hipStream_t s) {
   }
   if (a.tokens >= 2 * kEmbedRun) {
     const int64_t runs = a.tokens / kEmbedRun;
-    hipLaunchKernelGGL((embed_run_kernel<IO>), dim3(groups_of(runs)), dim3(256), 0, s, a, runs, pieces);
+    hipLaunchKernelGGL((embed_run_kernel<IO>), dim3(groups_of(runs), slices), dim3(256), 0, s, a, runs, pieces);
     if (a.part[1]) {
       const int64_t runs2 = runs / kEmbedRun;
-      hipLaunchKernelGGL(embed_run2_kernel, dim3(groups_of(runs2)), dim3(256), 0, s, a, runs2);
+      hipLaunchKernelGGL(embed_run2_kernel, dim3(groups_of(runs2), slices), dim3(256), 0, s, a, runs2);
     }
   }
   const int64_t busy = a.tokens > kBusy ? (a.tokens + kBusy - 1) / kBusy : 0;
-  hipLaunchKernelGGL((embed_rows_kernel<TB, IO>), dim3(groups_of(busy + (a.V + kRowsOf - 1) / kRowsOf)), dim3(256), 0, s, a, pieces, busy);
+  hipLaunchKernelGGL((embed_rows_kernel<TB, IO>), dim3(groups_of(busy + (a.V + each - 1) / each), slices), dim3(256), 0, s, a, pieces, busy);
   return hipGetLastError();
 }
 
