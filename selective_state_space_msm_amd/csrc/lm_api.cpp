@@ -255,7 +255,7 @@ msm_status msm_embed_bwd(const int64_t* ids, const void* dy, void* dtable, int64
     a.pos[i] = reinterpret_cast<uint32_t*>(ws + l.pos[i]);
     a.part[i] = reinterpret_cast<float*>(ws + l.part[i]);
   }
-  if (tokens < 2 * msm::kEmbedRun * msm::kEmbedRun) a.part[1] = nullptr;
+  if (tokens < msm::kEmbedDeep) a.part[1] = nullptr;
   a.hist = reinterpret_cast<uint32_t*>(ws + l.hist);
   a.tokens = tokens;
   a.V = V;

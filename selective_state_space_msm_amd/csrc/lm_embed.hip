@@ -212,15 +212,17 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_move_kernel(const Embed
   }
 }
 
-// All passes in one workgroup, for up to kEmbedSmall places.
+// All passes in one workgroup, for up to kEmbedSmall places: a place's rank among its wavefront's is kept
+// from the counting to the moving.
 constexpr int kSmallWaves = 16;
 __global__ __launch_bounds__(64 * kSmallWaves) void embed_sort_small_kernel(const EmbedArgs p) {
+  constexpr int kSteps = kEmbedSmall / (64 * kSmallWaves);
   __shared__ uint32_t keys[2][kEmbedSmall];
   __shared__ uint16_t places[2][kEmbedSmall];
   __shared__ uint32_t lds[kSmallWaves][kBins];
   __shared__ uint32_t sums[kSmallWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = 1 << p.bits, b = threadIdx.x;
-  const int n = (int)p.tokens, per = ((n + kSmallWaves * 64 - 1) / (kSmallWaves * 64)) * 64;
+  const int n = (int)p.tokens, steps = (n + kSmallWaves * 64 - 1) / (kSmallWaves * 64);
   for (int i = threadIdx.x; i < n; i += 64 * kSmallWaves) {
     keys[0][i] = key_of(p, i);
     places[0][i] = (uint16_t)i;
@@ -228,12 +230,15 @@ __global__ __launch_bounds__(64 * kSmallWaves) void embed_sort_small_kernel(cons
   uint32_t* bins = lds[wave];
   for (int pass = 0; pass < p.passes; ++pass) {
     const int from = pass & 1, shift = pass * p.bits;
+    uint32_t key[kSteps], rank[kSteps];
     for (int j = lane; j < nb; j += 64) bins[j] = 0;
     __syncthreads();
-    for (int k = 0; k < per; k += 64) {
-      const int i = wave * per + k + lane;
-      const bool on = i < n;
-      count_digit(bins, ((on ? keys[from][i] : 0) >> shift) & (nb - 1), p.bits, on, lane);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int i = (wave * steps + k) * 64 + lane;
+      const bool on = k < steps && i < n;
+      key[k] = on ? keys[from][i] : 0;
+      if (k < steps) rank[k] = take_place(bins, (key[k] >> shift) & (nb - 1), p.bits, on, lane);
       wave_order();
     }
     __syncthreads();
@@ -248,14 +253,12 @@ __global__ __launch_bounds__(64 * kSmallWaves) void embed_sort_small_kernel(cons
         at += c;
       }
     __syncthreads();
-    for (int k = 0; k < per; k += 64) {
-      const int i = wave * per + k + lane;
-      const bool on = i < n;
-      const uint32_t key = on ? keys[from][i] : 0;
-      const uint32_t to = take_place(bins, (key >> shift) & (nb - 1), p.bits, on, lane);
-      wave_order();
-      if (on) {
-        keys[from ^ 1][to] = key;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int i = (wave * steps + k) * 64 + lane;
+      if (k < steps && i < n) {
+        const uint32_t to = bins[(key[k] >> shift) & (nb - 1)] + rank[k];
+        keys[from ^ 1][to] = key[k];
         places[from ^ 1][to] = places[from][i];
       }
     }

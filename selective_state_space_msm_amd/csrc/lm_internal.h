@@ -30,6 +30,7 @@ struct EmbedArgs {
 
 constexpr int kEmbedMostBits = 9;      // of a digit: 512 bins
 constexpr int kEmbedSmall = 4096;      // places that one workgroup sorts in LDS
+constexpr int kEmbedDeep = 8192;       // places from which there are sums of the second level
 constexpr int kEmbedRun = 32;          // places of a sum of the first level, and sums of the second
 hipError_t launch_embed_fwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s);
 hipError_t launch_embed_bwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s);

@@ -61,7 +61,8 @@ def msm_embed_fwd(ids, table, scale=1.0, *, io=None, y=None, stream=None):
     _check(table, "table", (V, D), table.dtype, dev)
     if y is None:
         y = own.empty(shape + (D,), io, dev)
-    _check(y, "y", shape + (D,), io, dev)
+    else:
+        _check(y, "y", shape + (D,), io, dev)
     st = lib.msm_embed_fwd(_ptr(ids), _ptr(table), _ptr(y), ids.numel(), V, D, float(scale), *codes,
                            _stream_handle(stream, dev))
     own.done()
@@ -91,7 +92,8 @@ def msm_embed_bwd(ids, dy, V, scale=1.0, *, table_dtype=None, dtable=None, works
     _check(dy, "dy", shape + (D,), dy.dtype, dev)
     if dtable is None:
         dtable = own.empty((V, D), table_dtype, dev)
-    _check(dtable, "dtable", (V, D), table_dtype, dev)
+    else:
+        _check(dtable, "dtable", (V, D), table_dtype, dev)
     tokens = ids.numel()
     ws, wsb = _workspace(int(lib.msm_embed_bwd_workspace_bytes(tokens, V, D)), workspace, dev, own)
     st = lib.msm_embed_bwd(_ptr(ids), _ptr(dy), _ptr(dtable), tokens, V, D, float(scale), *codes, _ptr(ws), wsb,
@@ -132,24 +134,28 @@ def msm_block_norm_fwd(r, weight=None, o=None, post_weight=None, z=None, scale=1
     shape = tuple(r.shape)
     _check(r, "r", shape, io, dev)
     _block_inputs(weight, o, post_weight, z, shape, io, dev)
+    # what the binding allocates needs no check
     if o is None:
         if post_rstd is not None or (r_out is not None and r_out is not r):
             raise ValueError("r_out and post_rstd belong to o")
         r_out = None
+    elif r_out is None:
+        r_out = own.empty(shape, io, dev)
     else:
-        if r_out is None:
-            r_out = own.empty(shape, io, dev)
         _check(r_out, "r_out", shape, io, dev)
     if y is None:
         y = own.empty(shape, io, dev)
-    _check(y, "y", shape, io, dev)
-    if return_stats:
-        rstd = own.empty(shape[:-1], torch.float32, dev) if rstd is None else rstd
-        if o is not None:
-            post_rstd = own.empty(shape[:-1], torch.float32, dev) if post_rstd is None else post_rstd
-    for t, nm in ((rstd, "rstd"), (post_rstd, "post_rstd")):
-        if t is not None:
-            _check(t, nm, shape[:-1], torch.float32, dev)
+    else:
+        _check(y, "y", shape, io, dev)
+    lead = shape[:-1]
+    if rstd is not None:
+        _check(rstd, "rstd", lead, torch.float32, dev)
+    elif return_stats:
+        rstd = own.empty(lead, torch.float32, dev)
+    if post_rstd is not None:
+        _check(post_rstd, "post_rstd", lead, torch.float32, dev)
+    elif return_stats and o is not None:
+        post_rstd = own.empty(lead, torch.float32, dev)
     st = lib.msm_block_norm_fwd(_ptr(r), _ptr(weight), _ptr(o), _ptr(post_weight), _ptr(z), _ptr(r_out), _ptr(y),
                                 _ptr(rstd), _ptr(post_rstd), rows, D, float(scale), float(eps), code,
                                 _stream_handle(stream, dev))
@@ -196,7 +202,8 @@ def msm_block_norm_bwd(r_out, dy, rstd, weight=None, o=None, post_rstd=None, pos
             continue
         if nm not in d:
             d[nm] = own.empty(shp, dt, dev)
-        _check(d[nm], nm, shp, dt, dev)
+        else:
+            _check(d[nm], nm, shp, dt, dev)
     ws, wsb = _workspace(int(lib.msm_block_norm_bwd_workspace_bytes(rows, D, code)), workspace, dev, own)
     st = lib.msm_block_norm_bwd(_ptr(r_out), _ptr(dy), _ptr(rstd), _ptr(weight), _ptr(o), _ptr(post_rstd),
                                 _ptr(post_weight), _ptr(z), _ptr(dr_out), _ptr(d["dr"]), _ptr(d["do"]), _ptr(d["dz"]),
@@ -275,7 +282,8 @@ def msm_linear_cross_entropy_bwd(x, weight, targets, lse, dloss, scale=1.0, *, d
             continue
         if nm not in d:
             d[nm] = own.empty(shp, io, dev)
-        _check(d[nm], nm, shp, io, dev)
+        else:
+            _check(d[nm], nm, shp, io, dev)
     ws, wsb = _workspace(int(lib.msm_linear_cross_entropy_bwd_workspace_bytes(*sizes, code)), workspace, dev, own)
     st = lib.msm_linear_cross_entropy_bwd(_ptr(x), _ptr(weight), _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dlse),
                                           _ptr(d["dx"]), _ptr(d["dweight"]), *sizes, float(scale), code, _ptr(ws), wsb,
