@@ -60,6 +60,28 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedArgs p, int64
   }
 }
 
+// ---- zeros ----
+
+// Where the vocabulary outnumbers the tokens most rows of dtable are zero.  They are written while few
+// workgroups sort: launch `at` of `of` of the sort fills its share of dtable, by the workgroups behind the
+// sorting ones, and only the rows that have tokens are written again.  (With the zeros written row by row
+// behind the sort: 136 us for 16384 tokens of 65536, D = 2048, bf16; FILL_TIME this way.)
+struct Fill {
+  int64_t bytes;  // of dtable, 0: nothing to fill
+  int at, of;
+};
+template <int THREADS>
+__device__ __forceinline__ void fill_share(const EmbedArgs& p, const Fill& f, int first, int groups) {
+  const int64_t units = (f.bytes + 15) / 16, lo = units * f.at / f.of, hi = units * (f.at + 1) / f.of;
+  char* const to = static_cast<char*>(p.dtable);
+  for (int64_t i = lo + (int64_t)(blockIdx.x - first) * THREADS + threadIdx.x; i < hi; i += (int64_t)(groups - first) * THREADS) {
+    if (i * 16 + 16 <= f.bytes)
+      *reinterpret_cast<u32x4_any*>(to + i * 16) = u32x4{0, 0, 0, 0};
+    else
+      for (int64_t b = i * 16; b < f.bytes; b += 2) *reinterpret_cast<uint16_t*>(to + b) = 0;
+  }
+}
+
 // ---- sorting ----
 
 __device__ __forceinline__ uint32_t key_of(const EmbedArgs& p, int64_t i) {
@@ -109,7 +131,8 @@ __device__ __forceinline__ void place_of(const EmbedArgs& p, int pass, int64_t i
 }
 
 template <bool FIRST>
-__global__ __launch_bounds__(64 * kSortWaves) void embed_count_kernel(const EmbedArgs p, int pass) {
+__global__ __launch_bounds__(64 * kSortWaves) void embed_count_kernel(const EmbedArgs p, int pass, int sorting, const Fill f) {
+  if ((int)blockIdx.x >= sorting) return fill_share<64 * kSortWaves>(p, f, sorting, gridDim.x);
   __shared__ uint32_t lds[kSortWaves][kBins];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = 1 << p.bits;
   const int64_t w = (int64_t)blockIdx.x * kSortWaves + wave;
@@ -154,7 +177,8 @@ __device__ __forceinline__ uint32_t exclusive_sum(uint32_t v, uint32_t* lds) {
 }
 
 template <bool FIRST>
-__global__ __launch_bounds__(64 * kSortWaves) void embed_move_kernel(const EmbedArgs p, int pass) {
+__global__ __launch_bounds__(64 * kSortWaves) void embed_move_kernel(const EmbedArgs p, int pass, int sorting, const Fill f) {
+  if ((int)blockIdx.x >= sorting) return fill_share<64 * kSortWaves>(p, f, sorting, gridDim.x);
   static_assert(64 * kSortWaves == kBins, "a thread for every bin");
   __shared__ uint32_t lds[kSortWaves][kBins];
   __shared__ uint32_t sums[kSortWaves];
@@ -215,7 +239,8 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_move_kernel(const Embed
 // All passes in one workgroup, for up to kEmbedSmall places: a place's rank among its wavefront's is kept
 // from the counting to the moving.
 constexpr int kSmallWaves = 16;
-__global__ __launch_bounds__(64 * kSmallWaves) void embed_sort_small_kernel(const EmbedArgs p) {
+__global__ __launch_bounds__(64 * kSmallWaves) void embed_sort_small_kernel(const EmbedArgs p, const Fill f) {
+  if (blockIdx.x > 0) return fill_share<64 * kSmallWaves>(p, f, 1, gridDim.x);
   constexpr int kSteps = kEmbedSmall / (64 * kSmallWaves);
   __shared__ uint32_t keys[2][kEmbedSmall];
   __shared__ uint16_t places[2][kEmbedSmall];
@@ -469,10 +494,75 @@ __device__ __forceinline__ void store_row(const EmbedArgs& p, int64_t v, int64_t
   }
 }
 
+// The row of the places i0 ... i1, more than kBusy, by a workgroup.
+template <typename TB, typename IO>
+__device__ __forceinline__ void busy_row(const EmbedArgs& p, const Share& s, int64_t pieces, const uint32_t* pos, int64_t v, int64_t i0,
+                                         int64_t i1, float* lds) {
+  constexpr int VEC = Chunk<IO>::VEC;
+  const int64_t c = s.q * VEC;
+  float x[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+  const auto places = [&](int64_t a, int64_t b) { add_places<IO>(p, pos, cut(a, b, s, s.part), cut(a, b, s, s.part + 1), c, x); };
+  const auto sums = [&](const float* part, int64_t a, int64_t b, auto& y) {
+    add_sums<VEC>(part, cut(a, b, s, s.part), cut(a, b, s, s.part + 1), p.D, c, y);
+  };
+  if (!s.on) {
+  } else if (i1 - i0 < 2 * kEmbedRun) {
+    places(i0, i1);
+  } else {
+    constexpr int R = kEmbedRun;
+    const int64_t j0 = (i0 + R - 1) / R, j1 = i1 / R;  // whole runs
+    const int64_t m0 = (j0 + R - 1) / R, m1 = j1 / R;  // whole runs of runs
+    places(i0, j0 * R);
+    if (p.part[1] && m0 < m1) {
+      sums(p.part[0], j0, m0 * R, x);
+      double wide[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) wide[e] = x[e];
+      sums(p.part[1], m0, m1, wide);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] = (float)wide[e];
+      sums(p.part[0], m1 * R, j1, x);
+    } else {
+      sums(p.part[0], j0, j1, x);
+    }
+    places(j1 * R, i1);
+  }
+  join_shares<VEC>(s, pieces, x, lds);
+  if (s.on && s.part == 0) store_row<TB, VEC>(p, v, c, x);
+}
+
+// 16 bytes of a row of up to kBusy places; at(j): the position of place j.
+template <typename TB, typename IO, typename At>
+__device__ __forceinline__ void light_row(const EmbedArgs& p, int64_t v, int64_t c, int count, const At& at) {
+  constexpr int VEC = Chunk<IO>::VEC;
+  float x[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+  if (count > 0) {
+    Chunk<IO> in[kBusy];
+#pragma unroll
+    for (int j = 0; j < kBusy; ++j) {
+      in[j].zero();
+      if (j < count) in[j].load(p.dy, (int64_t)at(j) * p.D + c, p.D - c);
+    }
+#pragma unroll
+    for (int j = 0; j < kBusy; ++j) {
+      float y[VEC];
+      in[j].get(y);
+      if (j < count)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] += y[e];
+    }
+  }
+  store_row<TB, VEC>(p, v, c, x);
+}
+
 // All rows.  The first `busy` workgroups each look at one place in kBusy: a row of more places holds at
-// least one of these, and the workgroup of the first of them has the row.  The others take some rows each,
-// most of them empty: one batch of loads a row.  (With the busy rows among the others, the workgroup of the
-// first rows took 16 of them one after another: 500 us of 543 for 16384 tokens of 65536, D = 2048, bf16.)
+// least one of these, and the workgroup of the first of them has the row.  The others take some rows each:
+// one batch of loads a row.  (With the busy rows among the others, the workgroup of the first rows took 16 of
+// them one after another: 500 us of 543 for 16384 tokens of 65536, D = 2048, bf16.)
 template <typename TB, typename IO>
 __global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int64_t pieces, int64_t busy) {
   constexpr int VEC = Chunk<IO>::VEC;
@@ -494,39 +584,8 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int6
         if ((threadIdx.x & 63) == 0) ends[threadIdx.x >> 6] = (uint32_t)e;
       }
       __syncthreads();
-      const int64_t i0 = ends[0], i1 = ends[1], c = s.q * VEC;
-      if (i1 - i0 <= kBusy) continue;
-      float x[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
-      const auto places = [&](int64_t a, int64_t b) { add_places<IO>(p, pos, cut(a, b, s, s.part), cut(a, b, s, s.part + 1), c, x); };
-      const auto sums = [&](const float* part, int64_t a, int64_t b, auto& y) {
-        add_sums<VEC>(part, cut(a, b, s, s.part), cut(a, b, s, s.part + 1), p.D, c, y);
-      };
-      if (!s.on) {
-      } else if (i1 - i0 < 2 * kEmbedRun) {
-        places(i0, i1);
-      } else {
-        constexpr int R = kEmbedRun;
-        const int64_t j0 = (i0 + R - 1) / R, j1 = i1 / R;  // whole runs
-        const int64_t m0 = (j0 + R - 1) / R, m1 = j1 / R;  // whole runs of runs
-        places(i0, j0 * R);
-        if (p.part[1] && m0 < m1) {
-          sums(p.part[0], j0, m0 * R, x);
-          double wide[VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) wide[e] = x[e];
-          sums(p.part[1], m0, m1, wide);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) x[e] = (float)wide[e];
-          sums(p.part[0], m1 * R, j1, x);
-        } else {
-          sums(p.part[0], j0, j1, x);
-        }
-        places(j1 * R, i1);
-      }
-      join_shares<VEC>(s, pieces, x, lds);
-      if (s.on && s.part == 0) store_row<TB, VEC>(p, v, c, x);
+      const int64_t i0 = ends[0], i1 = ends[1];
+      if (i1 - i0 > kBusy) busy_row<TB, IO>(p, s, pieces, pos, v, i0, i1, lds);
       continue;
     }
     const int64_t v0 = (g - busy) * each;
@@ -537,44 +596,73 @@ __global__ __launch_bounds__(256) void embed_rows_kernel(const EmbedArgs p, int6
     const uint32_t here = (uint32_t)(pieces - q0 < 256 ? pieces - q0 : 256), all = rows * here;
     for (uint32_t k = threadIdx.x; k < all; k += 256) {
       const uint32_t r = k / here;
-      const int64_t c = (q0 + (k - r * here)) * VEC, n = p.D - c;
       const int64_t i0 = first[r];
       const int count = (int)(first[r + 1] - i0);
       if (count > kBusy) continue;
-      float x[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
-      if (count > 0) {
-        Chunk<IO> in[kBusy];
-#pragma unroll
-        for (int j = 0; j < kBusy; ++j) {
-          in[j].zero();
-          if (j < count) {
-            const int64_t at = i0 + j - ends[0];
-            in[j].load(p.dy, (int64_t)(at < 256 ? near[at] : pos[i0 + j]) * p.D + c, n);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kBusy; ++j) {
-          float v[VEC];
-          in[j].get(v);
-          if (j < count)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[e] += v[e];
-        }
-      }
-      store_row<TB, VEC>(p, v0 + r, c, x);
+      light_row<TB, IO>(p, v0 + r, (q0 + (k - r * here)) * VEC, count, [&](int j) {
+        const int64_t at = i0 + j - ends[0];
+        return at < 256 ? near[at] : pos[i0 + j];
+      });
+    }
+  }
+}
+
+// The rows that have tokens, where the others are filled already: a workgroup takes those whose first
+// place is among its kBusy places.
+template <typename TB, typename IO>
+__global__ __launch_bounds__(256) void embed_present_kernel(const EmbedArgs p, int64_t pieces) {
+  constexpr int VEC = Chunk<IO>::VEC, W = 2 * kBusy;
+  constexpr uint32_t kNone = 0xffffffffu;  // no key: V is below it
+  __shared__ uint32_t near_key[W + 1], near_pos[W];
+  __shared__ float lds[256 * VEC];
+  const uint32_t *key = p.key[(p.passes - 1) & 1], *pos = p.pos[(p.passes - 1) & 1];
+  const Share s = share_of(pieces);
+  const int64_t q0 = (int64_t)blockIdx.y * 256, groups = (p.tokens + kBusy - 1) / kBusy;
+  const uint32_t here = (uint32_t)(pieces - q0 < 256 ? pieces - q0 : 256);
+  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
+    const int64_t i0 = g * kBusy;
+    __syncthreads();  // the places before have been read
+    if (threadIdx.x <= W) {  // near_key[i + 1] is place i's
+      const int64_t i = i0 + (int)threadIdx.x - 1;
+      near_key[threadIdx.x] = i >= 0 && i < p.tokens ? key[i] : kNone;
+      if (threadIdx.x > 0) near_pos[threadIdx.x - 1] = i < p.tokens ? pos[i] : 0;
+    }
+    __syncthreads();
+    // places of the row that starts at place i, kBusy + 1 for more than kBusy, 0: none starts there
+    const auto count_of = [&](int i) {
+      const uint32_t v = near_key[i + 1];
+      if (v == near_key[i] || v >= (uint32_t)p.V) return 0;
+      int n = 1;
+      while (n <= kBusy && i + n < W && near_key[i + 1 + n] == v) ++n;
+      return n;
+    };
+    for (uint32_t k = threadIdx.x; k < kBusy * here; k += 256) {
+      const int i = (int)(k / here), count = count_of(i);
+      if (count == 0 || count > kBusy) continue;
+      light_row<TB, IO>(p, near_key[i + 1], (q0 + (k - i * here)) * VEC, count, [&](int j) { return near_pos[i + j]; });
+    }
+    for (int i = 0; i < kBusy; ++i) {
+      if (count_of(i) <= kBusy) continue;
+      const int64_t v = near_key[i + 1];
+      busy_row<TB, IO>(p, s, pieces, pos, v, i0 + i, first_place(key, i0 + i, p.tokens, v + 1), lds);
     }
   }
 }
 
 unsigned groups_of(int64_t n) { return (unsigned)(n < 1 ? 1 : (n < kMostGroups ? n : kMostGroups)); }
 
+// Workgroups that fill `bytes` beside a sort of `of` launches
+unsigned fill_groups(int64_t bytes, int of) {
+  const int64_t n = (bytes / of + 65535) / 65536;
+  return (unsigned)(n < 1024 ? n : 1024);
+}
+
 template <bool FIRST>
-hipError_t sort_pass(const EmbedArgs& a, int pass, hipStream_t s) {
-  const dim3 grid((unsigned)((a.waves + kSortWaves - 1) / kSortWaves)), block(64 * kSortWaves);
-  hipLaunchKernelGGL(embed_count_kernel<FIRST>, grid, block, 0, s, a, pass);
-  hipLaunchKernelGGL(embed_move_kernel<FIRST>, grid, block, 0, s, a, pass);
+hipError_t sort_pass(const EmbedArgs& a, int pass, int64_t fill, hipStream_t s) {
+  const int sorting = (a.waves + kSortWaves - 1) / kSortWaves, of = 2 * a.passes;
+  const dim3 grid(sorting + fill_groups(fill, of)), block(64 * kSortWaves);
+  hipLaunchKernelGGL(embed_count_kernel<FIRST>, grid, block, 0, s, a, pass, sorting, Fill{fill, 2 * pass, of});
+  hipLaunchKernelGGL(embed_move_kernel<FIRST>, grid, block, 0, s, a, pass, sorting, Fill{fill, 2 * pass + 1, of});
   return hipGetLastError();
 }
 
@@ -589,11 +677,13 @@ template <typename TB, typename IO>
 hipError_t bwd(const EmbedArgs& a, hipStream_t s) {
   const int64_t pieces = (a.D + Chunk<IO>::VEC - 1) / Chunk<IO>::VEC, each = rows_of(pieces);
   const unsigned slices = (unsigned)((pieces + 255) / 256);
+  const bool sparse = a.V >= a.tokens;
+  const int64_t fill = sparse ? a.V * a.D * io<TB>::es : 0;
   if (a.tokens <= kEmbedSmall) {
-    hipLaunchKernelGGL(embed_sort_small_kernel, dim3(1), dim3(64 * kSmallWaves), 0, s, a);
+    hipLaunchKernelGGL(embed_sort_small_kernel, dim3(1 + fill_groups(fill, 1)), dim3(64 * kSmallWaves), 0, s, a, Fill{fill, 0, 1});
   } else {
-    hipError_t e = sort_pass<true>(a, 0, s);
-    for (int pass = 1; pass < a.passes && e == hipSuccess; ++pass) e = sort_pass<false>(a, pass, s);
+    hipError_t e = sort_pass<true>(a, 0, fill, s);
+    for (int pass = 1; pass < a.passes && e == hipSuccess; ++pass) e = sort_pass<false>(a, pass, fill, s);
     if (e != hipSuccess) return e;
   }
   if (a.tokens >= 2 * kEmbedRun) {
@@ -604,8 +694,12 @@ hipError_t bwd(const EmbedArgs& a, hipStream_t s) {
       hipLaunchKernelGGL(embed_run2_kernel, dim3(groups_of(runs2), slices), dim3(256), 0, s, a, runs2);
     }
   }
-  const int64_t busy = a.tokens > kBusy ? (a.tokens + kBusy - 1) / kBusy : 0;
-  hipLaunchKernelGGL((embed_rows_kernel<TB, IO>), dim3(groups_of(busy + (a.V + each - 1) / each), slices), dim3(256), 0, s, a, pieces, busy);
+  if (sparse) {
+    hipLaunchKernelGGL((embed_present_kernel<TB, IO>), dim3(groups_of((a.tokens + kBusy - 1) / kBusy), slices), dim3(256), 0, s, a, pieces);
+  } else {
+    const int64_t busy = a.tokens > kBusy ? (a.tokens + kBusy - 1) / kBusy : 0;
+    hipLaunchKernelGGL((embed_rows_kernel<TB, IO>), dim3(groups_of(busy + (a.V + each - 1) / each), slices), dim3(256), 0, s, a, pieces, busy);
+  }
   return hipGetLastError();
 }
 
