@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedArgs p, int64
 // Where the vocabulary outnumbers the tokens most rows of dtable are zero.  They are written while few
 // workgroups sort: launch `at` of `of` of the sort fills its share of dtable, by the workgroups behind the
 // sorting ones, and only the rows that have tokens are written again.  (With the zeros written row by row
-// behind the sort: 136 us for 16384 tokens of 65536, D = 2048, bf16; FILL_TIME this way.)
+// behind the sort: 136 us for 16384 tokens of 65536, D = 2048, bf16; 114 us this way.)
 struct Fill {
   int64_t bytes;  // of dtable, 0: nothing to fill
   int at, of;

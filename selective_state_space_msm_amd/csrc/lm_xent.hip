@@ -19,13 +19,51 @@
 // bf16 inputs are multiplied as they are; g is rounded to bf16 for the products with W and x
 // (its relative error of 2^-9 is that of rounding the results, which it joins as a random error over
 // the summed terms).  fp32 values are cut into three bf16 parts, and the six products that matter are
-// summed (ops_delta.hpp), g too.  Rows without a target are left out of all products: the rows that
+// summed, g too.  Rows without a target are left out of all products: the rows that
 // take part are gathered in front, and what the others hold is never multiplied.
 #include "lm_internal.h"
 #include "ops_row.hpp"
 
 namespace msm {
 namespace {
+
+// ---- parts ----
+// fp32 values in three bf16 parts: the first 8 bits, the next 8 rounded, what is left (exact).  The products
+// of parts that are left out (second times third, third times third) are then of either sign and below 2^-23
+// of a product; with all parts cut off they would all have the product's sign and make logits too small.
+// The first part is not rounded, so the largest finite values stay finite.
+__device__ __forceinline__ void cut3(float x0, float x1, uint32_t (&w)[3]) {
+  const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
+  w[0] = pack_hi(u0, u1);
+  x0 -= __uint_as_float(u0 & 0xffff0000u);
+  x1 -= __uint_as_float(u1 & 0xffff0000u);
+#pragma unroll
+  for (int q = 1; q < 3; ++q) {
+    const uint32_t lo = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x0)), hi = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x1));
+    w[q] = lo | (hi << 16);
+    x0 -= __uint_as_float(lo << 16);
+    x1 -= __uint_as_float(hi << 16);
+  }
+}
+template <int P>
+__device__ __forceinline__ Part<P> parts_of(const float (&x)[8]) {
+  if constexpr (P == 1) {
+    return split<1>(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
+  } else {
+    Part<3> r;
+    u32x4 w[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t c[3];
+      cut3(x[2 * i], x[2 * i + 1], c);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) w[q][i] = c[q];
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) r.p[q] = __builtin_bit_cast(bf16x8, w[q]);
+    return r;
+  }
+}
 
 // ---- rows that take part ----
 
@@ -81,8 +119,7 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(const void* src, const i
       if (left > e) r.load(src, at + e, left - e);
       r.get(x + e);
     }
-    const Part<P> s = split<P>(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
-    store_parts(dst + row * DP + c, plane, s);
+    store_parts(dst + row * DP + c, plane, parts_of<P>(x));
   }
 }
 
@@ -343,7 +380,15 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
       else
         f.b[i / (MT + NT)][j - MT] = rb.read(st + kA, j - MT, 0);
     };
-    constexpr int pairs[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};  // smallest first
+    // The product of the first parts has a sum of its own: each term that is added to a sum rounds it, and
+    // the five small products would round the large sum five times as often for nothing (gradients at 192
+    // tokens of 610, D = 1776: 2.5e-6 off in one sum, 1.0e-6 in two; plain fp32 products 9.5e-7).
+    constexpr int pairs[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
+    f32x4 low[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) low[i][j] = zero4();
     const auto step = [&](const Factors& now, Factors& then) {
       sync_but<P * kLoads>();
       next();
@@ -358,8 +403,10 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.a[pairs[q][0]][i], now.b[pairs[q][1]][j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < NT; ++j) {
+            f32x4& to = q == 5 ? acc[i][j] : low[i][j];
+            to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.a[pairs[q][0]][i], now.b[pairs[q][1]][j], to, 0, 0, 0);
+          }
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -374,6 +421,10 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
       step(f1, f0);
     }
     if (s < steps) step(f0, f1);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] += low[i][j];
   }
   // the last step's loads, of nothing, still write zeros: not into LDS that is another workgroup's by then
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
@@ -434,10 +485,13 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
       if (n < N) row = p.rows[n];
       const int target = row.target - p.v0 - m0;
       const float both = row.both * p.scale, lse2 = row.lse * kLog2e;
+      // l - lse is rounded where it is small, not where its two terms are; in front of a g in bf16 one
+      // operation less is worth more
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = both * exp2_fast(fmaf(acc[i][j][r], to2, -lse2));
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = both * exp2_fast(P == 1 ? fmaf(acc[i][j][r], to2, -lse2) : fmaf(acc[i][j][r], p.scale, -row.lse) * kLog2e);
       if (__any(target >= 0 && target < BM)) {
         const float minus = row.dloss * p.scale;
 #pragma unroll
@@ -463,15 +517,11 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
           typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
           *reinterpret_cast<bf16x4*>(to) = bf16x4{(__bf16)acc[i][j][0], (__bf16)acc[i][j][1], (__bf16)acc[i][j][2], (__bf16)acc[i][j][3]};
         } else {
+          uint32_t lo[3], hi[3];
+          cut3(acc[i][j][0], acc[i][j][1], lo);
+          cut3(acc[i][j][2], acc[i][j][3], hi);
 #pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            uint2 w;
-            w.x = pack_hi(__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1]));
-            w.y = pack_hi(__float_as_uint(acc[i][j][2]), __float_as_uint(acc[i][j][3]));
-            *reinterpret_cast<uint2*>(to + q * p.plane_g) = w;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] -= __uint_as_float(__float_as_uint(acc[i][j][r]) & 0xffff0000u);
-          }
+          for (int q = 0; q < 3; ++q) *reinterpret_cast<uint2*>(to + q * p.plane_g) = uint2{lo[q], hi[q]};
         }
       }
     }
@@ -524,6 +574,13 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
 // takes 16 vocabulary rows at a time and its wavefronts a part of k each.
 constexpr int kFewWaves = 16;  // of a workgroup
 constexpr int kFewHeld = 8;    // pieces of 32 k that a wavefront holds
+// Wavefronts of a tile: as few as hold all of its k, so that short rows do not leave wavefronts idle (28
+// tokens of 96399, D = 141, bf16: 50 us with all 16 on a tile, 32 with one).
+__host__ __device__ constexpr int few_waves(int pieces) {
+  int n = 1;
+  while (n < kFewWaves && pieces > n * kFewHeld) n *= 2;
+  return n;
+}
 
 // Joins the largest logit (in units of log 2) and the sum of exponentials of another set of columns.
 __device__ __forceinline__ void join_sums(float& top, float& sum, float top2, float sum2) {
@@ -554,7 +611,10 @@ struct Eight {
       r.p[0] = __builtin_bit_cast(bf16x8, raw[0].raw);
       return r;
     } else {
-      return split<3>(__builtin_bit_cast(f32x4, raw[0].raw), __builtin_bit_cast(f32x4, raw[1].raw));
+      float x[8];
+      raw[0].get(x);
+      raw[1].get(x + 4);
+      return parts_of<3>(x);
     }
   }
 };
@@ -582,20 +642,21 @@ __device__ __forceinline__ void sync_lds_only() {
 // and a tile's weights are loaded during the tile before; else the tokens are read again for every tile, in
 // the matrix cores' order (x is p.xp).  16 tokens of 65536, D = 4096, bf16: 93 and 116 us.
 // (fp32 tokens in three parts do not fit the registers: 16 of 65536, D = 4096, 250 us, 4.3 TB/s.)
-template <typename IO, int NT, bool HOLD>
+template <typename IO, int NT, bool HOLD, bool ALL>
 __global__ __launch_bounds__(64 * kFewWaves) void xent_few_kernel(const XentArgs p, int tiles) {
   constexpr int kAhead = HOLD ? kFewHeld : kFewHeld / (NT * (io<IO>::es / 2));  // what the registers hold
   constexpr int P = Eight<IO>::P;
   __shared__ f32x4 sums[2][kFewWaves][NT][64];
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
   const int k8 = 8 * (lane >> 4);
-  // this wavefront's pieces of 32 k
-  const int pieces = (int)((p.D + 31) / 32), whole = (int)(p.D / 32);
-  const int each = (pieces + kFewWaves - 1) / kFewWaves, c0 = wave * each, c1 = c0 + each < pieces ? c0 + each : pieces;
+  // `kw` wavefronts share a tile's k, the others have tiles of their own; this wavefront's pieces of 32 k
+  const int pieces = (int)((p.D + 31) / 32), whole = (int)(p.D / 32), kw = ALL ? kFewWaves : few_waves(pieces), side = kFewWaves / kw;
+  const int each = (pieces + kw - 1) / kw, c0 = wave % kw * each, c1 = c0 + each < pieces ? c0 + each : pieces, own = wave / kw;
   const bf16x8* const xs = static_cast<const bf16x8*>(p.xp) + lane;
-  // the first threads join the parts, each one value of every tile: token t, row 4 g + r of the tile
-  const int cell = threadIdx.x, t = cell / 256 * 16 + (cell & 15), g = (cell >> 4) & 3, r = (cell >> 6) & 3;
-  const bool joins = cell < NT * 256 && t < p.T;
+  // the threads join the parts, each one value of some tiles: token t, row 4 g + r of the tile
+  constexpr int kCells = NT * 256, kTurns = 64 * kFewWaves / kCells;
+  const int cell = threadIdx.x % kCells, t = cell / 256 * 16 + (cell & 15), g = (cell >> 4) & 3, r = (cell >> 6) & 3;
+  const bool joins = t < p.T;
   const int64_t target = joins ? p.targets[t] : -1;
   float top = -INFINITY, sum = 0.f;
   int turn = 0;
@@ -626,14 +687,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void xent_few_kernel(const XentArgs
         v.load(p.x, (token < p.T ? token : 0) * p.D + k, c0 + u < c1 && token < p.T ? p.D - k : 0);
         x[u][j] = v.parts();
       }
-    if ((int)blockIdx.x < tiles) fetch(c0, blockIdx.x);
+    if ((int)blockIdx.x * side < tiles) fetch(c0, blockIdx.x * side + own);
   }
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+  const int stride = gridDim.x * side;
+  for (int tile = blockIdx.x * side; tile < tiles; tile += stride, turn ^= 1) {
     f32x4 acc[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j] = zero4();
     for (int c = c0; c < c1; c += kAhead) {
-      if constexpr (!HOLD) fetch(c, tile);
+      if constexpr (!HOLD) fetch(c, tile + own);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
         if (c + u < c1) {
@@ -644,16 +706,20 @@ __global__ __launch_bounds__(64 * kFewWaves) void xent_few_kernel(const XentArgs
     }
     if constexpr (HOLD) {
       __builtin_amdgcn_sched_barrier(0);
-      if (tile + (int)gridDim.x < tiles) fetch(c0, tile + gridDim.x);
+      if (tile + stride < tiles) fetch(c0, tile + stride + own);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) sums[turn][wave][j][lane] = acc[j];
     sync_lds_only();  // and what was read two tiles ago may be written
-    if (joins) {
+    for (int sub = threadIdx.x / kCells; joins && sub < side; sub += kTurns) {
       float l = 0.f;
+      if constexpr (ALL) {
 #pragma unroll
-      for (int i = 0; i < kFewWaves; ++i) l += sums[turn][i][cell / 256][g * 16 + (cell & 15)][r];
-      const int64_t v = (int64_t)tile * 16 + 4 * g + r;
+        for (int i = 0; i < kFewWaves; ++i) l += sums[turn][i][cell / 256][g * 16 + (cell & 15)][r];
+      } else {
+        for (int i = 0; i < kw; ++i) l += sums[turn][sub * kw + i][cell / 256][g * 16 + (cell & 15)][r];
+      }
+      const int64_t v = (int64_t)(tile + sub) * 16 + 4 * g + r;
       if (v < p.V) {
         if (v == target) p.at_target[t] = l * p.scale;
         l *= p.scale * kLog2e;
@@ -662,35 +728,49 @@ __global__ __launch_bounds__(64 * kFewWaves) void xent_few_kernel(const XentArgs
     }
   }
   __syncthreads();
-  // one pair of sums a token from its 16 threads
+  // one pair of sums a token from its threads
+  constexpr int kThreads = 16 * kTurns;  // of a token
   float* all = reinterpret_cast<float*>(sums);
   if (joins) {
-    all[(t * 16 + g * 4 + r) * 2] = top;
-    all[(t * 16 + g * 4 + r) * 2 + 1] = sum;
+    const int at = t * kThreads + (threadIdx.x / kCells) * 16 + g * 4 + r;
+    all[at * 2] = top;
+    all[at * 2 + 1] = sum;
   }
   __syncthreads();
   if (threadIdx.x < p.T) {
     top = -INFINITY;
     sum = 0.f;
-    for (int i = 0; i < 16; ++i) join_sums(top, sum, all[(threadIdx.x * 16 + i) * 2], all[(threadIdx.x * 16 + i) * 2 + 1]);
+    for (int i = 0; i < kThreads; ++i) join_sums(top, sum, all[(threadIdx.x * kThreads + i) * 2], all[(threadIdx.x * kThreads + i) * 2 + 1]);
     float* to = p.stat + ((int64_t)blockIdx.x * p.T + threadIdx.x) * 2;
     to[0] = top;
     to[1] = sum;
   }
 }
 
+int few_groups(const XentArgs& a) {
+  const int side = kFewWaves / few_waves((int)((a.D + 31) / 32)), n = (int)(((a.V + 15) / 16 + side - 1) / side);
+  return n < kXentFewGroups ? n : kXentFewGroups;
+}
+
 template <typename IO, int NT>
 hipError_t few(const XentArgs& a, hipStream_t s) {
-  const int pieces = (int)((a.D + 31) / 32), tiles = (int)((a.V + 15) / 16);
-  const int groups = tiles < kXentFewGroups ? tiles : kXentFewGroups;
+  const int pieces = (int)((a.D + 31) / 32), tiles = (int)((a.V + 15) / 16), groups = few_groups(a);
+  const bool all = few_waves(pieces) == kFewWaves;
+  const dim3 block(64 * kFewWaves);
   if constexpr (io<IO>::es == 2) {
     if (pieces <= kFewWaves * kFewHeld) {
-      hipLaunchKernelGGL((xent_few_kernel<IO, NT, true>), dim3(groups), dim3(64 * kFewWaves), 0, s, a, tiles);
+      if (all)
+        hipLaunchKernelGGL((xent_few_kernel<IO, NT, true, true>), dim3(groups), block, 0, s, a, tiles);
+      else
+        hipLaunchKernelGGL((xent_few_kernel<IO, NT, true, false>), dim3(groups), block, 0, s, a, tiles);
       return hipGetLastError();
     }
   }
   hipLaunchKernelGGL((xent_few_pack_kernel<IO>), dim3((pieces * NT + 3) / 4), dim3(256), 0, s, a, pieces, NT);
-  hipLaunchKernelGGL((xent_few_kernel<IO, NT, false>), dim3(groups), dim3(64 * kFewWaves), 0, s, a, tiles);
+  if (all)
+    hipLaunchKernelGGL((xent_few_kernel<IO, NT, false, true>), dim3(groups), block, 0, s, a, tiles);
+  else
+    hipLaunchKernelGGL((xent_few_kernel<IO, NT, false, false>), dim3(groups), block, 0, s, a, tiles);
   return hipGetLastError();
 }
 
@@ -844,8 +924,7 @@ template <typename IO>
 hipError_t fwd(const XentArgs& a, hipStream_t s) {
   if (a.T <= kXentFew) {
     const hipError_t e = a.T <= 16 ? few<IO, 1>(a, s) : few<IO, 2>(a, s);
-    const int64_t groups = (a.V + 15) / 16;
-    return e != hipSuccess ? e : join(a, groups < kXentFewGroups ? groups : kXentFewGroups, s);
+    return e != hipSuccess ? e : join(a, few_groups(a), s);
   }
   hipError_t e = gather<IO>(a, s);
   const int64_t part = a.tile / 2;  // vocabulary rows of a pair of sums
