@@ -103,14 +103,14 @@ struct XentLayout {
   int tile;
 };
 
-constexpr int64_t kXentMost = (int64_t)1 << 22;
+constexpr int64_t kXentMost = (int64_t)1 << 22;       // T V at most 2^37: 2^23 tiles of 128, 2^15 rounds of 256 workgroups
 constexpr size_t kXentPiece = (size_t)256 << 20;      // bytes of a piece's g, and of its packed weights
 constexpr size_t kXentUnaligned = (size_t)16 << 20;   // bytes of weights packed for their address alone
 
 msm_status xent_check(int64_t T, int64_t V, int64_t D, msm_dtype io) {
   if (!known(io)) return MSM_ERR_UNSUPPORTED;
   if (T < 1 || V < 1 || D < 1) return MSM_ERR_INVALID_ARG;
-  if (T > kXentMost || V > kXentMost || D > ((int64_t)1 << 16) || T * V > ((int64_t)1 << 39)) return MSM_ERR_UNSUPPORTED;
+  if (T > kXentMost || V > kXentMost || D > ((int64_t)1 << 16) || T * V > ((int64_t)1 << 37)) return MSM_ERR_UNSUPPORTED;
   return MSM_OK;
 }
 
@@ -165,7 +165,13 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) 
     l.dx_sum = take((size_t)l.splits * T * l.DQ * 4);
     l.rest = take((size_t)T * 4);
   } else {
-    l.stat = take((size_t)(ceil_div(V, 32) + 4) * T * 8);
+    // pairs of sums of half a tile of the vocabulary, a piece at a time
+    int64_t pairs = 0;
+    for (int64_t piece : {l.piece, l.piece_packed}) {
+      const int64_t half = msm::xent_tile(piece < V ? piece : V, T, D, l.planes) / 2, n = 2 * (ceil_div(V, 2 * half) + ceil_div(V, piece));
+      if (n > pairs) pairs = n;
+    }
+    l.stat = take((size_t)pairs * T * 8);
     l.at_target = take((size_t)T * 4);
   }
   l.total = take.at;

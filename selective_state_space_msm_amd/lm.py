@@ -130,6 +130,8 @@ def msm_block_norm_fwd(r, weight=None, o=None, post_weight=None, z=None, scale=1
     own = _Owned(stream)
     dev, io = r.device, r.dtype
     code = _io_code(io)
+    if r.dim() == 0:
+        raise ValueError("r has no dimension")
     rows, D = _rows(r)
     shape = tuple(r.shape)
     _check(r, "r", shape, io, dev)
@@ -180,6 +182,8 @@ def msm_block_norm_bwd(r_out, dy, rstd, weight=None, o=None, post_rstd=None, pos
     own = _Owned(stream)
     dev, io = r_out.device, r_out.dtype
     code = _io_code(io)
+    if r_out.dim() == 0:
+        raise ValueError("r_out has no dimension")
     rows, D = _rows(r_out)
     shape = tuple(r_out.shape)
     _check(r_out, "r_out", shape, io, dev)

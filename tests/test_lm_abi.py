@@ -108,6 +108,7 @@ def test_xent_refusals(lib, bwd):
     for n in ("T", "V", "D"):
         assert call(**{n: 0}) == INVALID and call(**{n: -1}) == INVALID, n
     assert call(T=(1 << 22) + 1) == UNSUPPORTED and call(V=(1 << 22) + 1) == UNSUPPORTED and call(D=(1 << 16) + 1) == UNSUPPORTED
+    assert call(T=1 << 19, V=(1 << 18) + 1, wsb=1 << 60) == UNSUPPORTED
     assert call(io=3) == UNSUPPORTED
     assert call(scale=float("inf")) == INVALID
     assert call(t=0x100004) == INVALID and call(x=0x1000002) == INVALID and call(w=0x2000001, io=1) == INVALID
@@ -138,6 +139,8 @@ def test_binding_refuses():
         lambda: msm.msm_embed_bwd(ids, x[0], 5),
         lambda: msm.msm_embed_bwd(ids, x, 5, dtable=torch.zeros(4, 8)),
         lambda: msm.msm_block_norm_fwd(x, one),
+        lambda: msm.msm_block_norm_fwd(x[0, 0]),
+        lambda: msm.msm_block_norm_bwd(x[0, 0], x[0, 0], one),
         lambda: msm.msm_block_norm_fwd(x, None, None, torch.ones(8)),
         lambda: msm.msm_block_norm_fwd(x, None, None, None, x),
         lambda: msm.msm_block_norm_fwd(x, None, x.bfloat16()),
