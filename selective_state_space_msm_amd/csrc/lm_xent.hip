@@ -160,7 +160,7 @@ struct ProductArgs {
 template <int KS>
 __device__ __forceinline__ int swz_row(int r) {
   if constexpr (KS == 64) return r & 7;
-  return ((r >> 2) & 1) | (((r >> 1) ^ (r >> 3)) & 1) << 1;
+  return ((((r >> 2) ^ (r >> 3)) & 1) << 1) | ((r >> 3) & 1);
 }
 template <int R>
 __device__ __forceinline__ int swz(int k) {
