@@ -112,6 +112,7 @@ struct XentArgs {
   int32_t splits;          // of the vocabulary's pieces in the product of dx
 };
 constexpr int kXentFew = 32;         // rows that the forward takes without tiles
+constexpr int kXentPlaced = 512;     // rows that stay in their places, also those that are left out
 constexpr int kXentFewGroups = 256;  // workgroups it takes them with at most: one a CU
 // Side of the tiles of an M x N product over K.  256 or 128 by rounds of the 256 CUs (one workgroup a CU, or
 // two of the smaller tiles), a small tile taking a quarter of a large one's work at 0.8 of its rate; not 256

@@ -123,6 +123,46 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(const void* src, const i
   }
 }
 
+// Few rows stay where they are, those that are left out as zeros: their places need no launch of their own,
+// and the first piece of w, if it is packed, goes along (a
+// forward of 348 rows of 105, D = 45, bf16: 25.6 us with launches of their own, 19.5 with one).
+template <typename IO>
+__global__ __launch_bounds__(256) void xent_gather_kernel(const XentArgs p, int64_t w_rows) {
+  constexpr int P = io<IO>::es == 2 ? 1 : 3, VEC = Chunk<IO>::VEC;
+  const int64_t chunks = p.DP / 8, of_x = p.T * chunks, all = of_x + w_rows * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const bool is_x = i < of_x;
+    const int64_t at = is_x ? i : i - of_x, row = quotient(at, chunks), c = (at - row * chunks) * 8, left = p.D - c;
+    bool on = true;
+    if (is_x) {
+      const int64_t target = p.targets[row];
+      on = target >= 0 && target < p.V;
+      if (c == 0) {
+        XentRow r{0.f, 0.f, 0.f, -1};
+        if (on) {
+          r.target = (int32_t)target;
+          r.lse = p.dloss ? p.lse[row] : 0.f;
+          r.dloss = p.dloss ? p.dloss[row] : 0.f;
+          r.both = r.dloss + (p.dlse ? p.dlse[row] : 0.f);
+        }
+        p.rows[row] = r;
+        p.inverse[row] = on ? (int32_t)row : -1;
+        if (row == 0) *p.count = (int32_t)p.T;
+      }
+    }
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; e += VEC) {
+      Chunk<IO> r;
+      r.zero();
+      if (on && left > e) r.load(is_x ? p.x : p.w, row * p.D + c + e, left - e);
+      r.get(x + e);
+    }
+    uint16_t* const to = static_cast<uint16_t*>(is_x ? p.xp : p.wp) + row * p.DP + c;
+    store_parts(to, (is_x ? p.T : p.piece) * p.DP, parts_of<P>(x));
+  }
+}
+
 // ---- the product kernel ----
 
 enum class Fetch { kRows, kCols };
@@ -337,7 +377,9 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   // up for as long as the CU takes to accept them, 64 KB half a step (bf16 forward at 8192 tokens of 65536,
   // D = 2048: 1833 us, one by one 1710).
   if constexpr (P == 1) {
-    // the loads of S - 1 steps ahead; factors are read one tile of rows ahead
+    // The loads of S - 1 steps ahead; factors are read one tile of rows ahead; a wavefront that has its factors
+    // goes before one that is still loading (backward at 8192 tokens of 65536, D = 2048: 5301 us, without the
+    // priorities, and 5167).
     static_assert(kLoads <= 2 * MT, "a load between the products of each tile of rows");
     int stage = 0;
     for (int s = 0; s < steps; ++s) {
@@ -356,8 +398,10 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         if (kk == 0 && i >= MT - NT) b[1][i - (MT - NT)] = rb.read(tb, i - (MT - NT), 1);
         if (it < kLoads) load(it);
         __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[it & 1], b[kk][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -890,9 +934,15 @@ hipError_t pack(const void* src, const int32_t* map, const int32_t* count, int64
   return hipGetLastError();
 }
 
-// The rows that take part, gathered, and the left side's operand of a piece.
+// The rows that take part, gathered, and the left side's operand of a piece (the first one of few rows is
+// packed with them).
 template <typename IO>
 hipError_t gather(const XentArgs& a, hipStream_t s) {
+  if (a.T <= kXentPlaced) {
+    const int64_t first = a.w_direct ? 0 : (a.V < a.piece ? a.V : a.piece);
+    hipLaunchKernelGGL((xent_gather_kernel<IO>), dim3(groups_of(((a.T + first) * (a.DP / 8) + 255) / 256)), dim3(256), 0, s, a, first);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, s, a);
   return pack<IO>(a.x, a.map, a.count, a.T, a, a.T * a.DP, a.xp, s);
 }
@@ -908,6 +958,7 @@ hipError_t weights(const XentArgs& a, int64_t v0, int64_t n, ProductArgs* g, hip
   g->a = static_cast<const uint16_t*>(a.wp);
   g->lda = a.DP;
   g->plane_a = a.piece * a.DP;
+  if (v0 == 0 && a.T <= kXentPlaced) return hipSuccess;
   return pack<IO>(at, nullptr, nullptr, n, a, a.piece * a.DP, a.wp, s);
 }
 
