@@ -77,7 +77,7 @@ msm_status block_norm_check(int64_t rows, int64_t D, msm_dtype io) {
 int64_t block_norm_groups(int64_t rows, int64_t D) {
   const msm::BlockNormShape f = msm::block_norm_shape(D, true);
   if (f.T == 0) return rows < 64 ? rows : 64;
-  const int64_t in_flight = f.T < 256 ? 256 / f.T : 1, g = ceil_div(rows, 2 * in_flight), most = f.T == 1024 ? 256 : 512;
+  const int64_t in_flight = f.T <= 64 ? 256 / f.T : 1, g = ceil_div(rows, 2 * in_flight), most = f.T <= 64 ? 512 : 256 * (8 / (f.T / 64));  // a CU holds eight wavefronts
   return g > most ? most : g;
 }
 

@@ -21,20 +21,19 @@
 namespace msm {
 namespace {
 
-// Sum over the T threads of a row, the same value in each.  With more than a wavefront, `lds` must
-// not be the next sum's (the one after it may use it: a thread that writes there has passed the
+// Sum over the threads of a row, the same value in each: T of them, or (T = 0) the workgroup.  Then `lds`
+// must not be the next sum's (the one after it may use it: a thread that writes there has passed the
 // barrier in between).
 template <int T>
 __device__ __forceinline__ float group_sum(float v, float* lds) {
-  constexpr int W = T < 64 ? T : 64;
+  constexpr int W = T == 0 ? 64 : T;
 #pragma unroll
   for (int m = W / 2; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
-  if constexpr (T > 64) {
+  if constexpr (T == 0) {
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0.f;
-#pragma unroll
-    for (int i = 0; i < T / 64; ++i) v += lds[i];
+    for (unsigned i = 0; i < blockDim.x / 64; ++i) v += lds[i];
   }
   return v;
 }
@@ -44,17 +43,17 @@ __device__ __forceinline__ float rstd_of(double sum, double inv, float eps) {
   return (float)(1. / sqrt(sum * inv + (double)eps));
 }
 
-constexpr int block_threads(int T) { return T < 256 ? 256 : T; }
 constexpr int64_t kRowGroups = 2048;
 
-template <typename IO, int T, int E>
-__global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const BlockNormArgs p) {
-  constexpr int VEC = Chunk<IO>::VEC, NV = E / VEC, RW = block_threads(T) / T;
-  __shared__ float lds[2][T > 64 ? T / 64 : 1];
+// G threads to a row, 256 / G rows a workgroup; G = 0: a row for the workgroup, of up to MOST threads.
+template <typename IO, int G, int E, int MOST>
+__global__ __launch_bounds__(MOST) void block_norm_fwd_kernel(const BlockNormArgs p) {
+  constexpr int VEC = Chunk<IO>::VEC, NV = E / VEC, RW = G == 0 ? 1 : MOST / (G == 0 ? 1 : G);
+  __shared__ float lds[2][G == 0 ? MOST / 64 : 1];
   int turn = 0;
-  const int t = threadIdx.x % T;
+  const int T = G == 0 ? blockDim.x : G, t = G == 0 ? threadIdx.x : threadIdx.x % (G == 0 ? 1 : G);
   const int64_t step = (int64_t)gridDim.x * RW;
-  int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / T;
+  int64_t row = (int64_t)blockIdx.x * RW + (G == 0 ? 0 : threadIdx.x / (G == 0 ? 1 : G));
   if (row >= p.rows) return;  // whole rows leave: no sum crosses rows
   float w[NV][VEC], pw[NV][VEC];
   Chunk<IO> no[NV], nz[NV], nr[NV];
@@ -62,9 +61,9 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const 
   const auto fetch = [&](int i, int64_t at) {
     const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
     if (n <= 0) return;
-    nr[i].load(p.r, at + c, n);
-    if (block) no[i].load(p.o, at + c, n);
-    if (gate) nz[i].load(p.z, at + c, n);
+    nr[i].load_row(p.r, at, c, p.D);
+    if (block) no[i].load_row(p.o, at, c, p.D);
+    if (gate) nz[i].load_row(p.z, at, c, p.D);
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -87,14 +86,15 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const 
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      nr[i].get(x[i]);
+      const int by = Chunk<IO>::short_by(((int64_t)i * T + t) * VEC, p.D);
+      nr[i].get_row(x[i], by);
       if (block) {
-        no[i].get(f[i]);
+        no[i].get_row(f[i], by);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) q = fmaf(f[i][e], f[i][e], q);
         if (gate) {
           float z[VEC];
-          nz[i].get(z);
+          nz[i].get_row(z, by);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) f[i][e] *= silu_f(z[e]);
         }
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const 
       if (more) fetch(i, next);
     }
     if (block) {
-      q = rstd_of(group_sum<T>(q, lds[turn]), inv, p.eps);
+      q = rstd_of(group_sum<G>(q, lds[turn]), inv, p.eps);
       turn ^= 1;
       const float qs = q * p.scale;
 #pragma unroll
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const 
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s = fmaf(x[i][e], x[i][e], s);
-    const float rstd = rstd_of(group_sum<T>(s, lds[turn]), inv, p.eps);
+    const float rstd = rstd_of(group_sum<G>(s, lds[turn]), inv, p.eps);
     turn ^= 1;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -140,28 +140,28 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_fwd_kernel(const 
   }
 }
 
-template <typename IO, int T, int E>
-__global__ __launch_bounds__(block_threads(T)) void block_norm_bwd_kernel(const BlockNormArgs p) {
-  constexpr int VEC = Chunk<IO>::VEC, NV = E / VEC, BS = block_threads(T), RW = BS / T;
-  constexpr int kGroup = T > 64 ? T : 64, NG = BS / kGroup;
-  __shared__ float lds[2][T > 64 ? T / 64 : 1];
-  __shared__ float cols[NG > 1 ? NG : 1][NG > 1 ? T * VEC : 1];
+template <typename IO, int G, int E, int MOST>
+__global__ __launch_bounds__(MOST) void block_norm_bwd_kernel(const BlockNormArgs p) {
+  constexpr int VEC = Chunk<IO>::VEC, NV = E / VEC, RW = G == 0 ? 1 : MOST / (G == 0 ? 1 : G);
+  constexpr int NG = G == 0 ? 1 : MOST / 64;  // wavefronts whose column sums are joined
+  __shared__ float lds[2][G == 0 ? MOST / 64 : 1];
+  __shared__ float cols[NG][G == 0 ? 1 : G * VEC];
   int turn = 0;
-  const int t = threadIdx.x % T;
+  const int T = G == 0 ? blockDim.x : G, t = G == 0 ? threadIdx.x : threadIdx.x % (G == 0 ? 1 : G);
   const float inv = 1.f / (float)p.D;
   const int64_t step = (int64_t)gridDim.x * RW;
   const bool block = p.o != nullptr, gate = p.z != nullptr, residual = p.dr_out != nullptr;
   float w[NV][VEC], pw[NV][VEC], dw[NV][VEC], dpw[NV][VEC];
   Chunk<IO> ny[NV], nr[NV], nd[NV], no[NV], nz[NV];
-  int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / T;
+  int64_t row = (int64_t)blockIdx.x * RW + (G == 0 ? 0 : threadIdx.x / (G == 0 ? 1 : G));
   const auto fetch = [&](int i, int64_t at) {
     const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
     if (n <= 0) return;
-    ny[i].load(p.dy, at + c, n);
-    nr[i].load(p.r_out, at + c, n);
-    if (residual) nd[i].load(p.dr_out, at + c, n);
-    if (block) no[i].load(p.o, at + c, n);
-    if (gate) nz[i].load(p.z, at + c, n);
+    ny[i].load_row(p.dy, at, c, p.D);
+    nr[i].load_row(p.r_out, at, c, p.D);
+    if (residual) nd[i].load_row(p.dr_out, at, c, p.D);
+    if (block) no[i].load_row(p.o, at, c, p.D);
+    if (gate) nz[i].load_row(p.z, at, c, p.D);
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -187,11 +187,12 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_bwd_kernel(const 
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      ny[i].get(u[i]);
-      nr[i].get(h[i]);
-      nd[i].get(g[i]);
-      no[i].get(o[i]);
-      nz[i].get(z[i]);
+      const int by = Chunk<IO>::short_by(((int64_t)i * T + t) * VEC, p.D);
+      ny[i].get_row(u[i], by);
+      nr[i].get_row(h[i], by);
+      nd[i].get_row(g[i], by);
+      no[i].get_row(o[i], by);
+      nz[i].get_row(z[i], by);
       if (more) fetch(i, next);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_bwd_kernel(const 
         a = fmaf(u[i][e], h[i][e], a);
       }
     }
-    a = group_sum<T>(a, lds[turn]) * inv;
+    a = group_sum<G>(a, lds[turn]) * inv;
     turn ^= 1;
     float b = 0.f;
 #pragma unroll
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_bwd_kernel(const 
       }
     }
     if (!block) continue;
-    b = group_sum<T>(b, lds[turn]) * inv;
+    b = group_sum<G>(b, lds[turn]) * inv;
     turn ^= 1;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -259,14 +260,14 @@ __global__ __launch_bounds__(block_threads(T)) void block_norm_bwd_kernel(const 
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
 #pragma unroll
-        for (int m = T; m < 64; m *= 2) v[e] += __shfl_xor(v[e], m, 64);
+        for (int m = G == 0 ? 64 : G; m < 64; m *= 2) v[e] += __shfl_xor(v[e], m, 64);
       if constexpr (NG > 1) {
         __syncthreads();  // the last round has been read
-        if (T >= 64 || (threadIdx.x & 63) < T)
+        if ((threadIdx.x & 63) < G)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) cols[threadIdx.x / kGroup][t * VEC + e] = v[e];
+          for (int e = 0; e < VEC; ++e) cols[threadIdx.x / 64][t * VEC + e] = v[e];
         __syncthreads();
-        for (int k = threadIdx.x; k < T * VEC; k += BS) {
+        for (int k = threadIdx.x; k < G * VEC; k += MOST) {
           float s = 0.f;
 #pragma unroll
           for (int g = 0; g < NG; ++g) s += cols[g][k];
@@ -414,16 +415,17 @@ hipError_t join(const BlockNormArgs& a, hipStream_t s) {
   return launch_norm_join(n, a.groups, s);
 }
 
-template <typename IO, int T, int E>
-hipError_t go(const BlockNormArgs& a, bool bwd, hipStream_t s) {
-  constexpr int BS = block_threads(T), RW = BS / T;
+template <typename IO, int G, int E, int MOST>
+hipError_t go(const BlockNormArgs& a, int threads, bool bwd, hipStream_t s) {
+  constexpr int RW = G == 0 ? 1 : MOST / (G == 0 ? 1 : G);
+  const dim3 block(G == 0 ? threads : MOST);
   if (!bwd) {
     const int64_t all = (a.rows + RW - 1) / RW;
-    hipLaunchKernelGGL((block_norm_fwd_kernel<IO, T, E>), dim3((unsigned)(all < kRowGroups ? all : kRowGroups)), dim3(BS), 0, s, a);
+    hipLaunchKernelGGL((block_norm_fwd_kernel<IO, G, E, MOST>), dim3((unsigned)(all < kRowGroups ? all : kRowGroups)), block, 0, s, a);
     return hipGetLastError();
   }
-  if constexpr (T < 1024 || E == 8) {
-    hipLaunchKernelGGL((block_norm_bwd_kernel<IO, T, E>), dim3((unsigned)a.groups), dim3(BS), 0, s, a);
+  if constexpr (MOST <= 512) {
+    hipLaunchKernelGGL((block_norm_bwd_kernel<IO, G, E, MOST>), dim3((unsigned)a.groups), block, 0, s, a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || !a.part ? e : join(a, s);
   }
@@ -433,11 +435,13 @@ hipError_t go(const BlockNormArgs& a, bool bwd, hipStream_t s) {
 template <typename IO>
 hipError_t pick(const BlockNormArgs& a, bool bwd, hipStream_t s) {
   const BlockNormShape f = block_norm_shape(a.D, bwd);
-#define MSM_ROWS(TT, EE) \
-  if (f.T == TT && f.E == EE) return go<IO, TT, EE>(a, bwd, s);
-  MSM_ROWS(16, 8) MSM_ROWS(16, 16) MSM_ROWS(64, 8) MSM_ROWS(64, 16) MSM_ROWS(256, 8) MSM_ROWS(256, 16)
-  MSM_ROWS(1024, 8) MSM_ROWS(1024, 16)
+#define MSM_ROWS(GG, EE) \
+  if (f.T == GG && f.E == EE) return go<IO, GG, EE, 256>(a, GG, bwd, s);
+  MSM_ROWS(16, 8) MSM_ROWS(16, 16) MSM_ROWS(64, 8) MSM_ROWS(64, 16)
 #undef MSM_ROWS
+  if (f.T > 512) return go<IO, 0, 16, 1024>(a, f.T, bwd, s);
+  if (f.T > 256) return go<IO, 0, 16, 512>(a, f.T, bwd, s);
+  if (f.T > 0) return go<IO, 0, 16, 256>(a, f.T, bwd, s);
   const dim3 grid((unsigned)(a.rows < kLoopGroups ? a.rows : kLoopGroups));
   if (!bwd) {
     hipLaunchKernelGGL((block_norm_fwd_loop_kernel<IO>), grid, dim3(256), 0, s, a);

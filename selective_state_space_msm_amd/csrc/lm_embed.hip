@@ -303,7 +303,7 @@ template <typename IO>
 __device__ __forceinline__ void add_places(const EmbedArgs& p, const uint32_t* pos, int64_t i0, int64_t i1, int64_t c,
                                            float (&x)[Chunk<IO>::VEC]) {
   constexpr int VEC = Chunk<IO>::VEC, N = 8;
-  const int64_t n = p.D - c;
+  const int by = Chunk<IO>::short_by(c, p.D);
   for (int64_t i = i0; i < i1; i += N) {
     Chunk<IO> r[N];
     uint32_t at[N];
@@ -312,12 +312,12 @@ __device__ __forceinline__ void add_places(const EmbedArgs& p, const uint32_t* p
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       r[j].zero();
-      if (i + j < i1) r[j].load(p.dy, (int64_t)at[j] * p.D + c, n);
+      if (i + j < i1) r[j].load_row(p.dy, (int64_t)at[j] * p.D, c, p.D);
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       float v[VEC];
-      r[j].get(v);
+      r[j].get_row(v, by);
       if (i + j < i1)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) x[e] += v[e];
@@ -541,16 +541,17 @@ __device__ __forceinline__ void light_row(const EmbedArgs& p, int64_t v, int64_t
 #pragma unroll
   for (int e = 0; e < VEC; ++e) x[e] = 0.f;
   if (count > 0) {
+    const int by = Chunk<IO>::short_by(c, p.D);
     Chunk<IO> in[kBusy];
 #pragma unroll
     for (int j = 0; j < kBusy; ++j) {
       in[j].zero();
-      if (j < count) in[j].load(p.dy, (int64_t)at(j) * p.D + c, p.D - c);
+      if (j < count) in[j].load_row(p.dy, (int64_t)at(j) * p.D, c, p.D);
     }
 #pragma unroll
     for (int j = 0; j < kBusy; ++j) {
       float y[VEC];
-      in[j].get(y);
+      in[j].get_row(y, by);
       if (j < count)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) x[e] += y[e];

@@ -61,15 +61,18 @@ struct BlockNormArgs {
   int32_t groups;
 };
 
-// T threads hold a row, E elements each; T = 0: the row is walked in memory.
+// T threads hold a row, E elements each; T = 0: the row is walked in memory.  Rows of more than 1024 have as
+// many wavefronts as they need of 16 elements a thread (7098 x 2240, bf16, backward: 77 us; with 8
+// elements and 320 threads 106, the barriers holding more wavefronts for less work).
 struct BlockNormShape {
   int T, E;
 };
 constexpr BlockNormShape block_norm_shape(int64_t D, bool bwd) {
-  for (int T = 16; T <= 1024; T *= 4)
-    for (int E = 8; E <= (bwd && T == 1024 ? 8 : 16); E *= 2)
+  for (int T = 16; T <= 64; T *= 4)
+    for (int E = 8; E <= 16; E *= 2)
       if (D <= (int64_t)T * E) return BlockNormShape{T, E};
-  return BlockNormShape{0, 0};
+  if (D > (bwd ? 8192 : 16384)) return BlockNormShape{0, 0};
+  return BlockNormShape{(int)((D + 1023) / 1024) * 64, 16};
 }
 hipError_t launch_block_norm_fwd(const BlockNormArgs& a, int io_bf16, hipStream_t s);
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, int io_bf16, hipStream_t s);

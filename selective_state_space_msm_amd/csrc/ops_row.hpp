@@ -131,6 +131,31 @@ struct Chunk {
         }
     }
   }
+  // Elements [c, c + VEC) of a row of D that starts at element i.  A row's last piece, where it is short and
+  // not the only one, is taken as the 16 bytes that end the row: one load like the others, whose first
+  // short_by(c, D) elements get() leaves out, so that nothing waits for it before it is used.  (Element by
+  // element the wavefront waits where it loads: 30000 rows of 500, bf16, block norm backward: 135 us, and 56 this way.)
+  static __device__ __forceinline__ int short_by(int64_t c, int64_t D) { return c > 0 && c < D && D - c < VEC ? (int)(VEC - (D - c)) : 0; }
+  __device__ __forceinline__ void load_row(const void* p, int64_t i, int64_t c, int64_t D) {
+    const int by = short_by(c, D);
+    load(p, i + c - by, by ? VEC : D - c);
+  }
+  __device__ __forceinline__ void get_row(float* x, int by) const {
+    Chunk<IO> r = *this;
+    if (by) {
+      const int s = by * io<IO>::es * 8;
+      uint64_t lo = raw[0] | (uint64_t)raw[1] << 32, hi = raw[2] | (uint64_t)raw[3] << 32;
+      if (s >= 64) {
+        lo = hi >> (s - 64);
+        hi = 0;
+      } else {
+        lo = lo >> s | hi << (64 - s);
+        hi >>= s;
+      }
+      r.raw = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    }
+    r.get(x);
+  }
   __device__ __forceinline__ void get(float* x) const {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
