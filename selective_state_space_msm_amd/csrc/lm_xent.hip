@@ -717,7 +717,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void xent_few_kernel(const XentArgs
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int q = 0; q < P; ++q) x[u][j].p[q] = xs[((q * pieces + c + u) * NT + j) * 64];
+            for (int q = 0; q < P; ++q) {
+              x[u][j].p[q] = __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
+              if (j * 16 + (lane & 15) < p.T) x[u][j].p[q] = xs[((q * pieces + c + u) * NT + j) * 64];  // no bytes for no token
+            }
     }
     __builtin_amdgcn_sched_barrier(0);  // all loads in flight first: by itself the compiler keeps two or three
   };
@@ -879,6 +882,7 @@ __global__ __launch_bounds__(256) void xent_dx_kernel(const XentArgs p) {
       if (n >= 0 && c + e < p.DQ) {
         const float* from = p.dx_sum + n * p.DQ + c + e;
         v = *reinterpret_cast<const f32x4*>(from);
+#pragma unroll 8
         for (int z = 1; z < p.splits; ++z) v += *reinterpret_cast<const f32x4*>(from + z * (p.T * p.DQ));
       }
 #pragma unroll
