@@ -326,6 +326,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   constexpr int kLoads = LA::kLoads + LB::kLoads;  // of a plane
   __shared__ __attribute__((aligned(16))) uint16_t lds[S * P * (kA + kB)];
   const int N = p.count_n ? uniform(*p.count_n) : p.N, K = p.count_k ? uniform(*p.count_k) : p.K;
+  if (N <= 0) return;  // no row takes part: there are no tiles to divide among the XCDs
   const Place at = place_of((p.M + BM - 1) / BM, (N + BN - 1) / BN, BM == 256);
   const int32_t m0 = at.m * BM, n0 = at.n * BN;
   if (m0 >= p.M || n0 >= N) return;  // fewer rows than the grid was made for among these

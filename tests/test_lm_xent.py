@@ -181,6 +181,20 @@ def test_no_row_with_a_target(io):
     assert bool((loss == 0).all()) and bool((d["dx"] == 0).all()) and bool((d["dweight"] == 0).all())
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D", [(600, 1000, 64), (520, 8000, 136), (2100, 2048, 264), (513, 64, 1)])
+def test_no_row_of_many_with_a_target(io, T, V, D):
+    """More rows than stay in their places: none are gathered, the products have no tiles of rows."""
+    import selective_state_space_msm_amd as msm
+    x, w = torch.full((T, D), float("nan"), device="cuda").to(DT[io]), torch.randn(V, D, device="cuda").to(DT[io])
+    t = torch.full((T,), V, device="cuda")
+    one = torch.ones(T, device="cuda")
+    loss, lse = msm.msm_linear_cross_entropy_fwd(x, w, t, return_lse=True)
+    d = msm.msm_linear_cross_entropy_bwd(x, w, t, one, one, dlse=one)
+    assert bool((loss == 0).all()) and bool((lse == 0).all())
+    assert bool((d["dx"] == 0).all()) and bool((d["dweight"] == 0).all())
+
+
 @pytest.mark.parametrize("T", [4, 200])
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_nan_row_stays_in_its_row(io, T):
