@@ -554,6 +554,12 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
               if constexpr (P == 1) p.rest[n] = acc[i][j][r] - (float)(__bf16)acc[i][j][r];
             }
       }
+      if (__any(row.target < 0)) {  // left out but in its place: its zeros times an infinite weight are none
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = row.target < 0 ? 0.f : acc[i][j][r];
+      }
       if (ends) {  // the products' k behind the piece
 #pragma unroll
         for (int i = 0; i < MT; ++i)

@@ -228,6 +228,23 @@ def test_lowest_logits(io, T):
         assert torch.allclose(loss, rest, rtol=1e-5, atol=1e-5) and torch.allclose(lse, rest_lse, rtol=1e-5, atol=1e-5)
 
 
+@pytest.mark.parametrize("T", [8, 500, 700])
+def test_left_out_rows_add_nothing_to_infinite_weights(T):
+    """A weight row of minus infinity, a probability of 0 in every row: its gradient is 0, and the others' is as
+    it is without that row, also where rows are left out."""
+    import selective_state_space_msm_amd as msm
+    x, w = (torch.rand(T, 64, device="cuda") + 0.1).bfloat16(), torch.randn(300, 64, device="cuda").bfloat16()
+    w[299] = -float("inf")
+    t = torch.randint(299, (T,), device="cuda")
+    t[::3] = -1
+    one = torch.ones(T, device="cuda")
+    loss, lse = msm.msm_linear_cross_entropy_fwd(x, w, t, return_lse=True)
+    d = msm.msm_linear_cross_entropy_bwd(x, w, t, lse, one, dlse=one)
+    rest = msm.msm_linear_cross_entropy_bwd(x, w[:299].contiguous(), t, lse, one, dlse=one)
+    assert bool((d["dweight"][299] == 0).all()) and bool((d["dx"][::3] == 0).all())
+    assert torch.equal(d["dweight"][:299], rest["dweight"])
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [16, 400])
 def test_repeated_and_on_another_stream(io, T):
