@@ -181,6 +181,13 @@ def test_no_row_with_a_target(io):
     assert bool((loss == 0).all()) and bool((d["dx"] == 0).all()) and bool((d["dweight"] == 0).all())
 
 
+@pytest.mark.parametrize("io,T,V,D,ignored", [("bf16", 4100, 17000, 64, 0.97), ("bf16", 9000, 33000, 40, 0.9995),
+                                              ("bf16", 2300, 4200, 1032, 0.8), ("f32", 2500, 9000, 33, 0.9)])
+def test_most_rows_left_out(io, T, V, D, ignored):
+    """Far fewer tiles of rows than the launch is made for."""
+    check(io, T, V, D, ignored=ignored, on="cuda")
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("T,V,D", [(600, 1000, 64), (520, 8000, 136), (2100, 2048, 264), (513, 64, 1)])
 def test_no_row_of_many_with_a_target(io, T, V, D):
