@@ -74,21 +74,23 @@ msm_status block_norm_check(int64_t rows, int64_t D, msm_dtype io) {
 
 // Workgroups of the backward: each leaves 8 D bytes of column sums, so few enough that they stay
 // small beside the rows, and enough to fill the GPU.
-int64_t block_norm_groups(int64_t rows, int64_t D) {
-  const msm::BlockNormShape f = msm::block_norm_shape(D, true);
+int64_t block_norm_groups(int64_t rows, int64_t D, msm_dtype io) {
+  const msm::BlockNormShape f = msm::block_norm_shape(D, true, io == MSM_BF16);
   if (f.T == 0) return rows < 64 ? rows : 64;
-  const int64_t in_flight = f.T <= 64 ? 256 / f.T : 1, g = ceil_div(rows, 2 * in_flight), most = f.T <= 64 ? 512 : 256 * (8 / (f.T / 64));  // a CU holds eight wavefronts
+  const int64_t in_flight = f.T <= 64 ? 256 / f.T : 1, g = ceil_div(rows, 2 * in_flight);
+  const int waves = f.T / 64, held = f.E == 4 ? 16 : 8;  // of a row; that a CU's registers hold
+  const int64_t most = f.T <= 64 ? 512 : 256 * (waves < held ? held / waves : 1);
   return g > most ? most : g;
 }
 
 struct BlockNormLayout {
   size_t part, row_mean, total;
 };
-BlockNormLayout block_norm_layout(int64_t rows, int64_t D) {
+BlockNormLayout block_norm_layout(int64_t rows, int64_t D, msm_dtype io) {
   BlockNormLayout l{};
   Take take;
-  l.part = take((size_t)block_norm_groups(rows, D) * 8 * (size_t)D);
-  if (msm::block_norm_shape(D, true).T == 0) l.row_mean = take((size_t)rows * 4);
+  l.part = take((size_t)block_norm_groups(rows, D, io) * 8 * (size_t)D);
+  if (msm::block_norm_shape(D, true, io == MSM_BF16).T == 0) l.row_mean = take((size_t)rows * 4);
   l.total = take.at;
   return l;
 }
@@ -305,7 +307,7 @@ msm_status msm_block_norm_fwd(const void* r, const float* weight, const void* o,
 }
 
 size_t msm_block_norm_bwd_workspace_bytes(int64_t rows, int64_t D, msm_dtype io) {
-  return block_norm_check(rows, D, io) == MSM_OK ? block_norm_layout(rows, D).total : 0;
+  return block_norm_check(rows, D, io) == MSM_OK ? block_norm_layout(rows, D, io).total : 0;
 }
 
 msm_status msm_block_norm_bwd(const void* r_out, const void* dy, const float* rstd, const float* weight, const void* o,
@@ -320,7 +322,7 @@ msm_status msm_block_norm_bwd(const void* r_out, const void* dy, const float* rs
   for (const void* q : {r_out, dy, o, z, dr_out, (const void*)dr, (const void*)do_, (const void*)dz})
     if (!aligned(q, es)) return MSM_ERR_INVALID_ARG;
   const bool cols = dweight || dpost_weight;
-  const BlockNormLayout l = block_norm_layout(rows, D);
+  const BlockNormLayout l = block_norm_layout(rows, D, io);
   if (!workspace || workspace_bytes < l.total) return MSM_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return MSM_ERR_INVALID_ARG;
   const Range ins[] = {rng(r_out, n), rng(dy, n), rng(rstd, nr), rng(weight, nd), rng(o, n), rng(post_rstd, nr),
@@ -348,7 +350,7 @@ msm_status msm_block_norm_bwd(const void* r_out, const void* dy, const float* rs
   a.rows = rows;
   a.D = D;
   a.scale = scale;
-  a.groups = (int32_t)block_norm_groups(rows, D);
+  a.groups = (int32_t)block_norm_groups(rows, D, io);
   return status_of(msm::launch_block_norm_bwd(a, io == MSM_BF16, static_cast<hipStream_t>(stream)));
 }
 

@@ -14,8 +14,8 @@
 // 16-byte accesses); only a row's last piece may be taken element by element.  The backward's
 // column sums stay in registers over the rows of a workgroup and are joined by a second kernel
 // in a fixed order.  Rows past the registers are walked in memory with fp64 sums.
-// 16384 x 4096, bf16, with block and gate: forward 138 us (4.9 TB/s), backward 212 (5.1 TB/s); a copy of
-// 1 GiB reaches 5.1.  4095 x 1001, fp32, no gate: backward 40 us.
+// 16384 x 4096, bf16, with block and gate: forward 134 us (5.0 TB/s), backward 207 (5.2 TB/s); a copy of
+// 1 GiB reaches 5.1.  4095 x 1001, fp32, no gate: backward 26 us (3.8 TB/s).
 #include "lm_internal.h"
 #include "ops_internal.h"
 #include "ops_row.hpp"
@@ -420,13 +420,20 @@ hipError_t join(const BlockNormArgs& a, hipStream_t s) {
 template <typename IO, int G, int E, int MOST>
 hipError_t go(const BlockNormArgs& a, int threads, bool bwd, hipStream_t s) {
   constexpr int RW = G == 0 ? 1 : MOST / (G == 0 ? 1 : G);
+  // what block_norm_shape gives
+  constexpr bool f32 = io<IO>::es == 4;
+  constexpr bool of_fwd = G > 0 ? E >= 8 : E == 8 || (E == 16 && MOST == 1024);
+  constexpr bool of_bwd = G > 0 ? !(f32 && E == 16) : (f32 ? E == 4 || (E == 8 && MOST == 1024) : (E == 8 ? MOST == 256 : MOST <= 512));
   const dim3 block(G == 0 ? threads : MOST);
   if (!bwd) {
-    const int64_t all = (a.rows + RW - 1) / RW;
-    hipLaunchKernelGGL((block_norm_fwd_kernel<IO, G, E, MOST>), dim3((unsigned)(all < kRowGroups ? all : kRowGroups)), block, 0, s, a);
-    return hipGetLastError();
+    if constexpr (of_fwd) {
+      const int64_t all = (a.rows + RW - 1) / RW;
+      hipLaunchKernelGGL((block_norm_fwd_kernel<IO, G, E, MOST>), dim3((unsigned)(all < kRowGroups ? all : kRowGroups)), block, 0, s, a);
+      return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
   }
-  if constexpr (MOST <= 512) {
+  if constexpr (of_bwd) {
     hipLaunchKernelGGL((block_norm_bwd_kernel<IO, G, E, MOST>), dim3((unsigned)a.groups), block, 0, s, a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || !a.part ? e : join(a, s);
@@ -434,16 +441,25 @@ hipError_t go(const BlockNormArgs& a, int threads, bool bwd, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
+template <typename IO, int E>
+hipError_t go_wide(const BlockNormArgs& a, int threads, bool bwd, hipStream_t s) {
+  if (threads > 512) return go<IO, 0, E, 1024>(a, threads, bwd, s);
+  return threads > 256 ? go<IO, 0, E, 512>(a, threads, bwd, s) : go<IO, 0, E, 256>(a, threads, bwd, s);
+}
+
 template <typename IO>
 hipError_t pick(const BlockNormArgs& a, bool bwd, hipStream_t s) {
-  const BlockNormShape f = block_norm_shape(a.D, bwd);
+  const BlockNormShape f = block_norm_shape(a.D, bwd, io<IO>::es == 2);
 #define MSM_ROWS(GG, EE) \
   if (f.T == GG && f.E == EE) return go<IO, GG, EE, 256>(a, GG, bwd, s);
-  MSM_ROWS(16, 8) MSM_ROWS(16, 16) MSM_ROWS(64, 8) MSM_ROWS(64, 16)
+  MSM_ROWS(16, 8) MSM_ROWS(16, 16) MSM_ROWS(64, 8)
 #undef MSM_ROWS
-  if (f.T > 512) return go<IO, 0, 16, 1024>(a, f.T, bwd, s);
-  if (f.T > 256) return go<IO, 0, 16, 512>(a, f.T, bwd, s);
-  if (f.T > 0) return go<IO, 0, 16, 256>(a, f.T, bwd, s);
+  if constexpr (io<IO>::es == 4) {
+    if (f.T == 64 && f.E == 4) return go<IO, 64, 4, 256>(a, 64, bwd, s);
+    if (f.E == 4) return go_wide<IO, 4>(a, f.T, bwd, s);
+  }
+  if (f.E == 8) return go_wide<IO, 8>(a, f.T, bwd, s);
+  if (f.E == 16) return go_wide<IO, 16>(a, f.T, bwd, s);
   const dim3 grid((unsigned)(a.rows < kLoopGroups ? a.rows : kLoopGroups));
   if (!bwd) {
     hipLaunchKernelGGL((block_norm_fwd_loop_kernel<IO>), grid, dim3(256), 0, s, a);

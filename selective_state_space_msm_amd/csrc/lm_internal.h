@@ -61,18 +61,24 @@ struct BlockNormArgs {
   int32_t groups;
 };
 
-// T threads hold a row, E elements each; T = 0: the row is walked in memory.  Rows of more than 1024 have as
-// many wavefronts as they need of 16 elements a thread (7098 x 2240, bf16, backward: 77 us; with 8
-// elements and 320 threads 106, the barriers holding more wavefronts for less work).
+// T threads hold a row, E elements each; T = 0: the row is walked in memory.  Rows of more than 512 have as
+// many wavefronts as they need, with the elements a thread that leave the registers room for enough of
+// them: a backward's fp32 row has five arrays in flight and five in use, 256 registers a thread with 16
+// elements and 92 with 4 (16384 x 4096: 589 and 396 us; 4095 x 1001: 43 and 33), with 8 in 128 (4000 x 6000:
+// 358 and 285).  In bf16 16 elements are two loads an array, and fewer barriers for the same work (16384
+// x 4096, backward: 214 us, with 8 elements 257; 7098 x 2240: 77 and 106); up to 1024 columns 8 (20000 x 1000:
+// 99 with 16, 88).  A forward has three arrays: 8 elements (20000 x 1000: bf16 55 and 44 us, fp32 89 and 80).
 struct BlockNormShape {
   int T, E;
 };
-constexpr BlockNormShape block_norm_shape(int64_t D, bool bwd) {
+constexpr BlockNormShape block_norm_shape(int64_t D, bool bwd, bool bf16) {
+  if (bwd && !bf16 && D > 128 && D <= 256) return BlockNormShape{64, 4};
   for (int T = 16; T <= 64; T *= 4)
     for (int E = 8; E <= 16; E *= 2)
-      if (D <= (int64_t)T * E) return BlockNormShape{T, E};
+      if (D <= (int64_t)T * E && D <= 512) return BlockNormShape{T, E};
   if (D > (bwd ? 8192 : 16384)) return BlockNormShape{0, 0};
-  return BlockNormShape{(int)((D + 1023) / 1024) * 64, 16};
+  const int E = !bwd ? (D <= 8192 ? 8 : 16) : (bf16 ? (D <= 1024 ? 8 : 16) : (D <= 4096 ? 4 : 8));
+  return BlockNormShape{(int)((D + 64 * E - 1) / (64 * E)) * 64, E};
 }
 hipError_t launch_block_norm_fwd(const BlockNormArgs& a, int io_bf16, hipStream_t s);
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, int io_bf16, hipStream_t s);

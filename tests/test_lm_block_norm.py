@@ -95,6 +95,13 @@ def test_sizes(io, rows, D):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [128, 129, 256, 257, 512, 513, 768, 1024, 1025, 2048, 2049, 4095, 4096, 4097, 6001, 8192, 8193, 16384, 16385])
+@pytest.mark.parametrize("rows", [1, 300])
+def test_widths_where_the_shape_changes(io, rows, D):
+    check(io, rows, D)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("D", [48, 770, 4096, 5003, 17000])
 @pytest.mark.parametrize("block,gate,weights,residual", [(False, False, True, True), (False, False, False, False),
                                                          (True, False, True, False), (True, True, False, True)])
