@@ -422,8 +422,8 @@ hipError_t go(const BlockNormArgs& a, int threads, bool bwd, hipStream_t s) {
   constexpr int RW = G == 0 ? 1 : MOST / (G == 0 ? 1 : G);
   // what block_norm_shape gives
   constexpr bool f32 = io<IO>::es == 4;
-  constexpr bool of_fwd = G > 0 ? E >= 8 : E == 8 || (E == 16 && MOST == 1024);
-  constexpr bool of_bwd = G > 0 ? !(f32 && E == 16) : (f32 ? E == 4 || (E == 8 && MOST == 1024) : (E == 8 ? MOST == 256 : MOST <= 512));
+  constexpr bool of_fwd = E == 8 || (G == 0 && E == 16 && MOST == 1024);
+  constexpr bool of_bwd = G > 0 ? (f32 ? E == 4 || G == 64 : E == 8) : (f32 ? E == 4 || (E == 8 && MOST == 1024) : (E == 8 ? MOST == 256 : MOST <= 512));
   const dim3 block(G == 0 ? threads : MOST);
   if (!bwd) {
     if constexpr (of_fwd) {
@@ -452,10 +452,10 @@ hipError_t pick(const BlockNormArgs& a, bool bwd, hipStream_t s) {
   const BlockNormShape f = block_norm_shape(a.D, bwd, io<IO>::es == 2);
 #define MSM_ROWS(GG, EE) \
   if (f.T == GG && f.E == EE) return go<IO, GG, EE, 256>(a, GG, bwd, s);
-  MSM_ROWS(16, 8) MSM_ROWS(16, 16) MSM_ROWS(64, 8)
-#undef MSM_ROWS
+  MSM_ROWS(16, 8) MSM_ROWS(32, 8) MSM_ROWS(64, 8)
   if constexpr (io<IO>::es == 4) {
-    if (f.T == 64 && f.E == 4) return go<IO, 64, 4, 256>(a, 64, bwd, s);
+    MSM_ROWS(16, 4) MSM_ROWS(32, 4) MSM_ROWS(64, 4)
+#undef MSM_ROWS
     if (f.E == 4) return go_wide<IO, 4>(a, f.T, bwd, s);
   }
   if (f.E == 8) return go_wide<IO, 8>(a, f.T, bwd, s);

@@ -61,23 +61,22 @@ struct BlockNormArgs {
   int32_t groups;
 };
 
-// T threads hold a row, E elements each; T = 0: the row is walked in memory.  Rows of more than 512 have as
-// many wavefronts as they need, with the elements a thread that leave the registers room for enough of
-// them: a backward's fp32 row has five arrays in flight and five in use, 256 registers a thread with 16
-// elements and 92 with 4 (16384 x 4096: 589 and 396 us; 4095 x 1001: 43 and 33), with 8 in 128 (4000 x 6000:
-// 358 and 285).  In bf16 16 elements are two loads an array, and fewer barriers for the same work (16384
-// x 4096, backward: 214 us, with 8 elements 257; 7098 x 2240: 77 and 106); up to 1024 columns 8 (20000 x 1000:
-// 99 with 16, 88).  A forward has three arrays: 8 elements (20000 x 1000: bf16 55 and 44 us, fp32 89 and 80).
+// T threads hold a row, E elements each: 16, 32 or 64, or as many wavefronts as it takes; T = 0: the row is
+// walked in memory.  E leaves the registers room for enough wavefronts: a backward's fp32 row has five arrays in
+// flight and five in use, 256 registers a thread with 16 elements and 92 with 4 (16384 x 4096: 589 and 396 us;
+// 4095 x 1001: 43 and 28), with 8 in 128 (4000 x 6000: 358 and 283); up to 512 columns a wavefront a row, which
+// has no barriers (50000 x 400: 129, with 4 elements 134).  In bf16 16 elements are two loads an array, and fewer
+// barriers for the same work (16384 x 4096, backward: 205 us, with 8 elements 257; 7098 x 2240: 77 and 106); up
+// to 1024 columns 8 (20000 x 1000: 99 with 16, 81).  A forward has three arrays: 8 elements (20000 x 1000: bf16
+// 55 with 16, 44, fp32 89 and 80; 50000 x 200: bf16 41 and 29, fp32 57 and 38).
 struct BlockNormShape {
   int T, E;
 };
 constexpr BlockNormShape block_norm_shape(int64_t D, bool bwd, bool bf16) {
-  if (bwd && !bf16 && D > 128 && D <= 256) return BlockNormShape{64, 4};
-  for (int T = 16; T <= 64; T *= 4)
-    for (int E = 8; E <= 16; E *= 2)
-      if (D <= (int64_t)T * E && D <= 512) return BlockNormShape{T, E};
   if (D > (bwd ? 8192 : 16384)) return BlockNormShape{0, 0};
-  const int E = !bwd ? (D <= 8192 ? 8 : 16) : (bf16 ? (D <= 1024 ? 8 : 16) : (D <= 4096 ? 4 : 8));
+  const int E = !bwd ? (D <= 8192 ? 8 : 16) : (bf16 ? (D <= 1024 ? 8 : 16) : (D <= 256 || (D > 512 && D <= 4096) ? 4 : 8));
+  for (int T = 16; T <= 64; T *= 2)
+    if (D <= (int64_t)T * E) return BlockNormShape{T, E};
   return BlockNormShape{(int)((D + 64 * E - 1) / (64 * E)) * 64, E};
 }
 hipError_t launch_block_norm_fwd(const BlockNormArgs& a, int io_bf16, hipStream_t s);
