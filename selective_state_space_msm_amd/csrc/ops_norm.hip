@@ -10,8 +10,8 @@
 // keeps lanes busy on short rows.  The backward walks rows with a fixed grid: every thread owns
 // its columns and keeps their dw and db sums in registers over all rows of its workgroup; the
 // workgroups' sums are joined by a second kernel in a fixed order.  Longer rows are walked in
-// loops over memory.  16384 x 4096 bf16: forward 56 us (4.8 TB/s), backward 81 us with its join
-// (5.0 TB/s); a copy reaches 5.15 TB/s.
+// loops over memory.  16384 x 4096 bf16: forward 56 us (4.8 TB/s), backward 79 us with its join
+// (5.1 TB/s); a copy reaches 5.15 TB/s.
 #include "ops_row.hpp"
 
 namespace msm {
