@@ -23,7 +23,7 @@
 // take part are gathered in front, and what the others hold is never multiplied.
 //
 // 7780 of 8192 tokens take part, 65536 words, D = 2048, bf16: forward 1655 us (1262 TFLOP/s over those rows,
-// the products alone 1349 over whole tiles), backward 5135 (1220); a library product of 8192^3 reaches 1200 to
+// the products alone 1358 over whole tiles), backward 5135 (1220); a library product of 8192^3 reaches 1200 to
 // 1240.  What bounds the products is the clock under matrix load (1.9 to 2.1 GHz) and the matrix units, busy
 // 61 to 70% of it.  16 tokens, D = 4096: 98 us, 5.5 TB/s of weights.  fp32, 1000 of 1999 tokens of 10007,
 // D = 513, backward: 280 us, six bf16 products for each of fp32.
