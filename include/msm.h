@@ -458,8 +458,9 @@ msm_status msm_linear_cross_entropy_fwd(const void* x, const void* weight, const
  *     g[t][v] = scale * ((dloss[t] + dlse[t]) exp(l[t][v] - lse[t]) - dloss[t] [v = targets[t]])
  *     dx = g weight,  dweight = g^T x
  * dx (T, D), dweight (V, D) io; dweight may be NULL.  A row that is left out has dx = 0 and adds
- * nothing to dweight.  The vocabulary is taken in pieces, whose g (in bf16 for bf16 inputs, 24 bits
- * for fp32 ones) is in the workspace; sums are fp32. */
+ * nothing to dweight.  The vocabulary is taken in pieces, whose g (in bf16 for bf16 inputs, where what
+ * the target's entry loses by that is made up for in both gradients; 24 bits for fp32 ones) is in the
+ * workspace; sums are fp32. */
 size_t msm_linear_cross_entropy_bwd_workspace_bytes(int64_t T, int64_t V, int64_t D, msm_dtype io);
 msm_status msm_linear_cross_entropy_bwd(const void* x, const void* weight, const int64_t* targets,
                                         const float* lse, const float* dloss, const float* dlse,

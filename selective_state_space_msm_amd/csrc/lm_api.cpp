@@ -98,7 +98,8 @@ BlockNormLayout block_norm_layout(int64_t rows, int64_t D, msm_dtype io) {
 // ---- linear cross entropy ----
 
 struct XentLayout {
-  size_t count, map, inverse, rows, xp, wp, stat, at_target, g, dx_sum, rest, total;
+  size_t count, map, inverse, rows, xp, wp, stat, at_target, g, dx_sum, rest, sort, words, marks, lost, total;
+  EmbedLayout sorted;  // from `sort` on
   int64_t DP, DQ, piece, piece_packed;
   int planes, splits;
   bool direct, few;
@@ -166,6 +167,13 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t D, msm_dtype io, bool bwd) 
     l.splits = xent_splits(T, D, l.piece, l.planes);
     l.dx_sum = take((size_t)l.splits * T * l.DQ * 4);
     l.rest = take((size_t)T * 4);
+    if (l.planes == 1) {
+      l.sorted = embed_layout(T, V, 0);
+      l.sort = take(l.sorted.total);
+      l.words = take((size_t)V * sizeof(msm::XentPlaces));
+      l.marks = take((size_t)msm::xent_marks(V));
+      l.lost = take((size_t)(T * l.DQ + 256) * 4);  // a tile's columns behind the last row
+    }
   } else {
     // pairs of sums of half a tile of the vocabulary, a piece at a time
     int64_t pairs = 0;
@@ -406,7 +414,33 @@ msm_status msm_linear_cross_entropy_bwd(const void* x, const void* weight, const
   a.dlse = dlse;
   a.dx = dx;
   a.dw = dweight;
-  return status_of(msm::launch_xent_bwd(a, io == MSM_BF16, static_cast<hipStream_t>(stream)));
+  msm::EmbedArgs sort{};
+  if (dweight && l.planes == 1) {
+    char* const ws = static_cast<char*>(workspace);
+    for (int i = 0; i < 2; ++i) {
+      sort.key[i] = reinterpret_cast<uint32_t*>(ws + l.sort + l.sorted.key[i]);
+      sort.pos[i] = reinterpret_cast<uint32_t*>(ws + l.sort + l.sorted.pos[i]);
+    }
+    sort.hist = reinterpret_cast<uint32_t*>(ws + l.sort + l.sorted.hist);
+    sort.ids = targets;
+    sort.tokens = T;
+    sort.V = V;
+    sort.waves = l.sorted.waves;
+    sort.per = l.sorted.per;
+    sort.bits = l.sorted.bits;
+    sort.passes = l.sorted.passes;
+    a.key = sort.key[(sort.passes - 1) & 1];
+    a.pos = sort.pos[(sort.passes - 1) & 1];
+    a.words = reinterpret_cast<msm::XentPlaces*>(ws + l.words);
+    a.marks = reinterpret_cast<uint8_t*>(ws + l.marks);
+    a.clear = (int64_t)(l.marks - l.words) + msm::xent_marks(V);
+    sort.dtable = a.words;
+    sort.rows = a.inverse;
+    a.lost = reinterpret_cast<float*>(ws + l.lost);
+    a.log_run = 5;  // one more as the tokens quadruple: a frequent word has few runs, and a run few places
+    while ((int64_t)1 << (2 * a.log_run) < T) ++a.log_run;
+  }
+  return status_of(msm::launch_xent_bwd(a, sort, io == MSM_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

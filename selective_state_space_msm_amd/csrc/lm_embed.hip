@@ -128,7 +128,7 @@ template <bool FIRST>
 __device__ __forceinline__ void place_of(const EmbedArgs& p, int pass, int64_t i, uint32_t* key, uint32_t* pos) {
   if constexpr (FIRST) {
     *key = key_of(p, i);
-    *pos = (uint32_t)i;
+    *pos = p.rows ? (uint32_t)p.rows[i] : (uint32_t)i;
   } else {
     *key = p.key[(pass - 1) & 1][i];
     *pos = p.pos[(pass - 1) & 1][i];
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void embed_sort_small_kernel(cons
   const int last = p.passes & 1, out = (p.passes - 1) & 1;
   for (int i = threadIdx.x; i < n; i += 64 * kSmallWaves) {
     p.key[out][i] = keys[last][i];
-    p.pos[out][i] = places[last][i];
+    p.pos[out][i] = p.rows ? (uint32_t)p.rows[places[last][i]] : places[last][i];
   }
 }
 
@@ -679,19 +679,23 @@ hipError_t fwd(const EmbedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+hipError_t sort_all(const EmbedArgs& a, int64_t fill, hipStream_t s) {
+  if (a.tokens <= kEmbedSmall) {
+    hipLaunchKernelGGL(embed_sort_small_kernel, dim3(1 + fill_groups(fill, 1)), dim3(64 * kSmallWaves), 0, s, a, Fill{fill, 0, 1});
+    return hipGetLastError();
+  }
+  hipError_t e = sort_pass<true>(a, 0, fill, s);
+  for (int pass = 1; pass < a.passes && e == hipSuccess; ++pass) e = sort_pass<false>(a, pass, fill, s);
+  return e;
+}
+
 template <typename TB, typename IO>
 hipError_t bwd(const EmbedArgs& a, hipStream_t s) {
   const int64_t pieces = (a.D + Chunk<IO>::VEC - 1) / Chunk<IO>::VEC, each = rows_of(pieces);
   const unsigned slices = (unsigned)((pieces + 255) / 256);
   const bool sparse = a.V >= a.tokens;
-  const int64_t fill = sparse ? a.V * a.D * io<TB>::es : 0;
-  if (a.tokens <= kEmbedSmall) {
-    hipLaunchKernelGGL(embed_sort_small_kernel, dim3(1 + fill_groups(fill, 1)), dim3(64 * kSmallWaves), 0, s, a, Fill{fill, 0, 1});
-  } else {
-    hipError_t e = sort_pass<true>(a, 0, fill, s);
-    for (int pass = 1; pass < a.passes && e == hipSuccess; ++pass) e = sort_pass<false>(a, pass, fill, s);
-    if (e != hipSuccess) return e;
-  }
+  const hipError_t e = sort_all(a, sparse ? a.V * a.D * io<TB>::es : 0, s);
+  if (e != hipSuccess) return e;
   if (a.tokens >= 2 * kEmbedRun) {
     const int64_t runs = a.tokens / kEmbedRun;
     hipLaunchKernelGGL((embed_run_kernel<IO>), dim3(groups_of(runs), slices), dim3(256), 0, s, a, runs, pieces);
@@ -715,6 +719,7 @@ hipError_t launch_embed_fwd(const EmbedArgs& a, int table_bf16, int io_bf16, hip
   if (table_bf16) return io_bf16 ? fwd<bf16_storage, bf16_storage>(a, s) : fwd<bf16_storage, float>(a, s);
   return io_bf16 ? fwd<float, bf16_storage>(a, s) : fwd<float, float>(a, s);
 }
+hipError_t launch_embed_sort(const EmbedArgs& a, int64_t fill, hipStream_t s) { return sort_all(a, fill, s); }
 hipError_t launch_embed_bwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s) {
   if (table_bf16) return io_bf16 ? bwd<bf16_storage, bf16_storage>(a, s) : bwd<bf16_storage, float>(a, s);
   return io_bf16 ? bwd<float, bf16_storage>(a, s) : bwd<float, float>(a, s);

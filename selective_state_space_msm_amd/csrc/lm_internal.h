@@ -26,6 +26,7 @@ struct EmbedArgs {
   int32_t waves, per;  // wavefronts of a sorting pass and their places (a multiple of 64)
   int32_t bits;        // of a digit
   int32_t passes;
+  const int32_t* rows; // what a sorted position is to be given as, null: as it is
 };
 
 constexpr int kEmbedMostBits = 9;      // of a digit: 512 bins
@@ -34,6 +35,8 @@ constexpr int kEmbedDeep = 8192;       // places from which there are sums of th
 constexpr int kEmbedRun = 32;          // places of a sum of the first level, and sums of the second
 hipError_t launch_embed_fwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s);
 hipError_t launch_embed_bwd(const EmbedArgs& a, int table_bf16, int io_bf16, hipStream_t s);
+// The sort alone, stable, into key and pos [(passes - 1) & 1]; clears `fill` bytes at dtable.
+hipError_t launch_embed_sort(const EmbedArgs& a, int64_t fill, hipStream_t s);
 
 // ---- block norm ----
 
@@ -90,6 +93,11 @@ struct XentRow {
   int32_t target;
 };
 
+// A word's places among the targets in order.
+struct XentPlaces {
+  int32_t first, end;
+};
+
 struct XentArgs {
   const void* x;           // (T, D) I/O type
   const void* w;           // (V, D)
@@ -112,15 +120,25 @@ struct XentArgs {
   void* g;                 // backward: [planes][T][piece] gradient of a piece's logits
   float* dx_sum;           // backward: [splits][T][DQ]
   float* rest;             // backward, bf16: (T,) what the target's g lost to its rounding
+  uint32_t* key;           // and with dw: (T,) the targets in order, V for rows that are left out
+  uint32_t* pos;           // (T,) their places in xp
+  XentPlaces* words;       // (V,) each word's places among these, 0, 0: none; null: nothing of this is asked for
+  uint8_t* marks;          // for 16 words a byte: one of them has places
+  float* lost;             // (T, DQ) sums of rest x over a word's places in one run, at the first of them
   int64_t T, V, D, DP, DQ, piece;
   float scale;
   int32_t planes;          // 1, or 3 for fp32
   int32_t w_direct;
   int32_t tile;            // side of the forward's tiles
   int32_t splits;          // of the vocabulary's pieces in the product of dx
+  int32_t log_run;         // of the places of a run
+  int64_t clear;           // bytes of words and marks, which follow each other
 };
 constexpr int kXentFew = 32;         // rows that the forward takes without tiles
 constexpr int kXentPlaced = 512;     // rows that stay in their places, also those that are left out
+// Bytes of the marks: four at a time are read, and a piece begins at a multiple of 256 words.
+constexpr int64_t xent_marks(int64_t V) { return (V + 255) / 256 * 16; }
+constexpr int kXentRanked = 4096;    // rows whose targets are put in order by counting
 constexpr int kXentFewGroups = 256;  // workgroups it takes them with at most: one a CU
 // Side of the tiles of an M x N product over K.  256 or 128 by rounds of the 256 CUs (one workgroup a CU, or
 // two of the smaller tiles), a small tile taking a quarter of a large one's work at 0.8 of its rate; not 256
@@ -134,6 +152,7 @@ constexpr int xent_tile(int64_t M, int64_t N, int64_t K, int planes) {
   return small >= 384 ? 128 : 64;
 }
 hipError_t launch_xent_fwd(const XentArgs& a, int io_bf16, hipStream_t s);
-hipError_t launch_xent_bwd(const XentArgs& a, int io_bf16, hipStream_t s);
+// sort: of the targets, for bf16 with dw and more than kXentRanked rows
+hipError_t launch_xent_bwd(const XentArgs& a, const EmbedArgs& sort, int io_bf16, hipStream_t s);
 
 }  // namespace msm

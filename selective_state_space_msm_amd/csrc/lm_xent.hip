@@ -16,9 +16,10 @@
 // m of one n: logits are made as [v][t], so that the sums over v stay within a lane's registers but
 // for two exchanges; dx as [d][t] and dW as [d][v], stored four values at a time.
 //
-// bf16 inputs are multiplied as they are; g is rounded to bf16 for the products with W and x
-// (its relative error of at most 2^-8 is that of rounding the results, which it joins as a random error
-// over the summed terms).  fp32 values are cut into three bf16 parts, and the six products that matter are
+// bf16 inputs are multiplied as they are; g is rounded to bf16 for the products with W and x.  What the
+// target's entry, most of a row's g, loses by that is added to dx and to dweight in fp32 (without it
+// dweight of 8192 tokens of 65536, D = 2048, was off by 2.2e-3 of its size from its values in 32 bits); the other
+// entries' errors, of at most 2^-8 and either sign, are summed over many small terms.  fp32 values are cut into three bf16 parts, and the six products that matter are
 // summed, g too.  Rows without a target are left out of all products: the rows that
 // take part are gathered in front, and what the others hold is never multiplied.
 //
@@ -73,8 +74,45 @@ __device__ __forceinline__ Part<P> parts_of(const float (&x)[8]) {
 
 // ---- rows that take part ----
 
-// Their places in order, by one workgroup.
+// The targets in order, and the places of their rows in xp (`gathered`: the rows that take part in front), for up
+// to kXentRanked rows: a row's place is the number of rows before it, counted by a wavefront.  Workgroup `group` of
+// `groups` takes its share, and of clearing the words' places.
+template <int THREADS>
+__device__ __forceinline__ void order_targets(const XentArgs& p, int group, int groups, bool gathered) {
+  __shared__ uint32_t keys[kXentRanked];
+  const int lane = threadIdx.x & 63, T = (int)p.T;
+  for (int64_t i = (int64_t)group * THREADS + threadIdx.x; i < p.clear / 16; i += (int64_t)groups * THREADS)
+    reinterpret_cast<u32x4*>(p.words)[i] = u32x4{0, 0, 0, 0};
+  const uint32_t none = (uint32_t)p.V;
+  for (int t = threadIdx.x; t < T; t += THREADS) {
+    const int64_t id = p.targets[t];
+    keys[t] = id >= 0 && id < p.V ? (uint32_t)id : none;
+  }
+  __syncthreads();
+  for (int row = group * (THREADS / 64) + threadIdx.x / 64; row < T; row += groups * (THREADS / 64)) {
+    const uint32_t own = keys[row];
+    int before = 0, live = 0;
+#pragma unroll 4
+    for (int t = lane; t < T; t += 64) {
+      const uint32_t other = keys[t];
+      before += other < own + (t < row);  // V + 1 is below 2^32
+      live += t < row && other != none;
+    }
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) {
+      before += __shfl_xor(before, m, 64);
+      live += __shfl_xor(live, m, 64);
+    }
+    if (lane == 0) {
+      p.key[before] = own;
+      p.pos[before] = (uint32_t)(gathered ? live : row);
+    }
+  }
+}
+
+// Their places in order, by one workgroup; the others put the targets in order, if that is asked for.
 __global__ __launch_bounds__(1024) void xent_rows_kernel(const XentArgs p) {
+  if (blockIdx.x > 0) return order_targets<1024>(p, blockIdx.x - 1, gridDim.x - 1, true);
   __shared__ int sums[2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int base = 0, turn = 0;
@@ -135,6 +173,7 @@ __global__ __launch_bounds__(256) void xent_pack_kernel(const void* src, const i
 template <typename IO>
 __global__ __launch_bounds__(256) void xent_gather_kernel(const XentArgs p, int64_t w_rows) {
   constexpr int P = io<IO>::es == 2 ? 1 : 3, VEC = Chunk<IO>::VEC;
+  if (p.words) order_targets<256>(p, blockIdx.x, gridDim.x, false);
   const int64_t chunks = p.DP / 8, of_x = p.T * chunks, all = of_x + w_rows * chunks;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     const bool is_x = i < of_x;
@@ -169,6 +208,98 @@ __global__ __launch_bounds__(256) void xent_gather_kernel(const XentArgs p, int6
   }
 }
 
+// ---- what the targets' g lost, for dweight ----
+// g is held in bf16, and its entry of the target may be off by half a step the same way for all tokens of a word;
+// a rare word's gradient is that of its few targets.  So what these entries lost is made up for: a word's sum of
+// rest x over its tokens, in fp32 and in the order of the batch, is added to dweight's product before that is
+// rounded.  The tokens are put in the order of their targets; a word's places are summed in aligned runs, which the
+// product's end adds up, so that a frequent word is not one long sum.
+// 7780 of 8192 tokens, 65536 words, D = 2048: 1.3% of the backward (5048 and 5115 us), of which the order of the
+// targets takes 28 and the sums 46.  As a second product with the targets' rests, in the registers of the
+// first, it took 4%, and 1.7 times the time of the whole where few words have all tokens (16000 tokens of 300, D = 700:
+// 283 us, this way 206, without it 167).
+
+// A wavefront takes the sums that start among kLostPlaces places, for the words v0 ... v1 and 64 times eight columns.
+// It reads 64 places at once, one of them a lane's; most sums end among them.
+constexpr int kLostPlaces = 4;
+struct LostShare {
+  uint32_t v0, v1;
+  unsigned groups;  // workgroups over the places, and as many again for every 512 columns
+  unsigned all;     // workgroups; 0: nothing of this
+};
+__device__ __forceinline__ void sum_lost(const XentArgs& p, const LostShare& share) {
+  const unsigned slice = blockIdx.x / share.groups;
+  const int lane = threadIdx.x & 63, T = (int)p.T, i0 = uniform((int)((blockIdx.x - slice * share.groups) * 4 + threadIdx.x / 64)) * kLostPlaces;
+  if (i0 >= T) return;
+  const int64_t c = ((int64_t)slice * 64 + lane) * 8;
+  const uint16_t* const xp = static_cast<const uint16_t*>(p.xp) + (c < p.DQ ? c : 0);
+  struct Places {
+    uint32_t key;
+    int row;
+    float lost;
+  };
+  const auto in = [&](uint32_t v) { return v >= share.v0 && v < share.v1; };
+  const auto read = [&](int i) {
+    const bool there = i + lane < T;
+    Places w{there ? p.key[i + lane] : ~0u, there ? (int)p.pos[i + lane] : 0, 0.f};
+    if (in(w.key)) w.lost = p.rest[w.row];
+    return w;
+  };
+  const uint32_t before = i0 > 0 ? p.key[i0 - 1] : ~0u;
+  const Places here = read(i0);
+  if ((__ballot(in(here.key)) & ((1u << kLostPlaces) - 1)) == 0) return;
+  float x[8];
+  // its places u ... n, N of them with their loads in flight together
+  const auto some = [&](auto N, const Places& w, int u) {
+    constexpr int kN = decltype(N)::value;
+    Chunk<bf16_storage> r[kN];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) r[k].load(xp, (int64_t)__builtin_amdgcn_readlane(w.row, u + k) * p.DP, 8);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w.lost), u + k));
+      float y[8];
+      r[k].get(y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(f, y[e], x[e]);
+    }
+  };
+  const auto add = [&](const Places& w, int u, int n) {
+    for (; u + 16 <= n; u += 16) some(std::integral_constant<int, 16>{}, w, u);
+    for (; u + 4 <= n; u += 4) some(std::integral_constant<int, 4>{}, w, u);
+    for (; u < n; ++u) some(std::integral_constant<int, 1>{}, w, u);
+  };
+  for (int s = 0; s < kLostPlaces; ++s) {
+    const int i = i0 + s;
+    const uint32_t v = (uint32_t)__builtin_amdgcn_readlane((int)here.key, s), behind = (uint32_t)__builtin_amdgcn_readlane((int)here.key, s + 1);
+    const bool first = (s == 0 ? before : (uint32_t)__builtin_amdgcn_readlane((int)here.key, s - 1)) != v;
+    if (!in(v)) continue;  // nor is it behind the last place
+    if (slice == 0 && lane == 0) {
+      if (first) {
+        p.words[v].first = i;
+        p.marks[v / 16] = 1;
+      }
+      if (behind != v) p.words[v].end = i + 1;
+    }
+    if (!first && (i & ((1 << p.log_run) - 1)) != 0) continue;
+    const int run_end = ((i >> p.log_run) + 1) << p.log_run;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    // the word's places stand side by side
+    int n = s + __popcll(__ballot(here.key == v && lane >= s && i0 + lane < run_end));
+    add(here, s, n);
+    for (int j = i0 + 64; n == 64 && j < run_end; j += 64) {
+      const Places w = read(j);
+      n = __popcll(__ballot(w.key == v && j + lane < run_end));
+      add(w, 0, n);
+    }
+    float* const to = p.lost + i * p.DQ + c;
+#pragma unroll
+    for (int e = 0; e < 8; e += 4)
+      if (c + e < p.DQ) *reinterpret_cast<f32x4*>(to + e) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+  }
+}
+
 // ---- the product kernel ----
 
 enum class Fetch { kRows, kCols };
@@ -198,6 +329,11 @@ struct ProductArgs {
   float* rest;             // what the target's g lost to bf16
   void* dw;
   int64_t ld_dw;
+  const XentPlaces* words;  // bf16: what is to be added to dweight
+  const uint8_t* marks;     // words and marks of the piece
+  const float* lost;
+  int64_t ld_lost;
+  int32_t log_run;
 };
 
 // A step's tile of an operand, of one plane: R rows of KS k (64 or 32: 128 or 64 bytes), or KS k rows of R
@@ -332,6 +468,12 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
   if (m0 >= p.M || n0 >= N) return;  // fewer rows than the grid was made for among these
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), wm = wave % WM, wn = wave / WM;
   const lds_parts tiles = (lds_parts)lds;
+  // one of the wavefront's columns has a sum to be added: asked here, with the count of k, so that the end need not wait
+  bool marked = false;
+  if constexpr (END == Ends::kDw && P == 1) {
+    const int first = n0 / 16 + wn * NT;
+    marked = (reinterpret_cast<const uint32_t*>(p.marks)[first / 4] >> (first % 4 * 8) & (NT == 4 ? ~0u : (1u << (8 * NT % 32)) - 1)) != 0;
+  }
   LA la;
   LB lb;
   la.init(wave, lane, p.lda, m0, p.M);
@@ -596,6 +738,47 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
       }
     }
   } else {
+    if constexpr (P == 1) {
+      // The products' own registers end here, behind the wait states that a matrix instruction's result needs: with sums
+      // added to them the compiler moves them about inside the products' loop (64 tokens of 7178, D = 6656: 48 us, and 46).
+      asm volatile("s_nop 15\n\ts_nop 15" : "+v"(acc[0][0]));
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[i][j]));
+      // Before the first store, as a load's wait is also for the stores before it, and with several words' loads in flight.
+      if (marked) {
+        constexpr int kAtOnce = BM == 256 ? 2 : NT;  // of NT, what the registers hold
+        XentPlaces places[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int n = n0 + wn * NT * 16 + j * 16 + (lane & 15);
+          places[j] = n < N ? p.words[n] : XentPlaces{0, 0};
+        }
+        // (columns behind a row's end are the next row's, or what follows the last row, and are not stored)
+        const float* const lost = p.lost + ml;
+#pragma unroll
+        for (int j0 = 0; j0 < NT; j0 += kAtOnce) {
+          f32x4 x[kAtOnce][MT];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) x[j][i] = zero4();
+            if (places[j0 + j].end > 0)
+#pragma unroll
+              for (int i = 0; i < MT; ++i) x[j][i] = *reinterpret_cast<const f32x4*>(lost + places[j0 + j].first * p.ld_lost + i * 16);
+          }
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[i][j0 + j] += x[j][i];
+            for (int at = ((places[j0 + j].first >> p.log_run) + 1) << p.log_run; at < places[j0 + j].end; at += 1 << p.log_run)  // further runs
+#pragma unroll
+              for (int i = 0; i < MT; ++i) acc[i][j0 + j] += *reinterpret_cast<const f32x4*>(lost + at * p.ld_lost + i * 16);
+          }
+        }
+      }
+    }
     const bool whole = p.ld_dw % 4 == 0 && ((uintptr_t)p.dw & 15) == 0;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -877,15 +1060,18 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs p, int64_
   }
 }
 
-// dx from the sums over all pieces, of every split; zero for the rows that are left out.  With bf16 g,
-// what the target's g lost to its rounding is made up for here: it is most of a row's g as a rule, and
-// its rounding alone had dx off by 1.65 times the rounding of the result (2.8e-3 for 1.7e-3 of its size;
-// 8192 tokens of 65536, D = 2048).
+// The end of a piece: its words' sums for dweight, by the first workgroups (a launch of their own costs 39 tokens of
+// 1391, D = 318, 5 us of 32).  Behind the last piece the others make dx from the sums over all pieces, of every split;
+// zero for the rows that are left out.  With bf16 g, what the target's g lost to its rounding is made up for
+// here: it is most of a row's g as a rule, and its rounding alone had dx off by 1.65 times the rounding of
+// the result (2.8e-3 for 1.7e-3 of its size; 8192 tokens of 65536, D = 2048).
 template <typename IO>
-__global__ __launch_bounds__(256) void xent_dx_kernel(const XentArgs p) {
+__global__ __launch_bounds__(256) void xent_end_kernel(const XentArgs p, const LostShare share) {
   constexpr int VEC = Chunk<IO>::VEC;
+  if constexpr (io<IO>::es == 2)
+    if (blockIdx.x < share.all) return sum_lost(p, share);
   const int64_t pieces = (p.D + VEC - 1) / VEC, all = p.T * pieces;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)(blockIdx.x - share.all) * 256 + threadIdx.x; i < all; i += (int64_t)(gridDim.x - share.all) * 256) {
     const int64_t t = quotient(i, pieces), c = (i - t * pieces) * VEC;
     const int n = p.inverse[t];
     float x[VEC];
@@ -960,7 +1146,8 @@ hipError_t gather(const XentArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((xent_gather_kernel<IO>), dim3(groups_of(((a.T + first) * (a.DP / 8) + 255) / 256)), dim3(256), 0, s, a, first);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, s, a);
+  const unsigned order = a.words && a.T <= kXentRanked ? (unsigned)((a.T + 15) / 16) : 0;
+  hipLaunchKernelGGL(xent_rows_kernel, dim3(1 + order), dim3(1024), 0, s, a);
   return pack<IO>(a.x, a.map, a.count, a.T, a, a.T * a.DP, a.xp, s);
 }
 template <typename IO>
@@ -1023,8 +1210,10 @@ hipError_t fwd(const XentArgs& a, hipStream_t s) {
 }
 
 template <typename IO>
-hipError_t bwd(const XentArgs& a, hipStream_t s) {
+hipError_t bwd(const XentArgs& a, const EmbedArgs& sort, hipStream_t s) {
+  constexpr bool bf16 = io<IO>::es == 2;
   hipError_t e = gather<IO>(a, s);
+  if (bf16 && a.words && a.T > kXentRanked && e == hipSuccess) e = launch_embed_sort(sort, a.clear, s);
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += a.piece) {
     const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
     ProductArgs g{};
@@ -1065,6 +1254,15 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     x.splits = a.splits;
     x.first = v0 == 0;
     e = product<IO, Fetch::kCols, Fetch::kRows, Ends::kDx>(x, xent_tile(a.D, a.T, n, a.planes), s);
+    if (e != hipSuccess) break;
+    const bool last = v0 + n == a.V;
+    LostShare share{(uint32_t)v0, (uint32_t)(v0 + n), (unsigned)((a.T + 4 * kLostPlaces - 1) / (4 * kLostPlaces)), 0};
+    if (a.words) share.all = share.groups * (unsigned)((a.DQ + 511) / 512);
+    const unsigned of_dx = last ? groups_of((a.T * ((a.D * io<IO>::es + 15) / 16) + 255) / 256) : 0;
+    if (share.all + of_dx > 0) {
+      hipLaunchKernelGGL((xent_end_kernel<IO>), dim3(share.all + of_dx), dim3(256), 0, s, a, share);
+      e = hipGetLastError();
+    }
     if (e != hipSuccess || !a.dw) continue;
     ProductArgs d{};
     d.a = static_cast<const uint16_t*>(a.xp);
@@ -1080,12 +1278,14 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
     d.v0 = (int32_t)v0;
     d.dw = a.dw;
     d.ld_dw = a.D;
+    d.words = a.words + v0;
+    d.marks = a.marks + v0 / 16;
+    d.lost = a.lost;
+    d.ld_lost = a.DQ;
+    d.log_run = a.log_run;
     e = product<IO, Fetch::kCols, Fetch::kCols, Ends::kDw>(d, xent_tile(a.D, n, a.T, a.planes), s);
   }
-  if (e != hipSuccess) return e;
-  const int64_t pieces = (a.D * io<IO>::es + 15) / 16;
-  hipLaunchKernelGGL((xent_dx_kernel<IO>), dim3(groups_of((a.T * pieces + 255) / 256)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return e;
 }
 
 }  // namespace
@@ -1093,8 +1293,8 @@ hipError_t bwd(const XentArgs& a, hipStream_t s) {
 hipError_t launch_xent_fwd(const XentArgs& a, int io_bf16, hipStream_t s) {
   return io_bf16 ? fwd<bf16_storage>(a, s) : fwd<float>(a, s);
 }
-hipError_t launch_xent_bwd(const XentArgs& a, int io_bf16, hipStream_t s) {
-  return io_bf16 ? bwd<bf16_storage>(a, s) : bwd<float>(a, s);
+hipError_t launch_xent_bwd(const XentArgs& a, const EmbedArgs& sort, int io_bf16, hipStream_t s) {
+  return io_bf16 ? bwd<bf16_storage>(a, sort, s) : bwd<float>(a, sort, s);
 }
 
 }  // namespace msm
