@@ -77,7 +77,7 @@ __device__ __forceinline__ void store_parts(lds_parts p, int plane, const Part<N
   for (int n = 0; n < N; ++n) *(MSM_LDS bf16x8*)(p + n * plane) = s.p[n];
 }
 template <int N>
-__device__ __forceinline__ void store_parts(uint16_t* p, int plane, const Part<N>& s) {
+__device__ __forceinline__ void store_parts(uint16_t* p, int64_t plane, const Part<N>& s) {
 #pragma unroll
   for (int n = 0; n < N; ++n) *(bf16x8*)(p + n * plane) = s.p[n];
 }

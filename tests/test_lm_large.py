@@ -83,3 +83,47 @@ def test_weights_past_32_bits(T):
     tol = 2.0 ** -7 * ((-lse.double()).exp() @ x.double().abs())
     for v in (1, (1 << 20) - 1, V - 2):
         assert bool(((d["dweight"][v].double() - other).abs() <= tol).all()), v
+
+
+@pytest.mark.parametrize("T,io", [(262147, torch.float32), (524301, torch.float32), (524301, BF)])
+def test_parts_of_tokens_past_32_bits(T, io):
+    """fp32 rows in three parts that lie 1.1e9 and 2.2e9 elements apart, bf16 rows of 2.2e9, most rows left out: against
+    float64 on the rows that take part.  The workspaces hold NaN, so what is not written where it is read shows."""
+    import selective_state_space_msm_amd as msm
+    V, D = 64, 4100
+    gen = torch.Generator().manual_seed(T)
+    live = torch.cat([torch.randperm(T, generator=gen)[:150], torch.tensor([0, T - 1])]).unique()
+    x = torch.full((T, D), float("nan"), dtype=io, device="cuda")
+    x[live.cuda()] = torch.randn(len(live), D, generator=gen).to(io).cuda()
+    w = (D ** -0.5 * torch.randn(V, D, generator=gen)).to(io).cuda()
+    t = torch.full((T,), -100)
+    t[live] = torch.randint(V, (len(live),), generator=gen)
+    t, live = t.cuda(), live.cuda()
+    dl = torch.randn(T, generator=gen).cuda()
+
+    def space(size):
+        return torch.full((size(T, V, D, io),), 255, dtype=torch.uint8, device="cuda")
+
+    loss, lse = msm.msm_linear_cross_entropy_fwd(x, w, t, return_lse=True, workspace=space(msm.msm_linear_cross_entropy_fwd_workspace_bytes))
+    xd, wd, at = x[live].double(), w.double(), t[live]
+    logits = xd @ wd.t()
+    want = torch.logsumexp(logits, 1)
+    # a logit's products leave out less than 2^-20 of a term and are summed in six rounds of D terms; the terms are of
+    # either sign, and their errors as well: 16 standard deviations of the sum's
+    err = 16 * (6 * D) ** 0.5 * 2.0 ** -24 * (xd.square() @ wd.square().t()).sqrt().max() + 2.0 ** -20
+    assert bool(((lse[live].double() - want).abs() <= err + 2.0 ** -20 * want.abs()).all())
+    assert bool(((loss[live].double() - (want - logits.gather(1, at[:, None])[:, 0])).abs() <= 2 * err + 2.0 ** -19 * want.abs()).all())
+    left = torch.ones(T, dtype=torch.bool, device="cuda")
+    left[live] = False
+    assert not bool(loss[left].any()) and not bool(lse[left].any())
+    d = msm.msm_linear_cross_entropy_bwd(x, w, t, lse, dl, workspace=space(msm.msm_linear_cross_entropy_bwd_workspace_bytes))
+    g = (logits - lse[live].double()[:, None]).exp() * dl[live].double()[:, None]
+    g[torch.arange(len(live)), at] -= dl[live].double()
+    for name, got, ref, size in (("dx", d["dx"][live], g @ wd, g.abs() @ wd.abs()), ("dweight", d["dweight"], g.t() @ xd, g.abs().t() @ xd.abs())):
+        # g: its logit's error and 2^-20 of itself; the products' and the sum's 2^-20 and fewer than 64 + 152 roundings
+        tol = (err + 2.0 ** -18) * size + 6 * 256 * 2.0 ** -24 * size
+        if io == BF:  # g and the result are rounded to bf16
+            tol = tol + 2.0 ** -7 * size
+        assert bool(((got.double() - ref).abs() <= tol).all()), name
+    for i in range(0, T, 65536):  # dx of the rows that are left out
+        assert not bool(d["dx"][i : i + 65536][left[i : i + 65536]].any())
