@@ -443,7 +443,8 @@ msm_status msm_block_norm_bwd(const void* r_out, const void* dy, const float* rs
  * x (T, D), weight (V, D) io; targets (T,) int64; loss, lse (T,) fp32, lse may be NULL.  A row whose
  * target lies outside [0, V) is left out: its loss and lse are 0, whatever it holds (the other rows'
  * results do not depend on it).  Logits, sums and statistics are fp32; fp32 inputs are multiplied in
- * three bf16 parts that keep 24 bits (an infinite one gives NaN).
+ * three bf16 parts that keep 24 bits (an infinite one gives NaN).  A logit of plus infinity makes lse
+ * infinite, and the loss too, or NaN if it is the target's.
  * Requirements: T, V, D >= 1; T and V <= 2^22, T V <= 2^37, D <= 2^16 (else MSM_ERR_UNSUPPORTED);
  * scale finite.
  * bf16 weights with D a multiple of 8 that begin at a multiple of 16 bytes are read where they are;

@@ -656,7 +656,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float from = top == -INFINITY ? 0.f : top;  // nothing but minus infinity: a sum of 0
+      // nothing but minus infinity: a sum of 0; plus infinity among them: a sum of infinity
+      const float from = fabsf(top) == INFINITY ? 0.f : top;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -825,10 +826,10 @@ __host__ __device__ constexpr int few_waves(int pieces) {
 // Joins the largest logit (in units of log 2) and the sum of exponentials of another set of columns.
 __device__ __forceinline__ void join_sums(float& top, float& sum, float top2, float sum2) {
   const float m = fmaxf(top, top2);
-  if (m != -INFINITY)
+  if (fabsf(m) != INFINITY)
     sum = sum * exp2_fast(top - m) + sum2 * exp2_fast(top2 - m);
   else
-    sum += sum2;  // 0, or NaN
+    sum += sum2;  // not negative, or NaN; what it is but for that, does not matter beside m
   top = m;
 }
 
