@@ -116,7 +116,7 @@ struct XentArgs {
   void* xp;                // [planes][T][DP] bf16 parts of the rows that take part
   void* wp;                // [planes][piece][DP] the same of a piece of w, where w is not read directly
   float* stat;             // forward: [tiles of the vocabulary][T][2] largest logit, sum of exponentials
-  float* at_target;        // forward: (T,) logit of the target
+  float* at_target;        // forward: (T,) logit of the target, in units of log 2
   void* g;                 // backward: [planes][T][piece] gradient of a piece's logits
   float* dx_sum;           // backward: [splits][T][DQ]
   float* rest;             // backward, bf16: (T,) what the target's g lost to its rounding

@@ -637,7 +637,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (ml - m0 + i * 16 + r == target) p.at_target[n] = acc[i][j][r] * p.scale;
+            if (ml - m0 + i * 16 + r == target) p.at_target[n] = acc[i][j][r] * to2;
       }
       float top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -965,8 +965,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void xent_few_kernel(const XentArgs
       }
       const int64_t v = (int64_t)(tile + sub) * 16 + 4 * g + r;
       if (v < p.V) {
-        if (v == target) p.at_target[t] = l * p.scale;
         l *= p.scale * kLog2e;
+        if (v == target) p.at_target[t] = l;
         join_sums(top, sum, l, l == l ? 1.f : l);
       }
     }
@@ -1055,7 +1055,8 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const XentArgs p, int64_
     }
     if (part == 0) {
       const float lse = n < 0 ? 0.f : (top + log2f(sum)) * kLn2;
-      p.loss[t] = n < 0 ? 0.f : lse - p.at_target[n];
+      // the target's logit is taken from the largest as both were compared, before lse rounds: 0 for the largest
+      p.loss[t] = n < 0 ? 0.f : (top - p.at_target[n] + log2f(sum)) * kLn2;
       if (p.lse) p.lse[t] = lse;
     }
   }
