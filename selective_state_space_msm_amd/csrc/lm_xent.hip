@@ -1011,10 +1011,13 @@ hipError_t few(const XentArgs& a, hipStream_t s) {
     }
   }
   hipLaunchKernelGGL((xent_few_pack_kernel<IO>), dim3((pieces * NT + 3) / 4), dim3(256), 0, s, a, pieces, NT);
-  if (all)
-    hipLaunchKernelGGL((xent_few_kernel<IO, NT, false, true>), dim3(groups), block, 0, s, a, tiles);
-  else
-    hipLaunchKernelGGL((xent_few_kernel<IO, NT, false, false>), dim3(groups), block, 0, s, a, tiles);
+  if constexpr (io<IO>::es == 4)
+    if (!all) {
+      hipLaunchKernelGGL((xent_few_kernel<IO, NT, false, false>), dim3(groups), block, 0, s, a, tiles);
+      return hipGetLastError();
+    }
+  static_assert(io<IO>::es == 4 || few_waves(kFewWaves * kFewHeld + 1) == kFewWaves, "bf16 rows that are not held take all wavefronts");
+  hipLaunchKernelGGL((xent_few_kernel<IO, NT, false, true>), dim3(groups), block, 0, s, a, tiles);
   return hipGetLastError();
 }
 
