@@ -417,13 +417,29 @@ hipError_t join(const BlockNormArgs& a, hipStream_t s) {
   return launch_norm_join(n, a.groups, s);
 }
 
+// Threads that a workgroup has at most where a row has T, more than a wavefront.
+constexpr int most_threads(int T) { return T > 512 ? 1024 : (T > 256 ? 512 : 256); }
+// Whether some width has this shape (a shape is the same for all widths of (64 k, 64 k + 64]).
+constexpr bool shape_of_some(bool bwd, bool bf16, int G, int E, int most) {
+  for (int64_t D = 64; block_norm_shape(D, bwd, bf16).T > 0; D += 64) {
+    const BlockNormShape f = block_norm_shape(D, bwd, bf16);
+    if (f.E == E && (G > 0 ? f.T == G : f.T > 64 && most_threads(f.T) == most)) return true;
+  }
+  return false;
+}
+// Whether pick below has a kernel for every width that has a shape.
+constexpr bool all_picked(bool bwd, bool bf16) {
+  for (int64_t D = 64; block_norm_shape(D, bwd, bf16).T > 0; D += 64) {
+    const BlockNormShape f = block_norm_shape(D, bwd, bf16);
+    if (!(f.E == 8 || (f.E == 4 && !bf16) || (f.E == 16 && f.T > 64))) return false;
+  }
+  return true;
+}
+
 template <typename IO, int G, int E, int MOST>
 hipError_t go(const BlockNormArgs& a, int threads, bool bwd, hipStream_t s) {
   constexpr int RW = G == 0 ? 1 : MOST / (G == 0 ? 1 : G);
-  // what block_norm_shape gives
-  constexpr bool f32 = io<IO>::es == 4;
-  constexpr bool of_fwd = E == 8 || (G == 0 && E == 16 && MOST == 1024);
-  constexpr bool of_bwd = G > 0 ? (f32 ? E == 4 || G == 64 : E == 8) : (f32 ? E == 4 || (E == 8 && MOST == 1024) : (E == 8 ? MOST == 256 : MOST <= 512));
+  constexpr bool bf16 = io<IO>::es == 2, of_fwd = shape_of_some(false, bf16, G, E, MOST), of_bwd = shape_of_some(true, bf16, G, E, MOST);
   const dim3 block(G == 0 ? threads : MOST);
   if (!bwd) {
     if constexpr (of_fwd) {
@@ -443,12 +459,15 @@ hipError_t go(const BlockNormArgs& a, int threads, bool bwd, hipStream_t s) {
 
 template <typename IO, int E>
 hipError_t go_wide(const BlockNormArgs& a, int threads, bool bwd, hipStream_t s) {
-  if (threads > 512) return go<IO, 0, E, 1024>(a, threads, bwd, s);
-  return threads > 256 ? go<IO, 0, E, 512>(a, threads, bwd, s) : go<IO, 0, E, 256>(a, threads, bwd, s);
+  if (threads <= 64) return hipErrorInvalidValue;
+  const int most = most_threads(threads);
+  if (most == 1024) return go<IO, 0, E, 1024>(a, threads, bwd, s);
+  return most == 512 ? go<IO, 0, E, 512>(a, threads, bwd, s) : go<IO, 0, E, 256>(a, threads, bwd, s);
 }
 
 template <typename IO>
 hipError_t pick(const BlockNormArgs& a, bool bwd, hipStream_t s) {
+  static_assert(all_picked(false, io<IO>::es == 2) && all_picked(true, io<IO>::es == 2), "a kernel for every width");
   const BlockNormShape f = block_norm_shape(a.D, bwd, io<IO>::es == 2);
 #define MSM_ROWS(GG, EE) \
   if (f.T == GG && f.E == EE) return go<IO, GG, EE, 256>(a, GG, bwd, s);

@@ -181,3 +181,9 @@ def test_column_gradients_do_not_drift():
     want = rows * (dy[0].double() * (r[0].double() * rstd[0].double()))
     # a thread sums at most 40000 / (512 * 8) = 10 rows; 3 roundings of a term, 10 + 4 of sums
     assert bool(((d["dweight"].double() - want).abs() <= 20 * 2.0 ** -24 * want).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1023, 1024, 1025, 2048, 2049, 4096, 4097, 8192, 8193])
+def test_widths_at_which_rows_change_their_shape(io, D):
+    check(io, 3, D)
