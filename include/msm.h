@@ -399,13 +399,14 @@ msm_status msm_grad_clip(const void* const* grads, void* const* out, const int64
 
 /* Token embedding: y[t] = scale * table[ids[t]], ids (tokens,) int64, table (V, D) in table_io,
  * y (tokens, D) in io (any combination of the two types).  An id outside [0, V) gives a row of
- * zeros.  1 <= tokens, V < 2^31, 1 <= D <= 2^24, scale finite. */
+ * zeros.  1 <= tokens < 2^31, 1 <= V < 2^31 - 1, 1 <= D <= 2^24, tokens D and V D <= 2^48, scale
+ * finite. */
 msm_status msm_embed_fwd(const int64_t* ids, const void* table, void* y, int64_t tokens, int64_t V,
                          int64_t D, float scale, msm_dtype table_io, msm_dtype io, void* stream);
 
 /* Gradient of the table: dtable[v] = scale * sum of dy[t] over {t: ids[t] = v}, every row written
  * (zeros for a row without a token).  Ids outside [0, V) take no part.  Tokens are sorted by id and
- * added in the order of the batch: no atomics, the same result every time. */
+ * added in the order of the batch: no atomics, the same result every time.  Sizes as above. */
 size_t msm_embed_bwd_workspace_bytes(int64_t tokens, int64_t V, int64_t D);
 msm_status msm_embed_bwd(const int64_t* ids, const void* dy, void* dtable, int64_t tokens,
                          int64_t V, int64_t D, float scale, msm_dtype table_io, msm_dtype io,
@@ -419,16 +420,17 @@ msm_status msm_embed_bwd(const int64_t* ids, const void* dy, void* dtable, int64
  * post_weight: (D,) fp32, NULL meaning ones; rstd, post_rstd: (rows,) fp32, the reciprocal roots of
  * the two norms, written when non-NULL.  z NULL: no gate.  o NULL: y = weight * RMS(r) alone, and
  * post_weight, z, r_out and post_rstd are NULL.  r_out may be r itself (the stream is updated in
- * place); no other overlap.  1 <= rows < 2^31, 1 <= D <= 2^30, scale finite, eps >= 0 and finite. */
+ * place); no other overlap.  1 <= rows < 2^31, 1 <= D <= 2^30, rows D <= 2^50, scale finite, eps >= 0
+ * and finite. */
 msm_status msm_block_norm_fwd(const void* r, const float* weight, const void* o,
                               const float* post_weight, const void* z, void* r_out, void* y,
                               float* rstd, float* post_rstd, int64_t rows, int64_t D, float scale,
                               float eps, msm_dtype io, void* stream);
 
 /* Gradients of sum(dy * y) + sum(dr_out * r_out) (dr_out NULL: zero) from the forward's r_out and
- * statistics: dr (also r_out's own), do, dz in the io type, dweight, dpost_weight (D,) fp32, each
- * written when non-NULL.  Without o: r_out is r, and do, dz, dpost_weight and the block's inputs
- * are NULL.  dz is given exactly when z is. */
+ * statistics: dr (also r_out's own) and, with o, do in the io type; dz in it exactly when z is given;
+ * dweight and dpost_weight (D,) fp32, each written when non-NULL.  Without o: r_out is r, and do, dz,
+ * dpost_weight and the block's inputs are NULL.  Sizes as above. */
 size_t msm_block_norm_bwd_workspace_bytes(int64_t rows, int64_t D, msm_dtype io);
 msm_status msm_block_norm_bwd(const void* r_out, const void* dy, const float* rstd,
                               const float* weight, const void* o, const float* post_rstd,
