@@ -12,8 +12,8 @@
 // elements each, and the next row's loads are issued before the present one is reduced.  A piece
 // of a row is 16 bytes also where rows begin at odd addresses (the hardware takes unaligned
 // 16-byte accesses); only a row's last piece may be taken element by element.  The backward's
-// column sums stay in registers over the rows of a workgroup and are joined by a second kernel
-// in a fixed order.  Rows past the registers are walked in memory with fp64 sums.
+// column sums stay in registers over 64 rows of a thread, in LDS over the others, and the workgroups'
+// are joined by a second kernel in a fixed order.  Rows past the registers are walked in memory with fp64 sums.
 // 16384 x 4096, bf16, with block and gate: forward 134 us (5.0 TB/s), backward 207 (5.2 TB/s); a copy of
 // 1 GiB reaches 5.1.  4095 x 1001, fp32, no gate: backward 26 us (3.8 TB/s).
 #include "lm_internal.h"
@@ -46,6 +46,9 @@ __device__ __forceinline__ float rstd_of(double sum, double inv, float eps) {
 }
 
 constexpr int64_t kRowGroups = 2048;
+// Rows that a thread of the backward adds up in one fp32 sum, before that is added to those of the rows before:
+// 1024 rows of equal terms in one sum were off by 9e-6 of it.
+constexpr int kRowsOfSum = 64;
 
 // G threads to a row, 256 / G rows a workgroup; G = 0: a row for the workgroup, of up to MOST threads.
 template <typename IO, int G, int E, int MOST>
@@ -154,6 +157,10 @@ __global__ __launch_bounds__(MOST) void block_norm_bwd_kernel(const BlockNormArg
   const int64_t step = (int64_t)gridDim.x * RW;
   const bool block = p.o != nullptr, gate = p.z != nullptr, residual = p.dr_out != nullptr;
   float w[NV][VEC], pw[NV][VEC], dw[NV][VEC], dpw[NV][VEC];
+  // a thread's own sums of up to kRowsOfSum rows each; in registers they would push the rows' out (131072 x 4096,
+  // bf16: 2180 us, and 1532 this way; 1510 with one sum over all rows)
+  __shared__ float whole[2 * E * MOST];
+  const auto kept = [&](int which, int i, int e) -> float& { return whole[((which * NV + i) * VEC + e) * MOST + threadIdx.x]; };
   Chunk<IO> ny[NV], nr[NV], nd[NV], no[NV], nz[NV];
   int64_t row = (int64_t)blockIdx.x * RW + (G == 0 ? 0 : threadIdx.x / (G == 0 ? 1 : G));
   const auto fetch = [&](int i, int64_t at) {
@@ -178,79 +185,89 @@ __global__ __launch_bounds__(MOST) void block_norm_bwd_kernel(const BlockNormArg
     for (int e = 0; e < VEC; ++e) {
       w[i][e] = p.weight && c + e < p.D ? p.weight[c + e] : 1.f;
       pw[i][e] = p.post_weight && c + e < p.D ? p.post_weight[c + e] : 1.f;
-      dw[i][e] = dpw[i][e] = 0.f;
+      dw[i][e] = dpw[i][e] = kept(0, i, e) = kept(1, i, e) = 0.f;
     }
   }
-  for (; row < p.rows; row += step) {  // whole rows leave: no sum crosses rows
-    const int64_t at = row * p.D, next = (row + step) * p.D;
-    const bool more = row + step < p.rows;
-    const float rstd = p.rstd[row], q = block ? p.post_rstd[row] : 0.f;
-    float u[NV][VEC], h[NV][VEC], g[NV][VEC], o[NV][VEC], z[NV][VEC];
-    float a = 0.f;
+  while (row < p.rows) {
+    for (int left = kRowsOfSum; left > 0 && row < p.rows; --left, row += step) {  // whole rows leave: no sum crosses rows
+      const int64_t at = row * p.D, next = (row + step) * p.D;
+      const bool more = row + step < p.rows;
+      const float rstd = p.rstd[row], q = block ? p.post_rstd[row] : 0.f;
+      float u[NV][VEC], h[NV][VEC], g[NV][VEC], o[NV][VEC], z[NV][VEC];
+      float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int by = Chunk<IO>::short_by(((int64_t)i * T + t) * VEC, p.D);
-      ny[i].get_row(u[i], by);
-      nr[i].get_row(h[i], by);
-      nd[i].get_row(g[i], by);
-      no[i].get_row(o[i], by);
-      nz[i].get_row(z[i], by);
-      if (more) fetch(i, next);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        h[i][e] *= rstd;
-        dw[i][e] = fmaf(u[i][e], h[i][e], dw[i][e]);
-        u[i][e] *= w[i][e];
-        a = fmaf(u[i][e], h[i][e], a);
-      }
-    }
-    a = group_sum<G>(a, lds[turn]) * inv;
-    turn ^= 1;
-    float b = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
-      Chunk<IO> out;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) g[i][e] = fmaf(rstd, u[i][e] - h[i][e] * a, g[i][e]);
-      out.set(g[i]);
-      if (n > 0) out.store(p.dr, at + c, n);
-      if (!block) continue;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        o[i][e] *= q;
-        g[i][e] *= p.scale;
-      }
-      if (gate) {
-        float dz[VEC];
+      for (int i = 0; i < NV; ++i) {
+        const int by = Chunk<IO>::short_by(((int64_t)i * T + t) * VEC, p.D);
+        ny[i].get_row(u[i], by);
+        nr[i].get_row(h[i], by);
+        nd[i].get_row(g[i], by);
+        no[i].get_row(o[i], by);
+        nz[i].get_row(z[i], by);
+        if (more) fetch(i, next);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const Logistic l = logistic_f(z[i][e]);
-          dz[e] = g[i][e] * (o[i][e] * pw[i][e]) * (l.s * fmaf(z[i][e], l.sc, 1.f));
-          g[i][e] *= z[i][e] * l.s;
+          h[i][e] *= rstd;
+          dw[i][e] = fmaf(u[i][e], h[i][e], dw[i][e]);
+          u[i][e] *= w[i][e];
+          a = fmaf(u[i][e], h[i][e], a);
         }
-        out.set(dz);
-        if (n > 0) out.store(p.dz, at + c, n);
       }
+      a = group_sum<G>(a, lds[turn]) * inv;
+      turn ^= 1;
+      float b = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
+        Chunk<IO> out;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) g[i][e] = fmaf(rstd, u[i][e] - h[i][e] * a, g[i][e]);
+        out.set(g[i]);
+        if (n > 0) out.store(p.dr, at + c, n);
+        if (!block) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          o[i][e] *= q;
+          g[i][e] *= p.scale;
+        }
+        if (gate) {
+          float dz[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const Logistic l = logistic_f(z[i][e]);
+            dz[e] = g[i][e] * (o[i][e] * pw[i][e]) * (l.s * fmaf(z[i][e], l.sc, 1.f));
+            g[i][e] *= z[i][e] * l.s;
+          }
+          out.set(dz);
+          if (n > 0) out.store(p.dz, at + c, n);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          dpw[i][e] = fmaf(g[i][e], o[i][e], dpw[i][e]);
+          g[i][e] *= pw[i][e];
+          b = fmaf(g[i][e], o[i][e], b);
+        }
+      }
+      if (!block) continue;
+      b = group_sum<G>(b, lds[turn]) * inv;
+      turn ^= 1;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
+        Chunk<IO> out;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) g[i][e] = q * (g[i][e] - o[i][e] * b);
+        out.set(g[i]);
+        if (n > 0) out.store(p.do_, at + c, n);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        dpw[i][e] = fmaf(g[i][e], o[i][e], dpw[i][e]);
-        g[i][e] *= pw[i][e];
-        b = fmaf(g[i][e], o[i][e], b);
+        kept(0, i, e) += dw[i][e];
+        kept(1, i, e) += dpw[i][e];
+        dw[i][e] = dpw[i][e] = 0.f;
       }
-    }
-    if (!block) continue;
-    b = group_sum<G>(b, lds[turn]) * inv;
-    turn ^= 1;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = ((int64_t)i * T + t) * VEC, n = p.D - c;
-      Chunk<IO> out;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) g[i][e] = q * (g[i][e] - o[i][e] * b);
-      out.set(g[i]);
-      if (n > 0) out.store(p.do_, at + c, n);
-    }
   }
   if (!p.part) return;
   float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
@@ -259,6 +276,8 @@ __global__ __launch_bounds__(MOST) void block_norm_bwd_kernel(const BlockNormArg
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       float(&v)[VEC] = which ? dpw[i] : dw[i];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = kept(which, i, e);
 #pragma unroll
       for (int e = 0; e < VEC; ++e)
 #pragma unroll

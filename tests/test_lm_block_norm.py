@@ -187,3 +187,16 @@ def test_column_gradients_do_not_drift():
 @pytest.mark.parametrize("D", [63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1023, 1024, 1025, 2048, 2049, 4096, 4097, 8192, 8193])
 def test_widths_at_which_rows_change_their_shape(io, D):
     check(io, 3, D)
+
+
+@pytest.mark.parametrize("io,rows,D", [("f32", 1 << 22, 64), ("bf16", 1 << 22, 64), ("f32", 1 << 19, 520), ("bf16", 1 << 20, 1100)])
+def test_column_gradients_of_many_rows_do_not_drift(io, rows, D):
+    """Equal rows: a thread adds up at most 64 of them in one fp32 sum, and at most 32 such sums."""
+    import selective_state_space_msm_amd as msm
+    r = torch.full((rows, D), 1.1, device="cuda").to(DT[io])
+    dy = torch.full((rows, D), 0.7, device="cuda").to(DT[io])
+    rstd = torch.full((rows,), 1.3, device="cuda")
+    d = msm.msm_block_norm_bwd(r, dy, rstd, torch.ones(D, device="cuda"))
+    want = rows * (dy[0].double() * (r[0].double() * rstd[0].double()))
+    # 3 roundings of a term, 64 and 32 of a thread's sums, two exchanges and four wavefronts, the result's
+    assert bool(((d["dweight"].double() - want).abs() <= (3 + 64 + 32 + 6 + 1) * 2.0 ** -24 * want).all())
