@@ -9,8 +9,10 @@
 // (stable, digits of up to 9 bits), so that a vocabulary row's places stand side by side in the order
 // of the batch, and every row is summed in that order without atomics.  A frequent token has
 // thousands of places (of log-uniform ids over 65536, the first has 6% of them): aligned runs of 32
-// places that belong to one row are summed beforehand, and runs of 32 such sums again, so that a row
-// adds at most 62 places, 62 sums of 32 and one sum per 1024 places (those in fp64).
+// places that belong to one row are summed beforehand, and from 8192 places on runs of 32 such sums
+// again, so that a row adds at most 62 places, 62 sums of 32 and one sum per 1024 places (those in fp64);
+// of fewer places it adds up to 255 sums of 32.  Where several threads share 16 bytes of a row, what each
+// has summed is joined in fp32, at most 32 sums.
 //
 // A sorting pass is two launches: every wavefront counts the digits of its own places, then each
 // workgroup finds its wavefronts' first positions from the counts of all (at most 256 wavefronts,
