@@ -826,10 +826,9 @@ __host__ __device__ constexpr int few_waves(int pieces) {
 // Joins the largest logit (in units of log 2) and the sum of exponentials of another set of columns.
 __device__ __forceinline__ void join_sums(float& top, float& sum, float top2, float sum2) {
   const float m = fmaxf(top, top2);
-  if (fabsf(m) != INFINITY)
-    sum = sum * exp2_fast(top - m) + sum2 * exp2_fast(top2 - m);
-  else
-    sum += sum2;  // not negative, or NaN; what it is but for that, does not matter beside m
+  // minus infinity: a sum of 0; plus infinity: of infinity (a finite logit's sum is 1 at least); NaN stays
+  const float from = fabsf(m) == INFINITY ? 0.f : m;
+  sum = sum * exp2_fast(top - from) + sum2 * exp2_fast(top2 - from);
   top = m;
 }
 
