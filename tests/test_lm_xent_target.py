@@ -98,3 +98,38 @@ def test_what_was_lost_in_other_calls_is_not_added():
                for v in (0, 255, 66)]
         for d in got[1:]:
             assert torch.equal(d["dx"], got[0]["dx"]) and torch.equal(d["dweight"], got[0]["dweight"])
+
+
+@pytest.mark.parametrize("T,V", [(200, 700), (900, 3000), (4096, 900), (4097, 900), (5000, 60000)])
+def test_captured_and_replayed(T, V):
+    """Counting and sorting the targets in a graph: every replay on new inputs gives what a call of its own gives."""
+    import selective_state_space_msm_amd as msm
+    D = 72
+    gen = torch.Generator().manual_seed(T)
+    sets = []
+    for _ in range(3):
+        x, w, t = (a.cuda() for a in inputs("bf16", T, V, D, 0.2, gen))
+        sets.append((x, w, t, msm.msm_linear_cross_entropy_fwd(x, w, t, return_lse=True)[1], torch.randn(T, generator=gen).cuda()))
+    held = [a.clone() for a in sets[0]]
+    ws = torch.full((msm.msm_linear_cross_entropy_bwd_workspace_bytes(T, V, D, torch.bfloat16),), 255, dtype=torch.uint8, device="cuda")
+    out = {"dx": torch.empty_like(held[0]), "dweight": torch.empty_like(held[1])}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        msm.msm_linear_cross_entropy_bwd(*held, out=out, workspace=ws, stream=s)
+        s.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            msm.msm_linear_cross_entropy_bwd(*held, out=out, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for turn in range(6):
+        now = sets[turn % 3]
+        for a, b in zip(held, now):
+            a.copy_(b)
+        for a in out.values():
+            a.fill_(float("nan"))
+        want = msm.msm_linear_cross_entropy_bwd(*now)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out["dx"], want["dx"]) and torch.equal(out["dweight"], want["dweight"]), turn
