@@ -76,6 +76,13 @@ def test_many_tokens(T, V, D):
     check(T, V, D, ignored=0.02)
 
 
+@pytest.mark.parametrize("T,V,D,words", [(32768, 700, 40, None), (32769, 700, 40, None), (40000, 9000, 72, None), (50000, 300, 520, None),
+                                          (40000, 9000, 64, [0, 3327, 3328, 8999])])
+def test_far_more_tokens(T, V, D, words):
+    """Runs of up to 256 places, in one piece of the vocabulary and several."""
+    check(T, V, D, words, ignored=0.02)
+
+
 @pytest.mark.parametrize("T,V,D,words", [(400, 300, 64, [299]), (5000, 700, 72, [3]), (3000, 5000, 520, [0, 1, 17, 63, 64, 255, 256, 4999])])
 def test_words_of_many_tokens(T, V, D, words):
     check(T, V, D, words)
