@@ -420,7 +420,8 @@ msm_status msm_embed_bwd(const int64_t* ids, const void* dy, void* dtable, int64
  * post_weight: (D,) fp32, NULL meaning ones; rstd, post_rstd: (rows,) fp32, the reciprocal roots of
  * the two norms, written when non-NULL.  z NULL: no gate.  o NULL: y = weight * RMS(r) alone, and
  * post_weight, z, r_out and post_rstd are NULL.  r_out may be r itself (the stream is updated in
- * place); no other overlap.  1 <= rows < 2^31, 1 <= D <= 2^30, rows D <= 2^50, scale finite, eps >= 0
+ * place); no other overlap.  The sum of a row's squares, of o and of r_out, has to stay below 2^128, and
+ * with eps = 0 above 2^-126.  1 <= rows < 2^31, 1 <= D <= 2^30, rows D <= 2^50, scale finite, eps >= 0
  * and finite. */
 msm_status msm_block_norm_fwd(const void* r, const float* weight, const void* o,
                               const float* post_weight, const void* z, void* r_out, void* y,

@@ -14,8 +14,8 @@
 // 16-byte accesses); only a row's last piece may be taken element by element.  The backward's
 // column sums stay in registers over 64 rows of a thread, in LDS over the others, and the workgroups'
 // are joined by a second kernel in a fixed order.  Rows past the registers are walked in memory with fp64 sums.
-// 16384 x 4096, bf16, with block and gate: forward 134 us (5.0 TB/s), backward 207 (5.2 TB/s); a copy of
-// 1 GiB reaches 5.1.  4095 x 1001, fp32, no gate: backward 26 us (3.8 TB/s).
+// 16384 x 4096, bf16, with block and gate: forward 134 us (5.0 TB/s), backward 206 to 210 (5.2 TB/s); a
+// copy of 1 GiB reaches 5.1.  4095 x 1001, fp32, no gate: backward 26 us (3.8 TB/s).
 #include "lm_internal.h"
 #include "ops_internal.h"
 #include "ops_row.hpp"

@@ -23,11 +23,11 @@
 // summed, g too.  Rows without a target are left out of all products: the rows that
 // take part are gathered in front, and what the others hold is never multiplied.
 //
-// 7780 of 8192 tokens take part, 65536 words, D = 2048, bf16: forward 1655 us (1262 TFLOP/s over those rows,
-// the products alone 1358 over whole tiles), backward 5135 (1220); a library product of 8192^3 reaches 1200 to
-// 1240.  What bounds the products is the clock under matrix load (1.9 to 2.1 GHz) and the matrix units, busy
-// 61 to 70% of it.  16 tokens, D = 4096: 98 us, 5.5 TB/s of weights.  fp32, 1000 of 1999 tokens of 10007,
-// D = 513, backward: 280 us, six bf16 products for each of fp32.
+// 7780 of 8192 tokens take part, 65536 words, D = 2048, bf16: forward 1602 to 1682 us (1242 to 1304 TFLOP/s over
+// those rows, the products alone 1306 over whole tiles in a run of 1680), backward 5115 to 5270 (1189 to 1225); a
+// library product of 8192^3 reaches 1200 to 1240.  What bounds the products is the clock under matrix load (1.85 to
+// 2.05 GHz) and the matrix units, busy 61 to 70% of it.  16 tokens, D = 4096: 100 us, 5.4 TB/s of weights.  fp32,
+// 1000 of 1999 tokens of 10007, D = 513, backward: 278 to 290 us, six bf16 products for each of fp32.
 #include "lm_internal.h"
 #include "ops_row.hpp"
 
@@ -881,7 +881,8 @@ __device__ __forceinline__ void sync_lds_only() {
 // HOLD: a wavefront's pieces of k, at most kFewHeld, have their tokens in registers throughout (x is p.x),
 // and a tile's weights are loaded during the tile before; else the tokens are read again for every tile, in
 // the matrix cores' order (x is p.xp).  16 tokens of 65536, D = 4096, bf16: 93 and 116 us.
-// (fp32 tokens in three parts do not fit the registers: 16 of 65536, D = 4096, 250 us, 4.3 TB/s.)
+// (fp32 tokens in three parts do not fit the registers: 16 of 65536, D = 4096, 264 us, 4.1 TB/s; 17 to 32 bf16
+// tokens spill 28 to 40 bytes a thread: 20 of 65536 118 us.)
 template <typename IO, int NT, bool HOLD, bool ALL>
 __global__ __launch_bounds__(64 * kFewWaves) void xent_few_kernel(const XentArgs p, int tiles) {
   constexpr int kAhead = HOLD ? kFewHeld : kFewHeld / (NT * (io<IO>::es / 2));  // what the registers hold
